@@ -319,7 +319,7 @@ def _turn64(x, pos, rot, interleaved):
 
 def _act64(name, p):
     if name == "relu":
-        return p.clamp(min=0)
+        return torch.relu(p)                   # slope 0 at 0
     if name == "gelu":
         return p * torch.special.ndtr(p)
     if name == "gelu_tanh":                    # (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
