@@ -363,8 +363,8 @@ DIFFUSER_API int diffuser_qkv_projection(const void* X, const void* Wqkv, int64_
 /* Y[b][i] = concat_h Z[b][h][i] . Wo^T (the heads' concatenation and W_O). */
 DIFFUSER_API int diffuser_output_projection(const void* Z, const void* Wo, int64_t B, int64_t n, int32_t D,
                                             int32_t H, int32_t d, void* Y, diffuser_stream stream);
-/* Read (synchronously) the stand-alone projections' status word of the
- * current device; reset != 0 clears it. */
+/* Read (synchronously) the status word of the stand-alone projections and the
+ * dense products on the current device; reset != 0 clears it. */
 DIFFUSER_API int diffuser_projection_status(int* status, int reset);
 
 /*
@@ -381,6 +381,136 @@ DIFFUSER_API int diffuser_layer_forward(const void* X, const void* Wqkv, const v
                                         int32_t D, int32_t H, int32_t d, const diffuser_graph* g,
                                         int32_t hops, float alpha, void* Y, void* workspace,
                                         size_t workspace_bytes, diffuser_stream stream);
+
+/* ---------------------------------------------------------------- operators around the module
+ *
+ * What a transformer layer around the diffusion module needs besides it: norms of
+ * queries and keys with the position rotation (between the projection and the
+ * forward), the dense product with bias, activation and residual (the output
+ * projection with its residual, the feed-forward's products) and the gated product
+ * (the feed-forward's first half), each with its backward pass.  (The pages leave
+ * the residual and the feed-forward outside the module.)  All are asynchronous on
+ * `stream`, may be captured into a CUDA graph (the first call on a device too), use
+ * no atomics (repeated calls give identical bits) and accept a token count of 0 (forward: nothing
+ * is written; backward: the weights' gradients are set to 0).  Tensors are
+ * contiguous and 16-byte aligned, on the current device.  Unless stated otherwise
+ * an output may not overlap an input, another output or the workspace.
+ */
+
+/*
+ * Norms and rotation: every row x of 64 features (a token of a head) becomes
+ *   y = R(p) (r x w),  r = (mean x^2 + eps)^(-1/2),
+ * where R(p) turns pair i (i < rotary_dim / 2) by p theta^(-2i / rotary_dim)
+ * radians: (a, b) -> (a cos - b sin, a sin + b cos).  The pair is the features
+ * (i, i + rotary_dim / 2), or (2i, 2i + 1) with interleaved != 0; the features from
+ * rotary_dim on are not turned.
+ *   Q, Qo       device [B][Hq][n][64] in dtype      (Qo may be Q itself)
+ *   K, Ko       device [B][Hk][n][64] in dtype      (Ko may be K itself)
+ *   q_weight, k_weight   device [64] in dtype, or NULL (ones)
+ *   eps         > 0;  theta  >= 1;  rotary_dim  0, 16, 32, 48 or 64
+ *   positions   device int64 [B][n], any values; NULL: token i is at position i
+ *   position_offset      added to every position (a prompt's continuation, a
+ *               single new token)
+ *   B, n >= 0;  Hq, Hk 1..4096
+ * Angles are exact in the position (integer arithmetic modulo one turn); all else
+ * is fp32 with one rounding to dtype.  Errors: INVALID_ARG, UNSUPPORTED (d, dtype,
+ * rotary_dim), OVERFLOW, CUDA.
+ */
+DIFFUSER_API int diffuser_qk_norm_rope(const void* Q, const void* K, int32_t dtype, int64_t B, int64_t Hq,
+                                       int64_t Hk, int64_t n, int32_t d, const void* q_weight,
+                                       const void* k_weight, float eps, double theta, int32_t rotary_dim,
+                                       int32_t interleaved, const int64_t* positions,
+                                       int64_t position_offset, void* Qo, void* Ko,
+                                       diffuser_stream stream);
+/*
+ * Gradients of the above for dQo, dKo (shaped as Qo, Ko), recomputing r from Q and
+ * K: with g = R(-p) dy, dn = g w and xh = r x,
+ *   dx = r (dn - xh mean(dn xh)),   dw = sum over all rows of g xh  (fp32 sums).
+ * dQ, dK are written; dq_weight, dk_weight may be NULL, and must be where their
+ * weight is.  workspace: diffuser_qk_norm_rope_backward_workspace_size bytes,
+ * 256-byte aligned.  Errors: as above, WORKSPACE.
+ */
+DIFFUSER_API int diffuser_qk_norm_rope_backward_workspace_size(int64_t B, int64_t Hq, int64_t Hk, int64_t n,
+                                                               int32_t d, size_t* bytes);
+DIFFUSER_API int diffuser_qk_norm_rope_backward(const void* Q, const void* K, const void* dQo,
+                                                const void* dKo, int32_t dtype, int64_t B, int64_t Hq,
+                                                int64_t Hk, int64_t n, int32_t d, const void* q_weight,
+                                                const void* k_weight, float eps, double theta,
+                                                int32_t rotary_dim, int32_t interleaved,
+                                                const int64_t* positions, int64_t position_offset,
+                                                void* dQ, void* dK, void* dq_weight, void* dk_weight,
+                                                void* workspace, size_t workspace_bytes,
+                                                diffuser_stream stream);
+
+/* Activations of the dense and the gated product. */
+typedef enum {
+    DIFFUSER_ACT_NONE = 0,
+    DIFFUSER_ACT_RELU = 1,        /* max(p, 0); slope 0 at 0 */
+    DIFFUSER_ACT_GELU = 2,        /* p Phi(p), Phi the normal distribution function */
+    DIFFUSER_ACT_GELU_TANH = 3,   /* p (1 + tanh(sqrt(2/pi) (p + 0.044715 p^3))) / 2 */
+    DIFFUSER_ACT_SILU = 4         /* p / (1 + exp(-p)) */
+} diffuser_activation;
+
+/*
+ * Dense product with its epilogue, on the tcgen05 tensor cores (bf16 operands, fp32
+ * accumulation; bias, activation and residual in fp32, one rounding to bf16):
+ *   P = X W^T + bias,   Y = act(P) + residual.
+ *   X           device bf16 [T][D]
+ *   W           device bf16 [F][D]   ([out][in], as the projections' weights)
+ *   bias        device bf16 [F] or NULL
+ *   residual    device bf16 [T][F] or NULL; Y may be residual itself
+ *   Y           device bf16 [T][F]
+ *   pre         device bf16 [T][F] or NULL: P, kept for the backward pass
+ * T 0..2^30; D, F multiples of 8, at most 65536.  A kernel whose bounded wait gives
+ * up reports through diffuser_projection_status, as the projections do.
+ * Errors: INVALID_ARG, UNSUPPORTED, OVERFLOW, ALLOC, CUDA, DEVICE.
+ */
+DIFFUSER_API int diffuser_linear(const void* X, const void* W, const void* bias, const void* residual,
+                                 int64_t T, int32_t D, int32_t F, int32_t activation, void* Y, void* pre,
+                                 diffuser_stream stream);
+/*
+ * Its gradients for dY [T][F]:  dP = dY act'(P) (P as kept in pre; pre is not read
+ * with DIFFUSER_ACT_NONE),
+ *   dX = dP W,   dW = dP^T X,   dbias = column sums of dP
+ * (the residual's gradient is dY itself).  dX, dW, dbias: bf16, shaped as X, W, bias;
+ * a NULL one is not computed.  With an activation dP is rounded to bf16 once, as the
+ * operand of the two products; dbias is summed in fp32 before that rounding.
+ * workspace: diffuser_linear_backward_workspace_size bytes, 256-byte aligned.
+ * Errors: as diffuser_linear, WORKSPACE.
+ */
+DIFFUSER_API int diffuser_linear_backward_workspace_size(int64_t T, int32_t D, int32_t F,
+                                                         int32_t activation, size_t* bytes);
+DIFFUSER_API int diffuser_linear_backward(const void* X, const void* W, const void* dY, const void* pre,
+                                          int64_t T, int32_t D, int32_t F, int32_t activation, void* dX,
+                                          void* dW, void* dbias, void* workspace, size_t workspace_bytes,
+                                          diffuser_stream stream);
+
+/*
+ * Gated product: both projections, the activation and the product in one kernel,
+ *   G = X Wg^T,  U = X Wu^T,  H = act(G) U,
+ * G and U staying in the accumulators (fp32) unless they are asked for.
+ *   X           device bf16 [T][D]
+ *   Wgu         device bf16 [2 F][D]: Wg's F rows, then Wu's
+ *   H           device bf16 [T][F]
+ *   pre         device bf16 [T][2 F] or NULL: G's columns, then U's, for the backward
+ * T, D, F, status and errors as diffuser_linear.
+ */
+DIFFUSER_API int diffuser_gated_linear(const void* X, const void* Wgu, int64_t T, int32_t D, int32_t F,
+                                       int32_t activation, void* H, void* pre, diffuser_stream stream);
+/*
+ * Its gradients for dH [T][F], with G and U as kept in pre:
+ *   dG = dH act'(G) U,  dU = dH act(G)  (rounded to bf16 once, as operands),
+ *   dX = dG Wg + dU Wu,   dWgu = [dG | dU]^T X.
+ * dX, dWgu: bf16, shaped as X, Wgu; a NULL one is not computed.  workspace:
+ * diffuser_gated_linear_backward_workspace_size bytes, 256-byte aligned.
+ * Errors: as diffuser_gated_linear, WORKSPACE.
+ */
+DIFFUSER_API int diffuser_gated_linear_backward_workspace_size(int64_t T, int32_t D, int32_t F,
+                                                               size_t* bytes);
+DIFFUSER_API int diffuser_gated_linear_backward(const void* X, const void* Wgu, const void* dH,
+                                                const void* pre, int64_t T, int32_t D, int32_t F,
+                                                int32_t activation, void* dX, void* dWgu, void* workspace,
+                                                size_t workspace_bytes, diffuser_stream stream);
 
 /* ---------------------------------------------------------------- no-allocation forward */
 

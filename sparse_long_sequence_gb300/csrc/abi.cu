@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "internal.h"
+#include "layer_ops.h"
 
 namespace dfs {
 
@@ -907,16 +908,45 @@ int diffuser_forward_per_head(const void* Q, const void* K, const void* V, int32
 
 namespace {
 
-// Status block of the stand-alone projections on each device (the layout of a
-// graph's: word, padding, device address of a page-locked host mirror), made
-// on the first projection call on that device and kept for the process.
-struct ProjStatus {
-    int* d = nullptr;
-    int* h = nullptr;
-};
+// Status block of the stand-alone projections and dense products on each device
+// (the layout of a graph's: word, padding, device address of a page-locked host
+// mirror), made on the first such call on that device and kept for the process.
 std::mutex g_proj_mu;
 ProjStatus g_proj_status[kMaxReplayDevices];
 
+int make_projection_status(ProjStatus* ps) {
+    int* d = nullptr;
+    int* h = nullptr;
+    int* mirror_dev = nullptr;
+    cudaStream_t s = nullptr;
+    unsigned char block[kStatusBlockBytes] = {0};
+    cudaError_t err = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (err == cudaSuccess) err = cudaMalloc(&d, kStatusBlockBytes);
+    if (err == cudaSuccess) err = cudaHostAlloc(&h, sizeof(int), cudaHostAllocMapped);
+    if (err == cudaSuccess) {
+        *h = 0;
+        err = cudaHostGetDevicePointer(&mirror_dev, h, 0);
+    }
+    if (err == cudaSuccess) {
+        std::memcpy(block + 8, &mirror_dev, sizeof(mirror_dev));
+        err = cudaMemcpyAsync(d, block, kStatusBlockBytes, cudaMemcpyHostToDevice, s);
+    }
+    if (err == cudaSuccess) err = cudaStreamSynchronize(s);
+    if (s) cudaStreamDestroy(s);
+    if (err != cudaSuccess) {
+        cudaFree(d);
+        if (h) cudaFreeHost(h);
+        return cuda_fail(err, "projection status block");
+    }
+    ps->d = d;
+    ps->h = h;
+    return DIFFUSER_OK;
+}
+}  // namespace
+
+}  // extern "C"
+
+namespace dfs {
 int projection_status(ProjStatus* out) {
     int dev = -1;
     cudaError_t err = cudaGetDevice(&dev);
@@ -925,31 +955,21 @@ int projection_status(ProjStatus* out) {
     std::lock_guard<std::mutex> lk(g_proj_mu);
     ProjStatus& ps = g_proj_status[dev];
     if (!ps.d) {
-        int* d = nullptr;
-        int* h = nullptr;
-        int* mirror_dev = nullptr;
-        err = cudaMalloc(&d, kStatusBlockBytes);
-        if (err == cudaSuccess) err = cudaHostAlloc(&h, sizeof(int), cudaHostAllocMapped);
-        if (err == cudaSuccess) {
-            *h = 0;
-            err = cudaHostGetDevicePointer(&mirror_dev, h, 0);
-        }
-        if (err == cudaSuccess) {
-            unsigned char block[kStatusBlockBytes] = {0};
-            std::memcpy(block + 8, &mirror_dev, sizeof(mirror_dev));
-            err = cudaMemcpy(d, block, kStatusBlockBytes, cudaMemcpyHostToDevice);
-        }
-        if (err != cudaSuccess) {
-            cudaFree(d);
-            if (h) cudaFreeHost(h);
-            return cuda_fail(err, "projection status block");
-        }
-        ps.d = d;
-        ps.h = h;
+        // the caller's stream may be capturing: the block is made outside the capture
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        const int st = make_projection_status(&ps);
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (st) return st;
     }
     *out = ps;
     return DIFFUSER_OK;
 }
+}  // namespace dfs
+
+extern "C" {
+
+namespace {
 
 int check_projection_pointers(const void* const* in, int nin, void* const* outs, int nout,
                               const size_t* in_bytes, const size_t* out_bytes) {

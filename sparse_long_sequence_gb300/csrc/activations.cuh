@@ -1,0 +1,86 @@
+// The activations of the dense and gated products and their slopes, in fp32.
+//   relu       max(p, 0), slope 0 at p <= 0
+//   gelu       p Phi(p), Phi the normal distribution function
+//   gelu_tanh  p (1 + tanh u) / 2 = p / (1 + exp(-2u)), u = sqrt(2/pi) (p + 0.044715 p^3):
+//              the second form has no cancellation for p far below 0
+//   silu       p / (1 + exp(-p))
+// The logistic function uses the hardware exponential and reciprocal (relative
+// error below 2^-20, far under the results' bf16 half step 2^-9); its argument
+// saturates to exactly 0 and 1, so that infinite p give their limits.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/diffuser.h"
+#include "sm100_ptx.cuh"
+
+namespace dfs {
+namespace act {
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 1 / (1 + exp(-x))
+__device__ __forceinline__ float logistic(float x) {
+    return rcp_approx(1.f + ptx::ex2_approx(-1.4426950408889634f * x));
+}
+constexpr float kTanhC = 0.7978845608028654f;      // sqrt(2 / pi)
+constexpr float kTanhA = 0.044715f;
+constexpr float kPhiC = 0.3989422804014327f;       // 1 / sqrt(2 pi)
+
+// x * s with s in [0, 1] a saturating factor: 0 where s is 0 (x may be -inf there)
+__device__ __forceinline__ float gate(float x, float s) { return s == 0.f && x < 0.f ? 0.f : x * s; }
+
+template <int kAct>
+__device__ __forceinline__ float value(float p) {
+    if constexpr (kAct == DIFFUSER_ACT_RELU) {
+        return p > 0.f ? p : (p != p ? p : 0.f);
+    } else if constexpr (kAct == DIFFUSER_ACT_GELU) {
+        // erfc keeps the lower tail's digits
+        return gate(p, 0.5f * erfcf(-0.7071067811865476f * p));
+    } else if constexpr (kAct == DIFFUSER_ACT_GELU_TANH) {
+        return gate(p, logistic(2.f * kTanhC * p * fmaf(kTanhA * p, p, 1.f)));
+    } else if constexpr (kAct == DIFFUSER_ACT_SILU) {
+        return gate(p, logistic(p));
+    }
+    return p;
+}
+
+// value and slope at p
+template <int kAct>
+__device__ __forceinline__ float2 value_slope(float p) {
+    if constexpr (kAct == DIFFUSER_ACT_RELU) {
+        return make_float2(value<kAct>(p), p > 0.f ? 1.f : (p != p ? p : 0.f));
+    } else if constexpr (kAct == DIFFUSER_ACT_GELU) {
+        const float s = 0.5f * erfcf(-0.7071067811865476f * p);
+        const float e = ptx::ex2_approx(-0.7213475204444817f * p * p);   // exp(-p^2 / 2)
+        return make_float2(gate(p, s), s + (e == 0.f ? 0.f : p * e * kPhiC));
+    } else if constexpr (kAct == DIFFUSER_ACT_GELU_TANH) {
+        const float p2 = p * p;
+        const float s = logistic(2.f * kTanhC * p * fmaf(kTanhA, p2, 1.f));
+        const float q = s * (1.f - s);
+        return make_float2(gate(p, s),
+                           s + (q == 0.f ? 0.f : 2.f * kTanhC * p * q * fmaf(3.f * kTanhA, p2, 1.f)));
+    } else if constexpr (kAct == DIFFUSER_ACT_SILU) {
+        const float s = logistic(p);
+        const float q = s * (1.f - s);
+        return make_float2(gate(p, s), s + (q == 0.f ? 0.f : p * q));
+    }
+    return make_float2(p, 1.f);
+}
+
+// value<act> for an activation known at run time (uniform over the launch)
+__device__ __forceinline__ float value_of(int a, float p) {
+    switch (a) {
+        case DIFFUSER_ACT_RELU: return value<DIFFUSER_ACT_RELU>(p);
+        case DIFFUSER_ACT_GELU: return value<DIFFUSER_ACT_GELU>(p);
+        case DIFFUSER_ACT_GELU_TANH: return value<DIFFUSER_ACT_GELU_TANH>(p);
+        case DIFFUSER_ACT_SILU: return value<DIFFUSER_ACT_SILU>(p);
+        default: return p;
+    }
+}
+
+}  // namespace act
+}  // namespace dfs

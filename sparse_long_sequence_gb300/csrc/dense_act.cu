@@ -1,0 +1,205 @@
+// The elementwise half of the dense products' backward passes.
+//
+//   dense   dP[t][f] = dY[t][f] act'(P[t][f]),  db[f] = sum_t dP[t][f]
+//   gated   dP[t][f] = dH[t][f] act'(g) u,  dP[t][F + f] = dH[t][f] act(g),
+//           g = P[t][f], u = P[t][F + f]
+// dP is the operand of the two tensor-core products that follow, so it is rounded to
+// bf16 here; the bias gradient is summed in fp32 from the unrounded values, over a
+// block's rows and then over the blocks in a fixed order.
+// Bound by memory: every array is read or written once, 16 bytes a lane.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "activations.cuh"
+#include "layer_ops.h"
+
+namespace dfs {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kPer = 8;                          // columns of a lane (16 bytes)
+constexpr int kBlockCols = 32 * kPer;            // columns of a block; its warps take rows in turn
+
+__device__ __forceinline__ void widen8(const uint4& r, float (&v)[kPer]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 round8(const float (&v)[kPer]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// block (x, y): columns 256 x .. +255, rows [y chunk, (y + 1) chunk)
+template <int kAct>
+__global__ void __launch_bounds__(kThreads)
+act_backward_kernel(const __nv_bfloat16* dY, const __nv_bfloat16* P, int64_t rows, int32_t F, int64_t chunk,
+                    __nv_bfloat16* dP, float* partial) {
+    __shared__ float sums[kWarps][kBlockCols];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = (int)blockIdx.x * kBlockCols + lane * kPer;
+    const int64_t r1 = min(rows, ((int64_t)blockIdx.y + 1) * chunk);
+    float sum[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) sum[j] = 0.f;
+    if (c < F) {
+#pragma unroll 2
+        for (int64_t r = (int64_t)blockIdx.y * chunk + warp; r < r1; r += kWarps) {
+            float d[kPer];
+            widen8(load8(dY + r * F + c), d);
+            if constexpr (kAct != DIFFUSER_ACT_NONE) {
+                float p[kPer];
+                widen8(load8(P + r * F + c), p);
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) d[j] *= act::value_slope<kAct>(p[j]).y;
+                *reinterpret_cast<uint4*>(dP + r * F + c) = round8(d);
+            }
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) sum[j] += d[j];
+        }
+    }
+    if (!partial) return;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) sums[warp][lane * kPer + j] = sum[j];
+    __syncthreads();
+    const int col = (int)blockIdx.x * kBlockCols + (int)threadIdx.x;
+    if (col >= F) return;
+    float t = 0.f;
+    for (int w = 0; w < kWarps; ++w) t += sums[w][threadIdx.x];
+    partial[(int64_t)blockIdx.y * F + col] = t;
+}
+
+// column sums over the chunks: 32 columns a block, its warps take every eighth chunk
+__global__ void __launch_bounds__(kThreads) colsum_kernel(const float* partial, int64_t chunks, int32_t F, __nv_bfloat16* out) {
+    __shared__ float sums[kWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int col = (int)blockIdx.x * 32 + lane;
+    float t = 0.f;
+    if (col < F)
+        for (int64_t k = warp; k < chunks; k += kWarps) t += partial[k * F + col];
+    sums[warp][lane] = t;
+    __syncthreads();
+    if (warp || col >= F) return;
+    t = 0.f;
+    for (int w = 0; w < kWarps; ++w) t += sums[w][lane];
+    out[col] = __float2bfloat16_rn(t);
+}
+
+template <int kAct>
+__global__ void __launch_bounds__(kThreads)
+gated_backward_kernel(const __nv_bfloat16* dH, const __nv_bfloat16* P, int64_t items, int32_t F8, __nv_bfloat16* dP) {
+    const int64_t F = (int64_t)F8 * kPer;
+    for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < items; e += (int64_t)gridDim.x * kThreads) {
+        const int64_t r = e / F8, c = (e - r * F8) * kPer;
+        float d[kPer], g[kPer], u[kPer];
+        widen8(load8(dH + r * F + c), d);
+        widen8(load8(P + r * 2 * F + c), g);
+        widen8(load8(P + r * 2 * F + F + c), u);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const float2 vs = act::value_slope<kAct>(g[j]);
+            const float dh = d[j];
+            d[j] = dh * u[j] * vs.y;
+            u[j] = dh * vs.x;
+        }
+        *reinterpret_cast<uint4*>(dP + r * 2 * F + c) = round8(d);
+        *reinterpret_cast<uint4*>(dP + r * 2 * F + F + c) = round8(u);
+    }
+}
+
+// one instantiation per activation
+template <template <int> class Launch, class... Args>
+void by_activation(int32_t act, Args... args) {
+    switch (act) {
+        case DIFFUSER_ACT_RELU: Launch<DIFFUSER_ACT_RELU>::go(args...); break;
+        case DIFFUSER_ACT_GELU: Launch<DIFFUSER_ACT_GELU>::go(args...); break;
+        case DIFFUSER_ACT_GELU_TANH: Launch<DIFFUSER_ACT_GELU_TANH>::go(args...); break;
+        case DIFFUSER_ACT_SILU: Launch<DIFFUSER_ACT_SILU>::go(args...); break;
+        default: Launch<DIFFUSER_ACT_NONE>::go(args...); break;
+    }
+}
+template <int kAct>
+struct DenseBackward {
+    static void go(dim3 grid, cudaStream_t s, const __nv_bfloat16* dY, const __nv_bfloat16* P, int64_t rows, int32_t F,
+                   int64_t chunk, __nv_bfloat16* dP, float* partial) {
+        act_backward_kernel<kAct><<<grid, kThreads, 0, s>>>(dY, P, rows, F, chunk, dP, partial);
+    }
+};
+template <int kAct>
+struct GatedBackward {
+    static void go(dim3 grid, cudaStream_t s, const __nv_bfloat16* dH, const __nv_bfloat16* P, int64_t items, int32_t F8,
+                   __nv_bfloat16* dP) {
+        gated_backward_kernel<kAct><<<grid, kThreads, 0, s>>>(dH, P, items, F8, dP);
+    }
+};
+
+constexpr int64_t kManyBlocks = 152 * 8;         // the blocks that are resident at once
+
+int64_t chunk_rows(int64_t rows, int32_t F) {
+    const int64_t col_blocks = (F + kBlockCols - 1) / kBlockCols;
+    const int64_t want = (kManyBlocks + col_blocks - 1) / col_blocks;
+    const int64_t per = (rows + want - 1) / want;
+    // at least two rows a warp, and at most 65535 chunks (the grid's y extent)
+    const int64_t least = rows / 65535 + 1;
+    const int64_t c = per < 2 * kWarps ? 2 * kWarps : per;
+    return c < least ? least : c;
+}
+
+}  // namespace
+
+int64_t act_chunks(int64_t rows, int32_t F) {
+    if (rows <= 0) return 0;
+    const int64_t c = chunk_rows(rows, F);
+    return (rows + c - 1) / c;
+}
+
+int launch_act_backward(const void* dY, const void* P, int64_t rows, int32_t F, int32_t act, void* dP, void* colsum,
+                        float* partial, cudaStream_t stream) {
+    const int64_t chunk = chunk_rows(rows, F), chunks = act_chunks(rows, F);
+    const dim3 grid((unsigned)((F + kBlockCols - 1) / kBlockCols), (unsigned)chunks);
+    {
+        LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
+        by_activation<DenseBackward>(act, grid, stream, static_cast<const __nv_bfloat16*>(dY),
+                                     static_cast<const __nv_bfloat16*>(P), rows, F, chunk,
+                                     static_cast<__nv_bfloat16*>(dP), colsum ? partial : nullptr);
+    }
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return cuda_fail(err, "act_backward_kernel");
+    if (!colsum) return DIFFUSER_OK;
+    {
+        LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
+        colsum_kernel<<<(unsigned)((F + 31) / 32), kThreads, 0, stream>>>(partial, chunks, F,
+                                                                         static_cast<__nv_bfloat16*>(colsum));
+    }
+    err = cudaGetLastError();
+    return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "colsum_kernel");
+}
+
+int launch_gated_backward(const void* dH, const void* P, int64_t rows, int32_t F, int32_t act, void* dP,
+                          cudaStream_t stream) {
+    const int64_t items = rows * (F / kPer);
+    int64_t blocks = (items + kThreads - 1) / kThreads;
+    if (blocks > kManyBlocks) blocks = kManyBlocks;
+    {
+        LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
+        by_activation<GatedBackward>(act, dim3((unsigned)blocks), stream, static_cast<const __nv_bfloat16*>(dH),
+                                     static_cast<const __nv_bfloat16*>(P), items, F / kPer,
+                                     static_cast<__nv_bfloat16*>(dP));
+    }
+    const cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "gated_backward_kernel");
+}
+
+}  // namespace dfs

@@ -1,0 +1,94 @@
+// Internal declarations of the operators around the module: the per-head norms
+// with the position rotation (qk_norm_rope.cu), the dense product with its
+// epilogue and the gated product (dense_split.cu, dense_act.cu), and their entry
+// points (layer_ops_abi.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include <cstdint>
+
+#include "internal.h"
+
+namespace dfs {
+
+// Status block of the projections and dense products on the current device
+// (abi.cu): the block's device address and its page-locked host mirror.
+struct ProjStatus {
+    int* d = nullptr;
+    int* h = nullptr;
+};
+int projection_status(ProjStatus* out);
+int check_workspace_bytes(size_t need, void* ws, size_t ws_bytes);
+
+// cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel and device.
+// `done` is the kernel's own word, one bit per device.
+template <class Kernel>
+cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (err == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return err;
+}
+
+// ---- norms and rotation (qk_norm_rope.cu) ------------------------------------
+struct QkArgs {
+    const void *q, *k;              // [B][Hq][n][64], [B][Hk][n][64]
+    const void *dqo, *dko;          // backward: gradients of the results
+    void *qo, *ko;                  // results (forward) or gradients dQ, dK
+    const void *wq, *wk;            // [64] or null (ones)
+    const int64_t* pos;             // [B][n] or null
+    int64_t pos0;                   // added to every position
+    int64_t tokens;                 // B n
+    int64_t n;
+    int32_t Hq, Hk;
+    int32_t rot;                    // rotated features: 0, 16, 32, 48, 64
+    float eps;
+    float* partial;                 // backward: [blocks][2][64] sums of the weight gradients
+    uint64_t freq[kHeadDim / 2];    // turns per position of pair i, in units of 2^-64
+};
+int launch_qk_norm_rope(const QkArgs& a, int32_t dtype, bool interleaved, cudaStream_t stream);
+// blocks of the backward kernel (rows of `partial`)
+int64_t qk_backward_blocks(int64_t tokens, int64_t heads);
+int launch_qk_norm_rope_backward(const QkArgs& a, int32_t dtype, bool interleaved, void* dwq, void* dwk,
+                                 cudaStream_t stream);
+
+// ---- dense products (dense_split.cu) -----------------------------------------
+// Which product: Y[t][f] = sum_k X[t][k] W[f][k] (forward),
+// dX[t][k] = sum_f dP[t][f] W[f][k], dW[f][k] = sum_t dP[t][f] X[t][k].
+enum DenseForm { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
+
+struct DenseArgs {
+    const void* a;                  // left matrix: X (forward), dP (both gradients)
+    const void* b;                  // right matrix: W (forward, input gradient), X (weight gradient)
+    int64_t rows;                   // tokens T
+    int32_t inner;                  // D: width of X and of W's rows
+    int32_t cols;                   // width of dP; rows of W (2 F for the gated product)
+    void* out;                      // bf16; forward [T][cols] or [T][F] (gated), dX [T][D], dW [cols][D]
+    void* pre;                      // forward: bf16 [T][cols] or null
+    const void* bias;               // forward: bf16 [cols] or null
+    const void* residual;           // forward: bf16 [T][cols] or null
+    int32_t act;                    // forward: diffuser_activation
+    bool gated;                     // forward: out = act(P[:, :F]) * P[:, F:], F = cols / 2
+    int* status;
+};
+int launch_dense(DenseForm form, const DenseArgs& a, cudaStream_t stream);
+
+// ---- the activations' backward (dense_act.cu) --------------------------------
+// dP[t][f] = dY[t][f] act'(P[t][f]); colsum (or null): bf16 [F], the column sums
+// of dP in fp32 through `partial` ([act_chunks][F]).  dP may be null with act none
+// (dP is dY itself).
+int64_t act_chunks(int64_t rows, int32_t F);
+int launch_act_backward(const void* dY, const void* P, int64_t rows, int32_t F, int32_t act, void* dP,
+                        void* colsum, float* partial, cudaStream_t stream);
+// gated: P [T][2F]; dP[t][f] = dH act'(g) u, dP[t][F + f] = dH act(g)
+int launch_gated_backward(const void* dH, const void* P, int64_t rows, int32_t F, int32_t act, void* dP,
+                          cudaStream_t stream);
+
+}  // namespace dfs
