@@ -11,6 +11,7 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -462,62 +463,72 @@ DIFFUSER_ACT_NONE, DIFFUSER_ACT_RELU, DIFFUSER_ACT_GELU = 0, 1, 2
 DIFFUSER_ACT_GELU_TANH, DIFFUSER_ACT_SILU = 3, 4
 
 
-class _On:
-    """Runs a call on its tensors' device and on `stream`: what is allocated inside
-    (outputs, workspace) belongs to that stream, so that a workspace freed on return
-    is not handed to another stream while the kernels still use it."""
+def _on_stream(op):
+    """Runs `op` on its first tensor's device and on `stream` (None: that device's current
+    stream), given to it as an address.  What it allocates (outputs, workspace) belongs to
+    that stream, so that a workspace freed on return is not handed to another stream while
+    the kernels still use it."""
+    name = op.__code__.co_varnames[0]
 
-    def __init__(self, t, stream):
+    @functools.wraps(op)
+    def call(*args, stream=None, **kw):
         import torch
-        if not t.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
-        if stream is not None and stream.device != t.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-        self._ctx = None
+        first = args[0] if args else kw.get(name)
+        if first is None or not first.is_cuda:
+            raise ValueError(f"{name} must be a tensor on a CUDA device")
+        dev = first.get_device()
         if stream is not None:
-            self._ctx = torch.cuda.stream(stream)
-        elif t.device.index != torch.cuda.current_device():
-            self._ctx = torch.cuda.device(t.device)
-        self._stream = stream
-
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return _stream(self._stream)
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+            if stream.device != first.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
+            with torch.cuda.stream(stream):
+                return op(*args, stream=stream.cuda_stream, **kw)
+        if dev != torch._C._cuda_getDevice():
+            with torch.cuda.device(dev):
+                return op(*args, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
+        return op(*args, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
+    return call
 
 
-def _need(t, name, shape, dtype, device, optional=False):
-    """The tensor's address, after its checks (None where it is optional and absent)."""
+def _refuse(t, name, shape, like, dtype):
     if t is None:
-        if optional:
-            return None
         raise ValueError(f"{name} is needed")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _need(t, name, shape, like, dtype=None):
+    """The tensor's address, after its checks against `like` (dtype unless given, device)."""
+    dtype = dtype or like.dtype
+    if t is None or t.dtype != dtype or t.shape != shape or t.get_device() != like.get_device() or \
+            not t.is_contiguous():
+        _refuse(t, name, shape, like, dtype)
     return t.data_ptr()
+
+
+def _may(t, name, shape, like, dtype=None):
+    """As _need; None where the tensor is left out."""
+    return None if t is None else _need(t, name, shape, like, dtype)
 
 
 def _empty(t, shape, like):
     """`t`, or a new tensor of that shape in like's dtype and device."""
-    return like.new_empty(shape) if t is None else t
+    if t is not None:
+        return t
+    import torch
+    return torch.empty(shape, dtype=like.dtype, device=like.device)
 
 
-def _workspace(workspace, nbytes, device):
+def _workspace(workspace, nbytes, like):
     import torch
     if workspace is None:
-        return alloc_workspace(nbytes, device)
-    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+        return alloc_workspace(nbytes, like.device)
+    if workspace.device != like.device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {like.device}")
     return workspace
 
 
@@ -529,6 +540,7 @@ def _qk_shapes(Q, K):
     return code, B, Hq, K.shape[1], n, d
 
 
+@_on_stream
 def diffuser_qk_norm_rope(Q, K, q_weight=None, k_weight=None, positions=None, position_offset: int = 0,
                           eps: float = 1e-6, theta: float = 10000.0, rotary_dim: int = 64,
                           interleaved: bool = False, Qo=None, Ko=None, stream=None):
@@ -537,15 +549,13 @@ def diffuser_qk_norm_rope(Q, K, q_weight=None, k_weight=None, positions=None, po
     Qo=Q and Ko=K work in place."""
     import torch
     code, B, Hq, Hk, n, d = _qk_shapes(Q, K)
-    dev, dt = Q.device, Q.dtype
-    with _On(Q, stream) as s:
-        Qo, Ko = _empty(Qo, Q.shape, Q), _empty(Ko, K.shape, Q)
-        _check(_lib.diffuser_qk_norm_rope(
-            _need(Q, "Q", Q.shape, dt, dev), _need(K, "K", K.shape, dt, dev), code, B, Hq, Hk, n, d,
-            _need(q_weight, "q_weight", (d,), dt, dev, True), _need(k_weight, "k_weight", (d,), dt, dev, True),
-            eps, theta, rotary_dim, int(interleaved),
-            _need(positions, "positions", (B, n), torch.int64, dev, True), position_offset,
-            _need(Qo, "Qo", Q.shape, dt, dev), _need(Ko, "Ko", K.shape, dt, dev), s), "diffuser_qk_norm_rope")
+    Qo, Ko = _empty(Qo, Q.shape, Q), _empty(Ko, K.shape, Q)
+    _check(_lib.diffuser_qk_norm_rope(
+        _need(Q, "Q", Q.shape, Q), _need(K, "K", K.shape, Q), code, B, Hq, Hk, n, d,
+        _may(q_weight, "q_weight", (d,), Q), _may(k_weight, "k_weight", (d,), Q),
+        eps, theta, rotary_dim, int(interleaved),
+        _may(positions, "positions", (B, n), Q, torch.int64), position_offset,
+        _need(Qo, "Qo", Q.shape, Q), _need(Ko, "Ko", K.shape, Q), stream), "diffuser_qk_norm_rope")
     return Qo, Ko
 
 
@@ -556,6 +566,7 @@ def diffuser_qk_norm_rope_backward_workspace_size(B: int, Hq: int, Hk: int, n: i
     return b.value
 
 
+@_on_stream
 def diffuser_qk_norm_rope_backward(Q, K, dQo, dKo, q_weight=None, k_weight=None, positions=None,
                                    position_offset: int = 0, eps: float = 1e-6, theta: float = 10000.0,
                                    rotary_dim: int = 64, interleaved: bool = False, dQ=None, dK=None,
@@ -564,54 +575,52 @@ def diffuser_qk_norm_rope_backward(Q, K, dQo, dKo, q_weight=None, k_weight=None,
     where the weight is."""
     import torch
     code, B, Hq, Hk, n, d = _qk_shapes(Q, K)
-    dev, dt = Q.device, Q.dtype
-    with _On(Q, stream) as s:
-        dQ, dK = _empty(dQ, Q.shape, Q), _empty(dK, K.shape, Q)
-        if q_weight is not None:
-            dq_weight = _empty(dq_weight, (d,), Q)
-        if k_weight is not None:
-            dk_weight = _empty(dk_weight, (d,), Q)
-        ws = _workspace(workspace, diffuser_qk_norm_rope_backward_workspace_size(B, Hq, Hk, n, d), dev)
-        _check(_lib.diffuser_qk_norm_rope_backward(
-            _need(Q, "Q", Q.shape, dt, dev), _need(K, "K", K.shape, dt, dev),
-            _need(dQo, "dQo", Q.shape, dt, dev), _need(dKo, "dKo", K.shape, dt, dev), code, B, Hq, Hk, n, d,
-            _need(q_weight, "q_weight", (d,), dt, dev, True), _need(k_weight, "k_weight", (d,), dt, dev, True),
-            eps, theta, rotary_dim, int(interleaved),
-            _need(positions, "positions", (B, n), torch.int64, dev, True), position_offset,
-            _need(dQ, "dQ", Q.shape, dt, dev), _need(dK, "dK", K.shape, dt, dev),
-            _need(dq_weight, "dq_weight", (d,), dt, dev, True), _need(dk_weight, "dk_weight", (d,), dt, dev, True),
-            ws.data_ptr(), ws.numel(), s), "diffuser_qk_norm_rope_backward")
+    dQ, dK = _empty(dQ, Q.shape, Q), _empty(dK, K.shape, Q)
+    if q_weight is not None:
+        dq_weight = _empty(dq_weight, (d,), Q)
+    if k_weight is not None:
+        dk_weight = _empty(dk_weight, (d,), Q)
+    ws = _workspace(workspace, diffuser_qk_norm_rope_backward_workspace_size(B, Hq, Hk, n, d), Q)
+    _check(_lib.diffuser_qk_norm_rope_backward(
+        _need(Q, "Q", Q.shape, Q), _need(K, "K", K.shape, Q),
+        _need(dQo, "dQo", Q.shape, Q), _need(dKo, "dKo", K.shape, Q), code, B, Hq, Hk, n, d,
+        _may(q_weight, "q_weight", (d,), Q), _may(k_weight, "k_weight", (d,), Q),
+        eps, theta, rotary_dim, int(interleaved),
+        _may(positions, "positions", (B, n), Q, torch.int64), position_offset,
+        _need(dQ, "dQ", Q.shape, Q), _need(dK, "dK", K.shape, Q),
+        _may(dq_weight, "dq_weight", (d,), Q), _may(dk_weight, "dk_weight", (d,), Q),
+        ws.data_ptr(), ws.numel(), stream), "diffuser_qk_norm_rope_backward")
     return dQ, dK, dq_weight, dk_weight
 
 
 def _dense_shapes(X, W, halves=1):
+    """Leading shape, T, D, F of X [...][D] and W [halves F][D]."""
     import torch
     if X.dtype != torch.bfloat16:
         raise TypeError(f"unsupported dtype {X.dtype}; use bfloat16")
-    if X.dim() < 1 or W.dim() != 2 or W.shape[1] != X.shape[-1] or W.shape[0] % halves:
+    shape, D = X.shape, X.shape[-1] if X.dim() else -1
+    if W.dim() != 2 or W.shape[1] != D or W.shape[0] % halves:
         raise ValueError(f"expected [...][D] and [{'2 F' if halves == 2 else 'F'}][D], got "
-                         f"{tuple(X.shape)} and {tuple(W.shape)}")
-    D, F = X.shape[-1], W.shape[0] // halves
-    lead = X.shape[:-1]
-    return lead, lead.numel(), D, F
+                         f"{tuple(shape)} and {tuple(W.shape)}")
+    lead = shape[:-1]
+    return lead, lead.numel(), D, W.shape[0] // halves
 
 
+@_on_stream
 def diffuser_linear(X, W, bias=None, residual=None, activation: int = DIFFUSER_ACT_NONE, save_pre: bool = False,
                     Y=None, pre=None, stream=None):
     """Y = act(X W^T + bias) + residual of bf16 tensors X [...][D], W [F][D], bias [F],
     residual [...][F]; with save_pre (or `pre` given) returns (Y, pre), pre the argument of
     the activation, as the backward pass wants it.  Y=residual works in place."""
-    import torch
     lead, T, D, F = _dense_shapes(X, W)
-    dev, bf, out = X.device, torch.bfloat16, (*lead, F)
-    with _On(X, stream) as s:
-        Y = _empty(Y, out, X)
-        if save_pre:
-            pre = _empty(pre, out, X)
-        _check(_lib.diffuser_linear(
-            _need(X, "X", X.shape, bf, dev), _need(W, "W", W.shape, bf, dev), _need(bias, "bias", (F,), bf, dev, True),
-            _need(residual, "residual", out, bf, dev, True), T, D, F, activation, _need(Y, "Y", out, bf, dev),
-            _need(pre, "pre", out, bf, dev, True), s), "diffuser_linear")
+    out = (*lead, F)
+    Y = _empty(Y, out, X)
+    if save_pre:
+        pre = _empty(pre, out, X)
+    _check(_lib.diffuser_linear(
+        _need(X, "X", X.shape, X), _need(W, "W", W.shape, X), _may(bias, "bias", (F,), X),
+        _may(residual, "residual", out, X), T, D, F, activation, _need(Y, "Y", out, X),
+        _may(pre, "pre", out, X), stream), "diffuser_linear")
     return Y if pre is None else (Y, pre)
 
 
@@ -622,42 +631,39 @@ def diffuser_linear_backward_workspace_size(T: int, D: int, F: int, activation: 
     return b.value
 
 
+@_on_stream
 def diffuser_linear_backward(X, W, dY, pre=None, activation: int = DIFFUSER_ACT_NONE, with_dX: bool = True,
                              with_dW: bool = True, with_bias: bool = True, dX=None, dW=None, dbias=None,
                              workspace=None, stream=None):
     """Gradients (dX, dW, dbias) of diffuser_linear for dY [...][F]; one whose with_ is False
     is None and not computed.  The residual's gradient is dY."""
-    import torch
     lead, T, D, F = _dense_shapes(X, W)
-    dev, bf, out = X.device, torch.bfloat16, (*lead, F)
-    with _On(X, stream) as s:
-        dX = _empty(dX, X.shape, X) if with_dX else None
-        dW = _empty(dW, W.shape, X) if with_dW else None
-        dbias = _empty(dbias, (F,), X) if with_bias else None
-        ws = _workspace(workspace, diffuser_linear_backward_workspace_size(T, D, F, activation), dev)
-        _check(_lib.diffuser_linear_backward(
-            _need(X, "X", X.shape, bf, dev), _need(W, "W", W.shape, bf, dev), _need(dY, "dY", out, bf, dev),
-            _need(pre, "pre", out, bf, dev, activation == DIFFUSER_ACT_NONE), T, D, F, activation,
-            _need(dX, "dX", X.shape, bf, dev, True), _need(dW, "dW", W.shape, bf, dev, True),
-            _need(dbias, "dbias", (F,), bf, dev, True), ws.data_ptr(), ws.numel(), s), "diffuser_linear_backward")
+    out = (*lead, F)
+    dX = _empty(dX, X.shape, X) if with_dX else None
+    dW = _empty(dW, W.shape, X) if with_dW else None
+    dbias = _empty(dbias, (F,), X) if with_bias else None
+    ws = _workspace(workspace, diffuser_linear_backward_workspace_size(T, D, F, activation), X)
+    _check(_lib.diffuser_linear_backward(
+        _need(X, "X", X.shape, X), _need(W, "W", W.shape, X), _need(dY, "dY", out, X),
+        (_may if activation == DIFFUSER_ACT_NONE else _need)(pre, "pre", out, X), T, D, F, activation,
+        _may(dX, "dX", X.shape, X), _may(dW, "dW", W.shape, X),
+        _may(dbias, "dbias", (F,), X), ws.data_ptr(), ws.numel(), stream), "diffuser_linear_backward")
     return dX, dW, dbias
 
 
+@_on_stream
 def diffuser_gated_linear(X, Wgu, activation: int = DIFFUSER_ACT_SILU, save_pre: bool = False, H=None, pre=None,
                           stream=None):
     """H [...][F] = act(X Wg^T) * (X Wu^T) of bf16 tensors X [...][D], Wgu [2 F][D] (Wg's rows,
     then Wu's); with save_pre (or `pre` given) returns (H, pre), pre [...][2 F] both products."""
-    import torch
     lead, T, D, F = _dense_shapes(X, Wgu, 2)
-    dev, bf = X.device, torch.bfloat16
-    with _On(X, stream) as s:
-        H = _empty(H, (*lead, F), X)
-        if save_pre:
-            pre = _empty(pre, (*lead, 2 * F), X)
-        _check(_lib.diffuser_gated_linear(
-            _need(X, "X", X.shape, bf, dev), _need(Wgu, "Wgu", Wgu.shape, bf, dev), T, D, F, activation,
-            _need(H, "H", (*lead, F), bf, dev), _need(pre, "pre", (*lead, 2 * F), bf, dev, True), s),
-            "diffuser_gated_linear")
+    H = _empty(H, (*lead, F), X)
+    if save_pre:
+        pre = _empty(pre, (*lead, 2 * F), X)
+    _check(_lib.diffuser_gated_linear(
+        _need(X, "X", X.shape, X), _need(Wgu, "Wgu", Wgu.shape, X), T, D, F, activation,
+        _need(H, "H", (*lead, F), X), _may(pre, "pre", (*lead, 2 * F), X), stream),
+        "diffuser_gated_linear")
     return H if pre is None else (H, pre)
 
 
@@ -668,22 +674,20 @@ def diffuser_gated_linear_backward_workspace_size(T: int, D: int, F: int) -> int
     return b.value
 
 
+@_on_stream
 def diffuser_gated_linear_backward(X, Wgu, dH, pre, activation: int = DIFFUSER_ACT_SILU, with_dX: bool = True,
                                    with_dW: bool = True, dX=None, dWgu=None, workspace=None, stream=None):
     """Gradients (dX, dWgu) of diffuser_gated_linear for dH [...][F], pre as the forward kept it;
     one whose with_ is False is None and not computed."""
-    import torch
     lead, T, D, F = _dense_shapes(X, Wgu, 2)
-    dev, bf = X.device, torch.bfloat16
-    with _On(X, stream) as s:
-        dX = _empty(dX, X.shape, X) if with_dX else None
-        dWgu = _empty(dWgu, Wgu.shape, X) if with_dW else None
-        ws = _workspace(workspace, diffuser_gated_linear_backward_workspace_size(T, D, F), dev)
-        _check(_lib.diffuser_gated_linear_backward(
-            _need(X, "X", X.shape, bf, dev), _need(Wgu, "Wgu", Wgu.shape, bf, dev),
-            _need(dH, "dH", (*lead, F), bf, dev), _need(pre, "pre", (*lead, 2 * F), bf, dev), T, D, F, activation,
-            _need(dX, "dX", X.shape, bf, dev, True), _need(dWgu, "dWgu", Wgu.shape, bf, dev, True),
-            ws.data_ptr(), ws.numel(), s), "diffuser_gated_linear_backward")
+    dX = _empty(dX, X.shape, X) if with_dX else None
+    dWgu = _empty(dWgu, Wgu.shape, X) if with_dW else None
+    ws = _workspace(workspace, diffuser_gated_linear_backward_workspace_size(T, D, F), X)
+    _check(_lib.diffuser_gated_linear_backward(
+        _need(X, "X", X.shape, X), _need(Wgu, "Wgu", Wgu.shape, X),
+        _need(dH, "dH", (*lead, F), X), _need(pre, "pre", (*lead, 2 * F), X), T, D, F, activation,
+        _may(dX, "dX", X.shape, X), _may(dWgu, "dWgu", Wgu.shape, X),
+        ws.data_ptr(), ws.numel(), stream), "diffuser_gated_linear_backward")
     return dX, dWgu
 
 

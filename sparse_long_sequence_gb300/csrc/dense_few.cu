@@ -1,22 +1,16 @@
-// Dense products with few output tiles: the sum over K is split over the CTAs of a
-// cluster and joined through their shared memory.
+// Forward products of a few tokens (a decoding step, a short batch): the weights' bytes
+// bound them.
 //
-// Computes C[j][i] = sum_k A[i][k] B[j][k] in tiles of 128 (i) x bn (j), i being the
-// contiguous index of the result:
-//   forward      i = output feature (A = W, K-major), j = token (B = X, K-major)
-//   input grad   i = input feature (A = W, i-major), j = token (B = dP, K-major)
-//   weight grad  i = input feature (A = X, i-major), j = output feature (B = dP, j-major)
-// Features are the MMA's 128 rows and tokens its columns, so a step of few tokens
-// pads to 16 columns and not to 128 rows, and a warp's 32 accumulator lanes are
-// neighbouring features of one token.
+// Y[t][f] = sum_k W[f][k] X[t][k] in tiles of 128 features x bn tokens.  Features are the
+// MMA's 128 rows and tokens its columns, so a step of few tokens pads to 16 columns and not
+// to 128 rows, and a warp's 32 accumulator lanes are neighbouring features of one token.
+// Gated: 64 gate rows and 64 up rows of the weights a tile.
 //
-// CTA s of a cluster of S takes K steps [s kb/S, (s+1) kb/S) through a TMA ring into
-// tcgen05 MMAs (fp32 accumulators in tensor memory), writes its partial tile to its own
-// shared memory, and after a cluster barrier every CTA sums its share of the elements
-// over the S partials in rank order (the result does not depend on timing), applies the
-// epilogue and stores.  One launch, no workspace, no atomics.
-//
-// For a few tokens the weights' bytes bound it: the split keeps every SM loading.
+// K is split over the CTAs of a cluster: CTA s of S takes K steps [s kb/S, (s+1) kb/S)
+// through a TMA ring into tcgen05 MMAs (fp32 accumulators in tensor memory), writes its
+// partial tile to its own shared memory, and after a cluster barrier every CTA sums its share
+// of the elements over the S partials in rank order (the result does not depend on timing),
+// applies the epilogue and stores.  One launch, no workspace, no atomics.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -37,11 +31,13 @@ namespace {
 constexpr int kTI = 128;                         // tile rows (i)
 constexpr int kTK = 64;                          // K step: 64 bf16, one 128-byte row
 constexpr int kABytes = kTI * kTK * 2;           // 16 KB
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 5;                  // 18 or 20 KB each: two CTAs an SM
 constexpr int kThreads = 256;                    // warp 0 loads, warp 1 multiplies, all reduce
-constexpr int kMaxSplit = 8;                     // the portable cluster size
+constexpr int kMaxSplit = 4;
 
-struct SplitArgs {
+constexpr int kMaxSmem = 1024 + kMaxStages * (kABytes + 32 * kTK * 2);
+
+struct FewArgs {
     int32_t I, J;              // result extents (gated: I = F, the tile has 64 gate and 64 up rows)
     int32_t k_blocks;          // K steps of 64 in all
     int32_t i_tiles;
@@ -63,9 +59,9 @@ __device__ __forceinline__ void put_bf16x2(__nv_bfloat16* p, float x, float y) {
     *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(x, y);
 }
 
-template <bool kAMn, bool kBMn, bool kGated>
+template <bool kGated>
 __global__ void __launch_bounds__(kThreads)
-dense_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, SplitArgs a) {
+dense_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, FewArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[1];
@@ -104,27 +100,16 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
                 ptx::mbar_arrive_expect_tx(&full[s], (uint32_t)stage_bytes);
                 if constexpr (kGated) {
                     ptx::tma_load_3d(sa, &tmA, &full[s], kb * kTK, i0, 0);       // 64 gate rows, 64 up rows
-                } else if constexpr (kAMn) {
-                    ptx::tma_load_2d(sa, &tmA, &full[s], i0, kb * kTK);
-                    ptx::tma_load_2d(sa + kABytes / 2, &tmA, &full[s], i0 + 64, kb * kTK);
                 } else {
                     ptx::tma_load_2d(sa, &tmA, &full[s], kb * kTK, i0);
                 }
-                if constexpr (kBMn) {
-                    for (int c = 0; c < a.bn; c += 64)
-                        ptx::tma_load_2d(sb + c * kTK * 2, &tmB, &full[s], j0 + c, kb * kTK);
-                } else {
-                    ptx::tma_load_2d(sb, &tmB, &full[s], kb * kTK, j0);
-                }
+                ptx::tma_load_2d(sb, &tmB, &full[s], kb * kTK, j0);
             }
         }
     } else if (warp == 1) {
-        const uint32_t idesc = ptx::mma_idesc_bf16(kTI, (uint32_t)a.bn, kAMn, kBMn);
-        // MN-major: 64 x 64 boxes of 8 KB, 16 K rows (one MMA) are 2048 bytes
-        constexpr uint32_t kBox = 64 * kTK * 2;
-        const uint32_t sa0 = ptx::smem_u32(smem);
-        const uint64_t ad0 = kAMn ? ptx::sw128_mnmajor_desc(sa0, kBox) : ptx::sw128_kmajor_desc(sa0);
-        const uint64_t bd0 = kBMn ? ptx::sw128_mnmajor_desc(sa0 + kABytes, kBox) : ptx::sw128_kmajor_desc(sa0 + kABytes);
+        const uint32_t idesc = ptx::mma_idesc_bf16(kTI, (uint32_t)a.bn, false, false);
+        const uint64_t ad0 = ptx::sw128_kmajor_desc(ptx::smem_u32(smem));
+        const uint64_t bd0 = ptx::sw128_kmajor_desc(ptx::smem_u32(smem) + kABytes);
         for (int kb = kb0, g = 0; kb < kb1; ++kb, ++g) {
             const int s = g % a.stages;
             ptx::mbar_wait(&full[s], (g / a.stages) & 1, a.status);
@@ -135,7 +120,7 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 #pragma unroll
             for (int ks = 0; ks < kTK / 16; ++ks)
                 if (ptx::elect_one())
-                    ptx::mma_bf16_ss(tmem, ad + (kAMn ? 128 : 2) * ks, bd + (kBMn ? 128 : 2) * ks, idesc, g > 0 || ks > 0);
+                    ptx::mma_bf16_ss(tmem, ad + 2 * ks, bd + 2 * ks, idesc, g > 0 || ks > 0);
             if (ptx::elect_one()) ptx::mma_commit(&empty[s]);
         }
         if (ptx::elect_one()) ptx::mma_commit(acc_full);
@@ -216,15 +201,15 @@ dense_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     ptx::cluster_sync();                              // nobody leaves while its partials are read
 }
 
-template <bool kAMn, bool kBMn, bool kGated>
-int launch_split_as(const CUtensorMap& tmA, const CUtensorMap& tmB, const SplitArgs& a, int64_t tiles,
+template <bool kGated>
+int launch_few_as(const CUtensorMap& tmA, const CUtensorMap& tmB, const FewArgs& a, int64_t tiles,
                     cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
     const int stage_bytes = kABytes + a.bn * kTK * 2;
     const int ring = a.stages * stage_bytes, part = a.bn * kTI * 4;
     const int smem = 1024 + (ring > part ? ring : part);
-    cudaError_t err = allow_smem(dense_split_kernel<kAMn, kBMn, kGated>, 226 * 1024, done);
-    if (err != cudaSuccess) return cuda_fail(err, "cudaFuncSetAttribute(dense split kernel)");
+    cudaError_t err = allow_smem(dense_few_kernel<kGated>, kMaxSmem, done);
+    if (err != cudaSuccess) return cuda_fail(err, "cudaFuncSetAttribute(dense few kernel)");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * a.splits));
     cfg.blockDim = dim3(kThreads);
@@ -239,34 +224,33 @@ int launch_split_as(const CUtensorMap& tmA, const CUtensorMap& tmB, const SplitA
     cfg.numAttrs = 1;
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        err = cudaLaunchKernelEx(&cfg, dense_split_kernel<kAMn, kBMn, kGated>, tmA, tmB, a);
+        err = cudaLaunchKernelEx(&cfg, dense_few_kernel<kGated>, tmA, tmB, a);
     }
-    return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "dense_split_kernel");
+    return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "dense_few_kernel");
 }
 
 }  // namespace
 
-int launch_dense(DenseForm form, const DenseArgs& d, cudaStream_t stream) {
-    SplitArgs a{};
-    int64_t I, J, K;
-    if (form == kForward) { I = d.gated ? d.cols / 2 : d.cols; J = d.rows; K = d.inner; }
-    else if (form == kInputGrad) { I = d.inner; J = d.rows; K = d.cols; }
-    else { I = d.inner; J = d.cols; K = d.rows; }
-    const int rows_i = d.gated && form == kForward ? kTI / 2 : kTI;
-    a.I = (int32_t)I;
-    a.J = (int32_t)J;
-    a.k_blocks = (int32_t)((K + kTK - 1) / kTK);
-    a.i_tiles = (int32_t)((I + rows_i - 1) / rows_i);
-    a.bn = J > 64 ? 128 : J > 32 ? 64 : J > 16 ? 32 : 16;
-    if (form == kWeightGrad && a.bn < 64) a.bn = 64;             // j-major boxes hold 64
-    a.tmem_cols = a.bn < 32 ? 32 : a.bn;
-    const int64_t tiles = (int64_t)a.i_tiles * ((J + a.bn - 1) / a.bn);
+// bn: 16 up to 16 tokens, 32 above (the accumulator's columns).  splits: as many as leave every
+// CTA two K steps and the grid within two CTAs an SM, at most 4: a cluster of 8 costs more to
+// start than it saves (512 x 512 to 768 x 2048, 16 tokens: 5.4 to 6.6 us with 8, 5.1 to 5.4 with
+// 4, 6.9 to 8.0 with 1).
+int launch_dense_few(const DenseArgs& d, cudaStream_t stream) {
+    FewArgs a{};
+    const int64_t F = d.gated ? d.cols / 2 : d.cols;
+    const int rows_i = d.gated ? kTI / 2 : kTI;
+    a.I = (int32_t)F;
+    a.J = (int32_t)d.rows;
+    a.k_blocks = (d.inner + kTK - 1) / kTK;
+    a.i_tiles = (int32_t)((F + rows_i - 1) / rows_i);
+    a.bn = d.rows <= 16 ? 16 : 32;
+    a.tmem_cols = 32;
+    const int64_t tiles = (int64_t)a.i_tiles * ((d.rows + a.bn - 1) / a.bn);
     if (tiles > INT32_MAX / kMaxSplit) return fail(DIFFUSER_ERR_OVERFLOW, "dense product too large");
-    int splits = 1;
-    while (splits < kMaxSplit && tiles * splits * 2 <= 2 * 152 && a.k_blocks >= 2 * splits * 2) splits *= 2;
-    a.splits = splits;
-    const int steps = (a.k_blocks + splits - 1) / splits;
-    a.stages = steps < 4 ? steps : 4;
+    a.splits = 1;
+    while (a.splits < kMaxSplit && tiles * a.splits * 2 <= 2 * 152 && a.k_blocks >= 4 * a.splits) a.splits *= 2;
+    const int steps = (a.k_blocks + a.splits - 1) / a.splits;
+    a.stages = steps < kMaxStages ? steps : kMaxStages;
     a.out = static_cast<__nv_bfloat16*>(d.out);
     a.pre = static_cast<__nv_bfloat16*>(d.pre);
     a.bias = static_cast<const __nv_bfloat16*>(d.bias);
@@ -274,23 +258,10 @@ int launch_dense(DenseForm form, const DenseArgs& d, cudaStream_t stream) {
     a.act = d.act;
     a.status = d.status;
     CUtensorMap tmA, tmB;
-    int st;
-    if (form == kForward) {
-        st = d.gated ? map_halves(&tmA, d.b, d.inner, I, kTK, kTI / 2) : map_matrix(&tmA, d.b, d.inner, I, kTK, kTI);
-        if (!st) st = map_matrix(&tmB, d.a, d.inner, d.rows, kTK, a.bn);
-    } else if (form == kInputGrad) {
-        st = map_matrix(&tmA, d.b, d.inner, d.cols, 64, kTK);
-        if (!st) st = map_matrix(&tmB, d.a, d.cols, d.rows, kTK, a.bn);
-    } else {
-        st = map_matrix(&tmA, d.b, d.inner, d.rows, 64, kTK);
-        if (!st) st = map_matrix(&tmB, d.a, d.cols, d.rows, 64, kTK);
-    }
+    int st = d.gated ? map_halves(&tmA, d.b, d.inner, F, kTK, kTI / 2, 2) : map_matrix(&tmA, d.b, d.inner, F, kTK, kTI);
+    if (!st) st = map_matrix(&tmB, d.a, d.inner, d.rows, kTK, a.bn);
     if (st) return st;
-    if (form == kForward)
-        return d.gated ? launch_split_as<false, false, true>(tmA, tmB, a, tiles, stream)
-                       : launch_split_as<false, false, false>(tmA, tmB, a, tiles, stream);
-    return form == kInputGrad ? launch_split_as<true, false, false>(tmA, tmB, a, tiles, stream)
-                              : launch_split_as<true, true, false>(tmA, tmB, a, tiles, stream);
+    return d.gated ? launch_few_as<true>(tmA, tmB, a, tiles, stream) : launch_few_as<false>(tmA, tmB, a, tiles, stream);
 }
 
 }  // namespace dfs

@@ -1,0 +1,668 @@
+// Dense products with many output tiles: a persistent kernel of CTA pairs.
+//
+// Computes C[i][j] = sum_k A[i][k] B[j][k] in tiles of 256 (i) x kBn (j), j being the
+// contiguous index of the result:
+//   forward      A = X (K-major), B = W (K-major)            C = P [T][F]
+//   input grad   A = dP (K-major), B = W (j-major)           C = dX [T][D]
+//   weight grad  A = dP (i-major), B = X (j-major)           C = dW [F][D]
+// Operands stay in their row-major layout: where the summed index is not the contiguous
+// one, the 64 x 64 boxes load as they are and the MMA reads them MN-major.
+//
+// The two CTAs of a cluster work on one tile (tcgen05 cta_group::2, M = 256): each loads
+// its 128 rows of A and half of B's rows, so B crosses shared memory once per pair and
+// not once per CTA, and one thread of CTA 0 issues the MMAs for both.  Each CTA holds its
+// 128 x kBn fp32 accumulator in tensor memory, twice, so that a tile's epilogue overlaps
+// the next tile's MMAs.
+//
+// Warps of a CTA: 0 loads (TMA, a ring of K steps of 64), 1 multiplies (CTA 0 only),
+// 2..9 are two epilogue groups of four warps (one accumulator lane a thread), each on its
+// 64-column chunks: tensor memory -> registers (bias, activation, residual) -> a swizzled
+// 128 x 64 shared buffer -> TMA store, which drops what lies outside the result.  The
+// residual arrives by TMA in the buffer the result leaves from.  Gated: B's rows are 128
+// gate rows (CTA 0) and 128 up rows (CTA 1), so columns c and 128 + c of an accumulator
+// lane are g and u of one element.
+// Every barrier wait is bounded and records a status instead of hanging.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "activations.cuh"
+#include "dense_ptx.cuh"
+#include "dense_tma.h"
+#include "layer_ops.h"
+
+namespace dfs {
+namespace {
+
+constexpr int kTI = 256;                          // tile rows of a pair, 128 a CTA
+constexpr int kTK = 64;                           // K step: 64 bf16, one 128-byte row
+constexpr int kBox = 64 * kTK * 2;                // an MN-major box: 64 x 64, 8 KB
+constexpr int kABytes = 128 * kTK * 2;            // 16 KB a CTA
+constexpr int kThreads = 320;
+constexpr int kEpiWarp0 = 2, kGroups = 2;
+constexpr int kChunk = 64;                        // columns of an epilogue step
+constexpr int kBufBytes = 128 * kChunk * 2;       // 16 KB
+constexpr int kBufs = 2;                          // a group's buffers
+constexpr int kGroupTiles = 8;                    // i tiles walked together (L2 reuse of both operands)
+
+constexpr int b_bytes(int bn) { return bn / 2 * kTK * 2; }
+constexpr int stage_count(int bn) {
+    return (226 * 1024 - 1024 - 512 - kGroups * kBufs * kBufBytes) / (kABytes + b_bytes(bn));
+}
+constexpr int smem_bytes(int bn) {
+    return 1024 + stage_count(bn) * (kABytes + b_bytes(bn)) + kGroups * kBufs * kBufBytes + 512;
+}
+static_assert(stage_count(256) == 5 && smem_bytes(256) <= 227 * 1024, "shared memory per CTA");
+static_assert(stage_count(128) == 6 && smem_bytes(128) <= 227 * 1024, "shared memory per CTA");
+
+struct PairArgs {
+    int32_t I, J;              // result extents (gated: J = F)
+    int32_t k_blocks;
+    int32_t i_tiles, j_tiles;
+    int32_t act;
+    bool pre, residual;        // their maps are valid
+    const __nv_bfloat16* bias;
+    int* status;
+};
+
+struct Tile { int i0, j0; };
+// tile t: groups of kGroupTiles i tiles, i fastest inside a group
+__device__ __forceinline__ Tile tile_at(const PairArgs& a, int t, int width) {
+    const int per = kGroupTiles * a.j_tiles;
+    const int grp = t / per, in = t - grp * per;
+    const int rows = min(kGroupTiles, a.i_tiles - grp * kGroupTiles);
+    return {(grp * kGroupTiles + in % rows) * kTI, in / rows * width};
+}
+
+// v = act(v) for 32 values (the activation is uniform over the launch)
+__device__ __forceinline__ void activate(int which, float (&v)[32]) {
+#define DFS_EACH(A) case A: _Pragma("unroll") for (int c = 0; c < 32; ++c) v[c] = act::value<A>(v[c]); break;
+    switch (which) {
+        DFS_EACH(DIFFUSER_ACT_RELU)
+        DFS_EACH(DIFFUSER_ACT_GELU)
+        DFS_EACH(DIFFUSER_ACT_GELU_TANH)
+        DFS_EACH(DIFFUSER_ACT_SILU)
+        default: break;
+    }
+#undef DFS_EACH
+}
+
+// 32 columns of a lane's row into the swizzled buffer: chunk q of 16 bytes at q ^ (row & 7)
+__device__ __forceinline__ void put_row(uint8_t* row, int sw, int q0, const float (&v)[32]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * q + 2 * p], v[8 * q + 2 * p + 1]);
+            w[p] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(row + (((q0 + q) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+__device__ __forceinline__ void add8(float* v, const uint4& r) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        v[2 * p] += __uint_as_float(w[p] << 16);
+        v[2 * p + 1] += __uint_as_float(w[p] & 0xffff0000u);
+    }
+}
+
+// ---- the roles both kernels share -------------------------------------------------
+template <bool kAMn, bool kBMn, bool kGated, int kBn>
+struct Roles {
+    static constexpr int kStages = stage_count(kBn);
+    static constexpr int kBBytes = b_bytes(kBn);
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kWidth = kGated ? kBn / 2 : kBn;     // result columns of a tile
+
+    // One K step of a tile (rows from ai, columns from bj: this CTA's shares) into stage s; `lead`
+    // is the cluster rank of the pair's first CTA, whose full barrier both CTAs' copies report to.
+    static __device__ __forceinline__ void load(uint8_t* smem, uint64_t* full, int s, const CUtensorMap* tmA,
+                                                const CUtensorMap* tmB, int ai, int bj, int kb, int rank, int lead) {
+        uint8_t* sa = smem + s * kStageBytes;
+        uint8_t* sb = sa + kABytes;
+        const uint32_t bar = ptx::map_rank(ptx::smem_u32(&full[s]), (uint32_t)lead);
+        if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+        if constexpr (kAMn) {
+            ptx::pair_load_2d(sa, tmA, bar, ai, kb * kTK);
+            ptx::pair_load_2d(sa + kBox, tmA, bar, ai + 64, kb * kTK);
+        } else {
+            ptx::pair_load_2d(sa, tmA, bar, kb * kTK, ai);
+        }
+        if constexpr (kGated) {
+            ptx::pair_load_3d(sb, tmB, bar, kb * kTK, bj, rank);
+        } else if constexpr (kBMn) {
+#pragma unroll
+            for (int c = 0; c < kBn / 2; c += 64) ptx::pair_load_2d(sb + c / 64 * kBox, tmB, bar, bj + c, kb * kTK);
+        } else {
+            ptx::pair_load_2d(sb, tmB, bar, kb * kTK, bj);
+        }
+    }
+    // first row and column of this CTA's shares of the operands
+    static __device__ __forceinline__ int a_row(const Tile& t, int rank) { return t.i0 + 128 * rank; }
+    static __device__ __forceinline__ int b_row(const Tile& t, int rank) { return t.j0 + (kGated ? 0 : kBn / 2 * rank); }
+
+    // The MMAs of stage s (one thread of the pair's first CTA), then the commit that frees it.
+    static __device__ __forceinline__ void multiply(uint32_t dacc, uint32_t sa0, int s, bool first, uint64_t* empty,
+                                                    uint16_t pair_mask) {
+        constexpr uint32_t idesc = ptx::mma_idesc_bf16(kTI, kBn, kAMn, kBMn);
+        const uint32_t sa = sa0 + s * kStageBytes, sb = sa + kABytes;
+        const uint64_t ad = kAMn ? ptx::sw128_mnmajor_desc(sa, kBox) : ptx::sw128_kmajor_desc(sa);
+        const uint64_t bd = kBMn ? ptx::sw128_mnmajor_desc(sb, kBox) : ptx::sw128_kmajor_desc(sb);
+#pragma unroll
+        for (int ks = 0; ks < kTK / 16; ++ks)
+            ptx::pair_mma_bf16(dacc, ad + (kAMn ? 128 : 2) * ks, bd + (kBMn ? 128 : 2) * ks, idesc, !first || ks > 0);
+        ptx::pair_commit(&empty[s], pair_mask);
+    }
+    // after g steps: wait until the last commits have landed (before the CTA exits)
+    static __device__ __forceinline__ void drain(uint64_t* empty, int g, int* status) {
+        for (int s = 0; s < kStages; ++s) {
+            const int uses = (g - s + kStages - 1) / kStages;
+            if (uses > 0) ptx::mbar_wait(&empty[s], (uses - 1) & 1, status);
+        }
+    }
+};
+
+template <bool kAMn, bool kBMn, bool kGated, int kBn>
+__global__ void __launch_bounds__(kThreads, 1)
+dense_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmPre,
+                  const __grid_constant__ CUtensorMap tmRes, const __grid_constant__ PairArgs a) {
+    using R = Roles<kAMn, kBMn, kGated, kBn>;
+    constexpr int kStages = R::kStages, kWidth = R::kWidth;
+    constexpr int kChunks = kWidth / kChunk / kGroups;        // chunks of a group
+    static_assert(kChunks >= 1 && kChunks <= kBufs, "a group's chunks have a buffer each");
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* bufs = smem + kStages * R::kStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(bufs + kGroups * kBufs * kBufBytes);   // [kStages] (CTA 0's are used)
+    uint64_t* empty = full + kStages;                          // [kStages]
+    uint64_t* acc_full = empty + kStages;                      // [2]
+    uint64_t* acc_empty = acc_full + 2;                        // [2] (CTA 0's are used)
+    uint64_t* res_full = acc_empty + 2;                        // [kGroups][kBufs]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + kGroups * kBufs);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)ptx::cluster_ctarank();
+    const int pairs = (int)gridDim.x / 2, pair = (int)blockIdx.x / 2;
+    const int total = a.i_tiles * a.j_tiles;
+    const int my_tiles = pair < total ? (total - 1 - pair) / pairs + 1 : 0;
+
+    if (warp == 1) ptx::pair_tmem_alloc(tmem_slot, 512);
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) { ptx::mbar_init(&full[s], 1); ptx::mbar_init(&empty[s], 1); }
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(&acc_full[s], 1);
+            ptx::mbar_init(&acc_empty[s], 2 * kGroups * 4);
+        }
+        for (int s = 0; s < kGroups * kBufs; ++s) ptx::mbar_init(&res_full[s], 1);
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&tmA);
+        ptx::prefetch_tensormap(&tmB);
+        ptx::prefetch_tensormap(&tmOut);
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // (the whole warp runs the loop; the elected lane issues the copies)
+        int g = 0;
+        for (int lt = 0; lt < my_tiles; ++lt) {
+            const Tile tl = tile_at(a, pair + lt * pairs, kWidth);
+            for (int kb = 0; kb < a.k_blocks; ++kb, ++g) {
+                const int s = g % kStages;
+                if (g >= kStages) ptx::mbar_wait(&empty[s], ((g / kStages) - 1) & 1, a.status);
+                __syncwarp();
+                if (ptx::elect_one())
+                    R::load(smem, full, s, &tmA, &tmB, R::a_row(tl, rank), R::b_row(tl, rank), kb, rank, 0);
+            }
+        }
+        R::drain(empty, g, a.status);
+    } else if (warp == 1) {
+        if (rank == 0) {
+            int g = 0;
+            for (int lt = 0; lt < my_tiles; ++lt) {
+                const int buf = lt & 1;
+                // both CTAs' epilogues have read this accumulator's previous tile
+                if (lt >= 2) ptx::mbar_wait_cluster(&acc_empty[buf], ((lt / 2) - 1) & 1, a.status);
+                __syncwarp();
+                ptx::tc_fence_after();
+                for (int kb = 0; kb < a.k_blocks; ++kb, ++g) {
+                    const int s = g % kStages;
+                    ptx::mbar_wait(&full[s], (g / kStages) & 1, a.status);
+                    __syncwarp();
+                    ptx::tc_fence_after();
+                    if (ptx::elect_one()) R::multiply(tmem + buf * kBn, ptx::smem_u32(smem), s, kb == 0, empty, 3);
+                }
+                if (ptx::elect_one()) ptx::pair_commit(&acc_full[buf], 3);
+            }
+        }
+    } else {
+        const int grp = (warp - kEpiWarp0) >> 2, quad = warp & 3;
+        const int t = quad * 32 + lane, sw = t & 7;
+        const bool lead = ((warp - kEpiWarp0) & 3) == 0 && lane == 0;     // issues the group's copies
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        uint8_t* gbuf = bufs + grp * kBufs * kBufBytes;
+        uint64_t* rbar = res_full + grp * kBufs;
+        const uint32_t acc_empty0 = ptx::map_rank(ptx::smem_u32(acc_empty), 0);
+        int u = 0;                                  // the group's stores so far; buffer u % 2
+        uint32_t rphase = 0;                        // bit b: parity of buffer b's next residual
+        for (int lt = 0; lt < my_tiles; ++lt) {
+            const Tile tl = tile_at(a, pair + lt * pairs, kWidth);
+            const int buf = lt & 1;
+            const int row0 = tl.i0 + 128 * rank;
+            // chunks with something to store
+            const int c_first = tl.j0 + grp * kChunks * kChunk;
+            int live = (min(a.J, tl.j0 + kWidth) - c_first + kChunk - 1) / kChunk;
+            live = row0 < a.I ? max(0, min(kChunks, live)) : 0;
+            if (a.residual && lead && live) {
+                // without `pre` every chunk's residual fits its buffer now, with it the first one's
+                ptx::bulk_wait_read<0>();
+                for (int k = 0; k < (a.pre ? 1 : live); ++k) {
+                    const int b = (a.pre ? u + 1 : u + k) & 1;
+                    ptx::mbar_arrive_expect_tx(&rbar[b], kBufBytes);
+                    ptx::tma_load_2d(gbuf + b * kBufBytes, &tmRes, &rbar[b], c_first + k * kChunk, row0);
+                }
+            }
+            ptx::mbar_wait(&acc_full[buf], (lt / 2) & 1, a.status);
+            __syncwarp();
+            ptx::tc_fence_after();
+            const uint32_t acc = tmem + lane_base + buf * kBn + grp * kChunks * kChunk;
+            for (int k = 0; k < live; ++k) {
+                const int col = c_first + k * kChunk;
+                if (a.residual && a.pre && k && lead) {
+                    ptx::bulk_wait_read<0>();
+                    const int b = (u + 1) & 1;
+                    ptx::mbar_arrive_expect_tx(&rbar[b], kBufBytes);
+                    ptx::tma_load_2d(gbuf + b * kBufBytes, &tmRes, &rbar[b], col, row0);
+                }
+                // what is stored of the chunk: P (gated: G, then U), then the result
+                const int first = a.pre ? 0 : (kGated ? 2 : 1);
+                for (int part = first; part <= (kGated ? 2 : 1); ++part, ++u) {
+                    const bool result = part == (kGated ? 2 : 1);
+                    const int b = u & 1;
+                    uint8_t* row = gbuf + b * kBufBytes + t * 128;
+                    // the buffer's last store has left it
+                    if (lead) ptx::bulk_wait_read<1>();
+                    ptx::named_barrier_sync(1 + grp, 128);
+                    if (result && a.residual) {
+                        ptx::mbar_wait(&rbar[b], (rphase >> b) & 1, a.status);
+                        rphase ^= 1u << b;
+                    }
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        float v[32];
+                        if constexpr (kGated) {
+                            ptx::tmem_ld32(acc + (part == 1 ? kBn / 2 : 0) + k * kChunk + 32 * h, v);
+                            if (result) {
+                                float w[32];
+                                ptx::tmem_ld32(acc + kBn / 2 + k * kChunk + 32 * h, w);
+                                activate(a.act, v);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) v[c] *= w[c];
+                            }
+                        } else {
+                            ptx::tmem_ld32(acc + k * kChunk + 32 * h, v);
+                            if (a.bias) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    if (col + 32 * h + 8 * q < a.J)
+                                        add8(v + 8 * q, __ldg(reinterpret_cast<const uint4*>(a.bias + col + 32 * h + 8 * q)));
+                            }
+                            if (result) {
+                                activate(a.act, v);
+                                if (a.residual) {
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q)
+                                        add8(v + 8 * q, *reinterpret_cast<const uint4*>(row + (((4 * h + q) ^ sw) << 4)));
+                                }
+                            }
+                        }
+                        put_row(row, sw, 4 * h, v);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    ptx::named_barrier_sync(1 + grp, 128);
+                    if (lead) {
+                        if (result) {
+                            ptx::tma_store_2d(&tmOut, gbuf + b * kBufBytes, col, row0);
+                        } else {
+                            if constexpr (kGated) ptx::tma_store_3d(&tmPre, gbuf + b * kBufBytes, col, part, row0);
+                            else ptx::tma_store_2d(&tmPre, gbuf + b * kBufBytes, col, row0);
+                        }
+                        ptx::bulk_commit();
+                    }
+                }
+            }
+            // the accumulator is read: the MMAs of the tile after next may overwrite it
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(acc_empty0 + 8 * buf);
+        }
+        if (lead) ptx::bulk_wait<0>();
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::pair_tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---- few tiles, many K steps: K split over the pairs of a cluster -------------------
+// One tile a cluster of 2 S CTAs; pair s takes K steps [s kb/S, (s+1) kb/S).  Every CTA then
+// lays its 128 x kBn partial accumulator into its own shared memory (the ring is free; rows
+// padded by 16 bytes so that neither the rows' writes nor the row reads conflict), and after a
+// cluster barrier CTA (s, rank) sums rows [s 128/S, (s+1) 128/S) of its half of the tile over
+// the S partials in rank order, a warp a row, and stores 8 bytes a lane.
+__device__ __forceinline__ float4 widen4(const __nv_bfloat16* p) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float4& v) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+__device__ __forceinline__ float4 act4(int which, const float4& v) {
+    return make_float4(act::value_of(which, v.x), act::value_of(which, v.y), act::value_of(which, v.z),
+                       act::value_of(which, v.w));
+}
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+    a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+}
+
+struct Results {               // row-major [I][J]; pre [I][2 J] when gated
+    __nv_bfloat16* out;
+    __nv_bfloat16* pre;
+    const __nv_bfloat16* residual;
+};
+
+template <bool kAMn, bool kBMn, bool kGated, int kBn, int kSplits>
+__global__ void __launch_bounds__(kThreads, 1)
+dense_pair_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ PairArgs a, const __grid_constant__ Results r) {
+    using R = Roles<kAMn, kBMn, kGated, kBn>;
+    constexpr int kStages = R::kStages;
+    constexpr int kRowBytes = kBn * 4 + 16;
+    static_assert(128 * kRowBytes <= kStages * R::kStageBytes, "the partial tile fits the ring");
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * R::kStageBytes);
+    uint64_t* empty = full + kStages;
+    uint64_t* acc_full = empty + kStages;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int crank = (int)ptx::cluster_ctarank(), split = crank >> 1, rank = crank & 1;
+    const uint16_t pair_mask = (uint16_t)(3u << (2 * split));
+    const Tile tl = tile_at(a, (int)blockIdx.x / (2 * kSplits), R::kWidth);
+    const int kb0 = (int)((int64_t)a.k_blocks * split / kSplits);
+    const int kb1 = (int)((int64_t)a.k_blocks * (split + 1) / kSplits);
+
+    if (warp == 1) ptx::pair_tmem_alloc(tmem_slot, kBn);
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) { ptx::mbar_init(&full[s], 1); ptx::mbar_init(&empty[s], 1); }
+        ptx::mbar_init(acc_full, 1);
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&tmA);
+        ptx::prefetch_tensormap(&tmB);
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        int g = 0;
+        for (int kb = kb0; kb < kb1; ++kb, ++g) {
+            const int s = g % kStages;
+            if (g >= kStages) ptx::mbar_wait(&empty[s], ((g / kStages) - 1) & 1, a.status);
+            __syncwarp();
+            if (ptx::elect_one())
+                R::load(smem, full, s, &tmA, &tmB, R::a_row(tl, rank), R::b_row(tl, rank), kb, rank, 2 * split);
+        }
+        R::drain(empty, g, a.status);
+    } else if (warp == 1 && rank == 0) {
+        int g = 0;
+        for (int kb = kb0; kb < kb1; ++kb, ++g) {
+            const int s = g % kStages;
+            ptx::mbar_wait(&full[s], (g / kStages) & 1, a.status);
+            __syncwarp();
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) R::multiply(tmem, ptx::smem_u32(smem), s, kb == kb0, empty, pair_mask);
+        }
+        if (ptx::elect_one()) ptx::pair_commit(acc_full, pair_mask);
+    }
+    __syncwarp();
+    if (warp >= kEpiWarp0) {
+        // the pair's MMAs have read every stage of both CTAs and written the accumulators
+        ptx::mbar_wait(acc_full, 0, a.status);
+        __syncwarp();
+        ptx::tc_fence_after();
+        const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        uint8_t* row = smem + (quad * 32 + lane) * kRowBytes;
+#pragma unroll 1
+        for (int c0 = half * kBn / 2; c0 < (half + 1) * kBn / 2; c0 += 32) {
+            float v[32];
+            ptx::tmem_ld32(tmem + lane_base + c0, v);
+#pragma unroll
+            for (int c = 0; c < 32; c += 4)
+                *reinterpret_cast<float4*>(row + (c0 + c) * 4) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::pair_tmem_dealloc(tmem, kBn);
+    }
+
+    constexpr int kRows = 128 / kSplits;
+    uint32_t peer[kSplits];
+#pragma unroll
+    for (int s = 0; s < kSplits; ++s) peer[s] = ptx::map_rank(ptx::smem_u32(smem), (uint32_t)(2 * s + rank));
+    auto total = [&](int row, int col) {
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < kSplits; ++s) add4(t, ptx::ld_cluster_f4(peer[s] + row * kRowBytes + col * 4));
+        return t;
+    };
+    for (int k = warp; k < kRows; k += kThreads / 32) {
+        const int row = split * kRows + k;
+        const int64_t i = (int64_t)tl.i0 + 128 * rank + row;
+        if (i >= a.I) break;
+#pragma unroll
+        for (int c0 = 0; c0 < R::kWidth; c0 += 128) {
+            const int c = c0 + 4 * lane, j = tl.j0 + c;
+            if (j >= a.J) continue;                    // J is a multiple of 8: four columns are in or out
+            float4 v = total(row, c);
+            if constexpr (kGated) {
+                const float4 u = total(row, kBn / 2 + c);
+                if (r.pre) {
+                    store4(r.pre + i * 2 * a.J + j, v);
+                    store4(r.pre + i * 2 * a.J + a.J + j, u);
+                }
+                v = act4(a.act, v);
+                v = make_float4(v.x * u.x, v.y * u.y, v.z * u.z, v.w * u.w);
+            } else {
+                if (a.bias) add4(v, widen4(a.bias + j));
+                if (r.pre) store4(r.pre + i * a.J + j, v);
+                if (a.act) v = act4(a.act, v);
+                if (r.residual) add4(v, widen4(r.residual + i * a.J + j));
+            }
+            store4(r.out + i * a.J + j, v);
+        }
+    }
+    __syncwarp();
+    ptx::cluster_sync();                               // nobody leaves while its partial is read
+}
+
+// Clusters of `ctas` CTAs that run at once on the current device (0 on failure).
+template <class Kernel>
+int resident_clusters(Kernel kernel, int ctas, int smem) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+}
+
+template <class Kernel, class... Args>
+int launch_clusters(Kernel kernel, int ctas, int64_t clusters, int smem, cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ctas * clusters));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t err;
+    {
+        LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
+        err = cudaLaunchKernelEx(&cfg, kernel, args...);
+    }
+    return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "dense pair kernel");
+}
+
+template <bool kAMn, bool kBMn, bool kGated, int kBn>
+int launch_pair_as(const CUtensorMap (&tm)[5], const PairArgs& a, cudaStream_t stream) {
+    auto kernel = dense_pair_kernel<kAMn, kBMn, kGated, kBn>;
+    static std::atomic<uint64_t> done{0};
+    static std::atomic<int> fit[64];
+    const cudaError_t err = allow_smem(kernel, smem_bytes(kBn), done);
+    if (err != cudaSuccess) return cuda_fail(err, "cudaFuncSetAttribute(dense pair kernel)");
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+    int pairs = fit[dev & 63].load();
+    if (!pairs) {
+        pairs = resident_clusters(kernel, 2, smem_bytes(kBn));
+        if (pairs < 1) return fail(DIFFUSER_ERR_CUDA, "no CTA pair of the dense product fits the device");
+        fit[dev & 63].store(pairs);
+    }
+    const int64_t tiles = (int64_t)a.i_tiles * a.j_tiles;
+    return launch_clusters(kernel, 2, tiles < pairs ? tiles : pairs, smem_bytes(kBn), stream, tm[0], tm[1], tm[2], tm[3],
+                           tm[4], a);
+}
+
+template <bool kAMn, bool kBMn, bool kGated, int kBn, int kSplits>
+int launch_split_as(const CUtensorMap (&tm)[5], const PairArgs& a, const Results& r, cudaStream_t stream) {
+    auto kernel = dense_pair_split_kernel<kAMn, kBMn, kGated, kBn, kSplits>;
+    static std::atomic<uint64_t> done{0};
+    constexpr int kSmem = 1024 + stage_count(kBn) * (kABytes + b_bytes(kBn)) + 512;
+    const cudaError_t err = allow_smem(kernel, kSmem, done);
+    if (err != cudaSuccess) return cuda_fail(err, "cudaFuncSetAttribute(dense pair split kernel)");
+    return launch_clusters(kernel, 2 * kSplits, (int64_t)a.i_tiles * a.j_tiles, kSmem, stream, tm[0], tm[1], a, r);
+}
+
+template <bool kAMn, bool kBMn, bool kGated, int kBn>
+int launch_as(const CUtensorMap (&tm)[5], const PairArgs& a, const Results& r, int splits, cudaStream_t stream) {
+    if (splits == 4) return launch_split_as<kAMn, kBMn, kGated, kBn, 4>(tm, a, r, stream);
+    if (splits == 2) return launch_split_as<kAMn, kBMn, kGated, kBn, 2>(tm, a, r, stream);
+    return launch_pair_as<kAMn, kBMn, kGated, kBn>(tm, a, stream);
+}
+
+}  // namespace
+
+int dense_pair_clusters(int splits) {
+    static std::atomic<int> fit[3][64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+    std::atomic<int>& f = fit[splits >> 1][dev & 63];
+    int n = f.load();
+    if (!n) {
+        constexpr int kSmem = 1024 + stage_count(256) * (kABytes + b_bytes(256)) + 512;
+        if (splits == 4) {
+            static std::atomic<uint64_t> done{0};
+            auto kernel = dense_pair_split_kernel<false, false, false, 256, 4>;
+            if (allow_smem(kernel, kSmem, done) == cudaSuccess) n = resident_clusters(kernel, 8, kSmem);
+        } else if (splits == 2) {
+            static std::atomic<uint64_t> done{0};
+            auto kernel = dense_pair_split_kernel<false, false, false, 256, 2>;
+            if (allow_smem(kernel, kSmem, done) == cudaSuccess) n = resident_clusters(kernel, 4, kSmem);
+        } else {
+            static std::atomic<uint64_t> done{0};
+            auto kernel = dense_pair_kernel<false, false, false, 256>;
+            if (allow_smem(kernel, smem_bytes(256), done) == cudaSuccess) n = resident_clusters(kernel, 2, smem_bytes(256));
+        }
+        if (n < 1) n = 1;
+        f.store(n);
+    }
+    return n;
+}
+
+int launch_dense_pair(DenseForm form, const DenseArgs& d, int bn, int splits, cudaStream_t stream) {
+    const bool gated = form == kForward && d.gated;
+    PairArgs a{};
+    int64_t I, J, K;
+    if (form == kForward) { I = d.rows; J = gated ? d.cols / 2 : d.cols; K = d.inner; }
+    else if (form == kInputGrad) { I = d.rows; J = d.inner; K = d.cols; }
+    else { I = d.cols; J = d.inner; K = d.rows; }
+    const int width = gated ? bn / 2 : bn;
+    const int64_t it = (I + kTI - 1) / kTI, jt = (J + width - 1) / width;
+    if (it * jt > INT32_MAX / 8) return fail(DIFFUSER_ERR_OVERFLOW, "dense product too large");
+    a.I = (int32_t)I;
+    a.J = (int32_t)J;
+    a.k_blocks = (int32_t)((K + kTK - 1) / kTK);
+    while (splits > a.k_blocks) splits /= 2;       // every pair has a K step
+    a.i_tiles = (int32_t)it;
+    a.j_tiles = (int32_t)jt;
+    a.act = d.act;
+    a.pre = d.pre != nullptr;
+    a.residual = d.residual != nullptr;
+    a.bias = static_cast<const __nv_bfloat16*>(d.bias);
+    a.status = d.status;
+    const Results r{static_cast<__nv_bfloat16*>(d.out), static_cast<__nv_bfloat16*>(d.pre),
+                    static_cast<const __nv_bfloat16*>(d.residual)};
+    CUtensorMap tm[5] = {};                        // A, B, result, pre, residual
+    int st;
+    if (form == kWeightGrad) st = map_matrix(&tm[0], d.a, d.cols, d.rows, 64, kTK);
+    else st = map_matrix(&tm[0], d.a, K, I, kTK, 128);
+    if (!st) {
+        if (gated) st = map_halves(&tm[1], d.b, d.inner, J, kTK, 128, 1);
+        else if (form == kForward) st = map_matrix(&tm[1], d.b, d.inner, J, kTK, bn / 2);
+        else st = map_matrix(&tm[1], d.b, J, K, 64, kTK);
+    }
+    if (splits == 1) {
+        if (!st) st = map_matrix(&tm[2], d.out, J, I, kChunk, 128);
+        if (!st && a.pre)
+            st = gated ? map_column_halves(&tm[3], d.pre, J, I, kChunk, 128) : map_matrix(&tm[3], d.pre, J, I, kChunk, 128);
+        if (!st && a.residual) st = map_matrix(&tm[4], d.residual, J, I, kChunk, 128);
+    }
+    if (st) return st;
+    if (gated) return launch_as<false, false, true, 256>(tm, a, r, splits, stream);
+    if (form == kForward)
+        return bn == 256 ? launch_as<false, false, false, 256>(tm, a, r, splits, stream)
+                         : launch_as<false, false, false, 128>(tm, a, r, splits, stream);
+    if (form == kInputGrad)
+        return bn == 256 ? launch_as<false, true, false, 256>(tm, a, r, splits, stream)
+                         : launch_as<false, true, false, 128>(tm, a, r, splits, stream);
+    return bn == 256 ? launch_as<true, true, false, 256>(tm, a, r, splits, stream)
+                     : launch_as<true, true, false, 128>(tm, a, r, splits, stream);
+}
+
+}  // namespace dfs

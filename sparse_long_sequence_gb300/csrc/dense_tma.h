@@ -32,12 +32,22 @@ inline int map_matrix(CUtensorMap* m, const void* base, int64_t width, int64_t r
     return encode_bf16_map(m, base, 2, dims, strides, box);
 }
 
-// [2][rows][width] (the gate's rows, then the up rows), boxes of 2 x box_rows x box_width:
-// a box that passes the end of one half reads zeros, not the other half
-inline int map_halves(CUtensorMap* m, const void* base, int64_t width, int64_t rows, int box_width, int box_rows) {
+// [2][rows][width] (the gate's rows, then the up rows), boxes of box_halves x box_rows x
+// box_width: a box that passes the end of one half reads zeros, not the other half
+inline int map_halves(CUtensorMap* m, const void* base, int64_t width, int64_t rows, int box_width, int box_rows,
+                      int box_halves) {
     const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, 2};
     const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)width * 2 * (cuuint64_t)rows};
-    const cuuint32_t box[3] = {(cuuint32_t)box_width, (cuuint32_t)box_rows, 2};
+    const cuuint32_t box[3] = {(cuuint32_t)box_width, (cuuint32_t)box_rows, (cuuint32_t)box_halves};
+    return encode_bf16_map(m, base, 3, dims, strides, box);
+}
+
+// [rows][2][width] (a row's gate columns, then its up columns), boxes of box_rows x 1 x
+// box_width: a box that passes the end of the gate's columns is cut there
+inline int map_column_halves(CUtensorMap* m, const void* base, int64_t width, int64_t rows, int box_width, int box_rows) {
+    const cuuint64_t dims[3] = {(cuuint64_t)width, 2, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)width * 4};
+    const cuuint32_t box[3] = {(cuuint32_t)box_width, 1, (cuuint32_t)box_rows};
     return encode_bf16_map(m, base, 3, dims, strides, box);
 }
 

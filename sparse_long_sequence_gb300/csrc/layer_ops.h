@@ -1,6 +1,6 @@
 // Internal declarations of the operators around the module: the per-head norms
 // with the position rotation (qk_norm_rope.cu), the dense product with its
-// epilogue and the gated product (dense_split.cu, dense_act.cu), and their entry
+// epilogue and the gated product (dense_pick.cu, dense_pair.cu, dense_few.cu, dense_act.cu), and their entry
 // points (layer_ops_abi.cu).
 #pragma once
 
@@ -59,7 +59,7 @@ int64_t qk_backward_blocks(int64_t tokens, int64_t heads);
 int launch_qk_norm_rope_backward(const QkArgs& a, int32_t dtype, bool interleaved, void* dwq, void* dwk,
                                  cudaStream_t stream);
 
-// ---- dense products (dense_split.cu) -----------------------------------------
+// ---- dense products (dense_pick.cu chooses the kernel) -----------------------------------------
 // Which product: Y[t][f] = sum_k X[t][k] W[f][k] (forward),
 // dX[t][k] = sum_f dP[t][f] W[f][k], dW[f][k] = sum_t dP[t][f] X[t][k].
 enum DenseForm { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
@@ -78,6 +78,14 @@ struct DenseArgs {
     bool gated;                     // forward: out = act(P[:, :F]) * P[:, F:], F = cols / 2
     int* status;
 };
+// forward of up to 32 tokens (dense_few.cu)
+int launch_dense_few(const DenseArgs& a, cudaStream_t stream);
+// CTA pairs, 256 x bn tiles, bn 128 or 256 (gated: 256); splits 1: persistent, 2 or 4: K split
+// over that many pairs of a cluster (dense_pair.cu)
+int launch_dense_pair(DenseForm form, const DenseArgs& a, int bn, int splits, cudaStream_t stream);
+// clusters of 2 `splits` CTAs of the split kernel that run at once on the current device
+int dense_pair_clusters(int splits);
+// picks the kernel (dense_pick.cu)
 int launch_dense(DenseForm form, const DenseArgs& a, cudaStream_t stream);
 
 // ---- the activations' backward (dense_act.cu) --------------------------------

@@ -1,0 +1,129 @@
+"""Host models of the dense products' mbarrier protocols (csrc/dense_pair.cu and
+csrc/dense_split.cu), played out by tests/barrier_model.py: every role must finish for any
+tile and K-step count, and no wait may find its barrier two phases ahead.  They check the
+protocols as designed; keeping them in step with the kernels is a review duty whenever
+either changes.
+
+The pair kernel: CTA 0's full barriers take one arrival (the expected bytes) and both CTAs'
+copies; a commit arrives on both CTAs' barriers; the accumulators are freed by the 2 x 8
+epilogue warps of the pair; a group's residual barriers take one arrival per load.
+"""
+import pytest
+
+from tests.barrier_model import play
+
+GROUPS, BUFS, WARPS = 2, 2, 4
+
+
+def wait(bar, k):
+    return ("w", bar, k)
+
+
+def arrive(bar):
+    return ("a", bar)
+
+
+def pair(my, k_blocks, stages, chunks=2, residual=False, pre=False, acc_empty=2 * GROUPS * WARPS, ring=True,
+         live=lambda rank, grp, lt: 2):
+    counts = {("full", s): 2 for s in range(stages)}       # the expect and the peer's copies
+    for r in range(2):
+        counts.update({("empty", r, s): 1 for s in range(stages)})
+        counts.update({("accF", r, b): 1 for b in range(2)})
+        for g in range(GROUPS):
+            counts.update({("res", r, g, b): 1 for b in range(BUFS)})
+            counts[("left", r, g)] = 1
+    counts.update({("accE", b): acc_empty for b in range(2)})
+    roles = []
+    for r in range(2):
+        tma, n = [], 0
+        for _ in range(my * k_blocks):
+            s = n % stages
+            if n >= stages and ring:
+                tma.append(wait(("empty", r, s), n // stages - 1))
+            tma.append(arrive(("full", s)))
+            n += 1
+        for s in range(stages):
+            uses = (n - s + stages - 1) // stages
+            if uses > 0:
+                tma.append(wait(("empty", r, s), uses - 1))
+        roles.append(tma)
+    mma, n = [], 0
+    for lt in range(my):
+        if lt >= 2:
+            mma.append(wait(("accE", lt & 1), lt // 2 - 1))
+        for _ in range(k_blocks):
+            s = n % stages
+            mma += [wait(("full", s), n // stages), arrive(("empty", 0, s)), arrive(("empty", 1, s))]
+            n += 1
+        mma += [arrive(("accF", 0, lt & 1)), arrive(("accF", 1, lt & 1))]
+    roles.append(mma)
+    for r in range(2):
+        for g in range(GROUPS):
+            group, u, loads, waits = [], 0, [0, 0], [0, 0]
+            for lt in range(my):
+                now = min(chunks, live(r, g, lt))
+                def load(b):
+                    group.append(arrive(("res", r, g, b)))
+                    loads[b] += 1
+                    assert loads[b] - waits[b] <= 1, "a residual lands in a buffer that holds one"
+                if residual and now:
+                    for k in range(1 if pre else now):
+                        load((u + 1 if pre else u + k) & 1)
+                group.append(wait(("accF", r, lt & 1), lt // 2))
+                for k in range(now):
+                    if residual and pre and k:
+                        load((u + 1) & 1)
+                    for part in (["pre"] if pre else []) + ["out"]:
+                        if part == "out" and residual:
+                            group.append(wait(("res", r, g, u & 1), waits[u & 1]))
+                            waits[u & 1] += 1
+                        u += 1
+                group += [arrive(("accE", lt & 1))] * WARPS
+            roles.append(group)
+    return play(roles, counts)
+
+
+@pytest.mark.parametrize("stages", [5, 6])
+@pytest.mark.parametrize("k_blocks", [1, 2, 5, 7, 12])
+def test_pair_protocol_completes(stages, k_blocks):
+    for my in range(6):
+        for residual in (False, True):
+            for pre in (False, True):
+                for chunks in (1, 2):
+                    assert pair(my, k_blocks, stages, chunks, residual, pre) == "done"
+
+
+def test_pair_protocol_with_ragged_tiles():
+    # groups and CTAs with one or no chunk inside the result
+    for pre in (False, True):
+        assert pair(5, 3, 5, residual=True, pre=pre, live=lambda r, g, lt: (r + 2 * g + lt) % 3) == "done"
+
+
+def test_pair_model_detects_planted_mistakes():
+    assert pair(4, 12, 5, acc_empty=2 * GROUPS * WARPS + 1) == "stalled"
+    assert pair(4, 12, 5, ring=False) == "overrun"
+
+
+def split(steps, stages, drain=True):
+    counts = {("full", s): 1 for s in range(stages)}
+    counts.update({("empty", s): 1 for s in range(stages)})
+    counts["acc"] = 1
+    tma, mma = [], []
+    for n in range(steps):
+        s = n % stages
+        if n >= stages:
+            tma.append(wait(("empty", s), n // stages - 1))
+        tma.append(arrive(("full", s)))
+        mma += [wait(("full", s), n // stages), arrive(("empty", s))]
+    mma.append(arrive("acc"))
+    for s in range(stages):
+        uses = (steps - s + stages - 1) // stages
+        if uses > 0 and drain:
+            mma.append(wait(("empty", s), uses - 1))
+    return play([tma + [wait("acc", 0)], mma + [wait("acc", 0)], [wait("acc", 0)]], counts)
+
+
+@pytest.mark.parametrize("stages", range(1, 9))
+def test_split_protocol_completes(stages):
+    for steps in range(1, 30):
+        assert split(steps, stages) == "done"

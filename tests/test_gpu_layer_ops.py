@@ -72,7 +72,8 @@ def near(got, ref, what, limit=1.5 * U):
 
 # ------------------------------------------------------------------ dense product
 SHAPES = [(1, 8, 8), (1, 768, 768), (3, 72, 200), (16, 512, 1368), (17, 1024, 136), (64, 64, 64), (65, 1000, 72),
-          (127, 264, 520), (300, 768, 776), (1021, 200, 328), (2100, 136, 1048), (5000, 520, 264)]
+          (127, 264, 520), (300, 768, 776), (1021, 200, 328), (2100, 136, 1048), (5000, 520, 264),
+          (20000, 264, 520), (300, 2056, 4104)]      # several tiles a CTA pair: rows, weight gradients
 IDS = ["T%dD%dF%d" % s for s in SHAPES]
 
 
