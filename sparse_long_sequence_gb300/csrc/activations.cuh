@@ -30,8 +30,13 @@ constexpr float kTanhC = 0.7978845608028654f;      // sqrt(2 / pi)
 constexpr float kTanhA = 0.044715f;
 constexpr float kPhiC = 0.3989422804014327f;       // 1 / sqrt(2 pi)
 
-// x * s with s in [0, 1] a saturating factor: 0 where s is 0 (x may be -inf there)
-__device__ __forceinline__ float gate(float x, float s) { return s == 0.f && x < 0.f ? 0.f : x * s; }
+// x * s with s in [0, 1] a saturating factor, 0 at x = -inf: the lowest finite value stands in
+// for it (NaN stays NaN)
+__device__ __forceinline__ float gate(float x, float s) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-3.4028234663852886e38f));
+    return y * s;
+}
 
 template <int kAct>
 __device__ __forceinline__ float value(float p) {

@@ -14,13 +14,14 @@
 // 128 x kBn fp32 accumulator in tensor memory, twice, so that a tile's epilogue overlaps
 // the next tile's MMAs.
 //
-// Warps of a CTA: 0 loads (TMA, a ring of K steps of 64), 1 multiplies (CTA 0 only),
-// 2..9 are two epilogue groups of four warps (one accumulator lane a thread), each on its
-// 64-column chunks: tensor memory -> registers (bias, activation, residual) -> a swizzled
-// 128 x 64 shared buffer -> TMA store, which drops what lies outside the result.  The
-// residual arrives by TMA in the buffer the result leaves from.  Gated: B's rows are 128
-// gate rows (CTA 0) and 128 up rows (CTA 1), so columns c and 128 + c of an accumulator
-// lane are g and u of one element.
+// Warps of a CTA: 0 loads (TMA, a ring of K steps of 64), 1 multiplies (CTA 0 only), 2..9 are
+// the epilogue, each alone on its 32 accumulator lanes and half of the tile's columns, in blocks
+// of 32: tensor memory -> registers (bias, activation, residual) -> a swizzled 2 KB buffer of
+// its own (four, used in turn) -> TMA store, which drops what lies outside the result.  Warps
+// wait for no other warp: with 128 x 64 blocks shared by four warps the forward 512 -> 2048 of
+// 32768 tokens with gelu and kept pre-activations took 132 us.  The residual arrives by TMA in
+// the buffer the result leaves from.  Gated: B's rows are 128 gate rows (CTA 0) and 128 up rows
+// (CTA 1), so columns c and 128 + c of an accumulator lane are g and u of one element.
 // Every barrier wait is bounded and records a status instead of hanging.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -43,18 +44,20 @@ constexpr int kTK = 64;                           // K step: 64 bf16, one 128-by
 constexpr int kBox = 64 * kTK * 2;                // an MN-major box: 64 x 64, 8 KB
 constexpr int kABytes = 128 * kTK * 2;            // 16 KB a CTA
 constexpr int kThreads = 320;
-constexpr int kEpiWarp0 = 2, kGroups = 2;
-constexpr int kChunk = 64;                        // columns of an epilogue step
-constexpr int kBufBytes = 128 * kChunk * 2;       // 16 KB
-constexpr int kBufs = 2;                          // a group's buffers
+constexpr int kEpiWarp0 = 2, kEpiWarps = 8;
+constexpr int kBlock = 32;                        // an epilogue step: 32 rows x 32 columns of a warp
+constexpr int kBufBytes = 32 * kBlock * 2;        // 2 KB
+constexpr int kBufs = 4;                          // a warp's buffers
+constexpr int kEpiBytes = kEpiWarps * kBufs * kBufBytes;
+constexpr int kBarBytes = 1024;                   // barriers and the tensor memory's address
 constexpr int kGroupTiles = 8;                    // i tiles walked together (L2 reuse of both operands)
 
 constexpr int b_bytes(int bn) { return bn / 2 * kTK * 2; }
 constexpr int stage_count(int bn) {
-    return (226 * 1024 - 1024 - 512 - kGroups * kBufs * kBufBytes) / (kABytes + b_bytes(bn));
+    return (227 * 1024 - 1024 - kBarBytes - kEpiBytes) / (kABytes + b_bytes(bn));
 }
 constexpr int smem_bytes(int bn) {
-    return 1024 + stage_count(bn) * (kABytes + b_bytes(bn)) + kGroups * kBufs * kBufBytes + 512;
+    return 1024 + stage_count(bn) * (kABytes + b_bytes(bn)) + kEpiBytes + kBarBytes;
 }
 static_assert(stage_count(256) == 5 && smem_bytes(256) <= 227 * 1024, "shared memory per CTA");
 static_assert(stage_count(128) == 6 && smem_bytes(128) <= 227 * 1024, "shared memory per CTA");
@@ -91,8 +94,9 @@ __device__ __forceinline__ void activate(int which, float (&v)[32]) {
 #undef DFS_EACH
 }
 
-// 32 columns of a lane's row into the swizzled buffer: chunk q of 16 bytes at q ^ (row & 7)
-__device__ __forceinline__ void put_row(uint8_t* row, int sw, int q0, const float (&v)[32]) {
+// 32 columns of a lane's row into its swizzled buffer (64-byte rows: 16-byte piece q at
+// q ^ ((row / 2) % 4), so that eight neighbouring rows' writes fall in eight bank groups)
+__device__ __forceinline__ void put_row(uint8_t* row, int sw, const float (&v)[32]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         uint32_t w[4];
@@ -101,7 +105,7 @@ __device__ __forceinline__ void put_row(uint8_t* row, int sw, int q0, const floa
             const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * q + 2 * p], v[8 * q + 2 * p + 1]);
             w[p] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        *reinterpret_cast<uint4*>(row + (((q0 + q) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(row + ((q ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 __device__ __forceinline__ void add8(float* v, const uint4& r) {
@@ -176,17 +180,17 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                   const __grid_constant__ CUtensorMap tmRes, const __grid_constant__ PairArgs a) {
     using R = Roles<kAMn, kBMn, kGated, kBn>;
     constexpr int kStages = R::kStages, kWidth = R::kWidth;
-    constexpr int kChunks = kWidth / kChunk / kGroups;        // chunks of a group
-    static_assert(kChunks >= 1 && kChunks <= kBufs, "a group's chunks have a buffer each");
+    constexpr int kBlocks = kWidth / 2 / kBlock;              // column blocks of an epilogue warp
+    static_assert(kBlocks >= 1 && kBlocks <= kBufs, "a tile's residual blocks have a buffer each");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* bufs = smem + kStages * R::kStageBytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(bufs + kGroups * kBufs * kBufBytes);   // [kStages] (CTA 0's are used)
+    uint64_t* full = reinterpret_cast<uint64_t*>(bufs + kEpiBytes);   // [kStages] (CTA 0's are used)
     uint64_t* empty = full + kStages;                          // [kStages]
     uint64_t* acc_full = empty + kStages;                      // [2]
     uint64_t* acc_empty = acc_full + 2;                        // [2] (CTA 0's are used)
-    uint64_t* res_full = acc_empty + 2;                        // [kGroups][kBufs]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + kGroups * kBufs);
+    uint64_t* res_full = acc_empty + 2;                        // [kEpiWarps][kBufs]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + kEpiWarps * kBufs);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)ptx::cluster_ctarank();
@@ -199,9 +203,9 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         for (int s = 0; s < kStages; ++s) { ptx::mbar_init(&full[s], 1); ptx::mbar_init(&empty[s], 1); }
         for (int s = 0; s < 2; ++s) {
             ptx::mbar_init(&acc_full[s], 1);
-            ptx::mbar_init(&acc_empty[s], 2 * kGroups * 4);
+            ptx::mbar_init(&acc_empty[s], 2 * kEpiWarps);
         }
-        for (int s = 0; s < kGroups * kBufs; ++s) ptx::mbar_init(&res_full[s], 1);
+        for (int s = 0; s < kEpiWarps * kBufs; ++s) ptx::mbar_init(&res_full[s], 1);
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&tmA);
         ptx::prefetch_tensormap(&tmB);
@@ -247,104 +251,118 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         }
     } else {
         const int grp = (warp - kEpiWarp0) >> 2, quad = warp & 3;
-        const int t = quad * 32 + lane, sw = t & 7;
-        const bool lead = ((warp - kEpiWarp0) & 3) == 0 && lane == 0;     // issues the group's copies
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-        uint8_t* gbuf = bufs + grp * kBufs * kBufBytes;
-        uint64_t* rbar = res_full + grp * kBufs;
+        uint8_t* wbuf = bufs + (warp - kEpiWarp0) * kBufs * kBufBytes;
+        const int row_at = lane * 64, sw = (lane >> 1) & 3;    // a lane's row of a buffer and its swizzle
+        uint64_t* rbar = res_full + (warp - kEpiWarp0) * kBufs;
         const uint32_t acc_empty0 = ptx::map_rank(ptx::smem_u32(acc_empty), 0);
-        int u = 0;                                  // the group's stores so far; buffer u % 2
-        uint32_t rphase = 0;                        // bit b: parity of buffer b's next residual
+        const bool lead = lane == 0;                           // issues the warp's copies
+        int u = 0;                                             // the warp's stores so far; buffer u % kBufs
+        uint32_t rphase = 0;                                   // bit b: parity of buffer b's next residual
         for (int lt = 0; lt < my_tiles; ++lt) {
             const Tile tl = tile_at(a, pair + lt * pairs, kWidth);
             const int buf = lt & 1;
-            const int row0 = tl.i0 + 128 * rank;
-            // chunks with something to store
-            const int c_first = tl.j0 + grp * kChunks * kChunk;
-            int live = (min(a.J, tl.j0 + kWidth) - c_first + kChunk - 1) / kChunk;
-            live = row0 < a.I ? max(0, min(kChunks, live)) : 0;
+            const int row0 = tl.i0 + 128 * rank + 32 * quad;
+            const int c_first = tl.j0 + grp * (kWidth / 2);
+            // blocks with something to store
+            const int live = row0 < a.I ? max(0, min(kBlocks, (a.J - c_first + kBlock - 1) / kBlock)) : 0;
+            auto fetch_residual = [&](int k, int b) {
+                ptx::mbar_arrive_expect_tx(&rbar[b], kBufBytes);
+                ptx::tma_load_2d(wbuf + b * kBufBytes, &tmRes, &rbar[b], c_first + k * kBlock, row0);
+            };
             if (a.residual && lead && live) {
-                // without `pre` every chunk's residual fits its buffer now, with it the first one's
+                // without `pre` every block's residual fits its buffer now, with it the first one's
                 ptx::bulk_wait_read<0>();
-                for (int k = 0; k < (a.pre ? 1 : live); ++k) {
-                    const int b = (a.pre ? u + 1 : u + k) & 1;
-                    ptx::mbar_arrive_expect_tx(&rbar[b], kBufBytes);
-                    ptx::tma_load_2d(gbuf + b * kBufBytes, &tmRes, &rbar[b], c_first + k * kChunk, row0);
-                }
+                if (a.pre) fetch_residual(0, (u + 1) % kBufs);
+                else for (int k = 0; k < live; ++k) fetch_residual(k, (u + k) % kBufs);
             }
             ptx::mbar_wait(&acc_full[buf], (lt / 2) & 1, a.status);
             __syncwarp();
             ptx::tc_fence_after();
-            const uint32_t acc = tmem + lane_base + buf * kBn + grp * kChunks * kChunk;
+            const uint32_t acc = tmem + lane_base + buf * kBn + grp * (kWidth / 2);
+            uint32_t r[32], ru[kGated ? 32 : 1];
+            auto issue = [&](int k) {
+                ptx::tmem_ld32_issue(acc + k * kBlock, r);
+                if constexpr (kGated) ptx::tmem_ld32_issue(acc + kBn / 2 + k * kBlock, ru);
+            };
+            // the accumulator is read: the MMAs of the tile after next may overwrite it
+            auto release = [&]() {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lead) ptx::mbar_arrive_cluster(acc_empty0 + 8 * buf);
+            };
+            if (live) issue(0); else release();
             for (int k = 0; k < live; ++k) {
-                const int col = c_first + k * kChunk;
-                if (a.residual && a.pre && k && lead) {
-                    ptx::bulk_wait_read<0>();
-                    const int b = (u + 1) & 1;
-                    ptx::mbar_arrive_expect_tx(&rbar[b], kBufBytes);
-                    ptx::tma_load_2d(gbuf + b * kBufBytes, &tmRes, &rbar[b], col, row0);
+                float v[32], w[kGated ? 32 : 1];
+                ptx::tmem_ld_wait32(r);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
+                if constexpr (kGated) {
+                    ptx::tmem_ld_wait32(ru);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) w[c] = __uint_as_float(ru[c]);
                 }
-                // what is stored of the chunk: P (gated: G, then U), then the result
-                const int first = a.pre ? 0 : (kGated ? 2 : 1);
-                for (int part = first; part <= (kGated ? 2 : 1); ++part, ++u) {
-                    const bool result = part == (kGated ? 2 : 1);
-                    const int b = u & 1;
-                    uint8_t* row = gbuf + b * kBufBytes + t * 128;
-                    // the buffer's last store has left it
-                    if (lead) ptx::bulk_wait_read<1>();
-                    ptx::named_barrier_sync(1 + grp, 128);
-                    if (result && a.residual) {
+                if (k + 1 < live) issue(k + 1); else release();
+                const int col = c_first + k * kBlock;
+                if (lead) {
+                    // the last stores from this block's buffers have left them
+                    if (a.residual) {
+                        if (a.pre && k + 1 < live) {
+                            ptx::bulk_wait_read<0>();
+                            fetch_residual(k + 1, (u + 3) % kBufs);
+                        }
+                    } else if (!a.pre) {
+                        ptx::bulk_wait_read<kBufs - 1>();
+                    } else {
+                        ptx::bulk_wait_read<kBufs - (kGated ? 3 : 2)>();
+                    }
+                }
+                __syncwarp();
+                auto buffer = [&](int n) { return wbuf + (u + n) % kBufs * kBufBytes; };
+                int n = 0;                                     // stores of this block
+                if constexpr (kGated) {
+                    if (a.pre) {
+                        put_row(buffer(0) + row_at, sw, v);
+                        put_row(buffer(1) + row_at, sw, w);
+                        n = 2;
+                    }
+                    activate(a.act, v);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) v[c] *= w[c];
+                } else {
+                    if (a.bias) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (col + 8 * q < a.J) add8(v + 8 * q, __ldg(reinterpret_cast<const uint4*>(a.bias + col + 8 * q)));
+                    }
+                    if (a.pre) {
+                        put_row(buffer(0) + row_at, sw, v);
+                        n = 1;
+                    }
+                    activate(a.act, v);
+                    if (a.residual) {
+                        const int b = (u + n) % kBufs;
                         ptx::mbar_wait(&rbar[b], (rphase >> b) & 1, a.status);
                         rphase ^= 1u << b;
-                    }
-#pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        float v[32];
-                        if constexpr (kGated) {
-                            ptx::tmem_ld32(acc + (part == 1 ? kBn / 2 : 0) + k * kChunk + 32 * h, v);
-                            if (result) {
-                                float w[32];
-                                ptx::tmem_ld32(acc + kBn / 2 + k * kChunk + 32 * h, w);
-                                activate(a.act, v);
 #pragma unroll
-                                for (int c = 0; c < 32; ++c) v[c] *= w[c];
-                            }
-                        } else {
-                            ptx::tmem_ld32(acc + k * kChunk + 32 * h, v);
-                            if (a.bias) {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    if (col + 32 * h + 8 * q < a.J)
-                                        add8(v + 8 * q, __ldg(reinterpret_cast<const uint4*>(a.bias + col + 32 * h + 8 * q)));
-                            }
-                            if (result) {
-                                activate(a.act, v);
-                                if (a.residual) {
-#pragma unroll
-                                    for (int q = 0; q < 4; ++q)
-                                        add8(v + 8 * q, *reinterpret_cast<const uint4*>(row + (((4 * h + q) ^ sw) << 4)));
-                                }
-                            }
-                        }
-                        put_row(row, sw, 4 * h, v);
-                    }
-                    ptx::fence_proxy_async_smem();
-                    ptx::named_barrier_sync(1 + grp, 128);
-                    if (lead) {
-                        if (result) {
-                            ptx::tma_store_2d(&tmOut, gbuf + b * kBufBytes, col, row0);
-                        } else {
-                            if constexpr (kGated) ptx::tma_store_3d(&tmPre, gbuf + b * kBufBytes, col, part, row0);
-                            else ptx::tma_store_2d(&tmPre, gbuf + b * kBufBytes, col, row0);
-                        }
-                        ptx::bulk_commit();
+                        for (int q = 0; q < 4; ++q)
+                            add8(v + 8 * q, *reinterpret_cast<const uint4*>(buffer(n) + row_at + ((q ^ sw) << 4)));
                     }
                 }
+                put_row(buffer(n) + row_at, sw, v);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lead) {
+                    for (int part = 0; part < n; ++part) {
+                        if constexpr (kGated) ptx::tma_store_3d(&tmPre, buffer(part), col, part, row0);
+                        else ptx::tma_store_2d(&tmPre, buffer(part), col, row0);
+                        ptx::bulk_commit();
+                    }
+                    ptx::tma_store_2d(&tmOut, buffer(n), col, row0);
+                    ptx::bulk_commit();
+                }
+                u += n + 1;
             }
-            // the accumulator is read: the MMAs of the tile after next may overwrite it
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(acc_empty0 + 8 * buf);
         }
         if (lead) ptx::bulk_wait<0>();
     }
@@ -573,7 +591,7 @@ template <bool kAMn, bool kBMn, bool kGated, int kBn, int kSplits>
 int launch_split_as(const CUtensorMap (&tm)[5], const PairArgs& a, const Results& r, cudaStream_t stream) {
     auto kernel = dense_pair_split_kernel<kAMn, kBMn, kGated, kBn, kSplits>;
     static std::atomic<uint64_t> done{0};
-    constexpr int kSmem = 1024 + stage_count(kBn) * (kABytes + b_bytes(kBn)) + 512;
+    constexpr int kSmem = 1024 + stage_count(kBn) * (kABytes + b_bytes(kBn)) + kBarBytes;
     const cudaError_t err = allow_smem(kernel, kSmem, done);
     if (err != cudaSuccess) return cuda_fail(err, "cudaFuncSetAttribute(dense pair split kernel)");
     return launch_clusters(kernel, 2 * kSplits, (int64_t)a.i_tiles * a.j_tiles, kSmem, stream, tm[0], tm[1], a, r);
@@ -595,7 +613,7 @@ int dense_pair_clusters(int splits) {
     std::atomic<int>& f = fit[splits >> 1][dev & 63];
     int n = f.load();
     if (!n) {
-        constexpr int kSmem = 1024 + stage_count(256) * (kABytes + b_bytes(256)) + 512;
+        constexpr int kSmem = 1024 + stage_count(256) * (kABytes + b_bytes(256)) + kBarBytes;
         if (splits == 4) {
             static std::atomic<uint64_t> done{0};
             auto kernel = dense_pair_split_kernel<false, false, false, 256, 4>;
@@ -648,10 +666,10 @@ int launch_dense_pair(DenseForm form, const DenseArgs& d, int bn, int splits, cu
         else st = map_matrix(&tm[1], d.b, J, K, 64, kTK);
     }
     if (splits == 1) {
-        if (!st) st = map_matrix(&tm[2], d.out, J, I, kChunk, 128);
+        if (!st) st = map_matrix(&tm[2], d.out, J, I, kBlock, 32);
         if (!st && a.pre)
-            st = gated ? map_column_halves(&tm[3], d.pre, J, I, kChunk, 128) : map_matrix(&tm[3], d.pre, J, I, kChunk, 128);
-        if (!st && a.residual) st = map_matrix(&tm[4], d.residual, J, I, kChunk, 128);
+            st = gated ? map_column_halves(&tm[3], d.pre, J, I, kBlock, 32) : map_matrix(&tm[3], d.pre, J, I, kBlock, 32);
+        if (!st && a.residual) st = map_matrix(&tm[4], d.residual, J, I, kBlock, 32);
     }
     if (st) return st;
     if (gated) return launch_as<false, false, true, 256>(tm, a, r, splits, stream);

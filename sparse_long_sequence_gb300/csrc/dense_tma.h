@@ -1,4 +1,5 @@
-// Tensor maps of the dense products' row-major bf16 matrices (128-byte swizzle).
+// Tensor maps of the dense products' row-major bf16 matrices.  A box's rows are 128 bytes
+// (operands) or 64 bytes (results, residuals) and swizzled over as many.
 #pragma once
 
 #include <cuda.h>
@@ -17,14 +18,16 @@ inline int encode_bf16_map(CUtensorMap* m, const void* base, int rank, const cuu
     if (!fn) return fail(DIFFUSER_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
     const cuuint32_t es[3] = {1, 1, 1};
     const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          box[0] * 2 == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(DIFFUSER_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
     return DIFFUSER_OK;
 }
 
-// [rows][width], boxes of box_rows x box_width (64 at most: one swizzled 128-byte row)
+// [rows][width], boxes of box_rows x box_width (64 or 32)
 inline int map_matrix(CUtensorMap* m, const void* base, int64_t width, int64_t rows, int box_width, int box_rows) {
     const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)width * 2};

@@ -6,13 +6,13 @@ either changes.
 
 The pair kernel: CTA 0's full barriers take one arrival (the expected bytes) and both CTAs'
 copies; a commit arrives on both CTAs' barriers; the accumulators are freed by the 2 x 8
-epilogue warps of the pair; a group's residual barriers take one arrival per load.
+epilogue warps of the pair; a warp's residual barriers take one arrival per load.
 """
 import pytest
 
 from tests.barrier_model import play
 
-GROUPS, BUFS, WARPS = 2, 2, 4
+BUFS, WARPS = 4, 8
 
 
 def wait(bar, k):
@@ -23,15 +23,13 @@ def arrive(bar):
     return ("a", bar)
 
 
-def pair(my, k_blocks, stages, chunks=2, residual=False, pre=False, acc_empty=2 * GROUPS * WARPS, ring=True,
-         live=lambda rank, grp, lt: 2):
+def pair(my, k_blocks, stages, blocks=4, residual=False, pre=False, acc_empty=2 * WARPS, ring=True,
+         live=lambda rank, warp, lt: 4):
     counts = {("full", s): 2 for s in range(stages)}       # the expect and the peer's copies
     for r in range(2):
         counts.update({("empty", r, s): 1 for s in range(stages)})
         counts.update({("accF", r, b): 1 for b in range(2)})
-        for g in range(GROUPS):
-            counts.update({("res", r, g, b): 1 for b in range(BUFS)})
-            counts[("left", r, g)] = 1
+        counts.update({("res", r, w, b): 1 for w in range(WARPS) for b in range(BUFS)})
     counts.update({("accE", b): acc_empty for b in range(2)})
     roles = []
     for r in range(2):
@@ -58,49 +56,54 @@ def pair(my, k_blocks, stages, chunks=2, residual=False, pre=False, acc_empty=2 
         mma += [arrive(("accF", 0, lt & 1)), arrive(("accF", 1, lt & 1))]
     roles.append(mma)
     for r in range(2):
-        for g in range(GROUPS):
-            group, u, loads, waits = [], 0, [0, 0], [0, 0]
+        for w in range(WARPS):
+            ops, u, loads, waits = [], 0, [0] * BUFS, [0] * BUFS
             for lt in range(my):
-                now = min(chunks, live(r, g, lt))
+                now = min(blocks, live(r, w, lt))
+
                 def load(b):
-                    group.append(arrive(("res", r, g, b)))
+                    ops.append(arrive(("res", r, w, b)))
                     loads[b] += 1
                     assert loads[b] - waits[b] <= 1, "a residual lands in a buffer that holds one"
                 if residual and now:
                     for k in range(1 if pre else now):
-                        load((u + 1 if pre else u + k) & 1)
-                group.append(wait(("accF", r, lt & 1), lt // 2))
+                        load((u + 1 if pre else u + k) % BUFS)
+                ops.append(wait(("accF", r, lt & 1), lt // 2))
+                if not now:
+                    ops.append(arrive(("accE", lt & 1)))
                 for k in range(now):
-                    if residual and pre and k:
-                        load((u + 1) & 1)
-                    for part in (["pre"] if pre else []) + ["out"]:
-                        if part == "out" and residual:
-                            group.append(wait(("res", r, g, u & 1), waits[u & 1]))
-                            waits[u & 1] += 1
-                        u += 1
-                group += [arrive(("accE", lt & 1))] * WARPS
-            roles.append(group)
+                    if k + 1 == now:
+                        ops.append(arrive(("accE", lt & 1)))
+                    if residual and pre and k + 1 < now:
+                        load((u + 3) % BUFS)
+                    n = 1 if pre else 0
+                    if residual:
+                        b = (u + n) % BUFS
+                        ops.append(wait(("res", r, w, b), waits[b]))
+                        waits[b] += 1
+                    u += n + 1
+            roles.append(ops)
     return play(roles, counts)
 
 
 @pytest.mark.parametrize("stages", [5, 6])
-@pytest.mark.parametrize("k_blocks", [1, 2, 5, 7, 12])
+@pytest.mark.parametrize("k_blocks", [1, 2, 6, 12])
 def test_pair_protocol_completes(stages, k_blocks):
-    for my in range(6):
+    for my in (0, 1, 2, 5):
         for residual in (False, True):
             for pre in (False, True):
-                for chunks in (1, 2):
-                    assert pair(my, k_blocks, stages, chunks, residual, pre) == "done"
+                for blocks in (2, 4):
+                    assert pair(my, k_blocks, stages, blocks, residual, pre) == "done"
 
 
 def test_pair_protocol_with_ragged_tiles():
-    # groups and CTAs with one or no chunk inside the result
+    # warps with some or no block inside the result
     for pre in (False, True):
-        assert pair(5, 3, 5, residual=True, pre=pre, live=lambda r, g, lt: (r + 2 * g + lt) % 3) == "done"
+        assert pair(5, 3, 5, residual=True, pre=pre, live=lambda r, w, lt: (r + 2 * w + lt) % 5) == "done"
 
 
 def test_pair_model_detects_planted_mistakes():
-    assert pair(4, 12, 5, acc_empty=2 * GROUPS * WARPS + 1) == "stalled"
+    assert pair(4, 12, 5, acc_empty=2 * WARPS + 1) == "stalled"
     assert pair(4, 12, 5, ring=False) == "overrun"
 
 
