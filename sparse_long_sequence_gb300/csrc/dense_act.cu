@@ -21,6 +21,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = 8;                          // columns of a lane (16 bytes)
+constexpr int kAhead = 4;                        // rows of a warp whose loads are in flight together
 constexpr int kBlockCols = 32 * kPer;            // columns of a block; its warps take rows in turn
 
 __device__ __forceinline__ void widen8(const uint4& r, float (&v)[kPer]) {
@@ -55,19 +56,32 @@ act_backward_kernel(const __nv_bfloat16* dY, const __nv_bfloat16* P, int64_t row
 #pragma unroll
     for (int j = 0; j < kPer; ++j) sum[j] = 0.f;
     if (c < F) {
-#pragma unroll 2
-        for (int64_t r = (int64_t)blockIdx.y * chunk + warp; r < r1; r += kWarps) {
-            float d[kPer];
-            widen8(load8(dY + r * F + c), d);
-            if constexpr (kAct != DIFFUSER_ACT_NONE) {
-                float p[kPer];
-                widen8(load8(P + r * F + c), p);
+        for (int64_t r0 = (int64_t)blockIdx.y * chunk + warp; r0 < r1; r0 += kWarps * kAhead) {
+            uint4 dy[kAhead], pr[kAhead];
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) d[j] *= act::value_slope<kAct>(p[j]).y;
-                *reinterpret_cast<uint4*>(dP + r * F + c) = round8(d);
+            for (int k = 0; k < kAhead; ++k) {
+                const int64_t r = r0 + k * kWarps;
+                if (r < r1) {
+                    dy[k] = load8(dY + r * F + c);
+                    if constexpr (kAct != DIFFUSER_ACT_NONE) pr[k] = load8(P + r * F + c);
+                }
             }
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) sum[j] += d[j];
+            for (int k = 0; k < kAhead; ++k) {
+                const int64_t r = r0 + k * kWarps;
+                if (r >= r1) break;
+                float d[kPer];
+                widen8(dy[k], d);
+                if constexpr (kAct != DIFFUSER_ACT_NONE) {
+                    float p[kPer];
+                    widen8(pr[k], p);
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) d[j] *= act::value_slope<kAct>(p[j]).y;
+                    *reinterpret_cast<uint4*>(dP + r * F + c) = round8(d);
+                }
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) sum[j] += d[j];
+            }
         }
     }
     if (!partial) return;
@@ -100,22 +114,37 @@ __global__ void __launch_bounds__(kThreads) colsum_kernel(const float* partial, 
 template <int kAct>
 __global__ void __launch_bounds__(kThreads)
 gated_backward_kernel(const __nv_bfloat16* dH, const __nv_bfloat16* P, int64_t items, int32_t F8, __nv_bfloat16* dP) {
-    const int64_t F = (int64_t)F8 * kPer;
-    for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < items; e += (int64_t)gridDim.x * kThreads) {
-        const int64_t r = e / F8, c = (e - r * F8) * kPer;
-        float d[kPer], g[kPer], u[kPer];
-        widen8(load8(dH + r * F + c), d);
-        widen8(load8(P + r * 2 * F + c), g);
-        widen8(load8(P + r * 2 * F + F + c), u);
+    const int64_t F = (int64_t)F8 * kPer, step = (int64_t)gridDim.x * kThreads;
+    for (int64_t e0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; e0 < items; e0 += 2 * step) {
+        uint4 dh[2], pg[2], pu[2];
+        int64_t at[2];                                // of the gate's element; dH's is r F + c
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const float2 vs = act::value_slope<kAct>(g[j]);
-            const float dh = d[j];
-            d[j] = dh * u[j] * vs.y;
-            u[j] = dh * vs.x;
+        for (int k = 0; k < 2; ++k) {
+            const int64_t e = e0 + k * step;
+            if (e >= items) break;
+            const int64_t r = e / F8, c = (e - r * F8) * kPer;
+            at[k] = r * 2 * F + c;
+            dh[k] = load8(dH + r * F + c);
+            pg[k] = load8(P + at[k]);
+            pu[k] = load8(P + at[k] + F);
         }
-        *reinterpret_cast<uint4*>(dP + r * 2 * F + c) = round8(d);
-        *reinterpret_cast<uint4*>(dP + r * 2 * F + F + c) = round8(u);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (e0 + k * step >= items) break;
+            float d[kPer], g[kPer], u[kPer];
+            widen8(dh[k], d);
+            widen8(pg[k], g);
+            widen8(pu[k], u);
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const float2 vs = act::value_slope<kAct>(g[j]);
+                const float h = d[j];
+                d[j] = h * u[j] * vs.y;
+                u[j] = h * vs.x;
+            }
+            *reinterpret_cast<uint4*>(dP + at[k]) = round8(d);
+            *reinterpret_cast<uint4*>(dP + at[k] + F) = round8(u);
+        }
     }
 }
 

@@ -55,7 +55,7 @@ struct QkArgs {
 };
 int launch_qk_norm_rope(const QkArgs& a, int32_t dtype, bool interleaved, cudaStream_t stream);
 // blocks of the backward kernel (rows of `partial`)
-int64_t qk_backward_blocks(int64_t tokens, int64_t heads);
+int64_t qk_backward_blocks(int64_t tokens, int64_t Hq, int64_t Hk);
 int launch_qk_norm_rope_backward(const QkArgs& a, int32_t dtype, bool interleaved, void* dwq, void* dwk,
                                  cudaStream_t stream);
 

@@ -87,8 +87,8 @@ QkArgs qk_args(const void* Q, const void* K, int64_t B, int64_t Hq, int64_t Hk, 
     return a;
 }
 
-size_t qk_partial_bytes(int64_t tokens, int64_t heads) {
-    return tokens ? align256((size_t)qk_backward_blocks(tokens, heads) * 2 * kHeadDim * sizeof(float)) : 256;
+size_t qk_partial_bytes(int64_t tokens, int64_t Hq, int64_t Hk) {
+    return tokens ? align256((size_t)qk_backward_blocks(tokens, Hq, Hk) * 2 * kHeadDim * sizeof(float)) : 256;
 }
 
 // ---- dense products ---------------------------------------------------------------
@@ -167,7 +167,7 @@ int diffuser_qk_norm_rope_backward_workspace_size(int64_t B, int64_t Hq, int64_t
     if (!bytes) return fail(DIFFUSER_ERR_INVALID_ARG, "NULL argument");
     const int st = check_qk(DIFFUSER_DTYPE_FP32, B, Hq, Hk, n, d, 1.f, 1.0, 0);
     if (st) return st;
-    *bytes = qk_partial_bytes(B * n, Hq + Hk);
+    *bytes = qk_partial_bytes(B * n, Hq, Hk);
     return DIFFUSER_OK;
 } catch (...) {
     return fail(DIFFUSER_ERR_ALLOC, "unexpected exception");
@@ -195,7 +195,7 @@ int diffuser_qk_norm_rope_backward(const void* Q, const void* K, const void* dQo
     if ((st = check_span(in[4], "q_weight")) || (st = check_span(in[5], "k_weight")) ||
         (st = check_span(in[6], "positions", 8)) || (st = check_span(out[0], "dQ")) || (st = check_span(out[1], "dK")) ||
         (st = check_span(out[2], "dq_weight")) || (st = check_span(out[3], "dk_weight")) ||
-        (st = check_workspace_bytes(qk_partial_bytes(B * n, Hq + Hk), workspace, workspace_bytes)) ||
+        (st = check_workspace_bytes(qk_partial_bytes(B * n, Hq, Hk), workspace, workspace_bytes)) ||
         (st = check_overlaps(in, 7, out, 5)))
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

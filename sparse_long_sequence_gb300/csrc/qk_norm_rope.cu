@@ -7,12 +7,14 @@
 // dy: g = R(-p) dy, dn = g w, xh = r x:
 //   dx = r (dn - xh mean(dn xh)),  dw = sum over rows of g xh.
 //
-// Eight lanes hold a row (8 features each, one or two 16-byte loads), a warp four
-// consecutive tokens of a head, and goes on over heads with the tokens' cosines
-// and sines kept in registers: they depend on the token alone.  The angle is
-// exact integer arithmetic: theta^(-2i/rot) / (2 pi), in units of 2^-64 turns,
-// times the position modulo 2^64 leaves the fraction of a turn, so far positions
-// lose nothing (a float product would be off by p 2^-24 radians).
+// Eight lanes hold a row, a warp four consecutive tokens of a head, and goes on over a run of
+// the queries' or the keys' heads with the tokens' cosines and sines kept in registers: they
+// depend on the token alone.  A lane holds two pieces of four features, chosen so that it has
+// both features of each of its pairs (split halves: pieces t and t + rot / 8): the rotation
+// needs no exchange between lanes.  Arithmetic on packed pairs of fp32 (f32x2).
+// The angle is exact integer arithmetic: theta^(-2i/rot) / (2 pi), in units of 2^-64 turns,
+// times the position modulo 2^64 leaves the fraction of a turn, so far positions lose nothing
+// (a float product would be off by p 2^-24 radians).
 // Bound by HBM: every row is read and written once (backward: two reads).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -29,241 +31,321 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowLanes = 8;                 // lanes of a row
-constexpr int kPer = kHeadDim / kRowLanes;   // features of a lane
 constexpr int kTok = 32 / kRowLanes;         // tokens of a warp
 constexpr unsigned kFull = 0xffffffffu;
 
+// Two fp32 values in a 64-bit register: one instruction works on both.
+struct F2 { uint64_t w; };
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.w) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 un(F2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v.w));
+    return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.w) : "l"(a.w), "l"(b.w));
+    return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.w) : "l"(a.w), "l"(b.w), "l"(c.w));
+    return r;
+}
+__device__ __forceinline__ F2 both(float x) { return f2(x, x); }
+
+// A lane's eight features of a row: piece A in v[0], v[1], piece B in v[2], v[3].
 template <class T> struct Io;
 template <> struct Io<float> {
     struct Raw { float4 a, b; };
-    static __device__ __forceinline__ Raw load(const float* p) {
-        return {*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4)};
+    static __device__ __forceinline__ Raw load(const float* row, int oa, int ob) {
+        return {*reinterpret_cast<const float4*>(row + oa), *reinterpret_cast<const float4*>(row + ob)};
     }
-    static __device__ __forceinline__ void widen(const Raw& r, float (&v)[kPer]) {
-        v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
-        v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+    static __device__ __forceinline__ void widen(const Raw& r, F2 (&v)[4]) {
+        v[0] = f2(r.a.x, r.a.y); v[1] = f2(r.a.z, r.a.w);
+        v[2] = f2(r.b.x, r.b.y); v[3] = f2(r.b.z, r.b.w);
     }
-    static __device__ __forceinline__ void store(float* p, const float (&v)[kPer]) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    static __device__ __forceinline__ void store(float* row, int oa, int ob, const F2 (&v)[4]) {
+        const float2 p = un(v[0]), q = un(v[1]), s = un(v[2]), t = un(v[3]);
+        *reinterpret_cast<float4*>(row + oa) = make_float4(p.x, p.y, q.x, q.y);
+        *reinterpret_cast<float4*>(row + ob) = make_float4(s.x, s.y, t.x, t.y);
     }
     static __device__ __forceinline__ float round(float x) { return x; }
 };
 template <> struct Io<__nv_bfloat16> {
-    using Raw = uint4;
-    static __device__ __forceinline__ Raw load(const __nv_bfloat16* p) {
-        return *reinterpret_cast<const uint4*>(p);
+    struct Raw { uint2 a, b; };
+    static __device__ __forceinline__ Raw load(const __nv_bfloat16* row, int oa, int ob) {
+        return {*reinterpret_cast<const uint2*>(row + oa), *reinterpret_cast<const uint2*>(row + ob)};
     }
-    static __device__ __forceinline__ void widen(const Raw& r, float (&v)[kPer]) {
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(w[j] << 16);
-            v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
+    static __device__ __forceinline__ F2 two(uint32_t w) { return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
+    static __device__ __forceinline__ void widen(const Raw& r, F2 (&v)[4]) {
+        v[0] = two(r.a.x); v[1] = two(r.a.y); v[2] = two(r.b.x); v[3] = two(r.b.y);
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[kPer]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-            w[j] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    static __device__ __forceinline__ uint32_t pack(F2 v) {
+        const float2 f = un(v);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* row, int oa, int ob, const F2 (&v)[4]) {
+        *reinterpret_cast<uint2*>(row + oa) = make_uint2(pack(v[0]), pack(v[1]));
+        *reinterpret_cast<uint2*>(row + ob) = make_uint2(pack(v[2]), pack(v[3]));
     }
     static __device__ __forceinline__ __nv_bfloat16 round(float x) { return __float2bfloat16_rn(x); }
 };
 
-// Sum over the 8 lanes of a row.
-__device__ __forceinline__ float row_sum(float s) {
-    s += __shfl_xor_sync(kFull, s, 1);
-    s += __shfl_xor_sync(kFull, s, 2);
-    s += __shfl_xor_sync(kFull, s, 4);
-    return s;
+// Sum of a row's 64 products x y (8 lanes).
+__device__ __forceinline__ float row_dot(const F2 (&x)[4], const F2 (&y)[4]) {
+    F2 s = mul(x[0], y[0]);
+#pragma unroll
+    for (int j = 1; j < 4; ++j) s = fma(x[j], y[j], s);
+    const float2 p = un(s);
+    float t = p.x + p.y;
+    t += __shfl_xor_sync(kFull, t, 1);
+    t += __shfl_xor_sync(kFull, t, 2);
+    t += __shfl_xor_sync(kFull, t, 4);
+    return t;
 }
 
-// Cosines and sines of a lane's 8 features; a feature's turned value is
-// x cos + partner sin (the sine negated for the first of a pair; 1 and 0 past rot).
+// Offsets of a lane's two pieces in a row.  Split halves: pieces t and t + P of the P = rot / 8
+// pairs of pieces, then the pieces that are not turned, two a lane.  Neighbouring pairs: 2t, 2t + 1.
+template <bool kInterleaved>
+__device__ __forceinline__ void pieces(int rot, int lane, int* oa, int* ob) {
+    const int t = lane & (kRowLanes - 1), P = rot / 8;
+    if (kInterleaved || t >= P) {
+        *oa = (kInterleaved ? 2 * t : 2 * P + 2 * (t - P)) * 4;
+        *ob = *oa + 4;
+    } else {
+        *oa = 4 * t;
+        *ob = 4 * (t + P);
+    }
+}
+
+// Cosines and sines of a lane's four pairs (1 and 0 past rot), sin negated for the inverse.
+// Split halves: pair j is (A[j], B[j]); neighbouring: (v[j].x, v[j].y).
 template <bool kInterleaved>
 struct Turn {
-    float c[kInterleaved ? kPer / 2 : kPer], s[kInterleaved ? kPer / 2 : kPer];
-    int src;                                 // split halves: lane that holds the partners
+    F2 c[kInterleaved ? 4 : 2], s[kInterleaved ? 4 : 2];
 
+    template <int kSign>
     __device__ __forceinline__ void set(const uint64_t* freq, int rot, int64_t pos, int lane) {
         const int t = lane & (kRowLanes - 1);
-        const bool turned = t * kPer < rot;
-        const int half = rot / (2 * kPer);   // lanes of a half
-        const bool second = t >= half;
-        src = turned ? (second ? lane - half : lane + half) : lane;
-        constexpr int count = kInterleaved ? kPer / 2 : kPer;
-        const int i0 = kInterleaved ? t * (kPer / 2) : (second ? t - half : t) * kPer;
+        float cs[4], sn[4];
 #pragma unroll
-        for (int j = 0; j < count; ++j) {
-            c[j] = 1.f;
-            s[j] = 0.f;
-            if (turned) {
+        for (int j = 0; j < 4; ++j) {
+            cs[j] = 1.f;
+            sn[j] = 0.f;
+            if (t < rot / 8) {
                 // the fraction of a turn, in [-1/2, 1/2), times 2: sincospi's unit
-                const uint64_t phase = (uint64_t)pos * freq[i0 + j];
-                const float halfturns = (float)(int32_t)(phase >> 32) * 4.656612873077393e-10f;   // 2^-31
-                sincospif(halfturns, &s[j], &c[j]);
-                if (!kInterleaved && !second) s[j] = -s[j];
+                const uint64_t phase = (uint64_t)pos * freq[4 * t + j];
+                sincospif((float)(int32_t)(phase >> 32) * (kSign * 4.656612873077393e-10f), &sn[j], &cs[j]);   // 2^-31
             }
         }
-    }
-    // kSign +1: R(p), -1: R(-p)
-    template <int kSign>
-    __device__ __forceinline__ void apply(float (&v)[kPer]) const {
         if constexpr (kInterleaved) {
 #pragma unroll
-            for (int j = 0; j < kPer / 2; ++j) {
-                const float a = v[2 * j], b = v[2 * j + 1], sn = kSign * s[j];
-                v[2 * j] = a * c[j] - b * sn;
-                v[2 * j + 1] = a * sn + b * c[j];
+            for (int j = 0; j < 4; ++j) {
+                c[j] = both(cs[j]);
+                s[j] = f2(-sn[j], sn[j]);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const float other = __shfl_sync(kFull, v[j], src);
-                v[j] = v[j] * c[j] + other * (kSign * s[j]);
+            for (int j = 0; j < 2; ++j) {
+                c[j] = f2(cs[2 * j], cs[2 * j + 1]);
+                s[j] = f2(sn[2 * j], sn[2 * j + 1]);
+            }
+        }
+    }
+    // (a, b) -> (a cos - b sin, a sin + b cos)
+    __device__ __forceinline__ void apply(F2 (&v)[4]) const {
+        if constexpr (kInterleaved) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 p = un(v[j]);
+                v[j] = fma(v[j], c[j], mul(f2(p.y, p.x), s[j]));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const F2 a = v[j], b = v[2 + j];
+                const float2 n = un(s[j]);
+                v[j] = fma(a, c[j], mul(b, f2(-n.x, -n.y)));
+                v[2 + j] = fma(a, s[j], mul(b, c[j]));
             }
         }
     }
 };
 
 template <class T>
-__device__ __forceinline__ void load_weight(const void* w, int lane, float (&v)[kPer]) {
+__device__ __forceinline__ void load_weight(const T* w, int oa, int ob, F2 (&v)[4]) {
     if (w) {
-        Io<T>::widen(Io<T>::load(static_cast<const T*>(w) + (lane & (kRowLanes - 1)) * kPer), v);
+        Io<T>::widen(Io<T>::load(w, oa, ob), v);
     } else {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) v[j] = 1.f;
+        for (int j = 0; j < 4; ++j) v[j] = both(1.f);
     }
 }
 
-// A warp's share: 4 tokens and a run of heads.  Heads 0 .. Hq-1 are the queries',
-// Hq .. Hq+Hk-1 the keys'.
-struct Share {
-    int64_t token;                 // this lane's (clamped to the last: loads stay in bounds)
-    bool live;                     // the lane's token exists
-    int64_t b, i;
-    int h0, h1;
+// A warp's share: four tokens and a run of the queries' or the keys' heads.
+struct Work {
+    int64_t groups;                // of four tokens
+    int64_t units;                 // groups x (q_runs + k_runs)
+    int32_t per;                   // heads of a run
+    int32_t q_runs;
 };
-__device__ __forceinline__ Share share_of(const QkArgs& a, int64_t unit, int64_t groups, int per_warp, int lane) {
+struct Share {
+    bool key, live;                // the keys' heads; this lane's token exists
+    int h0, h1;
+    int64_t first;                 // offset of (h0, token) in its tensor
+    int64_t pos;
+};
+__device__ __forceinline__ Share share_of(const QkArgs& a, const Work& w, int64_t unit, int lane) {
     Share s;
-    const int64_t group = unit % groups;
-    s.h0 = (int)(unit / groups) * per_warp;
-    s.h1 = min(s.h0 + per_warp, a.Hq + a.Hk);
-    s.token = group * kTok + lane / kRowLanes;
-    s.live = s.token < a.tokens;
-    if (!s.live) s.token = a.tokens - 1;
-    s.b = s.token / a.n;
-    s.i = s.token - s.b * a.n;
+    const int64_t group = unit % w.groups;
+    const int run = (int)(unit / w.groups);
+    s.key = run >= w.q_runs;
+    const int heads = s.key ? a.Hk : a.Hq;
+    s.h0 = (s.key ? run - w.q_runs : run) * w.per;
+    s.h1 = min(s.h0 + w.per, heads);
+    int64_t token = group * kTok + lane / kRowLanes;
+    s.live = token < a.tokens;
+    if (!s.live) token = a.tokens - 1;        // (loads stay in bounds)
+    const int64_t b = token / a.n, i = token - b * a.n;
+    s.first = ((b * heads + s.h0) * a.n + i) * kHeadDim;
+    s.pos = a.pos0 + (a.pos ? a.pos[token] : i);
     return s;
-}
-// offset of this lane's features of head h in its own tensor
-__device__ __forceinline__ int64_t offset_of(const QkArgs& a, const Share& s, int h, int lane) {
-    const bool key = h >= a.Hq;
-    const int64_t heads = key ? a.Hk : a.Hq;
-    return ((s.b * heads + (key ? h - a.Hq : h)) * a.n + s.i) * kHeadDim + (lane & (kRowLanes - 1)) * kPer;
 }
 
 constexpr int kAhead = 4;          // heads whose loads are in flight together
 
 template <class T, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) qk_forward_kernel(const __grid_constant__ QkArgs a, int64_t groups,
-                                                              int per_warp, int64_t units) {
+__global__ void __launch_bounds__(kThreads) qk_forward_kernel(const __grid_constant__ QkArgs a, const Work w) {
     const int lane = threadIdx.x & 31;
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (unit >= units) return;
-    const Share s = share_of(a, unit, groups, per_warp, lane);
-    Turn<kInterleaved> turn;
-    turn.set(a.freq, a.rot, a.pos0 + (a.pos ? a.pos[s.token] : s.i), lane);
-    float wq[kPer], wk[kPer];
-    load_weight<T>(a.wq, lane, wq);
-    load_weight<T>(a.wk, lane, wk);
-    for (int h = s.h0; h < s.h1; h += kAhead) {
-        typename Io<T>::Raw raw[kAhead];
+    if (unit >= w.units) return;
+    const Share s = share_of(a, w, unit, lane);
+    int oa, ob;
+    pieces<kInterleaved>(a.rot, lane, &oa, &ob);
+    const int64_t step = a.n * kHeadDim;      // from head to head
+    const T* src = static_cast<const T*>(s.key ? a.k : a.q) + s.first;
+    T* dst = static_cast<T*>(s.key ? a.ko : a.qo) + s.first;
+    typename Io<T>::Raw raw[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u)
-            if (h + u < s.h1)
-                raw[u] = Io<T>::load(static_cast<const T*>(h + u >= a.Hq ? a.k : a.q) + offset_of(a, s, h + u, lane));
+    for (int u = 0; u < kAhead; ++u)
+        if (s.h0 + u < s.h1) raw[u] = Io<T>::load(src + u * step, oa, ob);
+    Turn<kInterleaved> turn;
+    turn.template set<1>(a.freq, a.rot, s.pos, lane);
+    F2 wt[4];
+    load_weight(static_cast<const T*>(s.key ? a.wk : a.wq), oa, ob, wt);
+    for (int h = s.h0; h < s.h1; h += kAhead, src += kAhead * step, dst += kAhead * step) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (h + u >= s.h1) break;
-            const bool key = h + u >= a.Hq;
-            float v[kPer];
+            F2 v[4];
             Io<T>::widen(raw[u], v);
-            float ss = 0.f;
+            if (h + u + kAhead < s.h1) raw[u] = Io<T>::load(src + (u + kAhead) * step, oa, ob);
+            const F2 r = both(rsqrtf(row_dot(v, v) * (1.f / kHeadDim) + a.eps));
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) ss = fmaf(v[j], v[j], ss);
-            const float r = rsqrtf(row_sum(ss) * (1.f / kHeadDim) + a.eps);
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) v[j] = v[j] * r * (key ? wk[j] : wq[j]);
-            turn.template apply<1>(v);
-            if (s.live) Io<T>::store(static_cast<T*>(key ? a.ko : a.qo) + offset_of(a, s, h + u, lane), v);
+            for (int j = 0; j < 4; ++j) v[j] = mul(mul(v[j], r), wt[j]);
+            turn.apply(v);
+            if (s.live) Io<T>::store(dst + u * step, oa, ob, v);
         }
     }
 }
 
+constexpr int kAheadBack = 2;
+
 template <class T, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) qk_backward_kernel(const __grid_constant__ QkArgs a, int64_t groups,
-                                                               int per_warp, int64_t units) {
+__global__ void __launch_bounds__(kThreads) qk_backward_kernel(const __grid_constant__ QkArgs a, const Work w) {
     __shared__ float sums[kWarps][2 * kHeadDim];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float wq[kPer], wk[kPer], gq[kPer], gk[kPer];
-    load_weight<T>(a.wq, lane, wq);
-    load_weight<T>(a.wk, lane, wk);
+    int oa, ob;
+    pieces<kInterleaved>(a.rot, lane, &oa, &ob);
+    const int64_t step = a.n * kHeadDim;
+    F2 gq[4], gk[4];                          // sums of the weights' gradients
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) gq[j] = gk[j] = 0.f;
-    for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < units; unit += (int64_t)gridDim.x * kWarps) {
-        const Share s = share_of(a, unit, groups, per_warp, lane);
+    for (int j = 0; j < 4; ++j) gq[j] = gk[j] = both(0.f);
+    for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < w.units; unit += (int64_t)gridDim.x * kWarps) {
+        const Share s = share_of(a, w, unit, lane);
+        const T* x_row = static_cast<const T*>(s.key ? a.k : a.q) + s.first;
+        const T* g_row = static_cast<const T*>(s.key ? a.dko : a.dqo) + s.first;
+        T* d_row = static_cast<T*>(s.key ? a.ko : a.qo) + s.first;
+        typename Io<T>::Raw rx[kAheadBack], rg[kAheadBack];
+#pragma unroll
+        for (int u = 0; u < kAheadBack; ++u)
+            if (s.h0 + u < s.h1) {
+                rx[u] = Io<T>::load(x_row + u * step, oa, ob);
+                rg[u] = Io<T>::load(g_row + u * step, oa, ob);
+            }
         Turn<kInterleaved> turn;
-        turn.set(a.freq, a.rot, a.pos0 + (a.pos ? a.pos[s.token] : s.i), lane);
-        for (int h = s.h0; h < s.h1; ++h) {
-            const bool key = h >= a.Hq;
-            const int64_t at = offset_of(a, s, h, lane);
-            float x[kPer], g[kPer];
-            const auto rx = Io<T>::load(static_cast<const T*>(key ? a.k : a.q) + at);
-            const auto rg = Io<T>::load(static_cast<const T*>(key ? a.dko : a.dqo) + at);
-            Io<T>::widen(rx, x);
-            Io<T>::widen(rg, g);
-            turn.template apply<-1>(g);
-            float ss = 0.f, sd = 0.f;
+        turn.template set<-1>(a.freq, a.rot, s.pos, lane);
+        F2 wt[4], acc[4];
+        load_weight(static_cast<const T*>(s.key ? a.wk : a.wq), oa, ob, wt);
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                ss = fmaf(x[j], x[j], ss);
-                sd = fmaf(g[j] * (key ? wk[j] : wq[j]), x[j], sd);
-            }
-            const float r = rsqrtf(row_sum(ss) * (1.f / kHeadDim) + a.eps);
-            const float m = row_sum(sd) * (r * (1.f / kHeadDim));      // mean(dn xh)
-            float d[kPer];
+        for (int j = 0; j < 4; ++j) acc[j] = both(0.f);
+        for (int h = s.h0; h < s.h1; h += kAheadBack) {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) {
-                const float xh = x[j] * r;
-                d[j] = r * (g[j] * (key ? wk[j] : wq[j]) - xh * m);
-                const float add = s.live ? g[j] * xh : 0.f;
-                if (key) gk[j] += add; else gq[j] += add;
+            for (int u = 0; u < kAheadBack; ++u) {
+                if (h + u >= s.h1) break;
+                F2 x[4], g[4], dn[4];
+                Io<T>::widen(rx[u], x);
+                Io<T>::widen(rg[u], g);
+                if (h + u + kAheadBack < s.h1) {
+                    rx[u] = Io<T>::load(x_row + kAheadBack * step, oa, ob);
+                    rg[u] = Io<T>::load(g_row + kAheadBack * step, oa, ob);
+                }
+                turn.apply(g);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) dn[j] = mul(g[j], wt[j]);
+                const float r = rsqrtf(row_dot(x, x) * (1.f / kHeadDim) + a.eps);
+                // xh mean(dn xh) = x r^2 (dn . x) / 64
+                const F2 m = both(row_dot(dn, x) * (-1.f / kHeadDim) * r * r), r2 = both(r);
+                F2 d[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    d[j] = mul(fma(x[j], m, dn[j]), r2);
+                    acc[j] = fma(g[j], mul(x[j], r2), acc[j]);
+                }
+                if (s.live) Io<T>::store(d_row, oa, ob, d);
+                x_row += step;
+                g_row += step;
+                d_row += step;
             }
-            if (s.live) Io<T>::store(static_cast<T*>(key ? a.ko : a.qo) + at, d);
+        }
+        const float to_q = s.live && !s.key ? 1.f : 0.f, to_k = s.live && s.key ? 1.f : 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (to_q != 0.f) gq[j] = fma(acc[j], both(to_q), gq[j]);
+            if (to_k != 0.f) gk[j] = fma(acc[j], both(to_k), gk[j]);
         }
     }
     if (!a.partial) return;
     // lanes of the four tokens, then the warps, in a fixed order
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        gq[j] += __shfl_xor_sync(kFull, gq[j], 8);
-        gk[j] += __shfl_xor_sync(kFull, gk[j], 8);
-        gq[j] += __shfl_xor_sync(kFull, gq[j], 16);
-        gk[j] += __shfl_xor_sync(kFull, gk[j], 16);
+    for (int j = 0; j < 4; ++j) {
+        float2 q = un(gq[j]), k = un(gk[j]);
+        q.x += __shfl_xor_sync(kFull, q.x, 8);
+        q.y += __shfl_xor_sync(kFull, q.y, 8);
+        k.x += __shfl_xor_sync(kFull, k.x, 8);
+        k.y += __shfl_xor_sync(kFull, k.y, 8);
+        q.x += __shfl_xor_sync(kFull, q.x, 16);
+        q.y += __shfl_xor_sync(kFull, q.y, 16);
+        k.x += __shfl_xor_sync(kFull, k.x, 16);
+        k.y += __shfl_xor_sync(kFull, k.y, 16);
         if (lane < kRowLanes) {
-            sums[warp][lane * kPer + j] = gq[j];
-            sums[warp][kHeadDim + lane * kPer + j] = gk[j];
+            const int c = (j < 2 ? oa : ob) + 2 * (j & 1);
+            sums[warp][c] = q.x;
+            sums[warp][c + 1] = q.y;
+            sums[warp][kHeadDim + c] = k.x;
+            sums[warp][kHeadDim + c + 1] = k.y;
         }
     }
     __syncthreads();
     if (threadIdx.x < 2 * kHeadDim) {
         float t = 0.f;
-        for (int w = 0; w < kWarps; ++w) t += sums[w][threadIdx.x];
+        for (int v = 0; v < kWarps; ++v) t += sums[v][threadIdx.x];
         a.partial[(int64_t)blockIdx.x * 2 * kHeadDim + threadIdx.x] = t;
     }
 }
@@ -289,27 +371,28 @@ qk_weight_kernel(const float* partial, int64_t blocks, T* dwq, T* dwk) {
 
 constexpr int64_t kManyWarps = 152 * 48;     // warps that fill the GPU
 
-// heads a warp takes in a row: all of them where the tokens alone make enough warps,
-// fewer (down to one) where they do not
-int heads_per_warp(int64_t groups, int64_t heads) {
-    const int64_t runs = (kManyWarps + groups - 1) / groups;
-    const int64_t per = (heads + runs - 1) / runs;
-    return (int)(per < 1 ? 1 : per);
+// A run is all the heads of a tensor where the tokens alone make enough warps, fewer (down to
+// one) where they do not.
+Work plan(int64_t tokens, int64_t Hq, int64_t Hk) {
+    Work w;
+    w.groups = (tokens + kTok - 1) / kTok;
+    const int64_t runs = (kManyWarps + w.groups - 1) / w.groups;
+    const int64_t per = (Hq + Hk + runs - 1) / runs, most = Hq > Hk ? Hq : Hk;
+    w.per = (int32_t)(per < 1 ? 1 : per < most ? per : most);
+    w.q_runs = (int32_t)((Hq + w.per - 1) / w.per);
+    w.units = w.groups * (w.q_runs + (Hk + w.per - 1) / w.per);
+    return w;
 }
 
 template <class T>
 int forward_as(const QkArgs& a, bool interleaved, cudaStream_t stream) {
-    const int64_t groups = (a.tokens + kTok - 1) / kTok, heads = (int64_t)a.Hq + a.Hk;
-    const int per = heads_per_warp(groups, heads);
-    const int64_t units = groups * ((heads + per - 1) / per);
-    const int64_t blocks = (units + kWarps - 1) / kWarps;
+    const Work w = plan(a.tokens, a.Hq, a.Hk);
+    const int64_t blocks = (w.units + kWarps - 1) / kWarps;
     if (blocks > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many rows");
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        if (interleaved)
-            qk_forward_kernel<T, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a, groups, per, units);
-        else
-            qk_forward_kernel<T, false><<<(unsigned)blocks, kThreads, 0, stream>>>(a, groups, per, units);
+        if (interleaved) qk_forward_kernel<T, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a, w);
+        else qk_forward_kernel<T, false><<<(unsigned)blocks, kThreads, 0, stream>>>(a, w);
     }
     const cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "qk_forward_kernel");
@@ -317,16 +400,12 @@ int forward_as(const QkArgs& a, bool interleaved, cudaStream_t stream) {
 
 template <class T>
 int backward_as(const QkArgs& a, bool interleaved, void* dwq, void* dwk, cudaStream_t stream) {
-    const int64_t groups = (a.tokens + kTok - 1) / kTok, heads = (int64_t)a.Hq + a.Hk;
-    const int per = heads_per_warp(groups, heads);
-    const int64_t units = groups * ((heads + per - 1) / per);
-    const int64_t blocks = qk_backward_blocks(a.tokens, heads);
+    const Work w = plan(a.tokens, a.Hq, a.Hk);
+    const int64_t blocks = qk_backward_blocks(a.tokens, a.Hq, a.Hk);
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        if (interleaved)
-            qk_backward_kernel<T, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a, groups, per, units);
-        else
-            qk_backward_kernel<T, false><<<(unsigned)blocks, kThreads, 0, stream>>>(a, groups, per, units);
+        if (interleaved) qk_backward_kernel<T, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a, w);
+        else qk_backward_kernel<T, false><<<(unsigned)blocks, kThreads, 0, stream>>>(a, w);
     }
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return cuda_fail(err, "qk_backward_kernel");
@@ -343,12 +422,10 @@ int backward_as(const QkArgs& a, bool interleaved, void* dwq, void* dwk, cudaStr
 }  // namespace
 
 // at most four blocks on each of 152 SMs: each block leaves one row of partial sums
-int64_t qk_backward_blocks(int64_t tokens, int64_t heads) {
-    const int64_t groups = (tokens + kTok - 1) / kTok;
-    const int per = heads_per_warp(groups, heads);
-    const int64_t units = groups * ((heads + per - 1) / per);
-    const int64_t blocks = (units + kWarps - 1) / kWarps;
-    return blocks < 152 * 4 ? blocks : 152 * 4;
+int64_t qk_backward_blocks(int64_t tokens, int64_t Hq, int64_t Hk) {
+    const int64_t blocks = (plan(tokens, Hq, Hk).units + kWarps - 1) / kWarps;
+    const int64_t rounds = (blocks + 152 * 4 - 1) / (152 * 4);
+    return (blocks + rounds - 1) / rounds;     // the same number of units a warp, but for the last
 }
 
 int launch_qk_norm_rope(const QkArgs& a, int32_t dtype, bool interleaved, cudaStream_t stream) {
