@@ -489,30 +489,28 @@ def _on_stream(op):
     return call
 
 
-def _refuse(t, name, shape, like, dtype):
+def _refuse(t, name, shape, dev, dtype):
     if t is None:
         raise ValueError(f"{name} is needed")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on device {dev}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
 
 
-def _need(t, name, shape, like, dtype=None):
-    """The tensor's address, after its checks against `like` (dtype unless given, device)."""
-    dtype = dtype or like.dtype
-    if t is None or t.dtype != dtype or t.shape != shape or t.get_device() != like.get_device() or \
-            not t.is_contiguous():
-        _refuse(t, name, shape, like, dtype)
+def _need(t, name, shape, dev, dtype):
+    """The tensor's address, after its checks."""
+    if t is None or t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, shape, dev, dtype)
     return t.data_ptr()
 
 
-def _may(t, name, shape, like, dtype=None):
+def _may(t, name, shape, dev, dtype):
     """As _need; None where the tensor is left out."""
-    return None if t is None else _need(t, name, shape, like, dtype)
+    return None if t is None else _need(t, name, shape, dev, dtype)
 
 
 def _empty(t, shape, like):
@@ -521,6 +519,14 @@ def _empty(t, shape, like):
         return t
     import torch
     return torch.empty(shape, dtype=like.dtype, device=like.device)
+
+
+def _as(t, like):
+    """`t`, or a new tensor as `like`."""
+    if t is not None:
+        return t
+    import torch
+    return torch.empty_like(like)
 
 
 def _workspace(workspace, nbytes, like):
@@ -549,13 +555,14 @@ def diffuser_qk_norm_rope(Q, K, q_weight=None, k_weight=None, positions=None, po
     Qo=Q and Ko=K work in place."""
     import torch
     code, B, Hq, Hk, n, d = _qk_shapes(Q, K)
-    Qo, Ko = _empty(Qo, Q.shape, Q), _empty(Ko, K.shape, Q)
+    dev, dt, qs, ks = Q.get_device(), Q.dtype, Q.shape, K.shape
+    Qo, Ko = _as(Qo, Q), _as(Ko, K)
     _check(_lib.diffuser_qk_norm_rope(
-        _need(Q, "Q", Q.shape, Q), _need(K, "K", K.shape, Q), code, B, Hq, Hk, n, d,
-        _may(q_weight, "q_weight", (d,), Q), _may(k_weight, "k_weight", (d,), Q),
+        _need(Q, "Q", qs, dev, dt), _need(K, "K", ks, dev, dt), code, B, Hq, Hk, n, d,
+        _may(q_weight, "q_weight", (d,), dev, dt), _may(k_weight, "k_weight", (d,), dev, dt),
         eps, theta, rotary_dim, int(interleaved),
-        _may(positions, "positions", (B, n), Q, torch.int64), position_offset,
-        _need(Qo, "Qo", Q.shape, Q), _need(Ko, "Ko", K.shape, Q), stream), "diffuser_qk_norm_rope")
+        _may(positions, "positions", (B, n), dev, torch.int64), position_offset,
+        _need(Qo, "Qo", qs, dev, dt), _need(Ko, "Ko", ks, dev, dt), stream), "diffuser_qk_norm_rope")
     return Qo, Ko
 
 
@@ -575,20 +582,21 @@ def diffuser_qk_norm_rope_backward(Q, K, dQo, dKo, q_weight=None, k_weight=None,
     where the weight is."""
     import torch
     code, B, Hq, Hk, n, d = _qk_shapes(Q, K)
-    dQ, dK = _empty(dQ, Q.shape, Q), _empty(dK, K.shape, Q)
+    dev, dt, qs, ks = Q.get_device(), Q.dtype, Q.shape, K.shape
+    dQ, dK = _as(dQ, Q), _as(dK, K)
     if q_weight is not None:
-        dq_weight = _empty(dq_weight, (d,), Q)
+        dq_weight = _as(dq_weight, q_weight)
     if k_weight is not None:
-        dk_weight = _empty(dk_weight, (d,), Q)
+        dk_weight = _as(dk_weight, k_weight)
     ws = _workspace(workspace, diffuser_qk_norm_rope_backward_workspace_size(B, Hq, Hk, n, d), Q)
     _check(_lib.diffuser_qk_norm_rope_backward(
-        _need(Q, "Q", Q.shape, Q), _need(K, "K", K.shape, Q),
-        _need(dQo, "dQo", Q.shape, Q), _need(dKo, "dKo", K.shape, Q), code, B, Hq, Hk, n, d,
-        _may(q_weight, "q_weight", (d,), Q), _may(k_weight, "k_weight", (d,), Q),
+        _need(Q, "Q", qs, dev, dt), _need(K, "K", ks, dev, dt),
+        _need(dQo, "dQo", qs, dev, dt), _need(dKo, "dKo", ks, dev, dt), code, B, Hq, Hk, n, d,
+        _may(q_weight, "q_weight", (d,), dev, dt), _may(k_weight, "k_weight", (d,), dev, dt),
         eps, theta, rotary_dim, int(interleaved),
-        _may(positions, "positions", (B, n), Q, torch.int64), position_offset,
-        _need(dQ, "dQ", Q.shape, Q), _need(dK, "dK", K.shape, Q),
-        _may(dq_weight, "dq_weight", (d,), Q), _may(dk_weight, "dk_weight", (d,), Q),
+        _may(positions, "positions", (B, n), dev, torch.int64), position_offset,
+        _need(dQ, "dQ", qs, dev, dt), _need(dK, "dK", ks, dev, dt),
+        _may(dq_weight, "dq_weight", (d,), dev, dt), _may(dk_weight, "dk_weight", (d,), dev, dt),
         ws.data_ptr(), ws.numel(), stream), "diffuser_qk_norm_rope_backward")
     return dQ, dK, dq_weight, dk_weight
 
@@ -613,14 +621,14 @@ def diffuser_linear(X, W, bias=None, residual=None, activation: int = DIFFUSER_A
     residual [...][F]; with save_pre (or `pre` given) returns (Y, pre), pre the argument of
     the activation, as the backward pass wants it.  Y=residual works in place."""
     lead, T, D, F = _dense_shapes(X, W)
-    out = (*lead, F)
+    dev, bf, out = X.get_device(), X.dtype, (*lead, F)
     Y = _empty(Y, out, X)
     if save_pre:
         pre = _empty(pre, out, X)
     _check(_lib.diffuser_linear(
-        _need(X, "X", X.shape, X), _need(W, "W", W.shape, X), _may(bias, "bias", (F,), X),
-        _may(residual, "residual", out, X), T, D, F, activation, _need(Y, "Y", out, X),
-        _may(pre, "pre", out, X), stream), "diffuser_linear")
+        _need(X, "X", X.shape, dev, bf), _need(W, "W", W.shape, dev, bf), _may(bias, "bias", (F,), dev, bf),
+        _may(residual, "residual", out, dev, bf), T, D, F, activation, _need(Y, "Y", out, dev, bf),
+        _may(pre, "pre", out, dev, bf), stream), "diffuser_linear")
     return Y if pre is None else (Y, pre)
 
 
@@ -638,16 +646,16 @@ def diffuser_linear_backward(X, W, dY, pre=None, activation: int = DIFFUSER_ACT_
     """Gradients (dX, dW, dbias) of diffuser_linear for dY [...][F]; one whose with_ is False
     is None and not computed.  The residual's gradient is dY."""
     lead, T, D, F = _dense_shapes(X, W)
-    out = (*lead, F)
-    dX = _empty(dX, X.shape, X) if with_dX else None
-    dW = _empty(dW, W.shape, X) if with_dW else None
+    dev, bf, out = X.get_device(), X.dtype, (*lead, F)
+    dX = _as(dX, X) if with_dX else None
+    dW = _as(dW, W) if with_dW else None
     dbias = _empty(dbias, (F,), X) if with_bias else None
     ws = _workspace(workspace, diffuser_linear_backward_workspace_size(T, D, F, activation), X)
     _check(_lib.diffuser_linear_backward(
-        _need(X, "X", X.shape, X), _need(W, "W", W.shape, X), _need(dY, "dY", out, X),
-        (_may if activation == DIFFUSER_ACT_NONE else _need)(pre, "pre", out, X), T, D, F, activation,
-        _may(dX, "dX", X.shape, X), _may(dW, "dW", W.shape, X),
-        _may(dbias, "dbias", (F,), X), ws.data_ptr(), ws.numel(), stream), "diffuser_linear_backward")
+        _need(X, "X", X.shape, dev, bf), _need(W, "W", W.shape, dev, bf), _need(dY, "dY", out, dev, bf),
+        (_may if activation == DIFFUSER_ACT_NONE else _need)(pre, "pre", out, dev, bf), T, D, F, activation,
+        _may(dX, "dX", X.shape, dev, bf), _may(dW, "dW", W.shape, dev, bf),
+        _may(dbias, "dbias", (F,), dev, bf), ws.data_ptr(), ws.numel(), stream), "diffuser_linear_backward")
     return dX, dW, dbias
 
 
@@ -657,12 +665,13 @@ def diffuser_gated_linear(X, Wgu, activation: int = DIFFUSER_ACT_SILU, save_pre:
     """H [...][F] = act(X Wg^T) * (X Wu^T) of bf16 tensors X [...][D], Wgu [2 F][D] (Wg's rows,
     then Wu's); with save_pre (or `pre` given) returns (H, pre), pre [...][2 F] both products."""
     lead, T, D, F = _dense_shapes(X, Wgu, 2)
-    H = _empty(H, (*lead, F), X)
+    dev, bf, out, both = X.get_device(), X.dtype, (*lead, F), (*lead, 2 * F)
+    H = _empty(H, out, X)
     if save_pre:
-        pre = _empty(pre, (*lead, 2 * F), X)
+        pre = _empty(pre, both, X)
     _check(_lib.diffuser_gated_linear(
-        _need(X, "X", X.shape, X), _need(Wgu, "Wgu", Wgu.shape, X), T, D, F, activation,
-        _need(H, "H", (*lead, F), X), _may(pre, "pre", (*lead, 2 * F), X), stream),
+        _need(X, "X", X.shape, dev, bf), _need(Wgu, "Wgu", Wgu.shape, dev, bf), T, D, F, activation,
+        _need(H, "H", out, dev, bf), _may(pre, "pre", both, dev, bf), stream),
         "diffuser_gated_linear")
     return H if pre is None else (H, pre)
 
@@ -680,13 +689,14 @@ def diffuser_gated_linear_backward(X, Wgu, dH, pre, activation: int = DIFFUSER_A
     """Gradients (dX, dWgu) of diffuser_gated_linear for dH [...][F], pre as the forward kept it;
     one whose with_ is False is None and not computed."""
     lead, T, D, F = _dense_shapes(X, Wgu, 2)
-    dX = _empty(dX, X.shape, X) if with_dX else None
-    dWgu = _empty(dWgu, Wgu.shape, X) if with_dW else None
+    dev, bf, out, both = X.get_device(), X.dtype, (*lead, F), (*lead, 2 * F)
+    dX = _as(dX, X) if with_dX else None
+    dWgu = _as(dWgu, Wgu) if with_dW else None
     ws = _workspace(workspace, diffuser_gated_linear_backward_workspace_size(T, D, F), X)
     _check(_lib.diffuser_gated_linear_backward(
-        _need(X, "X", X.shape, X), _need(Wgu, "Wgu", Wgu.shape, X),
-        _need(dH, "dH", (*lead, F), X), _need(pre, "pre", (*lead, 2 * F), X), T, D, F, activation,
-        _may(dX, "dX", X.shape, X), _may(dWgu, "dWgu", Wgu.shape, X),
+        _need(X, "X", X.shape, dev, bf), _need(Wgu, "Wgu", Wgu.shape, dev, bf),
+        _need(dH, "dH", out, dev, bf), _need(pre, "pre", both, dev, bf), T, D, F, activation,
+        _may(dX, "dX", X.shape, dev, bf), _may(dWgu, "dWgu", Wgu.shape, dev, bf),
         ws.data_ptr(), ws.numel(), stream), "diffuser_gated_linear_backward")
     return dX, dWgu
 

@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/diffuser.h"
+#include "packed.cuh"
 #include "sm100_ptx.cuh"
 
 namespace dfs {
@@ -30,13 +31,14 @@ constexpr float kTanhC = 0.7978845608028654f;      // sqrt(2 / pi)
 constexpr float kTanhA = 0.044715f;
 constexpr float kPhiC = 0.3989422804014327f;       // 1 / sqrt(2 pi)
 
-// x * s with s in [0, 1] a saturating factor, 0 at x = -inf: the lowest finite value stands in
-// for it (NaN stays NaN)
-__device__ __forceinline__ float gate(float x, float s) {
+// x, or the lowest finite value for -inf (NaN stays NaN)
+__device__ __forceinline__ float finite_below(float x) {
     float y;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-3.4028234663852886e38f));
-    return y * s;
+    return y;
 }
+// x * s with s in [0, 1] a saturating factor, 0 at x = -inf
+__device__ __forceinline__ float gate(float x, float s) { return finite_below(x) * s; }
 
 // The normal distribution function at p and exp(-p^2 / 2).  With x = |p|, Phi(-x) =
 // exp(-x^2 / 2) m(x), m the Mills ratio: t q(t) with t = 1 / (1 + 0.3 x) and q of degree 7, a
@@ -93,6 +95,29 @@ __device__ __forceinline__ float2 value_slope(float p) {
         return make_float2(gate(p, s), s + (q == 0.f ? 0.f : p * q));
     }
     return make_float2(p, 1.f);
+}
+
+// The same values two at a time: the products and sums of both in one instruction, which the
+// dense products' epilogues are bound by.
+template <int kAct>
+__device__ __forceinline__ packed::F2 value2(packed::F2 p) {
+    using namespace packed;
+    if constexpr (kAct == DIFFUSER_ACT_SILU || kAct == DIFFUSER_ACT_GELU_TANH) {
+        F2 x;                                    // exponent of 2 in 1 / (1 + 2^x)
+        if constexpr (kAct == DIFFUSER_ACT_SILU) {
+            x = mul(p, both(-1.4426950408889634f));
+        } else {
+            constexpr float c = -2.f * kTanhC * 1.4426950408889634f;
+            x = mul(p, fma(mul(p, p), both(c * kTanhA), both(c)));
+        }
+        const float2 e = un(x);
+        const float2 d = un(add(f2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y)), both(1.f)));
+        const float2 q = un(p);
+        return mul(f2(finite_below(q.x), finite_below(q.y)), f2(rcp_approx(d.x), rcp_approx(d.y)));
+    } else {
+        const float2 q = un(p);
+        return f2(value<kAct>(q.x), value<kAct>(q.y));
+    }
 }
 
 // value<act> for an activation known at run time (uniform over the launch)

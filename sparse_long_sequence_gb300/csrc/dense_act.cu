@@ -95,19 +95,22 @@ act_backward_kernel(const __nv_bfloat16* dY, const __nv_bfloat16* P, int64_t row
     partial[(int64_t)blockIdx.y * F + col] = t;
 }
 
-// column sums over the chunks: 32 columns a block, its warps take every eighth chunk
-__global__ void __launch_bounds__(kThreads) colsum_kernel(const float* partial, int64_t chunks, int32_t F, __nv_bfloat16* out) {
-    __shared__ float sums[kWarps][32];
+// column sums over the chunks: 32 columns a block, its 32 warps take every 32nd chunk
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(kSumWarps * 32) colsum_kernel(const float* partial, int64_t chunks, int32_t F, __nv_bfloat16* out) {
+    __shared__ float sums[kSumWarps][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = (int)blockIdx.x * 32 + lane;
     float t = 0.f;
-    if (col < F)
-        for (int64_t k = warp; k < chunks; k += kWarps) t += partial[k * F + col];
+    if (col < F) {
+#pragma unroll 8
+        for (int64_t k = warp; k < chunks; k += kSumWarps) t += partial[k * F + col];
+    }
     sums[warp][lane] = t;
     __syncthreads();
     if (warp || col >= F) return;
     t = 0.f;
-    for (int w = 0; w < kWarps; ++w) t += sums[w][lane];
+    for (int w = 0; w < kSumWarps; ++w) t += sums[w][lane];
     out[col] = __float2bfloat16_rn(t);
 }
 
@@ -209,7 +212,7 @@ int launch_act_backward(const void* dY, const void* P, int64_t rows, int32_t F, 
     if (!colsum) return DIFFUSER_OK;
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        colsum_kernel<<<(unsigned)((F + 31) / 32), kThreads, 0, stream>>>(partial, chunks, F,
+        colsum_kernel<<<(unsigned)((F + 31) / 32), kSumWarps * 32, 0, stream>>>(partial, chunks, F,
                                                                          static_cast<__nv_bfloat16*>(colsum));
     }
     err = cudaGetLastError();

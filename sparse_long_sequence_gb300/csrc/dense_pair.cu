@@ -14,10 +14,10 @@
 // 128 x kBn fp32 accumulator in tensor memory, twice, so that a tile's epilogue overlaps
 // the next tile's MMAs.
 //
-// Warps of a CTA: 0 loads (TMA, a ring of K steps of 64), 1 multiplies (CTA 0 only), 2..9 are
-// the epilogue, each alone on its 32 accumulator lanes and half of the tile's columns, in blocks
-// of 32: tensor memory -> registers (bias, activation, residual) -> a swizzled 2 KB buffer of
-// its own (four, used in turn) -> TMA store, which drops what lies outside the result.  Warps
+// Warps of a CTA: 0 loads (TMA, a ring of K steps of 64), 1 multiplies (CTA 0 only), the others
+// are the epilogue, each alone on its 32 accumulator lanes and some of the tile's columns, in blocks of
+// 32: tensor memory -> registers (bias, activation, residual) -> a swizzled 2 KB buffer of
+// its own (used in turn) -> TMA store, which drops what lies outside the result.  Warps
 // wait for no other warp: with 128 x 64 blocks shared by four warps the forward 512 -> 2048 of
 // 32768 tokens with gelu and kept pre-activations took 132 us.  The residual arrives by TMA in
 // the buffer the result leaves from.  Gated: B's rows are 128 gate rows (CTA 0) and 128 up rows
@@ -44,11 +44,10 @@ constexpr int kTK = 64;                           // K step: 64 bf16, one 128-by
 constexpr int kBox = 64 * kTK * 2;                // an MN-major box: 64 x 64, 8 KB
 constexpr int kABytes = 128 * kTK * 2;            // 16 KB a CTA
 constexpr int kThreads = 320;
-constexpr int kEpiWarp0 = 2, kEpiWarps = 8;
+constexpr int kEpiWarp0 = 2;
 constexpr int kBlock = 32;                        // an epilogue step: 32 rows x 32 columns of a warp
 constexpr int kBufBytes = 32 * kBlock * 2;        // 2 KB
-constexpr int kBufs = 4;                          // a warp's buffers
-constexpr int kEpiBytes = kEpiWarps * kBufs * kBufBytes;
+constexpr int kEpiBytes = 32 * kBufBytes;          // the epilogue warps' buffers: 2 of 16, 4 of 8
 constexpr int kBarBytes = 1024;                   // barriers and the tensor memory's address
 constexpr int kGroupTiles = 8;                    // i tiles walked together (L2 reuse of both operands)
 
@@ -81,9 +80,18 @@ __device__ __forceinline__ Tile tile_at(const PairArgs& a, int t, int width) {
     return {(grp * kGroupTiles + in % rows) * kTI, in / rows * width};
 }
 
-// v = act(v) for 32 values (the activation is uniform over the launch)
-__device__ __forceinline__ void activate(int which, float (&v)[32]) {
-#define DFS_EACH(A) case A: _Pragma("unroll") for (int c = 0; c < 32; ++c) v[c] = act::value<A>(v[c]); break;
+// 32 neighbouring columns of a lane's row as 16 packed pairs.
+using packed::F2;
+__device__ __forceinline__ void load_acc(uint32_t taddr, F2 (&v)[16]) {
+    uint32_t r[32];
+    ptx::tmem_ld32_issue(taddr, r);
+    ptx::tmem_ld_wait32(r);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) v[c] = packed::f2(__uint_as_float(r[2 * c]), __uint_as_float(r[2 * c + 1]));
+}
+// v = act(v) (the activation is uniform over the launch)
+__device__ __forceinline__ void activate(int which, F2 (&v)[16]) {
+#define DFS_EACH(A) case A: _Pragma("unroll") for (int c = 0; c < 16; ++c) v[c] = act::value2<A>(v[c]); break;
     switch (which) {
         DFS_EACH(DIFFUSER_ACT_RELU)
         DFS_EACH(DIFFUSER_ACT_GELU)
@@ -93,28 +101,27 @@ __device__ __forceinline__ void activate(int which, float (&v)[32]) {
     }
 #undef DFS_EACH
 }
-
-// 32 columns of a lane's row into its swizzled buffer (64-byte rows: 16-byte piece q at
-// q ^ ((row / 2) % 4), so that eight neighbouring rows' writes fall in eight bank groups)
-__device__ __forceinline__ void put_row(uint8_t* row, int sw, const float (&v)[32]) {
+// into the lane's row of a swizzled buffer (64-byte rows: 16-byte piece q at q ^ ((row / 2) % 4),
+// so that eight neighbouring rows' writes fall in eight bank groups)
+__device__ __forceinline__ void put_row(uint8_t* row, int sw, const F2 (&v)[16]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         uint32_t w[4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * q + 2 * p], v[8 * q + 2 * p + 1]);
+            const float2 x = packed::un(v[4 * q + p]);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
             w[p] = *reinterpret_cast<const uint32_t*>(&h);
         }
         *reinterpret_cast<uint4*>(row + ((q ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
-__device__ __forceinline__ void add8(float* v, const uint4& r) {
+// eight bf16 values added to v[0..3]
+__device__ __forceinline__ void add8(F2* v, const uint4& r) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        v[2 * p] += __uint_as_float(w[p] << 16);
-        v[2 * p + 1] += __uint_as_float(w[p] & 0xffff0000u);
-    }
+    for (int p = 0; p < 4; ++p)
+        v[p] = packed::add(v[p], packed::f2(__uint_as_float(w[p] << 16), __uint_as_float(w[p] & 0xffff0000u)));
 }
 
 // ---- the roles both kernels share -------------------------------------------------
@@ -173,14 +180,22 @@ struct Roles {
     }
 };
 
-template <bool kAMn, bool kBMn, bool kGated, int kBn>
-__global__ void __launch_bounds__(kThreads, 1)
+// kEpilogue: bias, activation, residual and kept pre-activations may be asked for; gated has one.
+// 16 epilogue warps then, as the accumulators' arithmetic outlasts the MMAs of a short K: with
+// 8 the forward 512 -> 2048 of 32768 tokens, gelu and kept pre-activations, took 99 us.
+constexpr int epi_warps(bool epilogue) { return epilogue ? 16 : 8; }
+constexpr int pair_threads(bool epilogue) { return 32 * (kEpiWarp0 + epi_warps(epilogue)); }
+
+template <bool kAMn, bool kBMn, bool kGated, int kBn, bool kEpilogue>
+__global__ void __launch_bounds__(pair_threads(kEpilogue), 1)
 dense_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmPre,
                   const __grid_constant__ CUtensorMap tmRes, const __grid_constant__ PairArgs a) {
     using R = Roles<kAMn, kBMn, kGated, kBn>;
     constexpr int kStages = R::kStages, kWidth = R::kWidth;
-    constexpr int kBlocks = kWidth / 2 / kBlock;              // column blocks of an epilogue warp
+    constexpr int kEpiWarps = epi_warps(kEpilogue), kBufs = kEpiBytes / kBufBytes / kEpiWarps;
+    constexpr int kEpiCols = kWidth / (kEpiWarps / 4);        // columns of an epilogue warp
+    constexpr int kBlocks = kEpiCols / kBlock;
     static_assert(kBlocks >= 1 && kBlocks <= kBufs, "a tile's residual blocks have a buffer each");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -263,105 +278,87 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             const Tile tl = tile_at(a, pair + lt * pairs, kWidth);
             const int buf = lt & 1;
             const int row0 = tl.i0 + 128 * rank + 32 * quad;
-            const int c_first = tl.j0 + grp * (kWidth / 2);
+            const int c_first = tl.j0 + grp * kEpiCols;
             // blocks with something to store
             const int live = row0 < a.I ? max(0, min(kBlocks, (a.J - c_first + kBlock - 1) / kBlock)) : 0;
             auto fetch_residual = [&](int k, int b) {
                 ptx::mbar_arrive_expect_tx(&rbar[b], kBufBytes);
                 ptx::tma_load_2d(wbuf + b * kBufBytes, &tmRes, &rbar[b], c_first + k * kBlock, row0);
             };
-            if (a.residual && lead && live) {
-                // without `pre` every block's residual fits its buffer now, with it the first one's
+            if (kEpilogue && a.residual && !a.pre && lead && live) {
+                // every block's residual into the buffer its result will leave from
                 ptx::bulk_wait_read<0>();
-                if (a.pre) fetch_residual(0, (u + 1) % kBufs);
-                else for (int k = 0; k < live; ++k) fetch_residual(k, (u + k) % kBufs);
+                for (int k = 0; k < live; ++k) fetch_residual(k, (u + k) % kBufs);
             }
             ptx::mbar_wait(&acc_full[buf], (lt / 2) & 1, a.status);
             __syncwarp();
             ptx::tc_fence_after();
-            const uint32_t acc = tmem + lane_base + buf * kBn + grp * (kWidth / 2);
-            uint32_t r[32], ru[kGated ? 32 : 1];
-            auto issue = [&](int k) {
-                ptx::tmem_ld32_issue(acc + k * kBlock, r);
-                if constexpr (kGated) ptx::tmem_ld32_issue(acc + kBn / 2 + k * kBlock, ru);
-            };
+            const uint32_t acc = tmem + lane_base + buf * kBn + grp * kEpiCols;
             // the accumulator is read: the MMAs of the tile after next may overwrite it
             auto release = [&]() {
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lead) ptx::mbar_arrive_cluster(acc_empty0 + 8 * buf);
             };
-            if (live) issue(0); else release();
+            if (!live) release();
             for (int k = 0; k < live; ++k) {
-                float v[32], w[kGated ? 32 : 1];
-                ptx::tmem_ld_wait32(r);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
-                if constexpr (kGated) {
-                    ptx::tmem_ld_wait32(ru);
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) w[c] = __uint_as_float(ru[c]);
-                }
-                if (k + 1 < live) issue(k + 1); else release();
                 const int col = c_first + k * kBlock;
-                if (lead) {
-                    // the last stores from this block's buffers have left them
-                    if (a.residual) {
-                        if (a.pre && k + 1 < live) {
-                            ptx::bulk_wait_read<0>();
-                            fetch_residual(k + 1, (u + 3) % kBufs);
-                        }
-                    } else if (!a.pre) {
-                        ptx::bulk_wait_read<kBufs - 1>();
-                    } else {
-                        ptx::bulk_wait_read<kBufs - (kGated ? 3 : 2)>();
-                    }
-                }
-                __syncwarp();
-                auto buffer = [&](int n) { return wbuf + (u + n) % kBufs * kBufBytes; };
-                int n = 0;                                     // stores of this block
-                if constexpr (kGated) {
-                    if (a.pre) {
-                        put_row(buffer(0) + row_at, sw, v);
-                        put_row(buffer(1) + row_at, sw, w);
-                        n = 2;
-                    }
-                    activate(a.act, v);
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) v[c] *= w[c];
-                } else {
-                    if (a.bias) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (col + 8 * q < a.J) add8(v + 8 * q, __ldg(reinterpret_cast<const uint4*>(a.bias + col + 8 * q)));
-                    }
-                    if (a.pre) {
-                        put_row(buffer(0) + row_at, sw, v);
-                        n = 1;
-                    }
-                    activate(a.act, v);
-                    if (a.residual) {
-                        const int b = (u + n) % kBufs;
-                        ptx::mbar_wait(&rbar[b], (rphase >> b) & 1, a.status);
-                        rphase ^= 1u << b;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            add8(v + 8 * q, *reinterpret_cast<const uint4*>(buffer(n) + row_at + ((q ^ sw) << 4)));
-                    }
-                }
-                put_row(buffer(n) + row_at, sw, v);
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lead) {
-                    for (int part = 0; part < n; ++part) {
-                        if constexpr (kGated) ptx::tma_store_3d(&tmPre, buffer(part), col, part, row0);
-                        else ptx::tma_store_2d(&tmPre, buffer(part), col, row0);
+                // one store: wait until its buffer's last one has left, write the rows, hand over
+                auto put = [&](const CUtensorMap& map, int part, const F2 (&v)[16]) {
+                    uint8_t* b = wbuf + u % kBufs * kBufBytes;
+                    if (lead) ptx::bulk_wait_read<kBufs - 1>();
+                    __syncwarp();
+                    put_row(b + row_at, sw, v);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lead) {
+                        if (part >= 0) ptx::tma_store_3d(&map, b, col, part, row0);
+                        else ptx::tma_store_2d(&map, b, col, row0);
                         ptx::bulk_commit();
                     }
-                    ptx::tma_store_2d(&tmOut, buffer(n), col, row0);
-                    ptx::bulk_commit();
+                    ++u;
+                };
+                if (kEpilogue && a.residual && a.pre && lead) {
+                    ptx::bulk_wait_read<0>();
+                    fetch_residual(k, (u + 1) % kBufs);
                 }
-                u += n + 1;
+                F2 v[16];
+                load_acc(acc + k * kBlock, v);
+                if constexpr (kGated) {
+                    // (u is read again after the activation: both at once would not fit 96 registers)
+                    F2 w[16];
+                    if (a.pre) {
+                        put(tmPre, 0, v);
+                        load_acc(acc + kBn / 2 + k * kBlock, w);
+                        put(tmPre, 1, w);
+                    }
+                    activate(a.act, v);
+                    load_acc(acc + kBn / 2 + k * kBlock, w);
+                    if (k + 1 == live) release();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) v[c] = packed::mul(v[c], w[c]);
+                } else {
+                    if (k + 1 == live) release();
+                    if constexpr (kEpilogue) {
+                        if (a.bias) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (col + 8 * q < a.J)
+                                    add8(v + 4 * q, __ldg(reinterpret_cast<const uint4*>(a.bias + col + 8 * q)));
+                        }
+                        if (a.pre) put(tmPre, -1, v);
+                        activate(a.act, v);
+                        if (a.residual) {
+                            const int b = u % kBufs;
+                            ptx::mbar_wait(&rbar[b], (rphase >> b) & 1, a.status);
+                            rphase ^= 1u << b;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                add8(v + 4 * q, *reinterpret_cast<const uint4*>(wbuf + b * kBufBytes + row_at + ((q ^ sw) << 4)));
+                        }
+                    }
+                }
+                put(tmOut, -1, v);
             }
         }
         if (lead) ptx::bulk_wait<0>();
@@ -529,10 +526,10 @@ dense_pair_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_co
 
 // Clusters of `ctas` CTAs that run at once on the current device (0 on failure).
 template <class Kernel>
-int resident_clusters(Kernel kernel, int ctas, int smem) {
+int resident_clusters(Kernel kernel, int ctas, int threads, int smem) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -546,10 +543,10 @@ int resident_clusters(Kernel kernel, int ctas, int smem) {
 }
 
 template <class Kernel, class... Args>
-int launch_clusters(Kernel kernel, int ctas, int64_t clusters, int smem, cudaStream_t stream, const Args&... args) {
+int launch_clusters(Kernel kernel, int ctas, int64_t clusters, int threads, int smem, cudaStream_t stream, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ctas * clusters));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -569,7 +566,9 @@ int launch_clusters(Kernel kernel, int ctas, int64_t clusters, int smem, cudaStr
 
 template <bool kAMn, bool kBMn, bool kGated, int kBn>
 int launch_pair_as(const CUtensorMap (&tm)[5], const PairArgs& a, cudaStream_t stream) {
-    auto kernel = dense_pair_kernel<kAMn, kBMn, kGated, kBn>;
+    constexpr bool kEpilogue = !kBMn;             // the gradients have none
+    constexpr int kAll = pair_threads(kEpilogue);
+    auto kernel = dense_pair_kernel<kAMn, kBMn, kGated, kBn, kEpilogue>;
     static std::atomic<uint64_t> done{0};
     static std::atomic<int> fit[64];
     const cudaError_t err = allow_smem(kernel, smem_bytes(kBn), done);
@@ -578,13 +577,13 @@ int launch_pair_as(const CUtensorMap (&tm)[5], const PairArgs& a, cudaStream_t s
     if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
     int pairs = fit[dev & 63].load();
     if (!pairs) {
-        pairs = resident_clusters(kernel, 2, smem_bytes(kBn));
+        pairs = resident_clusters(kernel, 2, kAll, smem_bytes(kBn));
         if (pairs < 1) return fail(DIFFUSER_ERR_CUDA, "no CTA pair of the dense product fits the device");
         fit[dev & 63].store(pairs);
     }
     const int64_t tiles = (int64_t)a.i_tiles * a.j_tiles;
-    return launch_clusters(kernel, 2, tiles < pairs ? tiles : pairs, smem_bytes(kBn), stream, tm[0], tm[1], tm[2], tm[3],
-                           tm[4], a);
+    return launch_clusters(kernel, 2, tiles < pairs ? tiles : pairs, kAll, smem_bytes(kBn), stream, tm[0], tm[1], tm[2],
+                           tm[3], tm[4], a);
 }
 
 template <bool kAMn, bool kBMn, bool kGated, int kBn, int kSplits>
@@ -594,7 +593,7 @@ int launch_split_as(const CUtensorMap (&tm)[5], const PairArgs& a, const Results
     constexpr int kSmem = 1024 + stage_count(kBn) * (kABytes + b_bytes(kBn)) + kBarBytes;
     const cudaError_t err = allow_smem(kernel, kSmem, done);
     if (err != cudaSuccess) return cuda_fail(err, "cudaFuncSetAttribute(dense pair split kernel)");
-    return launch_clusters(kernel, 2 * kSplits, (int64_t)a.i_tiles * a.j_tiles, kSmem, stream, tm[0], tm[1], a, r);
+    return launch_clusters(kernel, 2 * kSplits, (int64_t)a.i_tiles * a.j_tiles, kThreads, kSmem, stream, tm[0], tm[1], a, r);
 }
 
 template <bool kAMn, bool kBMn, bool kGated, int kBn>
@@ -617,15 +616,15 @@ int dense_pair_clusters(int splits) {
         if (splits == 4) {
             static std::atomic<uint64_t> done{0};
             auto kernel = dense_pair_split_kernel<false, false, false, 256, 4>;
-            if (allow_smem(kernel, kSmem, done) == cudaSuccess) n = resident_clusters(kernel, 8, kSmem);
+            if (allow_smem(kernel, kSmem, done) == cudaSuccess) n = resident_clusters(kernel, 8, kThreads, kSmem);
         } else if (splits == 2) {
             static std::atomic<uint64_t> done{0};
             auto kernel = dense_pair_split_kernel<false, false, false, 256, 2>;
-            if (allow_smem(kernel, kSmem, done) == cudaSuccess) n = resident_clusters(kernel, 4, kSmem);
+            if (allow_smem(kernel, kSmem, done) == cudaSuccess) n = resident_clusters(kernel, 4, kThreads, kSmem);
         } else {
             static std::atomic<uint64_t> done{0};
-            auto kernel = dense_pair_kernel<false, false, false, 256>;
-            if (allow_smem(kernel, smem_bytes(256), done) == cudaSuccess) n = resident_clusters(kernel, 2, smem_bytes(256));
+            auto kernel = dense_pair_kernel<false, false, false, 256, true>;
+            if (allow_smem(kernel, smem_bytes(256), done) == cudaSuccess) n = resident_clusters(kernel, 2, pair_threads(true), smem_bytes(256));
         }
         if (n < 1) n = 1;
         f.store(n);

@@ -23,7 +23,7 @@
 #include <cstdint>
 
 #include "layer_ops.h"
-#include "sm100_ptx.cuh"
+#include "packed.cuh"
 
 namespace dfs {
 namespace {
@@ -33,30 +33,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kRowLanes = 8;                 // lanes of a row
 constexpr int kTok = 32 / kRowLanes;         // tokens of a warp
 constexpr unsigned kFull = 0xffffffffu;
-
-// Two fp32 values in a 64-bit register: one instruction works on both.
-struct F2 { uint64_t w; };
-__device__ __forceinline__ F2 f2(float x, float y) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.w) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 un(F2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v.w));
-    return r;
-}
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.w) : "l"(a.w), "l"(b.w));
-    return r;
-}
-__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.w) : "l"(a.w), "l"(b.w), "l"(c.w));
-    return r;
-}
-__device__ __forceinline__ F2 both(float x) { return f2(x, x); }
+using namespace packed;
 
 // A lane's eight features of a row: piece A in v[0], v[1], piece B in v[2], v[3].
 template <class T> struct Io;

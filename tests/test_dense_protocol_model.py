@@ -5,14 +5,15 @@ protocols as designed; keeping them in step with the kernels is a review duty wh
 either changes.
 
 The pair kernel: CTA 0's full barriers take one arrival (the expected bytes) and both CTAs'
-copies; a commit arrives on both CTAs' barriers; the accumulators are freed by the 2 x 8
-epilogue warps of the pair; a warp's residual barriers take one arrival per load.
+copies; a commit arrives on both CTAs' barriers; the accumulators are freed by the pair's
+epilogue warps (16 a CTA, 8 for the gradients); a warp's residual barriers take one arrival
+per load.
 """
 import pytest
 
 from tests.barrier_model import play
 
-BUFS, WARPS = 4, 8
+BUFS, WARPS = 2, 16
 
 
 def wait(bar, k):
@@ -23,8 +24,8 @@ def arrive(bar):
     return ("a", bar)
 
 
-def pair(my, k_blocks, stages, blocks=4, residual=False, pre=False, acc_empty=2 * WARPS, ring=True,
-         live=lambda rank, warp, lt: 4):
+def pair(my, k_blocks, stages, blocks=2, residual=False, pre=False, acc_empty=2 * WARPS, ring=True,
+         live=lambda rank, warp, lt: 2):
     counts = {("full", s): 2 for s in range(stages)}       # the expect and the peer's copies
     for r in range(2):
         counts.update({("empty", r, s): 1 for s in range(stages)})
@@ -65,23 +66,23 @@ def pair(my, k_blocks, stages, blocks=4, residual=False, pre=False, acc_empty=2 
                     ops.append(arrive(("res", r, w, b)))
                     loads[b] += 1
                     assert loads[b] - waits[b] <= 1, "a residual lands in a buffer that holds one"
-                if residual and now:
-                    for k in range(1 if pre else now):
-                        load((u + 1 if pre else u + k) % BUFS)
+                if residual and not pre:
+                    for k in range(now):
+                        load((u + k) % BUFS)
                 ops.append(wait(("accF", r, lt & 1), lt // 2))
                 if not now:
                     ops.append(arrive(("accE", lt & 1)))
                 for k in range(now):
+                    if residual and pre:
+                        load((u + 1) % BUFS)
                     if k + 1 == now:
                         ops.append(arrive(("accE", lt & 1)))
-                    if residual and pre and k + 1 < now:
-                        load((u + 3) % BUFS)
-                    n = 1 if pre else 0
+                    u += 1 if pre else 0
                     if residual:
-                        b = (u + n) % BUFS
+                        b = u % BUFS
                         ops.append(wait(("res", r, w, b), waits[b]))
                         waits[b] += 1
-                    u += n + 1
+                    u += 1
             roles.append(ops)
     return play(roles, counts)
 
@@ -92,14 +93,14 @@ def test_pair_protocol_completes(stages, k_blocks):
     for my in (0, 1, 2, 5):
         for residual in (False, True):
             for pre in (False, True):
-                for blocks in (2, 4):
+                for blocks in (1, 2):
                     assert pair(my, k_blocks, stages, blocks, residual, pre) == "done"
 
 
 def test_pair_protocol_with_ragged_tiles():
     # warps with some or no block inside the result
     for pre in (False, True):
-        assert pair(5, 3, 5, residual=True, pre=pre, live=lambda r, w, lt: (r + 2 * w + lt) % 5) == "done"
+        assert pair(5, 3, 5, residual=True, pre=pre, live=lambda r, w, lt: (r + 2 * w + lt) % 3) == "done"
 
 
 def test_pair_model_detects_planted_mistakes():
