@@ -372,6 +372,178 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     }
 }
 
+// ---- both gradients of a product in one launch --------------------------------------
+// dX = dP W and dW = dP^T X need nothing of each other, and neither's tiles fill a whole number
+// of waves.  One persistent kernel runs both: a pair takes its share of the longer tiles (K
+// steps) first, then of the shorter ones, dealt on the host so that all pairs finish nearly
+// together (each pair's tiles follow one another, j fastest, so that it rereads its rows of A
+// from the L2).
+struct GradDeal {
+    int32_t longer;            // 0: dX has the longer tiles, 1: dW
+    int32_t a_pairs;           // pairs with one long tile more
+    int32_t longs;             // long tiles of the others
+    int32_t a_shorts, a_rest;  // short tiles of the first a_pairs pairs, one more for a_rest of them
+    int32_t b_shorts, b_rest;  // and of the others
+};
+struct GradArgs {
+    PairArgs p[2];             // dX, dW
+    GradDeal deal;
+};
+struct Share {
+    int l0, nl, s0, ns;        // first long and short tile and their counts
+};
+__device__ __forceinline__ Share share_of(const GradDeal& d, int pair) {
+    Share s;
+    s.nl = d.longs + (pair < d.a_pairs);
+    s.l0 = pair * d.longs + min(pair, d.a_pairs);
+    if (pair < d.a_pairs) {
+        s.ns = d.a_shorts + (pair < d.a_rest);
+        s.s0 = pair * d.a_shorts + min(pair, d.a_rest);
+    } else {
+        const int i = pair - d.a_pairs;
+        s.ns = d.b_shorts + (i < d.b_rest);
+        s.s0 = d.a_pairs * d.a_shorts + d.a_rest + i * d.b_shorts + min(i, d.b_rest);
+    }
+    return s;
+}
+
+template <int kBn>
+__global__ void __launch_bounds__(pair_threads(false), 1)
+dense_grads_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmB0,
+                   const __grid_constant__ CUtensorMap tmOut0, const __grid_constant__ CUtensorMap tmA1,
+                   const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmOut1,
+                   const __grid_constant__ GradArgs g) {
+    using X = Roles<false, true, false, kBn>;
+    using W = Roles<true, true, false, kBn>;
+    constexpr int kStages = X::kStages;
+    constexpr int kEpiWarps = epi_warps(false), kBufs = kEpiBytes / kBufBytes / kEpiWarps;
+    constexpr int kEpiCols = kBn / (kEpiWarps / 4), kBlocks = kEpiCols / kBlock;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* bufs = smem + kStages * X::kStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(bufs + kEpiBytes);
+    uint64_t* empty = full + kStages;
+    uint64_t* acc_full = empty + kStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)ptx::cluster_ctarank();
+    const Share sh = share_of(g.deal, (int)blockIdx.x / 2);
+    const int my_tiles = sh.nl + sh.ns;
+    int* const status = g.p[0].status;
+    // tile lt of this pair: whose it is (0 dX, 1 dW) and where
+    auto kind_of = [&](int lt) { return lt < sh.nl ? g.deal.longer : 1 - g.deal.longer; };
+    auto tile_of = [&](int lt, int kind) {
+        const int t = lt < sh.nl ? sh.l0 + lt : sh.s0 + lt - sh.nl, jt = g.p[kind].j_tiles;
+        return Tile{t / jt * kTI, t % jt * kBn};
+    };
+
+    if (warp == 1) ptx::pair_tmem_alloc(tmem_slot, 512);
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) { ptx::mbar_init(&full[s], 1); ptx::mbar_init(&empty[s], 1); }
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(&acc_full[s], 1);
+            ptx::mbar_init(&acc_empty[s], 2 * kEpiWarps);
+        }
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&tmA0);
+        ptx::prefetch_tensormap(&tmB0);
+        ptx::prefetch_tensormap(&tmA1);
+        ptx::prefetch_tensormap(&tmB1);
+    }
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        int n = 0;
+        for (int lt = 0; lt < my_tiles; ++lt) {
+            const int kind = kind_of(lt), kbs = g.p[kind].k_blocks;
+            const Tile tl = tile_of(lt, kind);
+            const int ai = X::a_row(tl, rank), bj = X::b_row(tl, rank);
+            for (int kb = 0; kb < kbs; ++kb, ++n) {
+                const int s = n % kStages;
+                if (n >= kStages) ptx::mbar_wait(&empty[s], ((n / kStages) - 1) & 1, status);
+                __syncwarp();
+                if (ptx::elect_one()) {
+                    if (kind == 0) X::load(smem, full, s, &tmA0, &tmB0, ai, bj, kb, rank, 0);
+                    else W::load(smem, full, s, &tmA1, &tmB1, ai, bj, kb, rank, 0);
+                }
+            }
+        }
+        X::drain(empty, n, status);
+    } else if (warp == 1) {
+        if (rank == 0) {
+            int n = 0;
+            for (int lt = 0; lt < my_tiles; ++lt) {
+                const int buf = lt & 1, kind = kind_of(lt), kbs = g.p[kind].k_blocks;
+                // both CTAs' epilogues have read this accumulator's previous tile
+                if (lt >= 2) ptx::mbar_wait_cluster(&acc_empty[buf], ((lt / 2) - 1) & 1, status);
+                __syncwarp();
+                ptx::tc_fence_after();
+                for (int kb = 0; kb < kbs; ++kb, ++n) {
+                    const int s = n % kStages;
+                    ptx::mbar_wait(&full[s], (n / kStages) & 1, status);
+                    __syncwarp();
+                    ptx::tc_fence_after();
+                    if (ptx::elect_one()) {
+                        if (kind == 0) X::multiply(tmem + buf * kBn, ptx::smem_u32(smem), s, kb == 0, empty, 3);
+                        else W::multiply(tmem + buf * kBn, ptx::smem_u32(smem), s, kb == 0, empty, 3);
+                    }
+                }
+                if (ptx::elect_one()) ptx::pair_commit(&acc_full[buf], 3);
+            }
+        }
+    } else {
+        const int grp = (warp - kEpiWarp0) >> 2, quad = warp & 3;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        uint8_t* wbuf = bufs + (warp - kEpiWarp0) * kBufs * kBufBytes;
+        const int row_at = lane * 64, sw = (lane >> 1) & 3;
+        const uint32_t acc_empty0 = ptx::map_rank(ptx::smem_u32(acc_empty), 0);
+        const bool lead = lane == 0;
+        int u = 0;                                             // the warp's stores so far; buffer u % kBufs
+        for (int lt = 0; lt < my_tiles; ++lt) {
+            const int buf = lt & 1, kind = kind_of(lt);
+            const Tile tl = tile_of(lt, kind);
+            const int row0 = tl.i0 + 128 * rank + 32 * quad, c_first = tl.j0 + grp * kEpiCols;
+            const int live =
+                row0 < g.p[kind].I ? max(0, min(kBlocks, (g.p[kind].J - c_first + kBlock - 1) / kBlock)) : 0;
+            ptx::mbar_wait(&acc_full[buf], (lt / 2) & 1, status);
+            __syncwarp();
+            ptx::tc_fence_after();
+            const uint32_t acc = tmem + lane_base + buf * kBn + grp * kEpiCols;
+            for (int k = 0; k < live; ++k, ++u) {
+                F2 v[16];
+                load_acc(acc + k * kBlock, v);
+                uint8_t* b = wbuf + u % kBufs * kBufBytes;
+                if (lead) ptx::bulk_wait_read<kBufs - 1>();
+                __syncwarp();
+                put_row(b + row_at, sw, v);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lead) {
+                    ptx::tma_store_2d(kind == 0 ? &tmOut0 : &tmOut1, b, c_first + k * kBlock, row0);
+                    ptx::bulk_commit();
+                }
+            }
+            // the accumulator is read: the MMAs of the tile after next may overwrite it
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lead) ptx::mbar_arrive_cluster(acc_empty0 + 8 * buf);
+        }
+        if (lead) ptx::bulk_wait<0>();
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::pair_tmem_dealloc(tmem, 512);
+    }
+}
+
 // ---- few tiles, many K steps: K split over the pairs of a cluster -------------------
 // One tile a cluster of 2 S CTAs; pair s takes K steps [s kb/S, (s+1) kb/S).  Every CTA then
 // lays its 128 x kBn partial accumulator into its own shared memory (the ring is free; rows
@@ -632,9 +804,11 @@ int dense_pair_clusters(int splits) {
     return n;
 }
 
-int launch_dense_pair(DenseForm form, const DenseArgs& d, int bn, int splits, cudaStream_t stream) {
+namespace {
+
+// extents, K steps and tiles of a product; OVERFLOW where tile indexes would not fit
+int plan_pair(DenseForm form, const DenseArgs& d, int bn, PairArgs* a) {
     const bool gated = form == kForward && d.gated;
-    PairArgs a{};
     int64_t I, J, K;
     if (form == kForward) { I = d.rows; J = gated ? d.cols / 2 : d.cols; K = d.inner; }
     else if (form == kInputGrad) { I = d.rows; J = d.inner; K = d.cols; }
@@ -642,33 +816,127 @@ int launch_dense_pair(DenseForm form, const DenseArgs& d, int bn, int splits, cu
     const int width = gated ? bn / 2 : bn;
     const int64_t it = (I + kTI - 1) / kTI, jt = (J + width - 1) / width;
     if (it * jt > INT32_MAX / 8) return fail(DIFFUSER_ERR_OVERFLOW, "dense product too large");
-    a.I = (int32_t)I;
-    a.J = (int32_t)J;
-    a.k_blocks = (int32_t)((K + kTK - 1) / kTK);
+    *a = PairArgs{};
+    a->I = (int32_t)I;
+    a->J = (int32_t)J;
+    a->k_blocks = (int32_t)((K + kTK - 1) / kTK);
+    a->i_tiles = (int32_t)it;
+    a->j_tiles = (int32_t)jt;
+    a->status = d.status;
+    return DIFFUSER_OK;
+}
+
+// the operands' maps
+int map_operands(DenseForm form, const DenseArgs& d, int bn, CUtensorMap* A, CUtensorMap* B) {
+    int st;
+    if (form == kWeightGrad) st = map_matrix(A, d.a, d.cols, d.rows, 64, kTK);
+    else st = map_matrix(A, d.a, form == kForward ? d.inner : d.cols, d.rows, kTK, 128);
+    if (st) return st;
+    if (form == kForward) {
+        return d.gated ? map_halves(B, d.b, d.inner, d.cols / 2, kTK, 128, 1)
+                       : map_matrix(B, d.b, d.inner, d.cols, kTK, bn / 2);
+    }
+    return map_matrix(B, d.b, d.inner, form == kInputGrad ? d.cols : d.rows, 64, kTK);
+}
+
+// Deals `longs` tiles of `long_steps` and `shorts` of `short_steps` to the pairs; returns the
+// largest load in steps.
+int64_t deal_tiles(int64_t longs, int64_t long_steps, int64_t shorts, int64_t short_steps, int pairs, GradDeal* d) {
+    d->longs = (int32_t)(longs / pairs);
+    d->a_pairs = (int32_t)(longs % pairs);
+    const int64_t na = d->a_pairs, nb = pairs - na;
+    const int64_t load_b = d->longs * long_steps, load_a = load_b + long_steps;
+    // short tiles go to the least loaded: first the b pairs, up to the a pairs' load, then all evenly
+    int64_t b = (long_steps + short_steps - 1) / short_steps, to_b = na ? nb * b : 0;
+    if (!na) {
+        to_b = shorts;
+    } else if (to_b >= shorts) {
+        to_b = shorts;
+    } else {
+        const int64_t rest = shorts - to_b;
+        to_b += rest / pairs * nb;
+        // the last, incomplete round: the b pairs when they stand lower, else the a pairs first
+        const int64_t last = rest % pairs, level_b = load_b + b * short_steps;
+        const int64_t first = level_b <= load_a ? nb : na;
+        const int64_t to_first = last < first ? last : first;
+        to_b += level_b <= load_a ? to_first : last - to_first;
+    }
+    const int64_t to_a = shorts - to_b;
+    d->b_shorts = (int32_t)(to_b / nb);
+    d->b_rest = (int32_t)(to_b % nb);
+    d->a_shorts = na ? (int32_t)(to_a / na) : 0;
+    d->a_rest = na ? (int32_t)(to_a % na) : 0;
+    const int64_t most_b = load_b + (d->b_shorts + (d->b_rest ? 1 : 0)) * short_steps;
+    const int64_t most_a = na ? load_a + (d->a_shorts + (d->a_rest ? 1 : 0)) * short_steps : 0;
+    return most_a > most_b ? most_a : most_b;
+}
+
+GradDeal deal_grads(const PairArgs& x, const PairArgs& w, int pairs, int64_t* most) {
+    GradDeal d{};
+    const int64_t tx = (int64_t)x.i_tiles * x.j_tiles, tw = (int64_t)w.i_tiles * w.j_tiles;
+    d.longer = w.k_blocks >= x.k_blocks;
+    *most = d.longer ? deal_tiles(tw, w.k_blocks, tx, x.k_blocks, pairs, &d)
+                     : deal_tiles(tx, x.k_blocks, tw, w.k_blocks, pairs, &d);
+    return d;
+}
+
+template <int kBn>
+int launch_grads_as(const CUtensorMap (&tm)[6], GradArgs g, cudaStream_t stream) {
+    static std::atomic<uint64_t> done{0};
+    auto kernel = dense_grads_kernel<kBn>;
+    const cudaError_t err = allow_smem(kernel, smem_bytes(kBn), done);
+    if (err != cudaSuccess) return cuda_fail(err, "cudaFuncSetAttribute(dense gradients kernel)");
+    const int64_t tiles =
+        (int64_t)g.p[0].i_tiles * g.p[0].j_tiles + (int64_t)g.p[1].i_tiles * g.p[1].j_tiles;
+    int64_t pairs = dense_pair_clusters(1), most = 0;
+    if (tiles < pairs) pairs = tiles;
+    g.deal = deal_grads(g.p[0], g.p[1], (int)pairs, &most);
+    return launch_clusters(kernel, 2, pairs, pair_threads(false), smem_bytes(kBn), stream, tm[0], tm[1], tm[2], tm[3],
+                           tm[4], tm[5], g);
+}
+
+}  // namespace
+
+int64_t dense_grads_steps(const DenseArgs& x, int bn) {
+    PairArgs px, pw;
+    if (plan_pair(kInputGrad, x, bn, &px) || plan_pair(kWeightGrad, x, bn, &pw)) return INT64_MAX;
+    int64_t most = 0;
+    deal_grads(px, pw, dense_pair_clusters(1), &most);
+    return most;
+}
+
+int launch_dense_grads(const DenseArgs& x, const DenseArgs& w, int bn, cudaStream_t stream) {
+    GradArgs g{};
+    CUtensorMap tm[6] = {};                        // dX: A, B, result; dW: A, B, result
+    int st = plan_pair(kInputGrad, x, bn, &g.p[0]);
+    if (!st) st = plan_pair(kWeightGrad, w, bn, &g.p[1]);
+    if (!st) st = map_operands(kInputGrad, x, bn, &tm[0], &tm[1]);
+    if (!st) st = map_matrix(&tm[2], x.out, g.p[0].J, g.p[0].I, kBlock, 32);
+    if (!st) st = map_operands(kWeightGrad, w, bn, &tm[3], &tm[4]);
+    if (!st) st = map_matrix(&tm[5], w.out, g.p[1].J, g.p[1].I, kBlock, 32);
+    if (st) return st;
+    return bn == 256 ? launch_grads_as<256>(tm, g, stream) : launch_grads_as<128>(tm, g, stream);
+}
+
+int launch_dense_pair(DenseForm form, const DenseArgs& d, int bn, int splits, cudaStream_t stream) {
+    const bool gated = form == kForward && d.gated;
+    PairArgs a;
+    int st = plan_pair(form, d, bn, &a);
+    if (st) return st;
     while (splits > a.k_blocks) splits /= 2;       // every pair has a K step
-    a.i_tiles = (int32_t)it;
-    a.j_tiles = (int32_t)jt;
     a.act = d.act;
     a.pre = d.pre != nullptr;
     a.residual = d.residual != nullptr;
     a.bias = static_cast<const __nv_bfloat16*>(d.bias);
-    a.status = d.status;
     const Results r{static_cast<__nv_bfloat16*>(d.out), static_cast<__nv_bfloat16*>(d.pre),
                     static_cast<const __nv_bfloat16*>(d.residual)};
     CUtensorMap tm[5] = {};                        // A, B, result, pre, residual
-    int st;
-    if (form == kWeightGrad) st = map_matrix(&tm[0], d.a, d.cols, d.rows, 64, kTK);
-    else st = map_matrix(&tm[0], d.a, K, I, kTK, 128);
-    if (!st) {
-        if (gated) st = map_halves(&tm[1], d.b, d.inner, J, kTK, 128, 1);
-        else if (form == kForward) st = map_matrix(&tm[1], d.b, d.inner, J, kTK, bn / 2);
-        else st = map_matrix(&tm[1], d.b, J, K, 64, kTK);
-    }
+    st = map_operands(form, d, bn, &tm[0], &tm[1]);
     if (splits == 1) {
-        if (!st) st = map_matrix(&tm[2], d.out, J, I, kBlock, 32);
+        if (!st) st = map_matrix(&tm[2], d.out, a.J, a.I, kBlock, 32);
         if (!st && a.pre)
-            st = gated ? map_column_halves(&tm[3], d.pre, J, I, kBlock, 32) : map_matrix(&tm[3], d.pre, J, I, kBlock, 32);
-        if (!st && a.residual) st = map_matrix(&tm[4], d.residual, J, I, kBlock, 32);
+            st = gated ? map_column_halves(&tm[3], d.pre, a.J, a.I, kBlock, 32) : map_matrix(&tm[3], d.pre, a.J, a.I, kBlock, 32);
+        if (!st && a.residual) st = map_matrix(&tm[4], d.residual, a.J, a.I, kBlock, 32);
     }
     if (st) return st;
     if (gated) return launch_as<false, false, true, 256>(tm, a, r, splits, stream);

@@ -31,24 +31,49 @@ double estimate(const Shape& s, int bn, bool gated, int splits) {
     return (bn == 256 ? 5.2 : 3.6) + (double)(waves * ((steps + splits - 1) / splits)) * each + 6.0 * (double)(waves - 1);
 }
 
-}  // namespace
+struct Pick {
+    int bn, splits;
+    double us;
+};
 
-int launch_dense(DenseForm form, const DenseArgs& a, cudaStream_t stream) {
-    const bool gated = form == kForward && a.gated;
-    if (form == kForward && a.rows <= kFewTokens) return launch_dense_few(a, stream);
-    Shape s;
-    if (form == kForward) s = {a.rows, gated ? a.cols / 2 : a.cols, a.inner};
-    else if (form == kInputGrad) s = {a.rows, a.inner, a.cols};
-    else s = {a.cols, a.inner, a.rows};
-    int best_bn = 256, best_splits = 1;
-    double best = estimate(s, 256, gated, 1);
+Shape shape_of(DenseForm form, const DenseArgs& a) {
+    if (form == kForward) return {a.rows, a.gated ? a.cols / 2 : a.cols, a.inner};
+    if (form == kInputGrad) return {a.rows, a.inner, a.cols};
+    return {a.cols, a.inner, a.rows};
+}
+
+Pick pick(const Shape& s, bool gated) {
+    Pick best{256, 1, estimate(s, 256, gated, 1)};
     for (int bn = 256; bn >= (gated ? 256 : 128); bn -= 128)
         for (int splits = 1; splits <= 4; splits *= 2) {
             if ((s.K + 63) / 64 < 2 * splits && splits > 1) continue;
             const double t = estimate(s, bn, gated, splits);
-            if (t < best) { best = t; best_bn = bn; best_splits = splits; }
+            if (t < best.us) best = {bn, splits, t};
         }
-    return launch_dense_pair(form, a, best_bn, best_splits, stream);
+    return best;
+}
+
+}  // namespace
+
+int launch_dense(DenseForm form, const DenseArgs& a, cudaStream_t stream) {
+    if (form == kForward && a.rows <= kFewTokens) return launch_dense_few(a, stream);
+    const Pick p = pick(shape_of(form, a), form == kForward && a.gated);
+    return launch_dense_pair(form, a, p.bn, p.splits, stream);
+}
+
+// Both gradients: one launch where its busiest pair ends before the two kernels after each
+// other would (2 us for the second launch): 2.9 or 2.1 us and its K steps.
+//   gated backward, 16384 x 1024 x 2816: 289 us in one launch, 324 in two (with the activations')
+//   dense backward, 2048 x 1024 x 4096: 37.3 and 47.5;  1024 x 512 x 512: 12.4 and 18.4
+//   dense backward, 32768 x 768 x 768, where the weights' gradient wants K split: 139 and 110
+int launch_gradients(const DenseArgs& x, const DenseArgs& w, cudaStream_t stream) {
+    const Pick px = pick(shape_of(kInputGrad, x), false), pw = pick(shape_of(kWeightGrad, w), false);
+    const double at256 = 2.9 + 0.33 * (double)dense_grads_steps(x, 256);
+    const double at128 = 2.1 + 0.23 * (double)dense_grads_steps(x, 128);
+    if ((at256 < at128 ? at256 : at128) < px.us + pw.us + 2.0)
+        return launch_dense_grads(x, w, at256 <= at128 ? 256 : 128, stream);
+    const int st = launch_dense_pair(kInputGrad, x, px.bn, px.splits, stream);
+    return st ? st : launch_dense_pair(kWeightGrad, w, pw.bn, pw.splits, stream);
 }
 
 }  // namespace dfs

@@ -85,7 +85,11 @@ int launch_dense_few(const DenseArgs& a, cudaStream_t stream);
 int launch_dense_pair(DenseForm form, const DenseArgs& a, int bn, int splits, cudaStream_t stream);
 // clusters of 2 `splits` CTAs of the split kernel that run at once on the current device
 int dense_pair_clusters(int splits);
-// picks the kernel (dense_pick.cu)
+// both gradients in one launch (dense_pair.cu), and the K steps of its busiest CTA pair
+int launch_dense_grads(const DenseArgs& x, const DenseArgs& w, int bn, cudaStream_t stream);
+int64_t dense_grads_steps(const DenseArgs& x, int bn);
+// picks the kernel (dense_pick.cu); the gradients: x for dX and w for dW, of one product
+int launch_gradients(const DenseArgs& x, const DenseArgs& w, cudaStream_t stream);
 int launch_dense(DenseForm form, const DenseArgs& a, cudaStream_t stream);
 
 // ---- the activations' backward (dense_act.cu) --------------------------------

@@ -129,6 +129,19 @@ DenseBwd plan_dense_backward(int64_t T, int64_t F, int32_t act) {
     return L;
 }
 
+// dX = dP W and dW = dP^T X, a (dP, sizes, status) filled in; a null result is left out
+int launch_both(const DenseArgs& a, const void* W, void* dX, const void* X, void* dW, cudaStream_t stream) {
+    DenseArgs x = a, w = a;
+    x.b = W;
+    x.out = dX;
+    w.b = X;
+    w.out = dW;
+    if (dX && dW) return launch_gradients(x, w, stream);
+    if (dX) return launch_dense(kInputGrad, x, stream);
+    if (dW) return launch_dense(kWeightGrad, w, stream);
+    return DIFFUSER_OK;
+}
+
 }  // namespace
 }  // namespace dfs
 
@@ -289,17 +302,7 @@ int diffuser_linear_backward(const void* X, const void* W, const void* dY, const
     a.rows = T;
     a.inner = D;
     a.cols = F;
-    if (dX) {
-        a.b = W;
-        a.out = dX;
-        if ((st = launch_dense(kInputGrad, a, s))) return st;
-    }
-    if (dW) {
-        a.b = X;
-        a.out = dW;
-        if ((st = launch_dense(kWeightGrad, a, s))) return st;
-    }
-    return DIFFUSER_OK;
+    return launch_both(a, W, dX, X, dW, s);
 } catch (...) {
     return fail(DIFFUSER_ERR_ALLOC, "unexpected exception");
 }
@@ -363,17 +366,7 @@ int diffuser_gated_linear_backward(const void* X, const void* Wgu, const void* d
     a.rows = T;
     a.inner = D;
     a.cols = 2 * F;
-    if (dX) {
-        a.b = Wgu;
-        a.out = dX;
-        if ((st = launch_dense(kInputGrad, a, s))) return st;
-    }
-    if (dWgu) {
-        a.b = X;
-        a.out = dWgu;
-        if ((st = launch_dense(kWeightGrad, a, s))) return st;
-    }
-    return DIFFUSER_OK;
+    return launch_both(a, Wgu, dX, X, dWgu, s);
 } catch (...) {
     return fail(DIFFUSER_ERR_ALLOC, "unexpected exception");
 }

@@ -131,3 +131,59 @@ def split(steps, stages, drain=True):
 def test_split_protocol_completes(stages):
     for steps in range(1, 30):
         assert split(steps, stages) == "done"
+
+
+def deal(longs, long_steps, shorts, short_steps, pairs):
+    """csrc/dense_pair.cu's deal_tiles and share_of: (first, count) of the long and short tiles of each pair."""
+    per, na = divmod(longs, pairs)
+    nb = pairs - na
+    load_b = per * long_steps
+    load_a = load_b + long_steps
+    b = -(-long_steps // short_steps)
+    to_b = nb * b if na else 0
+    if not na or to_b >= shorts:
+        to_b = shorts
+    else:
+        rest = shorts - to_b
+        to_b += rest // pairs * nb
+        last = rest % pairs
+        lower = load_b + b * short_steps <= load_a
+        first = min(last, nb if lower else na)
+        to_b += first if lower else last - first
+    to_a = shorts - to_b
+    bs, br = divmod(to_b, nb)
+    as_, ar = divmod(to_a, na) if na else (0, 0)
+    out = []
+    for p in range(pairs):
+        nl, l0 = per + (p < na), p * per + min(p, na)
+        if p < na:
+            ns, s0 = as_ + (p < ar), p * as_ + min(p, ar)
+        else:
+            i = p - na
+            ns, s0 = bs + (i < br), na * as_ + ar + i * bs + min(i, br)
+        out.append((l0, nl, s0, ns))
+    return out
+
+
+@pytest.mark.parametrize("pairs", [1, 2, 7, 76])
+def test_gradient_tiles_are_dealt_once_and_evenly(pairs):
+    import random
+    rng = random.Random(pairs)
+    cases = [(64, 256, 256, 64), (88, 256, 256, 88), (9, 128, 96, 12), (1, 5, 0, 1), (pairs, 3, 2 * pairs, 3)]
+    cases += [(rng.randint(1, 400), rng.randint(1, 300), rng.randint(0, 600), 1) for _ in range(200)]
+    for longs, long_steps, shorts, short_steps in cases:
+        short_steps = short_steps if short_steps > 1 else rng.randint(1, long_steps)
+        n = min(pairs, longs + shorts)
+        shares = deal(longs, long_steps, shorts, short_steps, n)
+        at_l = at_s = 0
+        for l0, nl, s0, ns in shares:                    # one after the other: every tile once
+            assert (l0, s0) == (at_l, at_s) and nl >= 0 and ns >= 0
+            at_l, at_s = at_l + nl, at_s + ns
+        assert (at_l, at_s) == (longs, shorts)
+        most = max(nl * long_steps + ns * short_steps for _, nl, _, ns in shares)
+        loads = [0] * n                                  # the same by the greedy rule
+        for steps, count in ((long_steps, longs), (short_steps, shorts)):
+            for _ in range(count):
+                k = loads.index(min(loads))
+                loads[k] += steps
+        assert most <= max(loads) + short_steps
