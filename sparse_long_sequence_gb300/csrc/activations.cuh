@@ -97,6 +97,25 @@ __device__ __forceinline__ float2 value_slope(float p) {
     return make_float2(p, 1.f);
 }
 
+// min(|x|, the largest finite value); NaN stays NaN
+__device__ __forceinline__ float finite_abs(float x) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(fabsf(x)), "f"(3.4028234663852886e38f));
+    return y;
+}
+// q(t) of normal(), two at a time
+__device__ __forceinline__ packed::F2 mills2(packed::F2 t) {
+    using namespace packed;
+    F2 q = both(0.0330325861f);
+    q = fma(q, t, both(-0.146387965f));
+    q = fma(q, t, both(0.188117857f));
+    q = fma(q, t, both(-0.0373392124f));
+    q = fma(q, t, both(0.120191655f));
+    q = fma(q, t, both(0.10235086f));
+    q = fma(q, t, both(0.12038182f));
+    return fma(q, t, both(0.119652211f));
+}
+
 // The same values two at a time: the products and sums of both in one instruction, which the
 // dense products' epilogues are bound by.
 template <int kAct>
@@ -114,6 +133,15 @@ __device__ __forceinline__ packed::F2 value2(packed::F2 p) {
         const float2 d = un(add(f2(ptx::ex2_approx(e.x), ptx::ex2_approx(e.y)), both(1.f)));
         const float2 q = un(p);
         return mul(f2(finite_below(q.x), finite_below(q.y)), f2(rcp_approx(d.x), rcp_approx(d.y)));
+    } else if constexpr (kAct == DIFFUSER_ACT_GELU) {
+        // max(p, 0) - x Phi(-x), x = |p| (the largest finite value for infinity: 0 times it is 0)
+        const float2 v = un(p);
+        const F2 x = f2(finite_abs(v.x), finite_abs(v.y));
+        const float2 d = un(fma(x, both(0.3f), both(1.f)));
+        const F2 t = f2(rcp_approx(d.x), rcp_approx(d.y));
+        const float2 h = un(mul(mul(x, x), both(-0.7213475204444817f)));
+        const F2 tail = mul(mul(f2(ptx::ex2_approx(h.x), ptx::ex2_approx(h.y)), t), mills2(t));
+        return fma(mul(x, both(-1.f)), tail, f2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
     } else {
         const float2 q = un(p);
         return f2(value<kAct>(q.x), value<kAct>(q.y));

@@ -251,7 +251,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             for (int lt = 0; lt < my_tiles; ++lt) {
                 const int buf = lt & 1;
                 // both CTAs' epilogues have read this accumulator's previous tile
-                if (lt >= 2) ptx::mbar_wait_cluster(&acc_empty[buf], ((lt / 2) - 1) & 1, a.status);
+                if (lt >= 2) ptx::mbar_wait(&acc_empty[buf], ((lt / 2) - 1) & 1, a.status);
                 __syncwarp();
                 ptx::tc_fence_after();
                 for (int kb = 0; kb < a.k_blocks; ++kb, ++g) {
@@ -480,7 +480,7 @@ dense_grads_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
             for (int lt = 0; lt < my_tiles; ++lt) {
                 const int buf = lt & 1, kind = kind_of(lt), kbs = g.p[kind].k_blocks;
                 // both CTAs' epilogues have read this accumulator's previous tile
-                if (lt >= 2) ptx::mbar_wait_cluster(&acc_empty[buf], ((lt / 2) - 1) & 1, status);
+                if (lt >= 2) ptx::mbar_wait(&acc_empty[buf], ((lt / 2) - 1) & 1, status);
                 __syncwarp();
                 ptx::tc_fence_after();
                 for (int kb = 0; kb < kbs; ++kb, ++n) {

@@ -6,10 +6,10 @@
 //    lowest, in us.  A wave of tiles takes its K steps; a step takes `step` when a few pairs run
 //    and `busy` when all do (they share the L2's bandwidth).  Persistent tiles overlap their
 //    epilogues; split ones do not, and add the cluster's join.
-//      weight gradient 768 x 768 over 32768 tokens: 44 us at 256 x 4 pairs, 98 at 128, 142 at 256
-//      weight gradient 4096 x 1024 over 16384 tokens: 86 us at 256, 117 at 128, 170 at 256 x 2
-//      input gradient 1024 <- 4096 of 1024 tokens: 12.3 us at 128 x 2, 15.1 at 128, 22.9 at 256
-//      forward 768 -> 768 of 4096 tokens: 9.7 us at 256, 9.9 at 128, 19.6 at 256 x 2
+//      weight gradient 768 x 768 over 32768 tokens: 43 us at 256 x 4 pairs, 97 at 128, 141 at 256
+//      weight gradient 4096 x 1024 over 32768 tokens: 148 us at 256, 209 at 128, 173 at 256 x 2
+//      input gradient 1024 <- 4096 of 1024 tokens: 12.1 us at 128 x 2, 14.6 at 128, 22.0 at 256
+//      forward 768 -> 768 of 4096 tokens: 9.1 us at 256, 9.7 at 128, 19.4 at 256 x 2
 #include "layer_ops.h"
 
 namespace dfs {
@@ -20,7 +20,7 @@ constexpr int64_t kFewTokens = 32;
 struct Shape { int64_t I, J, K; };          // result rows and columns, summed length
 
 double estimate(const Shape& s, int bn, bool gated, int splits) {
-    const double step = bn == 256 ? 0.27 : 0.155, busy = bn == 256 ? 0.33 : 0.23;
+    const double step = bn == 256 ? 0.27 : 0.155, busy = bn == 256 ? 0.305 : 0.205;
     const int64_t width = gated ? bn / 2 : bn;
     const int64_t tiles = ((s.I + 255) / 256) * ((s.J + width - 1) / width);
     const int64_t steps = (s.K + 63) / 64, fit = dense_pair_clusters(splits);
@@ -68,8 +68,8 @@ int launch_dense(DenseForm form, const DenseArgs& a, cudaStream_t stream) {
 //   dense backward, 32768 x 768 x 768, where the weights' gradient wants K split: 139 and 110
 int launch_gradients(const DenseArgs& x, const DenseArgs& w, cudaStream_t stream) {
     const Pick px = pick(shape_of(kInputGrad, x), false), pw = pick(shape_of(kWeightGrad, w), false);
-    const double at256 = 2.9 + 0.33 * (double)dense_grads_steps(x, 256);
-    const double at128 = 2.1 + 0.23 * (double)dense_grads_steps(x, 128);
+    const double at256 = 2.9 + 0.305 * (double)dense_grads_steps(x, 256);
+    const double at128 = 2.1 + 0.205 * (double)dense_grads_steps(x, 128);
     if ((at256 < at128 ? at256 : at128) < px.us + pw.us + 2.0)
         return launch_dense_grads(x, w, at256 <= at128 ? 256 : 128, stream);
     const int st = launch_dense_pair(kInputGrad, x, px.bn, px.splits, stream);
