@@ -602,16 +602,17 @@ def diffuser_qk_norm_rope_backward(Q, K, dQo, dKo, q_weight=None, k_weight=None,
 
 
 def _dense_shapes(X, W, halves=1):
-    """Leading shape, T, D, F of X [...][D] and W [halves F][D]."""
+    """T, D, F and the leading shape of X [...][D] and W [halves F][D]."""
     import torch
     if X.dtype != torch.bfloat16:
         raise TypeError(f"unsupported dtype {X.dtype}; use bfloat16")
-    shape, D = X.shape, X.shape[-1] if X.dim() else -1
-    if W.dim() != 2 or W.shape[1] != D or W.shape[0] % halves:
-        raise ValueError(f"expected [...][D] and [{'2 F' if halves == 2 else 'F'}][D], got "
-                         f"{tuple(shape)} and {tuple(W.shape)}")
-    lead = shape[:-1]
-    return lead, lead.numel(), D, W.shape[0] // halves
+    xs, ws = X.shape, W.shape
+    if not xs or len(ws) != 2 or ws[1] != xs[-1] or ws[0] % halves:
+        raise ValueError(f"expected [...][D] and [{'2 F' if halves == 2 else 'F'}][D], got {tuple(xs)} and {tuple(ws)}")
+    if max(ws) > 2 ** 31 - 1:
+        raise ValueError(f"too wide: {tuple(ws)}")
+    lead = xs[:-1]
+    return lead, X.numel() // ws[1] if ws[1] else 0, ws[1], ws[0] // halves
 
 
 @_on_stream

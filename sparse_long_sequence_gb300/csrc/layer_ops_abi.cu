@@ -59,13 +59,19 @@ int check_qk(int32_t dtype, int64_t B, int64_t Hq, int64_t Hk, int64_t n, int32_
     return DIFFUSER_OK;
 }
 
-// theta^(-2i/rot) / (2 pi) turns per position, in units of 2^-64 turns: one power, then
-// products in long double (relative error below 2^-58 where that has 64 bits)
+// theta^(-2i/rot) / (2 pi) turns per position, in units of 2^-64 turns: one power, then products
+// of 64-bit fractions, each rounded to 2^-64 (a long double is emulated on Arm: 32 products of
+// it took 0.8 us)
 void set_turns(QkArgs* a, double theta) {
     if (!a->rot) return;
-    const long double ratio = std::pow((long double)theta, -2.0L / a->rot);
-    long double f = 2935890503282001226.49624383L;          // 2^64 / (2 pi)
-    for (int i = 0; i < a->rot / 2; ++i, f *= ratio) a->freq[i] = (uint64_t)(f + 0.5L);
+    const long double ratio = std::ldexp(std::pow((long double)theta, -2.0L / a->rot), 64);
+    const bool one = theta == 1.0;                           // (the ratio itself does not fit)
+    const uint64_t r = one ? 0 : (uint64_t)(ratio + 0.5L);
+    uint64_t f = 2935890503282001226u;                       // 2^64 / (2 pi)
+    for (int i = 0; i < a->rot / 2; ++i) {
+        a->freq[i] = f;
+        if (!one) f = (uint64_t)(((unsigned __int128)f * r + (uint64_t(1) << 63)) >> 64);
+    }
 }
 
 QkArgs qk_args(const void* Q, const void* K, int64_t B, int64_t Hq, int64_t Hk, int64_t n, const void* wq, const void* wk,

@@ -398,6 +398,81 @@ def test_qk_rows_of_zeros_and_extremes(dl):
         assert torch.isfinite(grads[0]).all() and torch.isfinite(grads[1]).all()
 
 
+# ------------------------------------------------------------------ where they write
+def guarded(rows, width, dtype=torch.bfloat16, fill=7.0):
+    """A [rows][width] buffer between rows of `fill`, and a check that those are as they were."""
+    whole = torch.full((rows + 4, width), fill, dtype=dtype, device="cuda")
+    inner = whole[2:rows + 2]
+    return inner, lambda: bool((whole[:2] == fill).all() and (whole[-2:] == fill).all())
+
+
+@pytest.mark.parametrize("shape", [(1, 64, 72), (19, 136, 88), (130, 72, 200), (2050, 200, 136), (20010, 72, 520),
+                                   (700, 2056, 328)], ids=lambda s: "T%dD%dF%d" % s)
+def test_nothing_is_written_outside(dl, shape):
+    T, D, F = shape
+    X, W, b = linear_inputs(T, D, F, seed=T)
+    W2 = draw(7, 2 * F, D, scale=D ** -0.5)
+    R, dY, code = draw(8, T, F), draw(9, T, F), dl.DIFFUSER_ACT_SILU
+    (Y, y_ok), (P, p_ok) = guarded(T, F), guarded(T, F)
+    dl.diffuser_linear(X, W, bias=b, residual=R, activation=code, Y=Y, pre=P)
+    want = dl.diffuser_linear(X, W, bias=b, residual=R, activation=code, save_pre=True)
+    assert y_ok() and p_ok() and torch.equal(Y, want[0]) and torch.equal(P, want[1])
+    (dX, dx_ok), (dW, dw_ok), (db, db_ok) = guarded(T, D), guarded(F, D), guarded(1, F)
+    dl.diffuser_linear_backward(X, W, dY, pre=P, activation=code, dX=dX, dW=dW, dbias=db[0])
+    assert dx_ok() and dw_ok() and db_ok()
+    check_linear_backward(X, W, dY, P, "silu", dX, dW, db[0])
+    (H, h_ok), (G, g_ok) = guarded(T, F), guarded(T, 2 * F)
+    dl.diffuser_gated_linear(X, W2, H=H, pre=G)
+    want = dl.diffuser_gated_linear(X, W2, save_pre=True)
+    assert h_ok() and g_ok() and torch.equal(H, want[0]) and torch.equal(G, want[1])
+    (dX, dx_ok), (dW, dw_ok) = guarded(T, D), guarded(2 * F, D)
+    dl.diffuser_gated_linear_backward(X, W2, dY, G, dX=dX, dWgu=dW)
+    again = dl.diffuser_gated_linear_backward(X, W2, dY, G)
+    assert dx_ok() and dw_ok() and torch.equal(dX, again[0]) and torch.equal(dW, again[1])
+
+
+def test_qk_writes_only_its_rows(dl):
+    for dtype in (torch.float32, torch.bfloat16):
+        for n in (1, 5, 33):
+            q, k = draw(1, 1, 2, n, 64, dtype=dtype), draw(2, 1, 3, n, 64, dtype=dtype)
+            outs = [guarded(r, 64, dtype) for r in (2 * n, 3 * n)]
+            dl.diffuser_qk_norm_rope(q, k, Qo=outs[0][0].view(1, 2, n, 64), Ko=outs[1][0].view(1, 3, n, 64))
+            assert all(ok() for _, ok in outs)
+            w = draw(3, 64, dtype=dtype)
+            small = [guarded(1, 64, dtype) for _ in range(2)]
+            dl.diffuser_qk_norm_rope_backward(q, k, q, k, w, w, dQ=outs[0][0].view(1, 2, n, 64),
+                                              dK=outs[1][0].view(1, 3, n, 64), dq_weight=small[0][0][0],
+                                              dk_weight=small[1][0][0])
+            assert all(ok() for _, ok in outs + small)
+
+
+def test_offsets_past_32_bits(dl):
+    # results of more than 2^31 elements: their last rows against the same rows alone
+    T, D, F = 600_011, 64, 4096
+    g = torch.Generator(device="cuda").manual_seed(5)
+    X = torch.randn(T, D, generator=g, device="cuda", dtype=torch.bfloat16)
+    W, b = draw(1, F, D, scale=D ** -0.5), draw(2, F)
+    tail = X[-300:].contiguous()
+    Y, P = dl.diffuser_linear(X, W, bias=b, activation=dl.DIFFUSER_ACT_GELU, save_pre=True)
+    y, p = dl.diffuser_linear(tail, W, bias=b, activation=dl.DIFFUSER_ACT_GELU, save_pre=True)
+    assert Y.numel() > 2 ** 31 and torch.equal(Y[-300:], y) and torch.equal(P[-300:], p)
+    dX = dl.diffuser_linear_backward(X, W, Y, pre=P, activation=dl.DIFFUSER_ACT_GELU, with_dW=False, with_bias=False)[0]
+    dx = dl.diffuser_linear_backward(tail, W, y, pre=p, activation=dl.DIFFUSER_ACT_GELU, with_dW=False, with_bias=False)[0]
+    near(dX[-300:], dx.double(), "dX")                    # another split of K, another order of the sum
+    del Y, P, dX
+    B, H, n = 1, 17, 2_000_003
+    q = torch.randn(B, H, n, 64, generator=g, device="cuda", dtype=torch.bfloat16)
+    k = q.new_zeros(B, 1, n, 64)
+    Q, _ = dl.diffuser_qk_norm_rope(q, k)
+    assert q.numel() > 2 ** 31
+    last = q[:, -1:, -40:].contiguous()
+    want = dl.diffuser_qk_norm_rope(last, last.clone(), position_offset=n - 40)[0]
+    assert torch.equal(Q[:, -1:, -40:], want)
+    dQ = dl.diffuser_qk_norm_rope_backward(q, k, Q, k)[0]
+    wd = dl.diffuser_qk_norm_rope_backward(last, last.clone(), want, last.clone(), position_offset=n - 40)[0]
+    assert torch.equal(dQ[:, -1:, -40:], wd)
+
+
 # ------------------------------------------------------------------ how they are called
 def test_empty_and_single(dl):
     X, W = draw(0, 0, 64), draw(1, 72, 64)
@@ -545,6 +620,32 @@ def test_two_captured_graphs_and_streams(dl):
     assert torch.equal(y, want[0][0])
 
 
+def test_calls_at_once_on_two_streams(dl):
+    # large products that fill the GPU, on two streams without waits between them
+    X, W, b = linear_inputs(5000, 264, 776, seed=31)
+    X2, W2, _ = linear_inputs(4100, 520, 392, seed=37, rows=784)
+    dY, dH = draw(1, 5000, 776), draw(2, 4100, 392)
+
+    def one():
+        y, p = dl.diffuser_linear(X, W, bias=b, activation=dl.DIFFUSER_ACT_RELU, save_pre=True)
+        return [y, p, *dl.diffuser_linear_backward(X, W, dY, pre=p, activation=dl.DIFFUSER_ACT_RELU)]
+
+    def two():
+        h, p = dl.diffuser_gated_linear(X2, W2, save_pre=True)
+        return [h, p, *dl.diffuser_gated_linear_backward(X2, W2, dH, p)]
+    want = one(), two()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(10):
+        for k, (s, f) in enumerate(zip(streams, (one, two))):
+            with torch.cuda.stream(s):
+                got[k].append(f())
+    torch.cuda.synchronize()
+    for outs, ref in zip(got, want):
+        for out in outs:
+            assert all(torch.equal(a, c) for a, c in zip(out, ref))
+
+
 def test_first_call_inside_a_capture(dl):
     # a new process whose first dense product is captured: the status block is made outside the capture
     import os
@@ -560,7 +661,7 @@ def test_first_call_inside_a_capture(dl):
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
 
 
-def test_status_word_refuses(dl):
+def test_status_word_is_clear(dl):
     X, W, _ = linear_inputs(5, 64, 72)
     assert dl.diffuser_projection_status(reset=True) == 0
     dl.diffuser_linear(X, W)
