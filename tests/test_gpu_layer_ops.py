@@ -646,16 +646,33 @@ def test_calls_at_once_on_two_streams(dl):
             assert all(torch.equal(a, c) for a, c in zip(out, ref))
 
 
-def test_first_call_inside_a_capture(dl):
-    # a new process whose first dense product is captured: the status block is made outside the capture
+@pytest.mark.parametrize("rows", [5, 300, 3000])
+def test_first_call_inside_a_capture(dl, rows):
+    # a new process whose first calls of all are captured: the status block and the kernels'
+    # attributes are made outside the capture
     import os
     import subprocess
     import sys
-    code = ("import torch\nfrom sparse_long_sequence_gb300 import binding as dl\n"
-            "x = torch.randn(5, 64, device='cuda').bfloat16(); w = torch.randn(72, 64, device='cuda').bfloat16()\n"
-            "torch.cuda.synchronize(); g = torch.cuda.CUDAGraph()\n"
-            "with torch.cuda.graph(g):\n    y = dl.diffuser_linear(x, w)\n"
-            "g.replay(); torch.cuda.synchronize(); assert torch.equal(y, dl.diffuser_linear(x, w)); print('fine')\n")
+    code = f"""
+import torch
+from sparse_long_sequence_gb300 import binding as dl
+r = lambda *s: torch.randn(*s, device='cuda').bfloat16()
+x, w, w2, dy, q = r({rows}, 64), r(264, 64), r(528, 64), r({rows}, 264), r(1, 2, {rows}, 64)
+torch.cuda.synchronize()
+def run():
+    y, p = dl.diffuser_linear(x, w, activation=dl.DIFFUSER_ACT_GELU, save_pre=True)
+    h, gu = dl.diffuser_gated_linear(x, w2, save_pre=True)
+    return [y, p, h, gu, *dl.diffuser_linear_backward(x, w, dy, pre=p, activation=dl.DIFFUSER_ACT_GELU),
+            *dl.diffuser_gated_linear_backward(x, w2, dy, gu), *dl.diffuser_qk_norm_rope(q, q.clone()),
+            *dl.diffuser_qk_norm_rope_backward(q, q.clone(), q.clone(), q.clone())[:2]]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    outs = run()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(outs, run()))
+print('fine')
+"""
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
