@@ -513,20 +513,14 @@ def _may(t, name, shape, dev, dtype):
     return None if t is None else _need(t, name, shape, dev, dtype)
 
 
-def _empty(t, shape, like):
-    """`t`, or a new tensor of that shape in like's dtype and device."""
-    if t is not None:
-        return t
-    import torch
-    return torch.empty(shape, dtype=like.dtype, device=like.device)
-
-
-def _as(t, like):
-    """`t`, or a new tensor as `like`."""
-    if t is not None:
-        return t
-    import torch
-    return torch.empty_like(like)
+def _out(t, name, shape, like):
+    """An output and its address: `t` after its checks, or a new tensor of that shape in like's
+    dtype and device."""
+    if t is None:
+        import torch
+        t = torch.empty_like(like) if shape == like.shape else torch.empty(shape, dtype=like.dtype, device=like.device)
+        return t, t.data_ptr()
+    return t, _need(t, name, shape, like.get_device(), like.dtype)
 
 
 def _workspace(workspace, nbytes, like):
@@ -556,13 +550,14 @@ def diffuser_qk_norm_rope(Q, K, q_weight=None, k_weight=None, positions=None, po
     import torch
     code, B, Hq, Hk, n, d = _qk_shapes(Q, K)
     dev, dt, qs, ks = Q.get_device(), Q.dtype, Q.shape, K.shape
-    Qo, Ko = _as(Qo, Q), _as(Ko, K)
+    q, k = _need(Q, "Q", qs, dev, dt), _need(K, "K", ks, dev, dt)
+    (Qo, qo), (Ko, ko) = _out(Qo, "Qo", qs, Q), _out(Ko, "Ko", ks, K)
     _check(_lib.diffuser_qk_norm_rope(
-        _need(Q, "Q", qs, dev, dt), _need(K, "K", ks, dev, dt), code, B, Hq, Hk, n, d,
+        q, k, code, B, Hq, Hk, n, d,
         _may(q_weight, "q_weight", (d,), dev, dt), _may(k_weight, "k_weight", (d,), dev, dt),
         eps, theta, rotary_dim, int(interleaved),
         _may(positions, "positions", (B, n), dev, torch.int64), position_offset,
-        _need(Qo, "Qo", qs, dev, dt), _need(Ko, "Ko", ks, dev, dt), stream), "diffuser_qk_norm_rope")
+        qo, ko, stream), "diffuser_qk_norm_rope")
     return Qo, Ko
 
 
@@ -583,20 +578,19 @@ def diffuser_qk_norm_rope_backward(Q, K, dQo, dKo, q_weight=None, k_weight=None,
     import torch
     code, B, Hq, Hk, n, d = _qk_shapes(Q, K)
     dev, dt, qs, ks = Q.get_device(), Q.dtype, Q.shape, K.shape
-    dQ, dK = _as(dQ, Q), _as(dK, K)
-    if q_weight is not None:
-        dq_weight = _as(dq_weight, q_weight)
-    if k_weight is not None:
-        dk_weight = _as(dk_weight, k_weight)
+    q, k = _need(Q, "Q", qs, dev, dt), _need(K, "K", ks, dev, dt)
+    wq, wk = _may(q_weight, "q_weight", (d,), dev, dt), _may(k_weight, "k_weight", (d,), dev, dt)
+    (dQ, dq), (dK, dk) = _out(dQ, "dQ", qs, Q), _out(dK, "dK", ks, K)
+    dwq, dwk = _may(dq_weight, "dq_weight", (d,), dev, dt), _may(dk_weight, "dk_weight", (d,), dev, dt)
+    if dwq is None and wq is not None:
+        dq_weight, dwq = _out(None, "dq_weight", (d,), q_weight)
+    if dwk is None and wk is not None:
+        dk_weight, dwk = _out(None, "dk_weight", (d,), k_weight)
     ws = _workspace(workspace, diffuser_qk_norm_rope_backward_workspace_size(B, Hq, Hk, n, d), Q)
     _check(_lib.diffuser_qk_norm_rope_backward(
-        _need(Q, "Q", qs, dev, dt), _need(K, "K", ks, dev, dt),
-        _need(dQo, "dQo", qs, dev, dt), _need(dKo, "dKo", ks, dev, dt), code, B, Hq, Hk, n, d,
-        _may(q_weight, "q_weight", (d,), dev, dt), _may(k_weight, "k_weight", (d,), dev, dt),
+        q, k, _need(dQo, "dQo", qs, dev, dt), _need(dKo, "dKo", ks, dev, dt), code, B, Hq, Hk, n, d, wq, wk,
         eps, theta, rotary_dim, int(interleaved),
-        _may(positions, "positions", (B, n), dev, torch.int64), position_offset,
-        _need(dQ, "dQ", qs, dev, dt), _need(dK, "dK", ks, dev, dt),
-        _may(dq_weight, "dq_weight", (d,), dev, dt), _may(dk_weight, "dk_weight", (d,), dev, dt),
+        _may(positions, "positions", (B, n), dev, torch.int64), position_offset, dq, dk, dwq, dwk,
         ws.data_ptr(), ws.numel(), stream), "diffuser_qk_norm_rope_backward")
     return dQ, dK, dq_weight, dk_weight
 
@@ -623,13 +617,13 @@ def diffuser_linear(X, W, bias=None, residual=None, activation: int = DIFFUSER_A
     the activation, as the backward pass wants it.  Y=residual works in place."""
     lead, T, D, F = _dense_shapes(X, W)
     dev, bf, out = X.get_device(), X.dtype, (*lead, F)
-    Y = _empty(Y, out, X)
-    if save_pre:
-        pre = _empty(pre, out, X)
+    x, w, p = _need(X, "X", X.shape, dev, bf), _need(W, "W", W.shape, dev, bf), None
+    Y, y = _out(Y, "Y", out, X)
+    if save_pre or pre is not None:
+        pre, p = _out(pre, "pre", out, Y)
     _check(_lib.diffuser_linear(
-        _need(X, "X", X.shape, dev, bf), _need(W, "W", W.shape, dev, bf), _may(bias, "bias", (F,), dev, bf),
-        _may(residual, "residual", out, dev, bf), T, D, F, activation, _need(Y, "Y", out, dev, bf),
-        _may(pre, "pre", out, dev, bf), stream), "diffuser_linear")
+        x, w, _may(bias, "bias", (F,), dev, bf), _may(residual, "residual", out, dev, bf), T, D, F, activation, y, p,
+        stream), "diffuser_linear")
     return Y if pre is None else (Y, pre)
 
 
@@ -648,15 +642,15 @@ def diffuser_linear_backward(X, W, dY, pre=None, activation: int = DIFFUSER_ACT_
     is None and not computed.  The residual's gradient is dY."""
     lead, T, D, F = _dense_shapes(X, W)
     dev, bf, out = X.get_device(), X.dtype, (*lead, F)
-    dX = _as(dX, X) if with_dX else None
-    dW = _as(dW, W) if with_dW else None
-    dbias = _empty(dbias, (F,), X) if with_bias else None
+    x, w = _need(X, "X", X.shape, dev, bf), _need(W, "W", W.shape, dev, bf)
+    dX, dx = _out(dX, "dX", X.shape, X) if with_dX else (None, None)
+    dW, dw = _out(dW, "dW", W.shape, W) if with_dW else (None, None)
+    dbias, db = _out(dbias, "dbias", (F,), X) if with_bias else (None, None)
     ws = _workspace(workspace, diffuser_linear_backward_workspace_size(T, D, F, activation), X)
     _check(_lib.diffuser_linear_backward(
-        _need(X, "X", X.shape, dev, bf), _need(W, "W", W.shape, dev, bf), _need(dY, "dY", out, dev, bf),
+        x, w, _need(dY, "dY", out, dev, bf),
         (_may if activation == DIFFUSER_ACT_NONE else _need)(pre, "pre", out, dev, bf), T, D, F, activation,
-        _may(dX, "dX", X.shape, dev, bf), _may(dW, "dW", W.shape, dev, bf),
-        _may(dbias, "dbias", (F,), dev, bf), ws.data_ptr(), ws.numel(), stream), "diffuser_linear_backward")
+        dx, dw, db, ws.data_ptr(), ws.numel(), stream), "diffuser_linear_backward")
     return dX, dW, dbias
 
 
@@ -667,13 +661,11 @@ def diffuser_gated_linear(X, Wgu, activation: int = DIFFUSER_ACT_SILU, save_pre:
     then Wu's); with save_pre (or `pre` given) returns (H, pre), pre [...][2 F] both products."""
     lead, T, D, F = _dense_shapes(X, Wgu, 2)
     dev, bf, out, both = X.get_device(), X.dtype, (*lead, F), (*lead, 2 * F)
-    H = _empty(H, out, X)
-    if save_pre:
-        pre = _empty(pre, both, X)
-    _check(_lib.diffuser_gated_linear(
-        _need(X, "X", X.shape, dev, bf), _need(Wgu, "Wgu", Wgu.shape, dev, bf), T, D, F, activation,
-        _need(H, "H", out, dev, bf), _may(pre, "pre", both, dev, bf), stream),
-        "diffuser_gated_linear")
+    x, w, p = _need(X, "X", X.shape, dev, bf), _need(Wgu, "Wgu", Wgu.shape, dev, bf), None
+    H, h = _out(H, "H", out, X)
+    if save_pre or pre is not None:
+        pre, p = _out(pre, "pre", both, X)
+    _check(_lib.diffuser_gated_linear(x, w, T, D, F, activation, h, p, stream), "diffuser_gated_linear")
     return H if pre is None else (H, pre)
 
 
@@ -691,13 +683,12 @@ def diffuser_gated_linear_backward(X, Wgu, dH, pre, activation: int = DIFFUSER_A
     one whose with_ is False is None and not computed."""
     lead, T, D, F = _dense_shapes(X, Wgu, 2)
     dev, bf, out, both = X.get_device(), X.dtype, (*lead, F), (*lead, 2 * F)
-    dX = _as(dX, X) if with_dX else None
-    dWgu = _as(dWgu, Wgu) if with_dW else None
+    x, w = _need(X, "X", X.shape, dev, bf), _need(Wgu, "Wgu", Wgu.shape, dev, bf)
+    dX, dx = _out(dX, "dX", X.shape, X) if with_dX else (None, None)
+    dWgu, dw = _out(dWgu, "dWgu", Wgu.shape, Wgu) if with_dW else (None, None)
     ws = _workspace(workspace, diffuser_gated_linear_backward_workspace_size(T, D, F), X)
     _check(_lib.diffuser_gated_linear_backward(
-        _need(X, "X", X.shape, dev, bf), _need(Wgu, "Wgu", Wgu.shape, dev, bf),
-        _need(dH, "dH", out, dev, bf), _need(pre, "pre", both, dev, bf), T, D, F, activation,
-        _may(dX, "dX", X.shape, dev, bf), _may(dWgu, "dWgu", Wgu.shape, dev, bf),
+        x, w, _need(dH, "dH", out, dev, bf), _need(pre, "pre", both, dev, bf), T, D, F, activation, dx, dw,
         ws.data_ptr(), ws.numel(), stream), "diffuser_gated_linear_backward")
     return dX, dWgu
 

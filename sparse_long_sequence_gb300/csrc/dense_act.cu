@@ -43,11 +43,12 @@ __device__ __forceinline__ uint4 round8(const float (&v)[kPer]) {
 }
 __device__ __forceinline__ uint4 load8(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
 
-// block (x, y): columns 256 x .. +255, rows [y chunk, (y + 1) chunk)
+// block (x, y): columns 256 x .. +255, rows [y chunk, (y + 1) chunk).  The column sums go to
+// `partial`, or, rounded, to `colsum` where one block has all the rows; both null: none asked for.
 template <int kAct>
 __global__ void __launch_bounds__(kThreads)
 act_backward_kernel(const __nv_bfloat16* dY, const __nv_bfloat16* P, int64_t rows, int32_t F, int64_t chunk,
-                    __nv_bfloat16* dP, float* partial) {
+                    __nv_bfloat16* dP, float* partial, __nv_bfloat16* colsum) {
     __shared__ float sums[kWarps][kBlockCols];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = (int)blockIdx.x * kBlockCols + lane * kPer;
@@ -84,7 +85,7 @@ act_backward_kernel(const __nv_bfloat16* dY, const __nv_bfloat16* P, int64_t row
             }
         }
     }
-    if (!partial) return;
+    if (!partial && !colsum) return;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) sums[warp][lane * kPer + j] = sum[j];
     __syncthreads();
@@ -92,7 +93,8 @@ act_backward_kernel(const __nv_bfloat16* dY, const __nv_bfloat16* P, int64_t row
     if (col >= F) return;
     float t = 0.f;
     for (int w = 0; w < kWarps; ++w) t += sums[w][threadIdx.x];
-    partial[(int64_t)blockIdx.y * F + col] = t;
+    if (colsum) colsum[col] = __float2bfloat16_rn(t);
+    else partial[(int64_t)blockIdx.y * F + col] = t;
 }
 
 // column sums over the chunks: 32 columns a block, its 32 warps take every 32nd chunk
@@ -165,8 +167,8 @@ void by_activation(int32_t act, Args... args) {
 template <int kAct>
 struct DenseBackward {
     static void go(dim3 grid, cudaStream_t s, const __nv_bfloat16* dY, const __nv_bfloat16* P, int64_t rows, int32_t F,
-                   int64_t chunk, __nv_bfloat16* dP, float* partial) {
-        act_backward_kernel<kAct><<<grid, kThreads, 0, s>>>(dY, P, rows, F, chunk, dP, partial);
+                   int64_t chunk, __nv_bfloat16* dP, float* partial, __nv_bfloat16* colsum) {
+        act_backward_kernel<kAct><<<grid, kThreads, 0, s>>>(dY, P, rows, F, chunk, dP, partial, colsum);
     }
 };
 template <int kAct>
@@ -179,7 +181,12 @@ struct GatedBackward {
 
 constexpr int64_t kManyBlocks = 152 * 8;         // the blocks that are resident at once
 
+// Up to 64 rows one block has them all and finishes the column sums itself: a launch less
+// (2.5 us on the host), while its 8 rows a warp take no longer than a launch (at 128 rows: 3 us more).
+constexpr int64_t kOneChunk = 64;
+
 int64_t chunk_rows(int64_t rows, int32_t F) {
+    if (rows <= kOneChunk) return kOneChunk;
     const int64_t col_blocks = (F + kBlockCols - 1) / kBlockCols;
     const int64_t want = (kManyBlocks + col_blocks - 1) / col_blocks;
     const int64_t per = (rows + want - 1) / want;
@@ -205,11 +212,12 @@ int launch_act_backward(const void* dY, const void* P, int64_t rows, int32_t F, 
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
         by_activation<DenseBackward>(act, grid, stream, static_cast<const __nv_bfloat16*>(dY),
                                      static_cast<const __nv_bfloat16*>(P), rows, F, chunk,
-                                     static_cast<__nv_bfloat16*>(dP), colsum ? partial : nullptr);
+                                     static_cast<__nv_bfloat16*>(dP), colsum && chunks > 1 ? partial : nullptr,
+                                     static_cast<__nv_bfloat16*>(chunks > 1 ? nullptr : colsum));
     }
     cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return cuda_fail(err, "act_backward_kernel");
-    if (!colsum) return DIFFUSER_OK;
+    if (!colsum || chunks == 1) return DIFFUSER_OK;
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
         colsum_kernel<<<(unsigned)((F + 31) / 32), kSumWarps * 32, 0, stream>>>(partial, chunks, F,
