@@ -474,7 +474,8 @@ DIFFUSER_API int diffuser_linear(const void* X, const void* W, const void* bias,
  *   dX = dP W,   dW = dP^T X,   dbias = column sums of dP
  * (the residual's gradient is dY itself).  dX, dW, dbias: bf16, shaped as X, W, bias;
  * a NULL one is not computed.  With an activation dP is rounded to bf16 once, as the
- * operand of the two products; dbias is summed in fp32 before that rounding.
+ * operand of the two products (not for T <= 4, where they take it in fp32); dbias is
+ * summed in fp32 before that rounding.
  * workspace: diffuser_linear_backward_workspace_size bytes, 256-byte aligned.
  * Errors: as diffuser_linear, WORKSPACE.
  */
@@ -499,7 +500,7 @@ DIFFUSER_API int diffuser_gated_linear(const void* X, const void* Wgu, int64_t T
                                        int32_t activation, void* H, void* pre, diffuser_stream stream);
 /*
  * Its gradients for dH [T][F], with G and U as kept in pre:
- *   dG = dH act'(G) U,  dU = dH act(G)  (rounded to bf16 once, as operands),
+ *   dG = dH act'(G) U,  dU = dH act(G)  (rounded to bf16 once, as operands, for T > 4),
  *   dX = dG Wg + dU Wu,   dWgu = [dG | dU]^T X.
  * dX, dWgu: bf16, shaped as X, Wgu; a NULL one is not computed.  workspace:
  * diffuser_gated_linear_backward_workspace_size bytes, 256-byte aligned.

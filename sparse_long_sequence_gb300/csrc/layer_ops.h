@@ -92,6 +92,12 @@ int64_t dense_grads_steps(const DenseArgs& x, int bn);
 int launch_gradients(const DenseArgs& x, const DenseArgs& w, cudaStream_t stream);
 int launch_dense(DenseForm form, const DenseArgs& a, cudaStream_t stream);
 
+// The whole backward of up to kFewBackward tokens in one launch (dense_few_backward.cu); null
+// results are left out.
+constexpr int64_t kFewBackward = 4;
+int launch_few_backward(const void* X, const void* W, const void* dY, const void* pre, int64_t T, int32_t D, int32_t F,
+                        int32_t act, bool gated, void* dX, void* dW, void* dbias, cudaStream_t stream);
+
 // ---- the activations' backward (dense_act.cu) --------------------------------
 // dP[t][f] = dY[t][f] act'(P[t][f]); colsum (or null): bf16 [F], the column sums
 // of dP in fp32 through `partial` ([act_chunks][F]).  dP may be null with act none

@@ -296,8 +296,10 @@ int diffuser_linear_backward(const void* X, const void* W, const void* dY, const
         if ((st = zero(dW, wb, s))) return st;
         return zero(dbias, (size_t)F * 2, s);
     }
+    if (!dX && !dW && !dbias) return DIFFUSER_OK;
     DenseArgs a{};
     if ((st = ready_status(&a.status))) return st;
+    if (T <= kFewBackward) return launch_few_backward(X, W, dY, pre, T, D, F, activation, false, dX, dW, dbias, s);
     char* ws = static_cast<char*>(workspace);
     const void* dP = has_act ? ws + L.dp : dY;
     if (dbias || (has_act && (dX || dW)))
@@ -367,6 +369,7 @@ int diffuser_gated_linear_backward(const void* X, const void* Wgu, const void* d
     if (!dX && !dWgu) return DIFFUSER_OK;
     DenseArgs a{};
     if ((st = ready_status(&a.status))) return st;
+    if (T <= kFewBackward) return launch_few_backward(X, Wgu, dH, pre, T, D, F, activation, true, dX, dWgu, nullptr, s);
     if ((st = launch_gated_backward(dH, pre, T, F, activation, workspace, s))) return st;
     a.a = workspace;
     a.rows = T;

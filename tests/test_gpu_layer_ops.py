@@ -136,6 +136,34 @@ def check_linear_backward(X, W, dY, pre, act, dX, dW, db):
         within(db, ref, U * ref.abs() + (1 + U) * slack, "dbias")
 
 
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("shape", [(1, 8, 8), (1, 72, 4104), (2, 1032, 16), (3, 264, 1000), (4, 64, 520), (4, 2048, 136)], ids=str)
+def test_backward_of_few_tokens(dl, shape, act):
+    # up to 4 tokens take a kernel of their own, with dP in fp32: one rounding an element
+    T, D, F = shape
+    X, W, b = linear_inputs(T, D, F, seed=F)
+    W2, dY, code = draw(3, 2 * F, D, scale=D ** -0.5), draw(F + 7, T, F), act_code(dl, act)
+    pre = (X.double() @ W.double().T + b.double()).bfloat16()
+    full = dl.diffuser_linear_backward(X, W, dY, pre=None if act == "none" else pre, activation=code)
+    check_linear_backward(X, W, dY, pre, act, *full)
+    dP = dY.double() * slope64(act, pre.double())
+    for got, ref in zip(full, (dP @ W.double(), dP.T @ X.double(), dP.sum(0))):
+        near(got, ref, "few", limit=U)
+    for keep in range(8):
+        part = dl.diffuser_linear_backward(X, W, dY, pre=pre, activation=code, with_dX=bool(keep & 1),
+                                           with_dW=bool(keep & 2), with_bias=bool(keep & 4))
+        for bit, (a, f) in enumerate(zip(part, full)):
+            assert (a is None) if not keep >> bit & 1 else torch.equal(a, f)
+    p2 = (X.double() @ W2.double().T).bfloat16()
+    dX, dW = dl.diffuser_gated_linear_backward(X, W2, dY, p2, activation=code)
+    g, u = p2.double()[:, :F], p2.double()[:, F:]
+    dP = torch.cat((dY.double() * u * slope64(act, g), dY.double() * act64(act, g)), -1)
+    near(dX, dP @ W2.double(), "gated dX", limit=U)
+    near(dW, dP.T @ X.double(), "gated dW", limit=U)
+    again = dl.diffuser_gated_linear_backward(X, W2, dY, p2, activation=code)
+    assert torch.equal(dX, again[0]) and torch.equal(dW, again[1])
+
+
 def test_linear_backward_by_differences(dl):
     # d/dh <dY, Y(X + h V, W + h M, b + h c)> from the forward formula in 64 bits
     T, D, F, act = 19, 40, 48, "gelu"
@@ -406,7 +434,7 @@ def guarded(rows, width, dtype=torch.bfloat16, fill=7.0):
     return inner, lambda: bool((whole[:2] == fill).all() and (whole[-2:] == fill).all())
 
 
-@pytest.mark.parametrize("shape", [(1, 64, 72), (19, 136, 88), (130, 72, 200), (2050, 200, 136), (20010, 72, 520),
+@pytest.mark.parametrize("shape", [(1, 64, 72), (3, 200, 88), (19, 136, 88), (130, 72, 200), (2050, 200, 136), (20010, 72, 520),
                                    (700, 2056, 328)], ids=lambda s: "T%dD%dF%d" % s)
 def test_nothing_is_written_outside(dl, shape):
     T, D, F = shape
