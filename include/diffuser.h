@@ -476,7 +476,8 @@ DIFFUSER_API int diffuser_linear(const void* X, const void* W, const void* bias,
  * a NULL one is not computed.  With an activation dP is rounded to bf16 once, as the
  * operand of the two products (not for T <= 4, where they take it in fp32); dbias is
  * summed in fp32 before that rounding.
- * workspace: diffuser_linear_backward_workspace_size bytes, 256-byte aligned.
+ * workspace: diffuser_linear_backward_workspace_size bytes, 256-byte aligned (0 bytes for
+ * T <= 4: NULL will do).
  * Errors: as diffuser_linear, WORKSPACE.
  */
 DIFFUSER_API int diffuser_linear_backward_workspace_size(int64_t T, int32_t D, int32_t F,
@@ -503,7 +504,8 @@ DIFFUSER_API int diffuser_gated_linear(const void* X, const void* Wgu, int64_t T
  *   dG = dH act'(G) U,  dU = dH act(G)  (rounded to bf16 once, as operands, for T > 4),
  *   dX = dG Wg + dU Wu,   dWgu = [dG | dU]^T X.
  * dX, dWgu: bf16, shaped as X, Wgu; a NULL one is not computed.  workspace:
- * diffuser_gated_linear_backward_workspace_size bytes, 256-byte aligned.
+ * diffuser_gated_linear_backward_workspace_size bytes, 256-byte aligned (0 bytes for
+ * T <= 4: NULL will do).
  * Errors: as diffuser_gated_linear, WORKSPACE.
  */
 DIFFUSER_API int diffuser_gated_linear_backward_workspace_size(int64_t T, int32_t D, int32_t F,

@@ -474,9 +474,9 @@ def _on_stream(op):
     def call(*args, stream=None, **kw):
         import torch
         first = args[0] if args else kw.get(name)
-        if first is None or not first.is_cuda:
+        dev = -1 if first is None else first.get_device()
+        if dev < 0:
             raise ValueError(f"{name} must be a tensor on a CUDA device")
-        dev = first.get_device()
         if stream is not None:
             if stream.device != first.device:
                 raise ValueError(f"the stream is on {stream.device}, the tensors on {first.device}")
@@ -508,6 +508,13 @@ def _need(t, name, shape, dev, dtype):
     return t.data_ptr()
 
 
+def _flat(t, name, dev, dtype):
+    """The address of a tensor whose shape is known to be right, after its other checks."""
+    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, t.shape, dev, dtype)
+    return t.data_ptr()
+
+
 def _may(t, name, shape, dev, dtype):
     """As _need; None where the tensor is left out."""
     return None if t is None else _need(t, name, shape, dev, dtype)
@@ -524,12 +531,15 @@ def _out(t, name, shape, like):
 
 
 def _workspace(workspace, nbytes, like):
+    """The workspace (kept alive by the caller), its address and its size; none where none is needed."""
     import torch
     if workspace is None:
-        return alloc_workspace(nbytes, like.device)
-    if workspace.device != like.device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        if not nbytes:
+            return None, None, 0
+        workspace = alloc_workspace(nbytes, like.device)
+    elif workspace.device != like.device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {like.device}")
-    return workspace
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def _qk_shapes(Q, K):
@@ -550,7 +560,7 @@ def diffuser_qk_norm_rope(Q, K, q_weight=None, k_weight=None, positions=None, po
     import torch
     code, B, Hq, Hk, n, d = _qk_shapes(Q, K)
     dev, dt, qs, ks = Q.get_device(), Q.dtype, Q.shape, K.shape
-    q, k = _need(Q, "Q", qs, dev, dt), _need(K, "K", ks, dev, dt)
+    q, k = _flat(Q, "Q", dev, dt), _flat(K, "K", dev, dt)
     (Qo, qo), (Ko, ko) = _out(Qo, "Qo", qs, Q), _out(Ko, "Ko", ks, K)
     _check(_lib.diffuser_qk_norm_rope(
         q, k, code, B, Hq, Hk, n, d,
@@ -578,7 +588,7 @@ def diffuser_qk_norm_rope_backward(Q, K, dQo, dKo, q_weight=None, k_weight=None,
     import torch
     code, B, Hq, Hk, n, d = _qk_shapes(Q, K)
     dev, dt, qs, ks = Q.get_device(), Q.dtype, Q.shape, K.shape
-    q, k = _need(Q, "Q", qs, dev, dt), _need(K, "K", ks, dev, dt)
+    q, k = _flat(Q, "Q", dev, dt), _flat(K, "K", dev, dt)
     wq, wk = _may(q_weight, "q_weight", (d,), dev, dt), _may(k_weight, "k_weight", (d,), dev, dt)
     (dQ, dq), (dK, dk) = _out(dQ, "dQ", qs, Q), _out(dK, "dK", ks, K)
     dwq, dwk = _may(dq_weight, "dq_weight", (d,), dev, dt), _may(dk_weight, "dk_weight", (d,), dev, dt)
@@ -586,12 +596,12 @@ def diffuser_qk_norm_rope_backward(Q, K, dQo, dKo, q_weight=None, k_weight=None,
         dq_weight, dwq = _out(None, "dq_weight", (d,), q_weight)
     if dwk is None and wk is not None:
         dk_weight, dwk = _out(None, "dk_weight", (d,), k_weight)
-    ws = _workspace(workspace, diffuser_qk_norm_rope_backward_workspace_size(B, Hq, Hk, n, d), Q)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, diffuser_qk_norm_rope_backward_workspace_size(B, Hq, Hk, n, d), Q)
     _check(_lib.diffuser_qk_norm_rope_backward(
         q, k, _need(dQo, "dQo", qs, dev, dt), _need(dKo, "dKo", ks, dev, dt), code, B, Hq, Hk, n, d, wq, wk,
         eps, theta, rotary_dim, int(interleaved),
         _may(positions, "positions", (B, n), dev, torch.int64), position_offset, dq, dk, dwq, dwk,
-        ws.data_ptr(), ws.numel(), stream), "diffuser_qk_norm_rope_backward")
+        ws_ptr, ws_bytes, stream), "diffuser_qk_norm_rope_backward")
     return dQ, dK, dq_weight, dk_weight
 
 
@@ -617,7 +627,7 @@ def diffuser_linear(X, W, bias=None, residual=None, activation: int = DIFFUSER_A
     the activation, as the backward pass wants it.  Y=residual works in place."""
     lead, T, D, F = _dense_shapes(X, W)
     dev, bf, out = X.get_device(), X.dtype, (*lead, F)
-    x, w, p = _need(X, "X", X.shape, dev, bf), _need(W, "W", W.shape, dev, bf), None
+    x, w, p = _flat(X, "X", dev, bf), _flat(W, "W", dev, bf), None
     Y, y = _out(Y, "Y", out, X)
     if save_pre or pre is not None:
         pre, p = _out(pre, "pre", out, Y)
@@ -642,15 +652,15 @@ def diffuser_linear_backward(X, W, dY, pre=None, activation: int = DIFFUSER_ACT_
     is None and not computed.  The residual's gradient is dY."""
     lead, T, D, F = _dense_shapes(X, W)
     dev, bf, out = X.get_device(), X.dtype, (*lead, F)
-    x, w = _need(X, "X", X.shape, dev, bf), _need(W, "W", W.shape, dev, bf)
+    x, w = _flat(X, "X", dev, bf), _flat(W, "W", dev, bf)
     dX, dx = _out(dX, "dX", X.shape, X) if with_dX else (None, None)
     dW, dw = _out(dW, "dW", W.shape, W) if with_dW else (None, None)
     dbias, db = _out(dbias, "dbias", (F,), X) if with_bias else (None, None)
-    ws = _workspace(workspace, diffuser_linear_backward_workspace_size(T, D, F, activation), X)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, diffuser_linear_backward_workspace_size(T, D, F, activation), X)
     _check(_lib.diffuser_linear_backward(
         x, w, _need(dY, "dY", out, dev, bf),
         (_may if activation == DIFFUSER_ACT_NONE else _need)(pre, "pre", out, dev, bf), T, D, F, activation,
-        dx, dw, db, ws.data_ptr(), ws.numel(), stream), "diffuser_linear_backward")
+        dx, dw, db, ws_ptr, ws_bytes, stream), "diffuser_linear_backward")
     return dX, dW, dbias
 
 
@@ -661,7 +671,7 @@ def diffuser_gated_linear(X, Wgu, activation: int = DIFFUSER_ACT_SILU, save_pre:
     then Wu's); with save_pre (or `pre` given) returns (H, pre), pre [...][2 F] both products."""
     lead, T, D, F = _dense_shapes(X, Wgu, 2)
     dev, bf, out, both = X.get_device(), X.dtype, (*lead, F), (*lead, 2 * F)
-    x, w, p = _need(X, "X", X.shape, dev, bf), _need(Wgu, "Wgu", Wgu.shape, dev, bf), None
+    x, w, p = _flat(X, "X", dev, bf), _flat(Wgu, "Wgu", dev, bf), None
     H, h = _out(H, "H", out, X)
     if save_pre or pre is not None:
         pre, p = _out(pre, "pre", both, X)
@@ -683,13 +693,13 @@ def diffuser_gated_linear_backward(X, Wgu, dH, pre, activation: int = DIFFUSER_A
     one whose with_ is False is None and not computed."""
     lead, T, D, F = _dense_shapes(X, Wgu, 2)
     dev, bf, out, both = X.get_device(), X.dtype, (*lead, F), (*lead, 2 * F)
-    x, w = _need(X, "X", X.shape, dev, bf), _need(Wgu, "Wgu", Wgu.shape, dev, bf)
+    x, w = _flat(X, "X", dev, bf), _flat(Wgu, "Wgu", dev, bf)
     dX, dx = _out(dX, "dX", X.shape, X) if with_dX else (None, None)
     dWgu, dw = _out(dWgu, "dWgu", Wgu.shape, Wgu) if with_dW else (None, None)
-    ws = _workspace(workspace, diffuser_gated_linear_backward_workspace_size(T, D, F), X)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, diffuser_gated_linear_backward_workspace_size(T, D, F), X)
     _check(_lib.diffuser_gated_linear_backward(
         x, w, _need(dH, "dH", out, dev, bf), _need(pre, "pre", both, dev, bf), T, D, F, activation, dx, dw,
-        ws.data_ptr(), ws.numel(), stream), "diffuser_gated_linear_backward")
+        ws_ptr, ws_bytes, stream), "diffuser_gated_linear_backward")
     return dX, dWgu
 
 

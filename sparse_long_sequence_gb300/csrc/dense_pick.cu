@@ -1,7 +1,8 @@
 // Which kernel a dense product runs on: a rule on its sizes.
 //
-//  * Forward of up to 32 tokens: dense_few.cu.  (1024 -> 4096: 5.8 us at 16 tokens, where the
-//    pairs take 7.1; 8.1 at 64 tokens, where they take 7.4.)
+//  * Forward of up to 32 tokens (gated: 64): dense_few.cu.  1024 -> 4096: 6.0 us at 16 tokens,
+//    where the pairs take 7.5; 8.1 at 64, where they take 7.2.  Gated, 768 -> 2048: 7.2 us at 64
+//    tokens and 14.9 at 256, where the pairs take 8.7 and 8.9.
 //  * Otherwise CTA pairs (dense_pair.cu) with the tile width and split that this estimate puts
 //    lowest, in us.  A wave of tiles takes its K steps; a step takes `step` when a few pairs run
 //    and `busy` when all do (they share the L2's bandwidth).  Persistent tiles overlap their
@@ -15,7 +16,7 @@
 namespace dfs {
 namespace {
 
-constexpr int64_t kFewTokens = 32;
+constexpr int64_t kFewTokens = 32, kFewTokensGated = 64;
 
 struct Shape { int64_t I, J, K; };          // result rows and columns, summed length
 
@@ -56,16 +57,16 @@ Pick pick(const Shape& s, bool gated) {
 }  // namespace
 
 int launch_dense(DenseForm form, const DenseArgs& a, cudaStream_t stream) {
-    if (form == kForward && a.rows <= kFewTokens) return launch_dense_few(a, stream);
+    if (form == kForward && a.rows <= (a.gated ? kFewTokensGated : kFewTokens)) return launch_dense_few(a, stream);
     const Pick p = pick(shape_of(form, a), form == kForward && a.gated);
     return launch_dense_pair(form, a, p.bn, p.splits, stream);
 }
 
 // Both gradients: one launch where its busiest pair ends before the two kernels after each
 // other would (2 us for the second launch): 2.9 or 2.1 us and its K steps.
-//   gated backward, 16384 x 1024 x 2816: 289 us in one launch, 324 in two (with the activations')
-//   dense backward, 2048 x 1024 x 4096: 37.3 and 47.5;  1024 x 512 x 512: 12.4 and 18.4
-//   dense backward, 32768 x 768 x 768, where the weights' gradient wants K split: 139 and 110
+//   gated backward, 16384 x 1024 x 2816: 284 us in one launch, 318 in two (with the activations')
+//   dense backward, 2048 x 1024 x 4096: 37 and 44;  1024 x 512 x 512: 12.2 and 17.7
+//   dense backward, 32768 x 768 x 768, where the weights' gradient wants K split: 141 and 110
 int launch_gradients(const DenseArgs& x, const DenseArgs& w, cudaStream_t stream) {
     const Pick px = pick(shape_of(kInputGrad, x), false), pw = pick(shape_of(kWeightGrad, w), false);
     const double at256 = 2.9 + 0.305 * (double)dense_grads_steps(x, 256);

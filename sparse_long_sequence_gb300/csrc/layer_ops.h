@@ -78,7 +78,7 @@ struct DenseArgs {
     bool gated;                     // forward: out = act(P[:, :F]) * P[:, F:], F = cols / 2
     int* status;
 };
-// forward of up to 32 tokens (dense_few.cu)
+// forward of a few tokens (dense_few.cu)
 int launch_dense_few(const DenseArgs& a, cudaStream_t stream);
 // CTA pairs, 256 x bn tiles, bn 128 or 256 (gated: 256); splits 1: persistent, 2 or 4: K split
 // over that many pairs of a cluster (dense_pair.cu)

@@ -128,11 +128,17 @@ struct DenseBwd {
 };
 DenseBwd plan_dense_backward(int64_t T, int64_t F, int32_t act) {
     DenseBwd L{};
+    if (T <= kFewBackward) return L;
     const size_t dp = act == DIFFUSER_ACT_NONE ? 0 : align256((size_t)T * F * 2);
     L.partial = dp;
     L.total = dp + align256((size_t)act_chunks(T, (int32_t)F) * F * sizeof(float));
-    if (L.total == 0) L.total = 256;
     return L;
+}
+size_t gated_backward_bytes(int64_t T, int64_t F) { return T <= kFewBackward ? 0 : align256((size_t)T * F * 4); }
+
+// a workspace that may be left out where none is needed
+int check_backward_workspace(size_t need, void* ws, size_t ws_bytes) {
+    return need ? check_workspace_bytes(need, ws, ws_bytes) : DIFFUSER_OK;
 }
 
 // dX = dP W and dW = dP^T X, a (dP, sizes, status) filled in; a null result is left out
@@ -288,7 +294,7 @@ int diffuser_linear_backward(const void* X, const void* W, const void* dY, const
     const DenseBwd L = plan_dense_backward(T, F, activation);
     if ((st = check_span(in[0], "X")) || (st = check_span(in[1], "W")) || (st = check_span(in[2], "dY")) ||
         (st = check_span(in[3], "pre")) || (st = check_span(out[0], "dX")) || (st = check_span(out[1], "dW")) ||
-        (st = check_span(out[2], "dbias")) || (st = check_workspace_bytes(L.total, workspace, workspace_bytes)) ||
+        (st = check_span(out[2], "dbias")) || (st = check_backward_workspace(L.total, workspace, workspace_bytes)) ||
         (st = check_overlaps(in, 4, out, 4)))
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -346,7 +352,7 @@ int diffuser_gated_linear_backward_workspace_size(int64_t T, int32_t D, int32_t 
     if (!bytes) return fail(DIFFUSER_ERR_INVALID_ARG, "NULL argument");
     const int st = check_dense(T, D, F, DIFFUSER_ACT_NONE);
     if (st) return st;
-    *bytes = T ? align256((size_t)T * F * 4) : 256;
+    *bytes = gated_backward_bytes(T, F);
     return DIFFUSER_OK;
 } catch (...) {
     return fail(DIFFUSER_ERR_ALLOC, "unexpected exception");
@@ -362,7 +368,7 @@ int diffuser_gated_linear_backward(const void* X, const void* Wgu, const void* d
     const Span out[3] = {{dX, dX ? xb : 0}, {dWgu, dWgu ? wb : 0}, {workspace, workspace_bytes}};
     if ((st = check_span(in[0], "X")) || (st = check_span(in[1], "Wgu")) || (st = check_span(in[2], "dH")) ||
         (st = check_span(in[3], "pre")) || (st = check_span(out[0], "dX")) || (st = check_span(out[1], "dWgu")) ||
-        (st = check_workspace_bytes(T ? 2 * hb : 0, workspace, workspace_bytes)) || (st = check_overlaps(in, 4, out, 3)))
+        (st = check_backward_workspace(gated_backward_bytes(T, F), workspace, workspace_bytes)) || (st = check_overlaps(in, 4, out, 3)))
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (T == 0) return zero(dWgu, wb, s);
