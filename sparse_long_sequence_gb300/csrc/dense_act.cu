@@ -101,6 +101,7 @@ act_backward_kernel(const __nv_bfloat16* dY, const __nv_bfloat16* P, int64_t row
 constexpr int kSumWarps = 32;
 __global__ void __launch_bounds__(kSumWarps * 32) colsum_kernel(const float* partial, int64_t chunks, int32_t F, __nv_bfloat16* out) {
     __shared__ float sums[kSumWarps][32];
+    ptx::griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = (int)blockIdx.x * 32 + lane;
     float t = 0.f;
@@ -204,8 +205,18 @@ int64_t act_chunks(int64_t rows, int32_t F) {
     return (rows + c - 1) / c;
 }
 
+int launch_colsum(const BiasSums& b, cudaStream_t stream) {
+    cudaError_t err;
+    {
+        LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
+        err = launch_pdl(colsum_kernel, dim3((unsigned)((b.F + 31) / 32)), dim3(kSumWarps * 32), 0, stream, b.partial,
+                         b.chunks, b.F, b.out);
+    }
+    return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "colsum_kernel");
+}
+
 int launch_act_backward(const void* dY, const void* P, int64_t rows, int32_t F, int32_t act, void* dP, void* colsum,
-                        float* partial, cudaStream_t stream) {
+                        float* partial, BiasSums* sums, cudaStream_t stream) {
     const int64_t chunk = chunk_rows(rows, F), chunks = act_chunks(rows, F);
     const dim3 grid((unsigned)((F + kBlockCols - 1) / kBlockCols), (unsigned)chunks);
     {
@@ -215,16 +226,11 @@ int launch_act_backward(const void* dY, const void* P, int64_t rows, int32_t F, 
                                      static_cast<__nv_bfloat16*>(dP), colsum && chunks > 1 ? partial : nullptr,
                                      static_cast<__nv_bfloat16*>(chunks > 1 ? nullptr : colsum));
     }
-    cudaError_t err = cudaGetLastError();
+    const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return cuda_fail(err, "act_backward_kernel");
-    if (!colsum || chunks == 1) return DIFFUSER_OK;
-    {
-        LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        colsum_kernel<<<(unsigned)((F + 31) / 32), kSumWarps * 32, 0, stream>>>(partial, chunks, F,
-                                                                         static_cast<__nv_bfloat16*>(colsum));
-    }
-    err = cudaGetLastError();
-    return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "colsum_kernel");
+    *sums = BiasSums{};
+    if (colsum && chunks > 1) *sums = {partial, chunks, F, static_cast<__nv_bfloat16*>(colsum)};
+    return DIFFUSER_OK;
 }
 
 int launch_gated_backward(const void* dH, const void* P, int64_t rows, int32_t F, int32_t act, void* dP,

@@ -230,6 +230,7 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     ptx::cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    ptx::griddep_wait();                                       // (dP, after the activations' kernel)
 
     if (warp == 0) {
         // (the whole warp runs the loop; the elected lane issues the copies)
@@ -376,8 +377,9 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
 // dX = dP W and dW = dP^T X need nothing of each other, and neither's tiles fill a whole number
 // of waves.  One persistent kernel runs both: a pair takes its share of the longer tiles (K
 // steps) first, then of the shorter ones, dealt on the host so that all pairs finish nearly
-// together (each pair's tiles follow one another, j fastest, so that it rereads its rows of A
-// from the L2).
+// together.  Neighbouring pairs work on neighbouring tiles (j fastest) at the same time and read
+// the same rows of dP from the L2; with a pair's tiles one after the other the gated backward
+// 16384 x 1024 x 2816 read 964 MB from memory and not 458.
 struct GradDeal {
     int32_t longer;            // 0: dX has the longer tiles, 1: dW
     int32_t a_pairs;           // pairs with one long tile more
@@ -388,23 +390,18 @@ struct GradDeal {
 struct GradArgs {
     PairArgs p[2];             // dX, dW
     GradDeal deal;
+    BiasSums bias;             // partial sums of the bias gradient to finish (null: none)
 };
-struct Share {
-    int l0, nl, s0, ns;        // first long and short tile and their counts
-};
-__device__ __forceinline__ Share share_of(const GradDeal& d, int pair) {
-    Share s;
-    s.nl = d.longs + (pair < d.a_pairs);
-    s.l0 = pair * d.longs + min(pair, d.a_pairs);
-    if (pair < d.a_pairs) {
-        s.ns = d.a_shorts + (pair < d.a_rest);
-        s.s0 = pair * d.a_shorts + min(pair, d.a_rest);
-    } else {
-        const int i = pair - d.a_pairs;
-        s.ns = d.b_shorts + (i < d.b_rest);
-        s.s0 = d.a_pairs * d.a_shorts + d.a_rest + i * d.b_shorts + min(i, d.b_rest);
-    }
-    return s;
+// counts of a pair's long and short tiles
+__device__ __forceinline__ int long_tiles(const GradDeal& d, int pair) { return d.longs + (pair < d.a_pairs); }
+__device__ __forceinline__ int short_tiles(const GradDeal& d, int pair) {
+    return pair < d.a_pairs ? d.a_shorts + (pair < d.a_rest) : d.b_shorts + (pair - d.a_pairs < d.b_rest);
+}
+// a pair's k-th long tile (all pairs in rounds) and short tile (the a pairs' rounds, then the b pairs')
+__device__ __forceinline__ int long_tile(int pairs, int pair, int k) { return k * pairs + pair; }
+__device__ __forceinline__ int short_tile(const GradDeal& d, int pairs, int pair, int k) {
+    if (pair < d.a_pairs) return k * d.a_pairs + pair;
+    return d.a_pairs * d.a_shorts + d.a_rest + k * (pairs - d.a_pairs) + pair - d.a_pairs;
 }
 
 template <int kBn>
@@ -429,13 +426,14 @@ dense_grads_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)ptx::cluster_ctarank();
-    const Share sh = share_of(g.deal, (int)blockIdx.x / 2);
-    const int my_tiles = sh.nl + sh.ns;
+    const int pairs = (int)gridDim.x / 2, pair = (int)blockIdx.x / 2;
+    const int my_longs = long_tiles(g.deal, pair), my_tiles = my_longs + short_tiles(g.deal, pair);
     int* const status = g.p[0].status;
     // tile lt of this pair: whose it is (0 dX, 1 dW) and where
-    auto kind_of = [&](int lt) { return lt < sh.nl ? g.deal.longer : 1 - g.deal.longer; };
+    auto kind_of = [&](int lt) { return lt < my_longs ? g.deal.longer : 1 - g.deal.longer; };
     auto tile_of = [&](int lt, int kind) {
-        const int t = lt < sh.nl ? sh.l0 + lt : sh.s0 + lt - sh.nl, jt = g.p[kind].j_tiles;
+        const int t = lt < my_longs ? long_tile(pairs, pair, lt) : short_tile(g.deal, pairs, pair, lt - my_longs);
+        const int jt = g.p[kind].j_tiles;
         return Tile{t / jt * kTI, t % jt * kBn};
     };
 
@@ -456,6 +454,7 @@ dense_grads_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
     ptx::cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    ptx::griddep_wait();                                       // dP and the bias's partial sums are there
 
     if (warp == 0) {
         int n = 0;
@@ -503,6 +502,29 @@ dense_grads_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
         const int row_at = lane * 64, sw = (lane >> 1) & 3;
         const uint32_t acc_empty0 = ptx::map_rank(ptx::smem_u32(acc_empty), 0);
         const bool lead = lane == 0;
+        if (g.bias.out) {
+            // until the first accumulator is full: the bias gradient, 32 columns a CTA at a time, every
+            // eighth partial sum a warp
+            float* sums = reinterpret_cast<float*>(bufs);
+            const int w = warp - kEpiWarp0;
+            for (int c0 = (int)blockIdx.x * 32; c0 < g.bias.F; c0 += (int)gridDim.x * 32) {
+                const int col = c0 + lane;
+                float t = 0.f;
+                if (col < g.bias.F) {
+#pragma unroll 8
+                    for (int64_t k = w; k < g.bias.chunks; k += kEpiWarps) t += g.bias.partial[k * g.bias.F + col];
+                }
+                sums[w * 32 + lane] = t;
+                ptx::named_barrier_sync(1, 32 * kEpiWarps);
+                if (w == 0 && col < g.bias.F) {
+                    t = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kEpiWarps; ++k) t += sums[k * 32 + lane];
+                    g.bias.out[col] = __float2bfloat16_rn(t);
+                }
+                ptx::named_barrier_sync(1, 32 * kEpiWarps);
+            }
+        }
         int u = 0;                                             // the warp's stores so far; buffer u % kBufs
         for (int lt = 0; lt < my_tiles; ++lt) {
             const int buf = lt & 1, kind = kind_of(lt);
@@ -608,6 +630,7 @@ dense_pair_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_co
     ptx::cluster_sync();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    ptx::griddep_wait();
 
     if (warp == 0) {
         int g = 0;
@@ -714,20 +737,24 @@ int resident_clusters(Kernel kernel, int ctas, int threads, int smem) {
     return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
 }
 
+// early: the kernel may start while the one before it on the stream ends (griddep_wait)
 template <class Kernel, class... Args>
-int launch_clusters(Kernel kernel, int ctas, int64_t clusters, int threads, int smem, cudaStream_t stream, const Args&... args) {
+int launch_clusters(Kernel kernel, int ctas, int64_t clusters, int threads, int smem, bool early, cudaStream_t stream,
+                    const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ctas * clusters));
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)ctas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = early ? 2 : 1;
     cudaError_t err;
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
@@ -754,8 +781,8 @@ int launch_pair_as(const CUtensorMap (&tm)[5], const PairArgs& a, cudaStream_t s
         fit[dev & 63].store(pairs);
     }
     const int64_t tiles = (int64_t)a.i_tiles * a.j_tiles;
-    return launch_clusters(kernel, 2, tiles < pairs ? tiles : pairs, kAll, smem_bytes(kBn), stream, tm[0], tm[1], tm[2],
-                           tm[3], tm[4], a);
+    return launch_clusters(kernel, 2, tiles < pairs ? tiles : pairs, kAll, smem_bytes(kBn), kBMn, stream, tm[0], tm[1],
+                           tm[2], tm[3], tm[4], a);
 }
 
 template <bool kAMn, bool kBMn, bool kGated, int kBn, int kSplits>
@@ -765,7 +792,8 @@ int launch_split_as(const CUtensorMap (&tm)[5], const PairArgs& a, const Results
     constexpr int kSmem = 1024 + stage_count(kBn) * (kABytes + b_bytes(kBn)) + kBarBytes;
     const cudaError_t err = allow_smem(kernel, kSmem, done);
     if (err != cudaSuccess) return cuda_fail(err, "cudaFuncSetAttribute(dense pair split kernel)");
-    return launch_clusters(kernel, 2 * kSplits, (int64_t)a.i_tiles * a.j_tiles, kThreads, kSmem, stream, tm[0], tm[1], a, r);
+    return launch_clusters(kernel, 2 * kSplits, (int64_t)a.i_tiles * a.j_tiles, kThreads, kSmem, kBMn, stream, tm[0], tm[1],
+                           a, r);
 }
 
 template <bool kAMn, bool kBMn, bool kGated, int kBn>
@@ -891,8 +919,8 @@ int launch_grads_as(const CUtensorMap (&tm)[6], GradArgs g, cudaStream_t stream)
     int64_t pairs = dense_pair_clusters(1), most = 0;
     if (tiles < pairs) pairs = tiles;
     g.deal = deal_grads(g.p[0], g.p[1], (int)pairs, &most);
-    return launch_clusters(kernel, 2, pairs, pair_threads(false), smem_bytes(kBn), stream, tm[0], tm[1], tm[2], tm[3],
-                           tm[4], tm[5], g);
+    return launch_clusters(kernel, 2, pairs, pair_threads(false), smem_bytes(kBn), true, stream, tm[0], tm[1], tm[2],
+                           tm[3], tm[4], tm[5], g);
 }
 
 }  // namespace
@@ -905,8 +933,9 @@ int64_t dense_grads_steps(const DenseArgs& x, int bn) {
     return most;
 }
 
-int launch_dense_grads(const DenseArgs& x, const DenseArgs& w, int bn, cudaStream_t stream) {
+int launch_dense_grads(const DenseArgs& x, const DenseArgs& w, const BiasSums& bias, int bn, cudaStream_t stream) {
     GradArgs g{};
+    g.bias = bias;
     CUtensorMap tm[6] = {};                        // dX: A, B, result; dW: A, B, result
     int st = plan_pair(kInputGrad, x, bn, &g.p[0]);
     if (!st) st = plan_pair(kWeightGrad, w, bn, &g.p[1]);

@@ -67,13 +67,14 @@ int launch_dense(DenseForm form, const DenseArgs& a, cudaStream_t stream) {
 //   gated backward, 16384 x 1024 x 2816: 284 us in one launch, 318 in two (with the activations')
 //   dense backward, 2048 x 1024 x 4096: 37 and 44;  1024 x 512 x 512: 12.2 and 17.7
 //   dense backward, 32768 x 768 x 768, where the weights' gradient wants K split: 141 and 110
-int launch_gradients(const DenseArgs& x, const DenseArgs& w, cudaStream_t stream) {
+int launch_gradients(const DenseArgs& x, const DenseArgs& w, const BiasSums& bias, cudaStream_t stream) {
     const Pick px = pick(shape_of(kInputGrad, x), false), pw = pick(shape_of(kWeightGrad, w), false);
     const double at256 = 2.9 + 0.305 * (double)dense_grads_steps(x, 256);
     const double at128 = 2.1 + 0.205 * (double)dense_grads_steps(x, 128);
     if ((at256 < at128 ? at256 : at128) < px.us + pw.us + 2.0)
-        return launch_dense_grads(x, w, at256 <= at128 ? 256 : 128, stream);
-    const int st = launch_dense_pair(kInputGrad, x, px.bn, px.splits, stream);
+        return launch_dense_grads(x, w, bias, at256 <= at128 ? 256 : 128, stream);
+    int st = bias.out ? launch_colsum(bias, stream) : DIFFUSER_OK;
+    if (!st) st = launch_dense_pair(kInputGrad, x, px.bn, px.splits, stream);
     return st ? st : launch_dense_pair(kWeightGrad, w, pw.bn, pw.splits, stream);
 }
 

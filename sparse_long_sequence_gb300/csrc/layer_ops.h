@@ -4,6 +4,7 @@
 // points (layer_ops_abi.cu).
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -50,7 +51,7 @@ struct QkArgs {
     int32_t Hq, Hk;
     int32_t rot;                    // rotated features: 0, 16, 32, 48, 64
     float eps;
-    float* partial;                 // backward: [blocks][2][64] sums of the weight gradients
+    float* partial;                 // backward: [blocks][64] sums of the weights' gradients, or null
     uint64_t freq[kHeadDim / 2];    // turns per position of pair i, in units of 2^-64
 };
 int launch_qk_norm_rope(const QkArgs& a, int32_t dtype, bool interleaved, cudaStream_t stream);
@@ -85,11 +86,19 @@ int launch_dense_few(const DenseArgs& a, cudaStream_t stream);
 int launch_dense_pair(DenseForm form, const DenseArgs& a, int bn, int splits, cudaStream_t stream);
 // clusters of 2 `splits` CTAs of the split kernel that run at once on the current device
 int dense_pair_clusters(int splits);
+// A bias gradient's fp32 partial sums [chunks][F] and where their sums go (null: nowhere)
+struct BiasSums {
+    const float* partial;
+    int64_t chunks;
+    int32_t F;
+    __nv_bfloat16* out;
+};
+int launch_colsum(const BiasSums& b, cudaStream_t stream);                   // dense_act.cu
 // both gradients in one launch (dense_pair.cu), and the K steps of its busiest CTA pair
-int launch_dense_grads(const DenseArgs& x, const DenseArgs& w, int bn, cudaStream_t stream);
+int launch_dense_grads(const DenseArgs& x, const DenseArgs& w, const BiasSums& bias, int bn, cudaStream_t stream);
 int64_t dense_grads_steps(const DenseArgs& x, int bn);
 // picks the kernel (dense_pick.cu); the gradients: x for dX and w for dW, of one product
-int launch_gradients(const DenseArgs& x, const DenseArgs& w, cudaStream_t stream);
+int launch_gradients(const DenseArgs& x, const DenseArgs& w, const BiasSums& bias, cudaStream_t stream);
 int launch_dense(DenseForm form, const DenseArgs& a, cudaStream_t stream);
 
 // The whole backward of up to kFewBackward tokens in one launch (dense_few_backward.cu); null
@@ -99,12 +108,12 @@ int launch_few_backward(const void* X, const void* W, const void* dY, const void
                         int32_t act, bool gated, void* dX, void* dW, void* dbias, cudaStream_t stream);
 
 // ---- the activations' backward (dense_act.cu) --------------------------------
-// dP[t][f] = dY[t][f] act'(P[t][f]); colsum (or null): bf16 [F], the column sums
-// of dP in fp32 through `partial` ([act_chunks][F]).  dP may be null with act none
-// (dP is dY itself).
+// dP[t][f] = dY[t][f] act'(P[t][f]); colsum (or null): bf16 [F], the column sums of dP in fp32:
+// written where the rows are one chunk, else left in `partial` ([act_chunks][F]) and described in
+// *sums for the caller to finish.  dP may be null with act none (dP is dY itself).
 int64_t act_chunks(int64_t rows, int32_t F);
 int launch_act_backward(const void* dY, const void* P, int64_t rows, int32_t F, int32_t act, void* dP,
-                        void* colsum, float* partial, cudaStream_t stream);
+                        void* colsum, float* partial, BiasSums* sums, cudaStream_t stream);
 // gated: P [T][2F]; dP[t][f] = dH act'(g) u, dP[t][F + f] = dH act(g)
 int launch_gated_backward(const void* dH, const void* P, int64_t rows, int32_t F, int32_t act, void* dP,
                           cudaStream_t stream);

@@ -94,7 +94,7 @@ QkArgs qk_args(const void* Q, const void* K, int64_t B, int64_t Hq, int64_t Hk, 
 }
 
 size_t qk_partial_bytes(int64_t tokens, int64_t Hq, int64_t Hk) {
-    return tokens ? align256((size_t)qk_backward_blocks(tokens, Hq, Hk) * 2 * kHeadDim * sizeof(float)) : 256;
+    return tokens ? align256((size_t)qk_backward_blocks(tokens, Hq, Hk) * kHeadDim * sizeof(float)) : 256;
 }
 
 // ---- dense products ---------------------------------------------------------------
@@ -141,14 +141,18 @@ int check_backward_workspace(size_t need, void* ws, size_t ws_bytes) {
     return need ? check_workspace_bytes(need, ws, ws_bytes) : DIFFUSER_OK;
 }
 
-// dX = dP W and dW = dP^T X, a (dP, sizes, status) filled in; a null result is left out
-int launch_both(const DenseArgs& a, const void* W, void* dX, const void* X, void* dW, cudaStream_t stream) {
+// dX = dP W and dW = dP^T X, a (dP, sizes, status) filled in, and what is left of the bias
+// gradient; a null result is left out
+int launch_both(const DenseArgs& a, const void* W, void* dX, const void* X, void* dW, const BiasSums& bias,
+                cudaStream_t stream) {
     DenseArgs x = a, w = a;
     x.b = W;
     x.out = dX;
     w.b = X;
     w.out = dW;
-    if (dX && dW) return launch_gradients(x, w, stream);
+    if (dX && dW) return launch_gradients(x, w, bias, stream);
+    if (bias.out)
+        if (const int st = launch_colsum(bias, stream)) return st;
     if (dX) return launch_dense(kInputGrad, x, stream);
     if (dW) return launch_dense(kWeightGrad, w, stream);
     return DIFFUSER_OK;
@@ -308,15 +312,16 @@ int diffuser_linear_backward(const void* X, const void* W, const void* dY, const
     if (T <= kFewBackward) return launch_few_backward(X, W, dY, pre, T, D, F, activation, false, dX, dW, dbias, s);
     char* ws = static_cast<char*>(workspace);
     const void* dP = has_act ? ws + L.dp : dY;
+    BiasSums bias{};
     if (dbias || (has_act && (dX || dW)))
         if ((st = launch_act_backward(dY, pre, T, F, activation, has_act ? ws + L.dp : nullptr, dbias,
-                                      reinterpret_cast<float*>(ws + L.partial), s)))
+                                      reinterpret_cast<float*>(ws + L.partial), &bias, s)))
             return st;
     a.a = dP;
     a.rows = T;
     a.inner = D;
     a.cols = F;
-    return launch_both(a, W, dX, X, dW, s);
+    return launch_both(a, W, dX, X, dW, bias, s);
 } catch (...) {
     return fail(DIFFUSER_ERR_ALLOC, "unexpected exception");
 }
@@ -381,7 +386,7 @@ int diffuser_gated_linear_backward(const void* X, const void* Wgu, const void* d
     a.rows = T;
     a.inner = D;
     a.cols = 2 * F;
-    return launch_both(a, Wgu, dX, X, dWgu, s);
+    return launch_both(a, Wgu, dX, X, dWgu, BiasSums{}, s);
 } catch (...) {
     return fail(DIFFUSER_ERR_ALLOC, "unexpected exception");
 }

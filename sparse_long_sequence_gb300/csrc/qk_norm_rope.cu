@@ -24,6 +24,7 @@
 
 #include "layer_ops.h"
 #include "packed.cuh"
+#include "sm100_ptx.cuh"
 
 namespace dfs {
 namespace {
@@ -165,26 +166,26 @@ __device__ __forceinline__ void load_weight(const T* w, int oa, int ob, F2 (&v)[
     }
 }
 
-// A warp's share: four tokens and a run of the queries' or the keys' heads.
+// A warp's share (a unit): four tokens and a run of the queries' or of the keys' heads.  All of
+// the queries' units come first.
 struct Work {
     int64_t groups;                // of four tokens
-    int64_t units;                 // groups x (q_runs + k_runs)
+    int64_t q_units, k_units;      // groups x runs
     int32_t per;                   // heads of a run
-    int32_t q_runs;
+    int32_t q_blocks, k_blocks;    // backward: blocks that take the queries' units, and the keys'
 };
 struct Share {
-    bool key, live;                // the keys' heads; this lane's token exists
+    bool live;                     // this lane's token exists
     int h0, h1;
     int64_t first;                 // offset of (h0, token) in its tensor
     int64_t pos;
 };
-__device__ __forceinline__ Share share_of(const QkArgs& a, const Work& w, int64_t unit, int lane) {
+// unit `unit` of the queries or (key) of the keys
+__device__ __forceinline__ Share share_of(const QkArgs& a, const Work& w, bool key, int64_t unit, int lane) {
     Share s;
     const int64_t group = unit % w.groups;
-    const int run = (int)(unit / w.groups);
-    s.key = run >= w.q_runs;
-    const int heads = s.key ? a.Hk : a.Hq;
-    s.h0 = (s.key ? run - w.q_runs : run) * w.per;
+    const int heads = key ? a.Hk : a.Hq;
+    s.h0 = (int)(unit / w.groups) * w.per;
     s.h1 = min(s.h0 + w.per, heads);
     int64_t token = group * kTok + lane / kRowLanes;
     s.live = token < a.tokens;
@@ -200,14 +201,16 @@ constexpr int kAhead = 4;          // heads whose loads are in flight together
 template <class T, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) qk_forward_kernel(const __grid_constant__ QkArgs a, const Work w) {
     const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (unit >= w.units) return;
-    const Share s = share_of(a, w, unit, lane);
+    int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (unit >= w.q_units + w.k_units) return;
+    const bool key = unit >= w.q_units;
+    if (key) unit -= w.q_units;
+    const Share s = share_of(a, w, key, unit, lane);
     int oa, ob;
     pieces<kInterleaved>(a.rot, lane, &oa, &ob);
     const int64_t step = a.n * kHeadDim;      // from head to head
-    const T* src = static_cast<const T*>(s.key ? a.k : a.q) + s.first;
-    T* dst = static_cast<T*>(s.key ? a.ko : a.qo) + s.first;
+    const T* src = static_cast<const T*>(key ? a.k : a.q) + s.first;
+    T* dst = static_cast<T*>(key ? a.ko : a.qo) + s.first;
     typename Io<T>::Raw raw[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) qk_forward_kernel(const __grid_const
     Turn<kInterleaved> turn;
     turn.template set<1>(a.freq, a.rot, s.pos, lane);
     F2 wt[4];
-    load_weight(static_cast<const T*>(s.key ? a.wk : a.wq), oa, ob, wt);
+    load_weight(static_cast<const T*>(key ? a.wk : a.wq), oa, ob, wt);
     for (int h = s.h0; h < s.h1; h += kAhead, src += kAhead * step, dst += kAhead * step) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
@@ -234,21 +237,26 @@ __global__ void __launch_bounds__(kThreads) qk_forward_kernel(const __grid_const
 
 constexpr int kAheadBack = 2;
 
+// A block takes units of the queries or of the keys alone, so that one weight and one sum of its
+// gradient are held.
 template <class T, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) qk_backward_kernel(const __grid_constant__ QkArgs a, const Work w) {
-    __shared__ float sums[kWarps][2 * kHeadDim];
+    __shared__ float sums[kWarps][kHeadDim];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool key = (int)blockIdx.x >= w.q_blocks;
+    const int block = key ? (int)blockIdx.x - w.q_blocks : (int)blockIdx.x, blocks = key ? w.k_blocks : w.q_blocks;
+    const int64_t units = key ? w.k_units : w.q_units, step = a.n * kHeadDim;
     int oa, ob;
     pieces<kInterleaved>(a.rot, lane, &oa, &ob);
-    const int64_t step = a.n * kHeadDim;
-    F2 gq[4], gk[4];                          // sums of the weights' gradients
+    F2 wt[4], acc[4];
+    load_weight(static_cast<const T*>(key ? a.wk : a.wq), oa, ob, wt);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) gq[j] = gk[j] = both(0.f);
-    for (int64_t unit = (int64_t)blockIdx.x * kWarps + warp; unit < w.units; unit += (int64_t)gridDim.x * kWarps) {
-        const Share s = share_of(a, w, unit, lane);
-        const T* x_row = static_cast<const T*>(s.key ? a.k : a.q) + s.first;
-        const T* g_row = static_cast<const T*>(s.key ? a.dko : a.dqo) + s.first;
-        T* d_row = static_cast<T*>(s.key ? a.ko : a.qo) + s.first;
+    for (int j = 0; j < 4; ++j) acc[j] = both(0.f);
+    for (int64_t unit = (int64_t)block * kWarps + warp; unit < units; unit += (int64_t)blocks * kWarps) {
+        const Share s = share_of(a, w, key, unit, lane);
+        const T* x_row = static_cast<const T*>(key ? a.k : a.q) + s.first;
+        const T* g_row = static_cast<const T*>(key ? a.dko : a.dqo) + s.first;
+        T* d_row = static_cast<T*>(key ? a.ko : a.qo) + s.first;
         typename Io<T>::Raw rx[kAheadBack], rg[kAheadBack];
 #pragma unroll
         for (int u = 0; u < kAheadBack; ++u)
@@ -258,10 +266,6 @@ __global__ void __launch_bounds__(kThreads) qk_backward_kernel(const __grid_cons
             }
         Turn<kInterleaved> turn;
         turn.template set<-1>(a.freq, a.rot, s.pos, lane);
-        F2 wt[4], acc[4];
-        load_weight(static_cast<const T*>(s.key ? a.wk : a.wq), oa, ob, wt);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = both(0.f);
         for (int h = s.h0; h < s.h1; h += kAheadBack) {
 #pragma unroll
             for (int u = 0; u < kAheadBack; ++u) {
@@ -279,92 +283,91 @@ __global__ void __launch_bounds__(kThreads) qk_backward_kernel(const __grid_cons
                 const float r = rsqrtf(row_dot(x, x) * (1.f / kHeadDim) + a.eps);
                 // xh mean(dn xh) = x r^2 (dn . x) / 64
                 const F2 m = both(row_dot(dn, x) * (-1.f / kHeadDim) * r * r), r2 = both(r);
-                F2 d[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    d[j] = mul(fma(x[j], m, dn[j]), r2);
-                    acc[j] = fma(g[j], mul(x[j], r2), acc[j]);
+                    dn[j] = mul(fma(x[j], m, dn[j]), r2);
+                    if (s.live) acc[j] = fma(g[j], mul(x[j], r2), acc[j]);
                 }
-                if (s.live) Io<T>::store(d_row, oa, ob, d);
+                if (s.live) Io<T>::store(d_row, oa, ob, dn);
                 x_row += step;
                 g_row += step;
                 d_row += step;
             }
-        }
-        const float to_q = s.live && !s.key ? 1.f : 0.f, to_k = s.live && s.key ? 1.f : 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (to_q != 0.f) gq[j] = fma(acc[j], both(to_q), gq[j]);
-            if (to_k != 0.f) gk[j] = fma(acc[j], both(to_k), gk[j]);
         }
     }
     if (!a.partial) return;
     // lanes of the four tokens, then the warps, in a fixed order
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        float2 q = un(gq[j]), k = un(gk[j]);
-        q.x += __shfl_xor_sync(kFull, q.x, 8);
-        q.y += __shfl_xor_sync(kFull, q.y, 8);
-        k.x += __shfl_xor_sync(kFull, k.x, 8);
-        k.y += __shfl_xor_sync(kFull, k.y, 8);
-        q.x += __shfl_xor_sync(kFull, q.x, 16);
-        q.y += __shfl_xor_sync(kFull, q.y, 16);
-        k.x += __shfl_xor_sync(kFull, k.x, 16);
-        k.y += __shfl_xor_sync(kFull, k.y, 16);
+        float2 v = un(acc[j]);
+        v.x += __shfl_xor_sync(kFull, v.x, 8);
+        v.y += __shfl_xor_sync(kFull, v.y, 8);
+        v.x += __shfl_xor_sync(kFull, v.x, 16);
+        v.y += __shfl_xor_sync(kFull, v.y, 16);
         if (lane < kRowLanes) {
             const int c = (j < 2 ? oa : ob) + 2 * (j & 1);
-            sums[warp][c] = q.x;
-            sums[warp][c + 1] = q.y;
-            sums[warp][kHeadDim + c] = k.x;
-            sums[warp][kHeadDim + c + 1] = k.y;
+            sums[warp][c] = v.x;
+            sums[warp][c + 1] = v.y;
         }
     }
     __syncthreads();
-    if (threadIdx.x < 2 * kHeadDim) {
+    if (threadIdx.x < kHeadDim) {
         float t = 0.f;
         for (int v = 0; v < kWarps; ++v) t += sums[v][threadIdx.x];
-        a.partial[(int64_t)blockIdx.x * 2 * kHeadDim + threadIdx.x] = t;
+        a.partial[(int64_t)blockIdx.x * kHeadDim + threadIdx.x] = t;
     }
 }
 
-// dw = the sum of the blocks' partial sums: 8 groups of threads take every eighth
-// block, then their sums are added in order.
+// dw = the sum of the blocks' partial sums (the queries' blocks, then the keys'): 8 groups of
+// threads take every eighth block, then their sums are added in order.
 constexpr int kFinishGroups = 8;
 template <class T>
 __global__ void __launch_bounds__(2 * kHeadDim * kFinishGroups)
-qk_weight_kernel(const float* partial, int64_t blocks, T* dwq, T* dwk) {
+qk_weight_kernel(const float* partial, int q_blocks, int k_blocks, T* dwq, T* dwk) {
     __shared__ float sums[kFinishGroups][2 * kHeadDim];
+    ptx::griddep_wait();
     const int c = threadIdx.x % (2 * kHeadDim), grp = threadIdx.x / (2 * kHeadDim);
+    const bool key = c >= kHeadDim;
+    const float* src = partial + (key ? (int64_t)q_blocks * kHeadDim : 0) + c % kHeadDim;
+    const int blocks = key ? k_blocks : q_blocks;
     float t = 0.f;
-    for (int64_t b = grp; b < blocks; b += kFinishGroups) t += partial[b * 2 * kHeadDim + c];
+#pragma unroll 8
+    for (int b = grp; b < blocks; b += kFinishGroups) t += src[(int64_t)b * kHeadDim];
     sums[grp][c] = t;
     __syncthreads();
     if (grp) return;
     t = 0.f;
     for (int k = 0; k < kFinishGroups; ++k) t += sums[k][c];
-    T* dst = c < kHeadDim ? dwq : dwk;
+    T* dst = key ? dwk : dwq;
     if (dst) dst[c % kHeadDim] = Io<T>::round(t);
 }
 
 constexpr int64_t kManyWarps = 152 * 48;     // warps that fill the GPU
+constexpr int64_t kBackBlocks = 152 * 2;     // the backward's blocks that run at once
 
 // A run is all the heads of a tensor where the tokens alone make enough warps, fewer (down to
 // one) where they do not.
-Work plan(int64_t tokens, int64_t Hq, int64_t Hk) {
+Work plan(int64_t tokens, int64_t Hq, int64_t Hk, bool backward) {
     Work w;
     w.groups = (tokens + kTok - 1) / kTok;
-    const int64_t runs = (kManyWarps + w.groups - 1) / w.groups;
+    const int64_t runs = ((backward ? 2 : 1) * kManyWarps + w.groups - 1) / w.groups;
     const int64_t per = (Hq + Hk + runs - 1) / runs, most = Hq > Hk ? Hq : Hk;
     w.per = (int32_t)(per < 1 ? 1 : per < most ? per : most);
-    w.q_runs = (int32_t)((Hq + w.per - 1) / w.per);
-    w.units = w.groups * (w.q_runs + (Hk + w.per - 1) / w.per);
+    w.q_units = w.groups * ((Hq + w.per - 1) / w.per);
+    w.k_units = w.groups * ((Hk + w.per - 1) / w.per);
+    // backward: as many blocks as run at once (each leaves a row of partial sums), their warps
+    // with the same number of units
+    const int64_t q = (w.q_units + kWarps - 1) / kWarps, k = (w.k_units + kWarps - 1) / kWarps;
+    const int64_t rounds = (q + k + kBackBlocks - 1) / kBackBlocks;
+    w.q_blocks = (int32_t)((q + rounds - 1) / rounds);
+    w.k_blocks = (int32_t)((k + rounds - 1) / rounds);
     return w;
 }
 
 template <class T>
 int forward_as(const QkArgs& a, bool interleaved, cudaStream_t stream) {
-    const Work w = plan(a.tokens, a.Hq, a.Hk);
-    const int64_t blocks = (w.units + kWarps - 1) / kWarps;
+    const Work w = plan(a.tokens, a.Hq, a.Hk, false);
+    const int64_t blocks = (w.q_units + w.k_units + kWarps - 1) / kWarps;
     if (blocks > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many rows");
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
@@ -377,8 +380,8 @@ int forward_as(const QkArgs& a, bool interleaved, cudaStream_t stream) {
 
 template <class T>
 int backward_as(const QkArgs& a, bool interleaved, void* dwq, void* dwk, cudaStream_t stream) {
-    const Work w = plan(a.tokens, a.Hq, a.Hk);
-    const int64_t blocks = qk_backward_blocks(a.tokens, a.Hq, a.Hk);
+    const Work w = plan(a.tokens, a.Hq, a.Hk, true);
+    const int blocks = w.q_blocks + w.k_blocks;
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
         if (interleaved) qk_backward_kernel<T, true><<<(unsigned)blocks, kThreads, 0, stream>>>(a, w);
@@ -389,20 +392,17 @@ int backward_as(const QkArgs& a, bool interleaved, void* dwq, void* dwk, cudaStr
     if (!dwq && !dwk) return DIFFUSER_OK;
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        qk_weight_kernel<T><<<1, 2 * kHeadDim * kFinishGroups, 0, stream>>>(a.partial, blocks, static_cast<T*>(dwq),
-                                                                           static_cast<T*>(dwk));
+        err = launch_pdl(qk_weight_kernel<T>, dim3(1), dim3(2 * kHeadDim * kFinishGroups), 0, stream, a.partial, w.q_blocks,
+                         w.k_blocks, static_cast<T*>(dwq), static_cast<T*>(dwk));
     }
-    err = cudaGetLastError();
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "qk_weight_kernel");
 }
 
 }  // namespace
 
-// at most four blocks on each of 152 SMs: each block leaves one row of partial sums
 int64_t qk_backward_blocks(int64_t tokens, int64_t Hq, int64_t Hk) {
-    const int64_t blocks = (plan(tokens, Hq, Hk).units + kWarps - 1) / kWarps;
-    const int64_t rounds = (blocks + 152 * 4 - 1) / (152 * 4);
-    return (blocks + rounds - 1) / rounds;     // the same number of units a warp, but for the last
+    const Work w = plan(tokens, Hq, Hk, true);
+    return w.q_blocks + w.k_blocks;
 }
 
 int launch_qk_norm_rope(const QkArgs& a, int32_t dtype, bool interleaved, cudaStream_t stream) {

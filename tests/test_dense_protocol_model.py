@@ -134,7 +134,7 @@ def test_split_protocol_completes(stages):
 
 
 def deal(longs, long_steps, shorts, short_steps, pairs):
-    """csrc/dense_pair.cu's deal_tiles and share_of: (first, count) of the long and short tiles of each pair."""
+    """csrc/dense_pair.cu's deal_tiles, long_tile and short_tile: the long and short tiles of each pair."""
     per, na = divmod(longs, pairs)
     nb = pairs - na
     load_b = per * long_steps
@@ -155,13 +155,12 @@ def deal(longs, long_steps, shorts, short_steps, pairs):
     as_, ar = divmod(to_a, na) if na else (0, 0)
     out = []
     for p in range(pairs):
-        nl, l0 = per + (p < na), p * per + min(p, na)
+        long = [k * pairs + p for k in range(per + (p < na))]
         if p < na:
-            ns, s0 = as_ + (p < ar), p * as_ + min(p, ar)
+            short = [k * na + p for k in range(as_ + (p < ar))]
         else:
-            i = p - na
-            ns, s0 = bs + (i < br), na * as_ + ar + i * bs + min(i, br)
-        out.append((l0, nl, s0, ns))
+            short = [na * as_ + ar + k * nb + p - na for k in range(bs + (p - na < br))]
+        out.append((long, short))
     return out
 
 
@@ -175,12 +174,9 @@ def test_gradient_tiles_are_dealt_once_and_evenly(pairs):
         short_steps = short_steps if short_steps > 1 else rng.randint(1, long_steps)
         n = min(pairs, longs + shorts)
         shares = deal(longs, long_steps, shorts, short_steps, n)
-        at_l = at_s = 0
-        for l0, nl, s0, ns in shares:                    # one after the other: every tile once
-            assert (l0, s0) == (at_l, at_s) and nl >= 0 and ns >= 0
-            at_l, at_s = at_l + nl, at_s + ns
-        assert (at_l, at_s) == (longs, shorts)
-        most = max(nl * long_steps + ns * short_steps for _, nl, _, ns in shares)
+        assert sorted(t for long, _ in shares for t in long) == list(range(longs))      # every tile once
+        assert sorted(t for _, short in shares for t in short) == list(range(shorts))
+        most = max(len(long) * long_steps + len(short) * short_steps for long, short in shares)
         loads = [0] * n                                  # the same by the greedy rule
         for steps, count in ((long_steps, longs), (short_steps, shorts)):
             for _ in range(count):
