@@ -426,6 +426,44 @@ def test_qk_rows_of_zeros_and_extremes(dl):
         assert torch.isfinite(grads[0]).all() and torch.isfinite(grads[1]).all()
 
 
+@pytest.mark.parametrize("shape", [(3, 65536, 8), (70, 65536, 16), (3, 8, 65536), (70, 8, 65536), (270, 24, 32776)], ids=str)
+def test_widest(dl, shape):
+    T, D, F = shape
+    X, W, b = linear_inputs(T, D, F, seed=F)
+    W2, dY, code = draw(3, 2 * F, D, scale=D ** -0.5), draw(F + 7, T, F), dl.DIFFUSER_ACT_SILU
+    Y, pre = dl.diffuser_linear(X, W, bias=b, activation=code, save_pre=True)
+    p = X.double() @ W.double().T + b.double()
+    dp = 2 * (D + 2) * E * (X.double().abs() @ W.double().abs().T + b.double().abs())
+    within(pre, p, U * p.abs() + (1 + U) * dp, "pre")
+    near(Y, act64("silu", p), "Y")
+    ws = torch.empty(dl.diffuser_linear_backward_workspace_size(T, D, F, code), dtype=torch.uint8, device="cuda")
+    check_linear_backward(X, W, dY, pre, "silu", *dl.diffuser_linear_backward(X, W, dY, pre=pre, activation=code,
+                                                                              workspace=ws if ws.numel() else None))
+    H, gu = dl.diffuser_gated_linear(X, W2, save_pre=True)
+    q = X.double() @ W2.double().T
+    near(H, act64("silu", q[:, :F]) * q[:, F:], "H")
+    dX, dW = dl.diffuser_gated_linear_backward(X, W2, dY, gu)
+    g, u, d = gu.double()[:, :F], gu.double()[:, F:], dY.double()
+    dP = torch.cat((d * u * slope64("silu", g), d * act64("silu", g)), -1)
+    near(dX, dP @ W2.double(), "gated dX")
+    near(dW, dP.T @ X.double(), "gated dW")
+
+
+def test_qk_of_many_heads(dl):
+    q, k = draw(1, 1, 4096, 3, 64), draw(2, 1, 2, 3, 64)
+    w = draw(3, 64, mean=1.0)
+    Qo, Ko = dl.diffuser_qk_norm_rope(q, k, w, w, position_offset=77)
+    for h in (0, 1, 2047, 4095):
+        one = q[:, h:h + 1].contiguous()
+        assert torch.equal(Qo[:, h:h + 1], dl.diffuser_qk_norm_rope(one, one.clone(), w, w, position_offset=77)[0])
+    dQ, _, dw, _ = dl.diffuser_qk_norm_rope_backward(q, k, Qo, Ko, w, w, position_offset=77)
+    # dy = y: g is the normed and weighted row, so dw = sum of w xh^2
+    xh = norm64(q.double(), None, 1e-6)
+    ref = (w.double() * xh.square()).sum((0, 1, 2))
+    mag = ref.abs()
+    within(dw, ref, U * mag + 2 * U * mag, "dw")          # its own rounding, and that of y
+
+
 # ------------------------------------------------------------------ where they write
 def guarded(rows, width, dtype=torch.bfloat16, fill=7.0):
     """A [rows][width] buffer between rows of `fill`, and a check that those are as they were."""
