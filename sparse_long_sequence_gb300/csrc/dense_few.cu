@@ -144,6 +144,7 @@ dense_few_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         for (int c0 = (warp >> 2) * 16; c0 < a.bn; c0 += 32) {
             float v[16];
+            __syncwarp();
             ptx::tmem_ld16(tmem + lane_base + c0, v);
 #pragma unroll
             for (int c = 0; c < 16; ++c) part[(c0 + c) * kTI + quad * 32 + lane] = v[c];

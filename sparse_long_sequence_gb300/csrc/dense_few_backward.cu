@@ -180,7 +180,6 @@ __global__ void __launch_bounds__(kThreads) few_backward_kernel(const FewBackArg
         }
         *reinterpret_cast<__nv_bfloat162*>(a.dx + (int64_t)t * a.D + d) = __floats2bfloat162_rn(s.x, s.y);
     }
-    __syncwarp();
     ptx::cluster_sync();                                     // nobody leaves while its sums are read
 }
 

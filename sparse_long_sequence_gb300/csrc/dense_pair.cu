@@ -80,10 +80,12 @@ __device__ __forceinline__ Tile tile_at(const PairArgs& a, int t, int width) {
     return {(grp * kGroupTiles + in % rows) * kTI, in / rows * width};
 }
 
-// 32 neighbouring columns of a lane's row as 16 packed pairs.
+// 32 neighbouring columns of a lane's row as 16 packed pairs.  (tcgen05.ld is a warp's instruction,
+// and lane 0 comes from issuing copies.)
 using packed::F2;
 __device__ __forceinline__ void load_acc(uint32_t taddr, F2 (&v)[16]) {
     uint32_t r[32];
+    __syncwarp();
     ptx::tmem_ld32_issue(taddr, r);
     ptx::tmem_ld_wait32(r);
 #pragma unroll
@@ -364,7 +366,6 @@ dense_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         }
         if (lead) ptx::bulk_wait<0>();
     }
-    __syncwarp();
     ptx::tc_fence_before();
     ptx::cluster_sync();
     if (warp == 1) {
@@ -515,6 +516,7 @@ dense_grads_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
                     for (int64_t k = w; k < g.bias.chunks; k += kEpiWarps) t += g.bias.partial[k * g.bias.F + col];
                 }
                 sums[w * 32 + lane] = t;
+                __syncwarp();                                  // (the last columns' lanes and the others)
                 ptx::named_barrier_sync(1, 32 * kEpiWarps);
                 if (w == 0 && col < g.bias.F) {
                     t = 0.f;
@@ -522,6 +524,7 @@ dense_grads_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
                     for (int k = 0; k < kEpiWarps; ++k) t += sums[k * 32 + lane];
                     g.bias.out[col] = __float2bfloat16_rn(t);
                 }
+                __syncwarp();
                 ptx::named_barrier_sync(1, 32 * kEpiWarps);
             }
         }
@@ -557,7 +560,6 @@ dense_grads_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_consta
         }
         if (lead) ptx::bulk_wait<0>();
     }
-    __syncwarp();
     ptx::tc_fence_before();
     ptx::cluster_sync();
     if (warp == 1) {
@@ -665,13 +667,13 @@ dense_pair_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_co
 #pragma unroll 1
         for (int c0 = half * kBn / 2; c0 < (half + 1) * kBn / 2; c0 += 32) {
             float v[32];
+            __syncwarp();
             ptx::tmem_ld32(tmem + lane_base + c0, v);
 #pragma unroll
             for (int c = 0; c < 32; c += 4)
                 *reinterpret_cast<float4*>(row + (c0 + c) * 4) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
         }
     }
-    __syncwarp();
     ptx::tc_fence_before();
     ptx::cluster_sync();
     if (warp == 1) {
@@ -715,7 +717,6 @@ dense_pair_split_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_co
             store4(r.out + i * a.J + j, v);
         }
     }
-    __syncwarp();
     ptx::cluster_sync();                               // nobody leaves while its partial is read
 }
 

@@ -17,8 +17,10 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-// All threads of all the cluster's CTAs; writes before it are visible after it.
+// All threads of all the cluster's CTAs; writes before it are visible after it.  The instruction
+// is a warp's (.aligned): lanes that left a branch or a loop at different times meet first.
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The shared::cluster address of `saddr` (this CTA's shared address) in CTA `rank`.
