@@ -410,10 +410,11 @@ DIFFUSER_API int diffuser_layer_forward(const void* X, const void* Wqkv, const v
  *   eps         > 0;  theta  >= 1;  rotary_dim  0, 16, 32, 48 or 64
  *   positions   device int64 [B][n], any values; NULL: token i is at position i
  *   position_offset      added to every position (a prompt's continuation, a
- *               single new token)
+ *               single new token); the sums are int64 (they wrap beyond)
  *   B, n >= 0;  Hq, Hk 1..4096
- * Angles are exact in the position (integer arithmetic modulo one turn); all else
- * is fp32 with one rounding to dtype.  Errors: INVALID_ARG, UNSUPPORTED (d, dtype,
+ * Angles are integer arithmetic modulo one turn, within 2^-31 turns for any position,
+ * before their cosine and sine are taken in fp32; all else is fp32 with one rounding to
+ * dtype.  Errors: INVALID_ARG, UNSUPPORTED (d, dtype,
  * rotary_dim), OVERFLOW, CUDA.
  */
 DIFFUSER_API int diffuser_qk_norm_rope(const void* Q, const void* K, int32_t dtype, int64_t B, int64_t Hq,

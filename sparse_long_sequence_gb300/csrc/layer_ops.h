@@ -52,7 +52,8 @@ struct QkArgs {
     int32_t rot;                    // rotated features: 0, 16, 32, 48, 64
     float eps;
     float* partial;                 // backward: [blocks][64] sums of the weights' gradients, or null
-    uint64_t freq[kHeadDim / 2];    // turns per position of pair i, in units of 2^-64
+    // turns per position of pair i, in units of 2^-64, and what is left of it, of 2^-128
+    uint64_t freq[kHeadDim / 2], freq_low[kHeadDim / 2];
 };
 int launch_qk_norm_rope(const QkArgs& a, int32_t dtype, bool interleaved, cudaStream_t stream);
 // blocks of the backward kernel (rows of `partial`)

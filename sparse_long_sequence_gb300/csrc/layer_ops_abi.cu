@@ -7,6 +7,7 @@
 #include <cstring>
 
 #include "layer_ops.h"
+#include "turns.h"
 
 namespace dfs {
 namespace {
@@ -59,21 +60,6 @@ int check_qk(int32_t dtype, int64_t B, int64_t Hq, int64_t Hk, int64_t n, int32_
     return DIFFUSER_OK;
 }
 
-// theta^(-2i/rot) / (2 pi) turns per position, in units of 2^-64 turns: one power, then products
-// of 64-bit fractions, each rounded to 2^-64 (a long double is emulated on Arm: 32 products of
-// it took 0.8 us)
-void set_turns(QkArgs* a, double theta) {
-    if (!a->rot) return;
-    const long double ratio = std::ldexp(std::pow((long double)theta, -2.0L / a->rot), 64);
-    const bool one = theta == 1.0;                           // (the ratio itself does not fit)
-    const uint64_t r = one ? 0 : (uint64_t)(ratio + 0.5L);
-    uint64_t f = 2935890503282001226u;                       // 2^64 / (2 pi)
-    for (int i = 0; i < a->rot / 2; ++i) {
-        a->freq[i] = f;
-        if (!one) f = (uint64_t)(((unsigned __int128)f * r + (uint64_t(1) << 63)) >> 64);
-    }
-}
-
 QkArgs qk_args(const void* Q, const void* K, int64_t B, int64_t Hq, int64_t Hk, int64_t n, const void* wq, const void* wk,
                float eps, double theta, int32_t rot, const int64_t* pos, int64_t pos0) {
     QkArgs a{};
@@ -89,7 +75,7 @@ QkArgs qk_args(const void* Q, const void* K, int64_t B, int64_t Hq, int64_t Hk, 
     a.Hk = (int32_t)Hk;
     a.rot = rot;
     a.eps = eps;
-    set_turns(&a, theta);
+    if (rot) turns::fill(a.freq, a.freq_low, theta, rot);
     return a;
 }
 

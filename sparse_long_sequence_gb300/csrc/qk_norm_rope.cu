@@ -12,9 +12,11 @@
 // depend on the token alone.  A lane holds two pieces of four features, chosen so that it has
 // both features of each of its pairs (split halves: pieces t and t + rot / 8): the rotation
 // needs no exchange between lanes.  Arithmetic on packed pairs of fp32 (f32x2).
-// The angle is exact integer arithmetic: theta^(-2i/rot) / (2 pi), in units of 2^-64 turns,
-// times the position modulo 2^64 leaves the fraction of a turn, so far positions lose nothing
-// (a float product would be off by p 2^-24 radians).
+// The angle is integer arithmetic modulo a turn: |p| times theta^(-2i/rot) / (2 pi), a 128-bit
+// fraction (turns.h), of which positions below 2^32 need the upper half alone.  Its upper 32 bits
+// are used: within 2^-31 turns for any 64-bit position (with a 64-bit fraction throughout the
+// worst pair was off by 1e-4 radians at 2^48, a float product would be by p 2^-24).  Both halves
+// for all positions cost 1 us of 10 at 2 x 24 heads x 4096 tokens.
 // Bound by HBM: every row is read and written once (backward: two reads).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -109,18 +111,29 @@ struct Turn {
     F2 c[kInterleaved ? 4 : 2], s[kInterleaved ? 4 : 2];
 
     template <int kSign>
-    __device__ __forceinline__ void set(const uint64_t* freq, int rot, int64_t pos, int lane) {
+    __device__ __forceinline__ void set(const QkArgs& a, int64_t pos, int lane) {
         const int t = lane & (kRowLanes - 1);
+        const bool turned = t < a.rot / 8;
+        const uint64_t far = pos < 0 ? 0 - (uint64_t)pos : (uint64_t)pos;
+        uint32_t phase[4] = {0, 0, 0, 0};        // |pos| turns modulo one, in units of 2^-32
+        if (turned) {
+            if (far >> 32) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    phase[j] = (uint32_t)((far * a.freq[4 * t + j] + __umul64hi(far, a.freq_low[4 * t + j])) >> 32);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) phase[j] = (uint32_t)(far * a.freq[4 * t + j] >> 32);
+            }
+        }
+        const float unit = (pos < 0) == (kSign < 0) ? 4.656612873077393e-10f : -4.656612873077393e-10f;   // +- 2^-31
         float cs[4], sn[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             cs[j] = 1.f;
             sn[j] = 0.f;
-            if (t < rot / 8) {
-                // the fraction of a turn, in [-1/2, 1/2), times 2: sincospi's unit
-                const uint64_t phase = (uint64_t)pos * freq[4 * t + j];
-                sincospif((float)(int32_t)(phase >> 32) * (kSign * 4.656612873077393e-10f), &sn[j], &cs[j]);   // 2^-31
-            }
+            // the fraction of a turn, in [-1/2, 1/2), times 2: sincospi's unit
+            if (turned) sincospif((float)(int32_t)phase[j] * unit, &sn[j], &cs[j]);
         }
         if constexpr (kInterleaved) {
 #pragma unroll
@@ -192,7 +205,7 @@ __device__ __forceinline__ Share share_of(const QkArgs& a, const Work& w, bool k
     if (!s.live) token = a.tokens - 1;        // (loads stay in bounds)
     const int64_t b = token / a.n, i = token - b * a.n;
     s.first = ((b * heads + s.h0) * a.n + i) * kHeadDim;
-    s.pos = a.pos0 + (a.pos ? a.pos[token] : i);
+    s.pos = (int64_t)((uint64_t)a.pos0 + (uint64_t)(a.pos ? a.pos[token] : i));
     return s;
 }
 
@@ -216,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) qk_forward_kernel(const __grid_const
     for (int u = 0; u < kAhead; ++u)
         if (s.h0 + u < s.h1) raw[u] = Io<T>::load(src + u * step, oa, ob);
     Turn<kInterleaved> turn;
-    turn.template set<1>(a.freq, a.rot, s.pos, lane);
+    turn.template set<1>(a, s.pos, lane);
     F2 wt[4];
     load_weight(static_cast<const T*>(key ? a.wk : a.wq), oa, ob, wt);
     for (int h = s.h0; h < s.h1; h += kAhead, src += kAhead * step, dst += kAhead * step) {
@@ -267,7 +280,7 @@ __global__ void __launch_bounds__(kThreads) qk_backward_kernel(const __grid_cons
                 rg[u] = Io<T>::load(g_row + u * step, oa, ob);
             }
         Turn<kInterleaved> turn;
-        turn.template set<-1>(a.freq, a.rot, s.pos, lane);
+        turn.template set<-1>(a, s.pos, lane);
         for (int h = s.h0; h < s.h1; h += kAheadBack) {
 #pragma unroll
             for (int u = 0; u < kAheadBack; ++u) {
