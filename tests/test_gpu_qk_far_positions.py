@@ -86,3 +86,20 @@ def test_offset_alone(dl):
         got = dl.diffuser_qk_norm_rope(q, k, position_offset=p, eps=1e-30)
         for g, ref in zip(got, expected(64, False, 10000.0, [p])):
             assert np.abs(g.double().cpu().numpy() - ref).max() <= TOL
+
+
+def test_digits_near_quarter_turns(dl):
+    # sines near half turns and cosines near odd quarter turns are small: they keep their digits.
+    # Within 2^-31 turns and eight fp32 steps of the value: the angle's own rounding, the sine's, the
+    # norm's and three products'.
+    p = np.arange(1, 1 << 21)
+    part = p / (2 * np.pi) % 0.25
+    at = [int(x) for x in p[np.minimum(part, 0.25 - part) < 2.0 ** -13]][:800]
+    assert 355 in at and 11 not in at and len(at) > 300
+    q, k = unit_rows(16, False, len(at), 0), unit_rows(16, False, len(at), 1)
+    pos = torch.tensor([at], dtype=torch.int64, device="cuda")
+    for sign in (1, -1):
+        got = dl.diffuser_qk_norm_rope(q, k, positions=sign * pos, eps=1e-30, theta=1.0, rotary_dim=16)
+        for g, ref in zip(got, expected(16, False, 1.0, [sign * a for a in at])):
+            err = np.abs(g.double().cpu().numpy() - ref) - 8 * 2 * np.pi * 2.0 ** -31 - 8 * E * np.abs(ref)
+            assert err.max() <= 0, err.max()
