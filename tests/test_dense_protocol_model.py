@@ -1,5 +1,5 @@
 """Host models of the dense products' mbarrier protocols (csrc/dense_pair.cu and
-csrc/dense_split.cu), played out by tests/barrier_model.py: every role must finish for any
+csrc/dense_few.cu), played out by tests/barrier_model.py: every role must finish for any
 tile and K-step count, and no wait may find its barrier two phases ahead.  They check the
 protocols as designed; keeping them in step with the kernels is a review duty whenever
 either changes.
