@@ -11,6 +11,11 @@
 //      weight gradient 4096 x 1024 over 32768 tokens: 148 us at 256, 209 at 128, 173 at 256 x 2
 //      input gradient 1024 <- 4096 of 1024 tokens: 12.1 us at 128 x 2, 14.6 at 128, 22.0 at 256
 //      forward 768 -> 768 of 4096 tokens: 9.1 us at 256, 9.7 at 128, 19.4 at 256 x 2
+//    It knows no epilogue, which costs either width about as much, so that the measured times lie
+//    above it; with bias and residual, or activation and kept pre-activations:
+//      forward 768 -> 768 of 8192 tokens, residual: 15.1 us at 256, 15.3 at 128 (without an epilogue
+//      13.4 and 12.6; estimated 10.2 and 9.5, so 128 is taken: three rounds of 192 tiles)
+//      forward 512 -> 2048 of 32768 tokens, gelu, kept: 63.9 us at 256, 70.9 at 128 (48.4 and 59.2)
 #include "layer_ops.h"
 
 namespace dfs {

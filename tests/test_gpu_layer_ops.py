@@ -6,7 +6,8 @@ e = 2^-24 half an fp32 step):
   * a dot product of K bf16 products in fp32, in any order, with truncating adders:
     at most 2 K e of the sum of the magnitudes;
   * activations: slopes at most 1.13 in magnitude, values and slopes computed within
-    2^-18 (|p| + 1): 2^-20 of the exponential and reciprocal, times |p| in the slope;
+    2^-18 (|p| + 1): 2^-20 + 2^-24 |p| of the exponential and reciprocal, relative to a factor
+    that falls as exp(-|p|) (the second part stays under 2^-25), times |p| in the slope;
   * an element of a product whose left operand was rounded to bf16 (the backward with an
     activation): additionally u times the sum of the magnitudes.  That is the worst case;
     the roundings are independent, so the 2-norm of the error stays under 1.5 u of the
