@@ -516,6 +516,118 @@ DIFFUSER_API int diffuser_gated_linear_backward(const void* X, const void* Wgu, 
                                                 int32_t activation, void* dX, void* dWgu, void* workspace,
                                                 size_t workspace_bytes, diffuser_stream stream);
 
+/* ---------------------------------------------------------------- rotation alone
+ *
+ * Positions for contexts longer than a model was trained on: the frequencies of a scaling,
+ * made once on the host, and the rotation of queries and keys by them, without norms.
+ * Streams, captures, alignment and overlaps as for the operators around the module.
+ */
+
+/* How frequencies theta^(-2i / rotary_dim) are scaled for contexts `factor` times the trained one. */
+typedef enum {
+    DIFFUSER_ROPE_NONE = 0,
+    DIFFUSER_ROPE_LINEAR = 1,     /* positions interpolated: every frequency over factor */
+    DIFFUSER_ROPE_NTK = 2,        /* theta factor^(r / (r - 2)) in place of theta, r = rotary_dim */
+    DIFFUSER_ROPE_YARN = 3        /* by parts: kept where the trained context holds 32 turns or more,
+                                     over factor where it holds 1 or less, linear in the turns between */
+} diffuser_rope_scaling;
+
+/*
+ * The rotary_dim / 2 frequencies of a scaling (host, radians per position) and the magnitude
+ * of the turned features (YaRN: 1 + 0.1 ln factor; the others: 1).  rotary_dim 16, 32, 48 or
+ * 64; theta >= 1; factor >= 1 (not read with NONE); original_length > 0, the trained context
+ * in tokens (read with YARN alone).  Nothing touches a device.  Errors: INVALID_ARG, UNSUPPORTED.
+ */
+DIFFUSER_API int diffuser_rope_frequencies(int32_t scaling, double theta, int32_t rotary_dim, double factor,
+                                           double original_length, double* frequencies, double* magnitude);
+
+/*
+ * Every row x of 64 features (a token of a head) becomes y = magnitude R(p) x on its first
+ * rotary_dim features; the others are copied.  R(p) turns pair i by p frequencies[i] radians,
+ * pairs, positions and in-place use as for diffuser_qk_norm_rope.
+ *   Q, Qo   device [B][Hq][n][64] in dtype;   K, Ko   device [B][Hk][n][64] in dtype
+ *   frequencies   HOST, rotary_dim / 2 values in [0, 4], read before the call returns
+ *   rotary_dim    16, 32, 48 or 64;   magnitude > 0
+ * Angles are integer arithmetic modulo one turn, within 2^-31 turns for the given frequency
+ * and any position; all else fp32 with one rounding to dtype.
+ * Errors: as diffuser_qk_norm_rope.
+ */
+DIFFUSER_API int diffuser_rope(const void* Q, const void* K, int32_t dtype, int64_t B, int64_t Hq, int64_t Hk,
+                               int64_t n, int32_t d, const double* frequencies, int32_t rotary_dim,
+                               int32_t interleaved, float magnitude, const int64_t* positions,
+                               int64_t position_offset, void* Qo, void* Ko, diffuser_stream stream);
+/* Its gradients: dx = magnitude R(-p) dy on the turned features (dQ may be dQo itself, dK dKo). */
+DIFFUSER_API int diffuser_rope_backward(const void* dQo, const void* dKo, int32_t dtype, int64_t B, int64_t Hq,
+                                        int64_t Hk, int64_t n, int32_t d, const double* frequencies,
+                                        int32_t rotary_dim, int32_t interleaved, float magnitude,
+                                        const int64_t* positions, int64_t position_offset, void* dQ, void* dK,
+                                        diffuser_stream stream);
+
+/* ---------------------------------------------------------------- attention over chosen blocks
+ *
+ * Sparsity that the data chooses, next to the fixed graphs: each query attends to the keys of
+ * up to top_k blocks of 64 keys, which a cheap score picks for it.  The means of key blocks,
+ * the choice, the attention and its backward pass are calls of their own; a serving step is the
+ * first three on a cache.  bf16 tensors, 64 features, fp32 arithmetic around the products.
+ *
+ * Queries [B][Hq][n][64] meet keys [B][Hk][m][64], Hq a multiple of Hk: the G = Hq / Hk query heads
+ * of a key head share its keys and its blocks.  With a cache m is its capacity.
+ *   lengths   device int32 [B], keys of each sequence, taken into [0, m]; NULL: m.  Keys behind a
+ *             length are not read.
+ *   starts    device int32 [B], the position of each sequence's query 0; NULL: length - n (the
+ *             queries are the last tokens).
+ * Query i of sequence b is at position p = start + i.  With 0 <= p < length it sees the keys up to p
+ * (causal != 0) or all below the length; otherwise none: its list is empty, its result 0.
+ * B >= 0, n and m 0..2^20, Hq 1..4096, top_k 1..64, d 64.  Tensors are contiguous and 16-byte aligned
+ * (lengths, starts: 4), on the current device; outputs overlap nothing else.  Calls are asynchronous on
+ * `stream`, may be captured, use no atomics on results (repeated calls give identical bits).
+ * Errors: INVALID_ARG, UNSUPPORTED, OVERFLOW, CUDA, and WORKSPACE where there is one.
+ */
+
+/*
+ * means[b][h][c] = the mean of block c's keys below the length (fp32 sums, one rounding): bf16
+ * [B][Hk][ceil(m / 64)][64].  recent 0: every block that has such keys; recent > 0: those alone
+ * that hold some of the sequence's last `recent` keys (the step after appending them).  Other
+ * blocks' means are left as they were.
+ */
+DIFFUSER_API int diffuser_block_means(const void* K, int64_t B, int64_t Hk, int64_t m, int32_t d,
+                                      const int32_t* lengths, int64_t recent, void* means,
+                                      diffuser_stream stream);
+
+/*
+ * For each query and key head, the blocks with visible keys that score highest,
+ *   score(i, c) = sum over the group's heads of q_i . means_c
+ * as if computed without rounding (ties: the lowest index; NaN counts as -infinity):
+ *   blocks   int32 [B][Hk][n][top_k], ascending, -1 behind the last
+ * The first sink_blocks blocks, and those less than local_blocks from the query's own (1: its own
+ * alone; causal: none after it), come before all others where they are visible; they count towards
+ * top_k, and more of them than top_k are refused.
+ * means are read for visible blocks alone.
+ */
+DIFFUSER_API int diffuser_select_blocks(const void* Q, const void* means, int64_t B, int64_t Hq, int64_t Hk,
+                                        int64_t n, int64_t m, int32_t d, int32_t top_k, int32_t sink_blocks,
+                                        int32_t local_blocks, int32_t causal, const int32_t* lengths,
+                                        const int32_t* starts, int32_t* blocks, diffuser_stream stream);
+
+/*
+ * out_i = sum_j A_ij v_j,  A_ij = exp(q_i.k_j / sqrt(d) - lse_i) over the visible keys j of the
+ * blocks that query i lists; a query without such keys: out 0, lse -infinity.
+ *   blocks   int32 [B][Hk][n][top_k], any values: an entry counts if it is above every entry before
+ *            it, is not negative and has visible keys; others are skipped
+ *   out      bf16 [B][Hq][n][64], rounded once from fp32 (the weights are rounded to bf16 as operands
+ *            of the tensor cores; their sum is taken before that)
+ *   lse      fp32 [B][Hq][n] or NULL: log of the sum of exp(q_i.k_j / sqrt(d)), for the backward
+ *   workspace   diffuser_selected_attention_workspace_size bytes, 256-byte aligned (0: NULL will do)
+ * Infinities and NaN among the keys that a query sees reach its result.
+ */
+DIFFUSER_API int diffuser_selected_attention_workspace_size(int64_t B, int64_t Hq, int64_t Hk, int64_t n,
+                                                            int64_t m, int32_t d, int32_t top_k, size_t* bytes);
+DIFFUSER_API int diffuser_selected_attention(const void* Q, const void* K, const void* V, const int32_t* blocks,
+                                             int64_t B, int64_t Hq, int64_t Hk, int64_t n, int64_t m, int32_t d,
+                                             int32_t top_k, int32_t causal, const int32_t* lengths,
+                                             const int32_t* starts, void* out, float* lse, void* workspace,
+                                             size_t workspace_bytes, diffuser_stream stream);
+
 /* ---------------------------------------------------------------- no-allocation forward */
 
 /*

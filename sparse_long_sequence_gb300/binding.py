@@ -101,6 +101,18 @@ def _load() -> ctypes.CDLL:
         "diffuser_gated_linear_backward_workspace_size": (c.c_int, [i64, i32, i32, c.POINTER(c.c_size_t)]),
         "diffuser_gated_linear_backward": (c.c_int, [vp, vp, vp, vp, i64, i32, i32, i32, vp, vp, vp, c.c_size_t,
                                                      vp]),
+        "diffuser_rope_frequencies": (c.c_int, [i32, c.c_double, i32, c.c_double, c.c_double, c.POINTER(c.c_double),
+                                                c.POINTER(c.c_double)]),
+        "diffuser_rope": (c.c_int, [vp, vp, i32, i64, i64, i64, i64, i32, c.POINTER(c.c_double), i32, i32, f32, vp, i64,
+                                    vp, vp, vp]),
+        "diffuser_rope_backward": (c.c_int, [vp, vp, i32, i64, i64, i64, i64, i32, c.POINTER(c.c_double), i32, i32, f32,
+                                             vp, i64, vp, vp, vp]),
+        "diffuser_block_means": (c.c_int, [vp, i64, i64, i64, i32, vp, i64, vp, vp]),
+        "diffuser_select_blocks": (c.c_int, [vp, vp, i64, i64, i64, i64, i64, i32, i32, i32, i32, i32, vp, vp, vp, vp]),
+        "diffuser_selected_attention_workspace_size": (c.c_int, [i64, i64, i64, i64, i64, i32, i32,
+                                                                 c.POINTER(c.c_size_t)]),
+        "diffuser_selected_attention": (c.c_int, [vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, i32, i32, vp, vp, vp, vp,
+                                                  vp, c.c_size_t, vp]),
         "diffuser_graph_status": (c.c_int, [vp, c.POINTER(c.c_int), c.c_int]),
         "diffuser_graph_set_status": (c.c_int, [vp, c.c_int]),
         "diffuser_launch_count": (c.c_int64, [i64p]),
@@ -701,6 +713,152 @@ def diffuser_gated_linear_backward(X, Wgu, dH, pre, activation: int = DIFFUSER_A
         x, w, _need(dH, "dH", out, dev, bf), _need(pre, "pre", both, dev, bf), T, D, F, activation, dx, dw,
         ws_ptr, ws_bytes, stream), "diffuser_gated_linear_backward")
     return dX, dWgu
+
+
+# ---------------------------------------------------------------- rotation alone
+DIFFUSER_ROPE_NONE, DIFFUSER_ROPE_LINEAR, DIFFUSER_ROPE_NTK, DIFFUSER_ROPE_YARN = 0, 1, 2, 3
+
+
+def diffuser_rope_frequencies(rotary_dim: int = 64, theta: float = 10000.0, scaling: int = DIFFUSER_ROPE_NONE,
+                              factor: float = 1.0, original_length: float = 0.0):
+    """(frequencies, magnitude) of a scaling for contexts `factor` times the trained one
+    (YaRN: of original_length tokens): a ctypes array of rotary_dim / 2 doubles, radians per
+    position, and the factor of the turned features.  Made once, then given to diffuser_rope."""
+    if not 0 <= rotary_dim <= 64:
+        raise ValueError(f"rotary_dim must lie in [1, 64], not {rotary_dim}")
+    freq, mag = (ctypes.c_double * (rotary_dim // 2))(), ctypes.c_double()
+    _check(_lib.diffuser_rope_frequencies(scaling, theta, rotary_dim, factor, original_length, freq, ctypes.byref(mag)),
+           "diffuser_rope_frequencies")
+    return freq, mag.value
+
+
+def _frequencies(f):
+    """Frequencies as a ctypes array of doubles, and the features that they turn."""
+    if not isinstance(f, ctypes.Array) or f._type_ is not ctypes.c_double:
+        f = (ctypes.c_double * len(f))(*f)
+    return f, 2 * len(f)
+
+
+def _rope(fn, name, names, Q, K, frequencies, magnitude, interleaved, positions, position_offset, Qo, Ko, stream):
+    import torch
+    code, B, Hq, Hk, n, d = _qk_shapes(Q, K)
+    dev, dt = Q.get_device(), Q.dtype
+    freq, rot = _frequencies(frequencies)
+    q, k = _flat(Q, names[0], dev, dt), _flat(K, names[1], dev, dt)
+    (Qo, qo), (Ko, ko) = _out(Qo, names[2], Q.shape, Q), _out(Ko, names[3], K.shape, K)
+    _check(fn(q, k, code, B, Hq, Hk, n, d, freq, rot, int(interleaved), magnitude,
+              _may(positions, "positions", (B, n), dev, torch.int64), position_offset, qo, ko, stream), name)
+    return Qo, Ko
+
+
+@_on_stream
+def diffuser_rope(Q, K, frequencies, magnitude: float = 1.0, interleaved: bool = False, positions=None,
+                  position_offset: int = 0, Qo=None, Ko=None, stream=None):
+    """The position rotation alone of Q [B][Hq][n][64] and K [B][Hk][n][64]: the first
+    2 len(frequencies) features of every row turned by position times frequency and multiplied
+    by magnitude; positions as for diffuser_qk_norm_rope.  Qo=Q and Ko=K work in place."""
+    return _rope(_lib.diffuser_rope, "diffuser_rope", ("Q", "K", "Qo", "Ko"), Q, K, frequencies, magnitude, interleaved,
+                 positions, position_offset, Qo, Ko, stream)
+
+
+@_on_stream
+def diffuser_rope_backward(dQo, dKo, frequencies, magnitude: float = 1.0, interleaved: bool = False, positions=None,
+                           position_offset: int = 0, dQ=None, dK=None, stream=None):
+    """Gradients (dQ, dK) of diffuser_rope.  dQ=dQo and dK=dKo work in place."""
+    return _rope(_lib.diffuser_rope_backward, "diffuser_rope_backward", ("dQo", "dKo", "dQ", "dK"), dQo, dKo, frequencies,
+                 magnitude, interleaved, positions, position_offset, dQ, dK, stream)
+
+
+# ---------------------------------------------------------------- attention over chosen blocks
+def _per_sequence(t, name, B, dev):
+    import torch
+    return None if t is None else _need(t, name, (B,), dev, torch.int32)
+
+
+def _bf16_4d(t, name, shape="[B][H][n][64]"):
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, not {t.dtype}")
+    if t.dim() != 4:
+        raise ValueError(f"expected {name} {shape}, got {tuple(t.shape)}")
+    return t.shape
+
+
+@_on_stream
+def diffuser_block_means(K, lengths=None, recent: int = 0, means=None, stream=None):
+    """Means [B][Hk][ceil(m / 64)][64] of the blocks of 64 keys of K [B][Hk][m][64] (bf16) below
+    lengths (int32 [B]; None: m).  recent > 0: only of the blocks that hold some of each sequence's
+    last `recent` keys; other blocks of `means` are left as they were (a new tensor's are 0)."""
+    import torch
+    B, Hk, m, d = _bf16_4d(K, "K")
+    dev, shape = K.get_device(), (B, Hk, -(-m // 64), d)
+    k = _flat(K, "K", dev, K.dtype)
+    if means is None:
+        means = (torch.empty if lengths is None and not recent else torch.zeros)(shape, dtype=K.dtype, device=K.device)
+    _check(_lib.diffuser_block_means(k, B, Hk, m, d, _per_sequence(lengths, "lengths", B, dev), recent,
+                                     _need(means, "means", shape, dev, K.dtype), stream), "diffuser_block_means")
+    return means
+
+
+@_on_stream
+def diffuser_select_blocks(Q, means, top_k: int, keys: int, sink_blocks: int = 0, local_blocks: int = 1,
+                           causal: bool = True, lengths=None, starts=None, blocks=None, stream=None):
+    """For each query of Q [B][Hq][n][64] and key head, the top_k visible blocks of 64 keys whose
+    means [B][Hk][ceil(keys / 64)][64] score highest with the group's queries: int32 [B][Hk][n][top_k],
+    ascending, -1 behind the last.  The first sink_blocks and those less than local_blocks from the
+    query's own are taken first.  keys: the keys' (or the cache's) size m; lengths, starts: int32 [B] or
+    None (keys; length - n)."""
+    import torch
+    B, Hq, n, d = _bf16_4d(Q, "Q")
+    Hk = _bf16_4d(means, "means")[1]
+    dev, shape = Q.get_device(), (B, Hk, n, top_k)
+    q, mean = _flat(Q, "Q", dev, Q.dtype), _need(means, "means", (B, Hk, -(-keys // 64), d), dev, Q.dtype)
+    if blocks is None:
+        blocks = torch.empty(shape, dtype=torch.int32, device=Q.device)
+    _check(_lib.diffuser_select_blocks(
+        q, mean, B, Hq, Hk, n, keys, d, top_k, sink_blocks, local_blocks, int(causal),
+        _per_sequence(lengths, "lengths", B, dev), _per_sequence(starts, "starts", B, dev),
+        _need(blocks, "blocks", shape, dev, torch.int32), stream), "diffuser_select_blocks")
+    return blocks
+
+
+def diffuser_selected_attention_workspace_size(B: int, Hq: int, Hk: int, n: int, m: int, top_k: int, d: int = 64) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.diffuser_selected_attention_workspace_size(B, Hq, Hk, n, m, d, top_k, ctypes.byref(b)),
+           "diffuser_selected_attention_workspace_size")
+    return b.value
+
+
+def _selected_shapes(Q, K, V, blocks):
+    """Sizes of a call and the addresses of its first four tensors, after their checks."""
+    import torch
+    B, Hq, n, d = _bf16_4d(Q, "Q")
+    Hk, m = _bf16_4d(K, "K")[1:3]
+    dev, bf, keys = Q.get_device(), Q.dtype, (B, Hk, m, d)
+    if blocks.dim() != 4:
+        raise ValueError(f"expected blocks [B][Hk][n][top_k], got {tuple(blocks.shape)}")
+    top = blocks.shape[3]
+    return (dev, B, Hq, Hk, n, m, d, top, _flat(Q, "Q", dev, bf), _need(K, "K", keys, dev, bf),
+            _need(V, "V", keys, dev, bf), _need(blocks, "blocks", (B, Hk, n, top), dev, torch.int32))
+
+
+@_on_stream
+def diffuser_selected_attention(Q, K, V, blocks, causal: bool = True, lengths=None, starts=None, save_lse: bool = False,
+                                out=None, lse=None, workspace=None, stream=None):
+    """Attention of Q [B][Hq][n][64] over the keys and values [B][Hk][m][64] of the blocks
+    (int32 [B][Hk][n][top_k]) that each query lists; with save_lse (or `lse` given) returns
+    (out, lse), lse fp32 [B][Hq][n] as the backward pass wants it."""
+    import torch
+    dev, B, Hq, Hk, n, m, d, top, q, k, v, idx = _selected_shapes(Q, K, V, blocks)
+    out, o = _out(out, "out", Q.shape, Q)
+    if save_lse and lse is None:
+        lse = torch.empty((B, Hq, n), dtype=torch.float32, device=Q.device)
+    ws, ws_ptr, ws_bytes = _workspace(workspace, diffuser_selected_attention_workspace_size(B, Hq, Hk, n, m, top, d), Q)
+    _check(_lib.diffuser_selected_attention(
+        q, k, v, idx, B, Hq, Hk, n, m, d, top, int(causal), _per_sequence(lengths, "lengths", B, dev),
+        _per_sequence(starts, "starts", B, dev), o, _may(lse, "lse", (B, Hq, n), dev, torch.float32), ws_ptr, ws_bytes,
+        stream), "diffuser_selected_attention")
+    return out if lse is None else (out, lse)
 
 
 def diffuser_set_path(path: int) -> None:

@@ -1,5 +1,5 @@
 // Internal declarations of the operators around the module: the per-head norms
-// with the position rotation (qk_norm_rope.cu), the dense product with its
+// with the position rotation and the rotation alone (qk_norm_rope.cu), the dense product with its
 // epilogue and the gated product (dense_pick.cu, dense_pair.cu, dense_few.cu, dense_act.cu), and their entry
 // points (layer_ops_abi.cu).
 #pragma once
@@ -51,11 +51,14 @@ struct QkArgs {
     int32_t Hq, Hk;
     int32_t rot;                    // rotated features: 0, 16, 32, 48, 64
     float eps;
+    float magnitude;                // the rotation alone: factor of the turned features
     float* partial;                 // backward: [blocks][64] sums of the weights' gradients, or null
     // turns per position of pair i, in units of 2^-64, and what is left of it, of 2^-128
     uint64_t freq[kHeadDim / 2], freq_low[kHeadDim / 2];
 };
 int launch_qk_norm_rope(const QkArgs& a, int32_t dtype, bool interleaved, cudaStream_t stream);
+// the rotation alone (q, k, qo, ko, pos and the turns); `back` turns the other way
+int launch_rope(const QkArgs& a, int32_t dtype, bool interleaved, bool back, cudaStream_t stream);
 // blocks of the backward kernel (rows of `partial`)
 int64_t qk_backward_blocks(int64_t tokens, int64_t Hq, int64_t Hk);
 int launch_qk_norm_rope_backward(const QkArgs& a, int32_t dtype, bool interleaved, void* dwq, void* dwk,

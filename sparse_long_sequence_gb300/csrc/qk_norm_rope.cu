@@ -158,6 +158,13 @@ struct Turn {
             }
         }
     }
+    __device__ __forceinline__ void scale(float x) {
+#pragma unroll
+        for (int j = 0; j < (kInterleaved ? 4 : 2); ++j) {
+            c[j] = mul(c[j], both(x));
+            s[j] = mul(s[j], both(x));
+        }
+    }
     // (a, b) -> (a cos - b sin, a sin + b cos)
     __device__ __forceinline__ void apply(F2 (&v)[4]) const {
         if constexpr (kInterleaved) {
@@ -366,6 +373,42 @@ qk_weight_kernel(const float* partial, int q_blocks, int k_blocks, T* dwq, T* dw
     if (dst) dst[c % kHeadDim] = Io<T>::round(t);
 }
 
+// The rotation alone: y = magnitude R(p) x on the turned features, the others as they are; kSign -1
+// turns back (the gradient).  The same rows, lanes and runs as above without the norm's sum: HBM alone
+// bounds it.
+template <class T, bool kInterleaved, int kSign>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ QkArgs a, const Work w) {
+    const int lane = threadIdx.x & 31;
+    int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (unit >= w.q_units + w.k_units) return;
+    const bool key = unit >= w.q_units;
+    if (key) unit -= w.q_units;
+    const Share s = share_of(a, w, key, unit, lane);
+    int oa, ob;
+    pieces<kInterleaved>(a.rot, lane, &oa, &ob);
+    const int64_t step = a.n * kHeadDim;      // from head to head
+    const T* src = static_cast<const T*>(key ? a.k : a.q) + s.first;
+    T* dst = static_cast<T*>(key ? a.ko : a.qo) + s.first;
+    typename Io<T>::Raw raw[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        if (s.h0 + u < s.h1) raw[u] = Io<T>::load(src + u * step, oa, ob);
+    Turn<kInterleaved> turn;
+    turn.template set<kSign>(a, s.pos, lane);
+    turn.scale((lane & (kRowLanes - 1)) < a.rot / 8 ? a.magnitude : 1.f);
+    for (int h = s.h0; h < s.h1; h += kAhead, src += kAhead * step, dst += kAhead * step) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (h + u >= s.h1) break;
+            F2 v[4];
+            Io<T>::widen(raw[u], v);
+            if (h + u + kAhead < s.h1) raw[u] = Io<T>::load(src + (u + kAhead) * step, oa, ob);
+            turn.apply(v);
+            if (s.live) Io<T>::store(dst + u * step, oa, ob, v);
+        }
+    }
+}
+
 constexpr int64_t kManyWarps = 152 * 48;     // warps that fill the GPU
 constexpr int64_t kBackBlocks = 152 * 2;     // the backward's blocks that run at once
 
@@ -404,6 +447,20 @@ int forward_as(const QkArgs& a, bool interleaved, cudaStream_t stream) {
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "qk_forward_kernel");
 }
 
+template <class T, int kSign>
+int rope_as(const QkArgs& a, bool interleaved, cudaStream_t stream) {
+    const Work w = plan(a.tokens, a.Hq, a.Hk, false);
+    const int64_t blocks = (w.q_units + w.k_units + kWarps - 1) / kWarps;
+    if (blocks > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many rows");
+    {
+        LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
+        if (interleaved) rope_kernel<T, true, kSign><<<(unsigned)blocks, kThreads, 0, stream>>>(a, w);
+        else rope_kernel<T, false, kSign><<<(unsigned)blocks, kThreads, 0, stream>>>(a, w);
+    }
+    const cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "rope_kernel");
+}
+
 template <class T>
 int backward_as(const QkArgs& a, bool interleaved, void* dwq, void* dwk, cudaStream_t stream) {
     const Work w = plan(a.tokens, a.Hq, a.Hk, true);
@@ -440,6 +497,12 @@ int launch_qk_norm_rope_backward(const QkArgs& a, int32_t dtype, bool interleave
                                  cudaStream_t stream) {
     return dtype == DIFFUSER_DTYPE_BF16 ? backward_as<__nv_bfloat16>(a, interleaved, dwq, dwk, stream)
                                         : backward_as<float>(a, interleaved, dwq, dwk, stream);
+}
+
+int launch_rope(const QkArgs& a, int32_t dtype, bool interleaved, bool back, cudaStream_t stream) {
+    if (dtype == DIFFUSER_DTYPE_BF16)
+        return back ? rope_as<__nv_bfloat16, -1>(a, interleaved, stream) : rope_as<__nv_bfloat16, 1>(a, interleaved, stream);
+    return back ? rope_as<float, -1>(a, interleaved, stream) : rope_as<float, 1>(a, interleaved, stream);
 }
 
 }  // namespace dfs

@@ -58,16 +58,31 @@ inline Wide ratio(double theta, int m) {
     return mul(x, c >= 0 ? Wide{f, -127} : Wide{f << 1, -128});
 }
 
+constexpr Wide kPerTurn = {((u128)0xa2f9836e4e441529ull << 64) | 0xfc2757d1f534ddc1ull, -130};   // 1 / (2 pi)
+
+// the upper and lower 64 bits of a fraction below 1
+inline void split(const Wide& f, uint64_t* hi, uint64_t* lo) {
+    const int down = -128 - f.exp;           // 0 or more
+    const u128 t = down < 128 ? f.mant >> down : 0;
+    *hi = (uint64_t)(t >> 64);
+    *lo = (uint64_t)t;
+}
+
+// given frequencies, radians per position from 0 to 4: f / (2 pi) to 2^-126 of itself
+inline void fill_given(uint64_t* hi, uint64_t* lo, const double* f, int pairs) {
+    for (int i = 0; i < pairs; ++i) {
+        hi[i] = lo[i] = 0;
+        if (f[i] > 0) split(mul(wide(f[i]), kPerTurn), &hi[i], &lo[i]);
+    }
+}
+
 // theta >= 1 and finite, rot 16, 32, 48 or 64: rot / 2 fractions, their upper and lower 64 bits
 inline void fill(uint64_t* hi, uint64_t* lo, double theta, int rot) {
     const int m = rot / 2;
     const Wide x = ratio(theta, m);
-    Wide f = {((u128)0xa2f9836e4e441529ull << 64) | 0xfc2757d1f534ddc1ull, -130};      // 1 / (2 pi)
+    Wide f = kPerTurn;
     for (int i = 0; i < m; ++i) {
-        const int down = -128 - f.exp;       // 2 or more
-        const u128 t = down < 128 ? f.mant >> down : 0;
-        hi[i] = (uint64_t)(t >> 64);
-        lo[i] = (uint64_t)t;
+        split(f, &hi[i], &lo[i]);
         if (i + 1 < m) f = mul(f, x);
     }
 }

@@ -1,0 +1,98 @@
+"""The rotation alone and the attention over chosen key blocks, from their definitions, in 64
+bits on the CPU."""
+import math
+
+import torch
+
+BLOCK = 64
+
+
+def rope(x, freq, magnitude, interleaved, pos):
+    """x [B][H][n][64], pos int64 [B][n]."""
+    r = 2 * len(freq)
+    a = pos.double()[:, None, :, None] * torch.tensor(list(freq), dtype=torch.float64)
+    z = torch.polar(torch.full_like(a, magnitude), a)
+    head, rest = x[..., :r].double(), x[..., r:].double()
+    if interleaved:
+        head = torch.view_as_real(torch.view_as_complex(head.unflatten(-1, (r // 2, 2)).contiguous()) * z).flatten(-2)
+    else:
+        w = torch.complex(head[..., :r // 2].contiguous(), head[..., r // 2:].contiguous()) * z
+        head = torch.cat((w.real, w.imag), -1)
+    return torch.cat((head, rest), -1)
+
+
+def limits(n, m, causal, length, start):
+    """How many of the first keys each query of a sequence sees."""
+    first = length - n if start is None else start
+    out = []
+    for i in range(n):
+        p = first + i
+        out.append(0 if p < 0 or p >= length else (p + 1 if causal else length))
+    return out
+
+
+def _sequences(B, n, m, lengths, starts):
+    for b in range(B):
+        length = m if lengths is None else min(max(int(lengths[b]), 0), m)
+        yield b, length, None if starts is None else int(starts[b])
+
+
+def means(K, lengths, old, recent=0):
+    out = old.double().clone()
+    B, _, m, _ = K.shape
+    for b, length, _ in _sequences(B, 1, m, lengths, None):
+        first = max(0, length - recent) // BLOCK if recent else 0
+        for c in range(first, -(-length // BLOCK)):
+            out[b, :, c] = K[b, :, c * BLOCK:min(length, (c + 1) * BLOCK)].double().sum(1) / (min(length, (c + 1) * BLOCK) - c * BLOCK)
+    return out
+
+
+def select(Q, mean, top, m, sink, local, causal, lengths, starts):
+    B, Hq, n, _ = Q.shape
+    Hk = mean.shape[1]
+    G = Hq // Hk
+    out = torch.full((B, Hk, n, top), -1, dtype=torch.int32)
+    for b, length, start in _sequences(B, n, m, lengths, starts):
+        first = length - n if start is None else start
+        lim = limits(n, m, causal, length, start)
+        for h in range(Hk):
+            q = Q[b, h * G:(h + 1) * G].double()
+            for i in range(n):
+                nv = -(-lim[i] // BLOCK)
+                score = (q[:, i] @ mean[b, h, :nv].double().T).sum(0).tolist()
+                score = [-math.inf if x != x else x for x in score]
+                home = (first + i) // BLOCK
+                rank = sorted(range(nv), key=lambda c: (not (c < sink or abs(c - home) < local), -score[c], c))
+                picked = sorted(rank[:top])
+                out[b, h, i, :len(picked)] = torch.tensor(picked, dtype=torch.int32)
+    return out
+
+
+def mask(blocks, n, m, causal, lengths, starts):
+    """Keys that each query sees, bool [B][Hk][n][m]."""
+    B, Hk, _, top = blocks.shape
+    out = torch.zeros((B, Hk, n, m), dtype=torch.bool)
+    for b, length, start in _sequences(B, n, m, lengths, starts):
+        lim = limits(n, m, causal, length, start)
+        for h in range(Hk):
+            for i in range(n):
+                before = -1
+                for c in blocks[b, h, i].tolist():
+                    if c > before:
+                        out[b, h, i, c * BLOCK:(c + 1) * BLOCK] = True
+                    before = max(before, c)
+                out[b, h, i, lim[i]:] = False
+    return out
+
+
+def attend(Q, K, V, seen):
+    """out, lse, and sum_j p_ij |v_j|, the measure of out's roundings."""
+    B, Hq, n, _ = Q.shape
+    G = Hq // K.shape[1]
+    on = seen.repeat_interleave(G, 1)
+    k = torch.where(seen.any(2)[..., None], K.double(), 0.0).repeat_interleave(G, 1)     # (a key that no query sees is not read)
+    v = torch.where(seen.any(2)[..., None], V.double(), 0.0).repeat_interleave(G, 1)
+    x = (Q.double() @ k.mT / 8).masked_fill(~on, -math.inf)
+    lse = torch.logsumexp(x, -1)
+    p = torch.exp(x - torch.where(lse > -math.inf, lse, 0.0)[..., None])
+    return p @ v, lse, p @ v.abs()
