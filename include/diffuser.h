@@ -628,6 +628,28 @@ DIFFUSER_API int diffuser_selected_attention(const void* Q, const void* K, const
                                              const int32_t* starts, void* out, float* lse, void* workspace,
                                              size_t workspace_bytes, diffuser_stream stream);
 
+/*
+ * Its gradients for dOut (shaped as out), with out and lse as the forward gave them and the same
+ * lists (the choice itself has no gradient): with delta_i = dout_i . out_i,
+ *   dS_ij = A_ij (dout_i . v_j - delta_i) / sqrt(d),
+ *   dq_i = sum_j dS_ij k_j,   dk_j = sum_i dS_ij q_i,   dv_j = sum_i A_ij dout_i,
+ * the sums for a key over the queries of all heads of its group.  A and dS are recomputed, and
+ * rounded to bf16 as operands of the tensor cores; sums in fp32 in a fixed order, one rounding.
+ *   dQ [B][Hq][n][64], dK, dV [B][Hk][m][64]: bf16, written whole (0 where no query sees a key)
+ *   workspace   diffuser_selected_attention_backward_workspace_size bytes, 256-byte aligned
+ */
+DIFFUSER_API int diffuser_selected_attention_backward_workspace_size(int64_t B, int64_t Hq, int64_t Hk, int64_t n,
+                                                                     int64_t m, int32_t d, int32_t top_k,
+                                                                     size_t* bytes);
+DIFFUSER_API int diffuser_selected_attention_backward(const void* Q, const void* K, const void* V,
+                                                      const int32_t* blocks, const void* out, const float* lse,
+                                                      const void* dOut, int64_t B, int64_t Hq, int64_t Hk,
+                                                      int64_t n, int64_t m, int32_t d, int32_t top_k,
+                                                      int32_t causal, const int32_t* lengths,
+                                                      const int32_t* starts, void* dQ, void* dK, void* dV,
+                                                      void* workspace, size_t workspace_bytes,
+                                                      diffuser_stream stream);
+
 /* ---------------------------------------------------------------- no-allocation forward */
 
 /*

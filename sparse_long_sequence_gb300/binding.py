@@ -113,6 +113,10 @@ def _load() -> ctypes.CDLL:
                                                                  c.POINTER(c.c_size_t)]),
         "diffuser_selected_attention": (c.c_int, [vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, i32, i32, vp, vp, vp, vp,
                                                   vp, c.c_size_t, vp]),
+        "diffuser_selected_attention_backward_workspace_size": (c.c_int, [i64, i64, i64, i64, i64, i32, i32,
+                                                                          c.POINTER(c.c_size_t)]),
+        "diffuser_selected_attention_backward": (c.c_int, [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, i32,
+                                                           i32, vp, vp, vp, vp, vp, vp, c.c_size_t, vp]),
         "diffuser_graph_status": (c.c_int, [vp, c.POINTER(c.c_int), c.c_int]),
         "diffuser_graph_set_status": (c.c_int, [vp, c.c_int]),
         "diffuser_launch_count": (c.c_int64, [i64p]),
@@ -859,6 +863,33 @@ def diffuser_selected_attention(Q, K, V, blocks, causal: bool = True, lengths=No
         _per_sequence(starts, "starts", B, dev), o, _may(lse, "lse", (B, Hq, n), dev, torch.float32), ws_ptr, ws_bytes,
         stream), "diffuser_selected_attention")
     return out if lse is None else (out, lse)
+
+
+def diffuser_selected_attention_backward_workspace_size(B: int, Hq: int, Hk: int, n: int, m: int, top_k: int,
+                                                        d: int = 64) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.diffuser_selected_attention_backward_workspace_size(B, Hq, Hk, n, m, d, top_k, ctypes.byref(b)),
+           "diffuser_selected_attention_backward_workspace_size")
+    return b.value
+
+
+@_on_stream
+def diffuser_selected_attention_backward(Q, K, V, blocks, out, lse, dOut, causal: bool = True, lengths=None, starts=None,
+                                         dQ=None, dK=None, dV=None, workspace=None, stream=None):
+    """Gradients (dQ, dK, dV) of diffuser_selected_attention for dOut [B][Hq][n][64], with out and lse
+    as the forward gave them (save_lse)."""
+    import torch
+    dev, B, Hq, Hk, n, m, d, top, q, k, v, idx = _selected_shapes(Q, K, V, blocks)
+    bf = Q.dtype
+    (dQ, dq), (dK, dk), (dV, dv) = _out(dQ, "dQ", Q.shape, Q), _out(dK, "dK", K.shape, K), _out(dV, "dV", K.shape, V)
+    ws, ws_ptr, ws_bytes = _workspace(
+        workspace, diffuser_selected_attention_backward_workspace_size(B, Hq, Hk, n, m, top, d), Q)
+    _check(_lib.diffuser_selected_attention_backward(
+        q, k, v, idx, _need(out, "out", Q.shape, dev, bf), _need(lse, "lse", (B, Hq, n), dev, torch.float32),
+        _need(dOut, "dOut", Q.shape, dev, bf), B, Hq, Hk, n, m, d, top, int(causal),
+        _per_sequence(lengths, "lengths", B, dev), _per_sequence(starts, "starts", B, dev), dq, dk, dv, ws_ptr, ws_bytes,
+        stream), "diffuser_selected_attention_backward")
+    return dQ, dK, dV
 
 
 def diffuser_set_path(path: int) -> None:

@@ -76,6 +76,7 @@ int check_selected(int64_t B, int64_t Hq, int64_t Hk, int64_t n, int64_t m, int3
     if (m > kMaxKeys || n > kMaxKeys) return fail(DIFFUSER_ERR_UNSUPPORTED, "more than 2^20 queries or keys");
     if (n && B * Hq > (int64_t(1) << 40) / (n * top)) return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
     if (m && B * Hk > (int64_t(1) << 40) / m) return fail(DIFFUSER_ERR_OVERFLOW, "too many keys");
+    if (n * (Hq / Hk) * top > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many queries of a key head");
     *s = SelectShape{};
     s->B = B;
     s->n = n;
@@ -233,6 +234,65 @@ int diffuser_selected_attention(const void* Q, const void* K, const void* V, con
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
     return launch_selected(a, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream));
+} catch (...) {
+    return fail(DIFFUSER_ERR_ALLOC, "unexpected exception");
+}
+
+int diffuser_selected_attention_backward_workspace_size(int64_t B, int64_t Hq, int64_t Hk, int64_t n, int64_t m,
+                                                        int32_t d, int32_t top_k, size_t* bytes) try {
+    if (!bytes) return fail(DIFFUSER_ERR_INVALID_ARG, "NULL argument");
+    SelectShape s;
+    const int st = check_selected(B, Hq, Hk, n, m, d, top_k, &s);
+    if (st) return st;
+    *bytes = selected_backward_workspace(s);
+    return DIFFUSER_OK;
+} catch (...) {
+    return fail(DIFFUSER_ERR_ALLOC, "unexpected exception");
+}
+
+int diffuser_selected_attention_backward(const void* Q, const void* K, const void* V, const int32_t* blocks,
+                                         const void* out, const float* lse, const void* dOut, int64_t B, int64_t Hq,
+                                         int64_t Hk, int64_t n, int64_t m, int32_t d, int32_t top_k, int32_t causal,
+                                         const int32_t* lengths, const int32_t* starts, void* dQ, void* dK, void* dV,
+                                         void* workspace, size_t workspace_bytes, diffuser_stream stream) try {
+    SelectedArgs a{};
+    int st = check_selected(B, Hq, Hk, n, m, d, top_k, &a.s);
+    if (st) return st;
+    const SelectShape& s = a.s;
+    a.s.causal = causal != 0;
+    a.s.lengths = lengths;
+    a.s.starts = starts;
+    const size_t qb = rows_bytes(s), kb = keys_bytes(s), need = selected_backward_workspace(s);
+    const Span in[9] = {{Q, qb}, {K, kb}, {V, kb}, {blocks, list_bytes(s)}, {out, qb}, {lse, qb / 32}, {dOut, qb},
+                        per_sequence(lengths, B), per_sequence(starts, B)};
+    const Span outs[4] = {{dQ, qb}, {dK, kb}, {dV, kb}, {workspace, workspace_bytes}};
+    const char* names[7] = {"Q", "K", "V", "blocks", "out", "lse", "dOut"};
+    for (int x = 0; x < 7; ++x)
+        if ((st = check_span(in[x], names[x]))) return st;
+    if ((st = check_span(in[7], "lengths", 4)) || (st = check_span(in[8], "starts", 4)) ||
+        (st = check_span(outs[0], "dQ")) || (st = check_span(outs[1], "dK")) || (st = check_span(outs[2], "dV")) ||
+        (need && (st = check_workspace_bytes(need, workspace, workspace_bytes))) || (st = check_overlaps(in, 9, outs, 4)))
+        return st;
+    const cudaStream_t stream_ = static_cast<cudaStream_t>(stream);
+    if (qb == 0 || kb == 0) {                // no query lists a key
+        for (const Span& g : {outs[0], outs[1], outs[2]})
+            if (g.bytes) {
+                const cudaError_t err = cudaMemsetAsync(const_cast<void*>(g.p), 0, g.bytes, stream_);
+                if (err != cudaSuccess) return cuda_fail(err, "zeroing a gradient");
+            }
+        return DIFFUSER_OK;
+    }
+    a.q = static_cast<const __nv_bfloat16*>(Q);
+    a.k = static_cast<const __nv_bfloat16*>(K);
+    a.v = static_cast<const __nv_bfloat16*>(V);
+    a.blocks = blocks;
+    a.out = static_cast<__nv_bfloat16*>(const_cast<void*>(out));
+    a.lse = const_cast<float*>(lse);
+    a.dout = static_cast<const __nv_bfloat16*>(dOut);
+    a.dq = static_cast<__nv_bfloat16*>(dQ);
+    a.dk = static_cast<__nv_bfloat16*>(dK);
+    a.dv = static_cast<__nv_bfloat16*>(dV);
+    return launch_selected_backward(a, static_cast<char*>(workspace), stream_);
 } catch (...) {
     return fail(DIFFUSER_ERR_ALLOC, "unexpected exception");
 }

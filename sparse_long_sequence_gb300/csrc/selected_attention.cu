@@ -8,6 +8,7 @@
 // memory into the products' registers.  Bound by the cache's bytes, or by a launch.
 #include <atomic>
 
+#include "block_lists.h"
 #include "mma_tiles.cuh"
 #include "selected.h"
 
@@ -144,10 +145,178 @@ int launch_few(const SelectedArgs& a, cudaStream_t stream) {
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "selected_few_kernel");
 }
 
+constexpr int kItemRows = 256;
+constexpr int kItemWarps = 4;
+constexpr size_t kGroupBytes = 64 << 20;     // partials of a group of units
+
+// Partials of the units u0 .. : slot x = ((u - u0) n + i) G + h) ranks + rank.
+struct Partials {
+    float* sums;                             // [slots][64], features by place_of
+    float2* stat;                            // [slots]: maximum (units of log 2), sum
+    int64_t u0;
+};
+
+__global__ void __launch_bounds__(32 * kItemWarps)
+selected_items_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials out) {
+    const SelectShape& s = a.s;
+    const int64_t u = out.u0 + blockIdx.x / l.most_items, b = u / s.Hk;
+    const ItemRows item = item_of(l, s, u, blockIdx.x % l.most_items);
+    if (!item.rows) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int32_t key0 = item.block * kBlockKeys;
+    const int rows = min(kBlockKeys, key_count(s, b) - key0);
+    uint32_t keys[8][8], values[8][8];
+    load_keys(a.k + (u * s.m + key0) * kHeadDim, rows, lane, keys);
+    load_keys(a.v + (u * s.m + key0) * kHeadDim, rows, lane, values);
+    turn_values(values);
+    const __nv_bfloat16* q0 = a.q + (b * s.Hq + (u % s.Hk) * s.G) * s.n * kHeadDim;
+    const int64_t slot0 = (u - out.u0) * s.n * s.G * l.ranks;
+
+    for (int r0 = 8 * warp; r0 < item.rows; r0 += 8 * kItemWarps) {
+        const bool live = r0 + g < item.rows;
+        const uint32_t r = item.first + (live ? r0 + g : 0), e = r / s.G, h = r - e * s.G;
+        const uint32_t entry = item.entries[e], i = entry >> 6;
+        uint32_t q[8];
+        load_row(q0 + ((int64_t)h * s.n + i) * kHeadDim, live, t, q);
+        const uint32_t mine = live ? (i * s.G + h) * l.ranks + (entry & 63) : ~0u;
+        const int sees = live ? row_limit(s, b, i) - key0 : 0;
+        float x[4][4];
+        score(keys, q, x);
+        int limit[2];
+        uint32_t slot[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            limit[c] = __shfl_sync(kFull, sees, 8 * t + 4 * c);
+            slot[c] = __shfl_sync(kFull, mine, 8 * t + 4 * c);
+        }
+        float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int M = 0; M < 4; ++M)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[M][j] = 16 * M + 8 * (j >> 1) + g < limit[j & 1] ? x[M][j] * kScale2 : -INFINITY;
+                m[j & 1] = fmaxf(m[j & 1], x[M][j]);
+            }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            m[c] = column_max(m[c]);
+            const float base = m[c] == -INFINITY ? 0.f : m[c];
+#pragma unroll
+            for (int M = 0; M < 4; ++M)
+#pragma unroll
+                for (int j = c; j < 4; j += 2) {
+                    x[M][j] = exp2_fast(x[M][j] - base);
+                    sum[c] += x[M][j];
+                }
+            sum[c] = column_sum(sum[c]);
+        }
+        float o[4][4];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j >> 2][j & 3] = 0.f;
+        weigh(values, x, o);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (slot[c] == ~0u) continue;
+            float4* dst = reinterpret_cast<float4*>(out.sums + (slot0 + slot[c]) * kHeadDim) + 2 * g;
+            dst[0] = make_float4(o[0][c], o[0][c + 2], o[1][c], o[1][c + 2]);
+            dst[1] = make_float4(o[2][c], o[2][c + 2], o[3][c], o[3][c + 2]);
+            if (g == 0) out.stat[slot0 + slot[c]] = make_float2(m[c], sum[c]);
+        }
+    }
+}
+
+// Sixteen lanes join a row's partials.
+__global__ void __launch_bounds__(256)
+selected_join_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials in,
+                     int64_t rows) {
+    const SelectShape& s = a.s;
+    const int lane = threadIdx.x & 15;
+    const unsigned half = 0xffffu << (threadIdx.x & 16);
+    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);       // ((u - u0) n + i) G + h
+    if (row >= rows) return;
+    const int64_t entry = row / s.G, u = in.u0 + entry / s.n, i = entry % s.n, h = row % s.G;
+    const int count = l.live[in.u0 * s.n + entry];
+    const float2* stat = in.stat + row * l.ranks;
+    float top = -INFINITY;
+    for (int x = lane; x < count; x += 16) top = fmaxf(top, stat[x].x);
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(half, top, off));
+    const float base = top == -INFINITY ? 0.f : top;
+    const float4* part = reinterpret_cast<const float4*>(in.sums + row * l.ranks * kHeadDim) + lane;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int x = 0; x < count; ++x) {
+        const float4 p = part[x * 16];
+        const float2 st = stat[x];
+        const float w = exp2_fast(st.x - base);
+        sum += w * st.y;
+        y.x += w * p.x;
+        y.y += w * p.y;
+        y.z += w * p.z;
+        y.w += w * p.w;
+    }
+    const float r = top != -INFINITY ? 1.f / sum : 0.f;
+    // this lane has features 2k + e of an eight, k = 0 .. 3, its neighbour two lanes on the other e
+    const int g = lane >> 1, e = g & 1;
+    const float z[4] = {y.x * r, y.y * r, y.z * r, y.w * r};
+    const float got0 = __shfl_xor_sync(half, e ? z[0] : z[2], 2), got1 = __shfl_xor_sync(half, e ? z[1] : z[3], 2);
+    const uint2 w = e ? make_uint2(pack(got0, z[2]), pack(got1, z[3])) : make_uint2(pack(z[0], got0), pack(z[1], got1));
+    const int64_t at = ((u / s.Hk * s.Hq) + (u % s.Hk) * s.G + h) * s.n + i;
+    *reinterpret_cast<uint2*>(a.out + at * kHeadDim + 32 * (lane & 1) + 8 * (g >> 1) + 4 * e) = w;
+    if (a.lse && lane == 0) a.lse[at] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+struct Plan {
+    BlockLists lists;
+    int64_t group;                           // units whose partials are held at once
+    size_t sums, stat, total;
+};
+Plan plan_items(const SelectShape& s, char* ws) {
+    Plan p;
+    p.sums = plan_block_lists(s, kItemRows, ws, &p.lists);
+    const int64_t units = s.B * s.Hk, slots = s.n * s.G * p.lists.ranks;
+    p.group = slots ? (int64_t)(kGroupBytes / (slots * 264)) : 1;
+    p.group = p.group < 1 ? 1 : p.group > units ? units : p.group;
+    p.stat = p.sums + p.group * slots * kHeadDim * 4;
+    p.total = p.stat + (p.group * slots * 8 + 255) / 256 * 256;
+    return p;
+}
+
+int launch_items(const SelectedArgs& a, char* ws, cudaStream_t stream) {
+    const SelectShape& s = a.s;
+    const Plan p = plan_items(s, ws);
+    int st = launch_block_lists(s, a.blocks, p.lists, stream);
+    if (st) return st;
+    const int64_t units = s.B * s.Hk;
+    for (int64_t u0 = 0; u0 < units; u0 += p.group) {
+        const int64_t here = units - u0 < p.group ? units - u0 : p.group, rows = here * s.n * s.G;
+        const Partials part{reinterpret_cast<float*>(ws + p.sums), reinterpret_cast<float2*>(ws + p.stat), u0};
+        if (here * p.lists.most_items > INT32_MAX || (rows + 15) / 16 > INT32_MAX)
+            return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
+        {
+            LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
+            selected_items_kernel<<<(unsigned)(here * p.lists.most_items), 32 * kItemWarps, 0, stream>>>(a, p.lists, part);
+        }
+        {
+            LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
+            selected_join_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, stream>>>(a, p.lists, part, rows);
+        }
+    }
+    const cudaError_t err = cudaGetLastError();
+    return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "selected_items_kernel");
+}
+
+// Few queries: what the lists, the partials and their joining would cost outweighs reading a block's
+// keys once for each query that lists it.
+bool by_query(const SelectShape& s) { return s.m == 0 || s.B * s.Hk * s.n * s.top <= 8192; }
+
 }  // namespace
 
-size_t selected_workspace(const SelectShape&) { return 0; }
+size_t selected_workspace(const SelectShape& s) { return by_query(s) || s.B * s.n == 0 ? 0 : plan_items(s, nullptr).total; }
 
-int launch_selected(const SelectedArgs& a, char*, cudaStream_t stream) { return launch_few(a, stream); }
+int launch_selected(const SelectedArgs& a, char* ws, cudaStream_t stream) {
+    return by_query(a.s) ? launch_few(a, stream) : launch_items(a, ws, stream);
+}
 
 }  // namespace dfs

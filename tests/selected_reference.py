@@ -96,3 +96,31 @@ def attend(Q, K, V, seen):
     lse = torch.logsumexp(x, -1)
     p = torch.exp(x - torch.where(lse > -math.inf, lse, 0.0)[..., None])
     return p @ v, lse, p @ v.abs()
+
+
+def gradients(Q, K, V, D, seen):
+    """dQ, dK, dV by the formula, and for each the measures of its roundings: the sums of the
+    absolute terms with dS (or P), and those with what dout.out's and dout.v's roundings make of dS."""
+    B, Hq, n, _ = Q.shape
+    Hk = K.shape[1]
+    G = Hq // Hk
+    on = seen.repeat_interleave(G, 1)
+    used = seen.any(2)[..., None]
+    k, v = (torch.where(used, x.double(), 0.0).repeat_interleave(G, 1) for x in (K, V))
+    q, d = Q.double(), D.double()
+    x = (q @ k.mT / 8).masked_fill(~on, -math.inf)
+    lse = torch.logsumexp(x, -1)
+    p = torch.exp(x - torch.where(lse > -math.inf, lse, 0.0)[..., None])
+    out = p @ v
+    dp = d @ v.mT
+    ds = p * (dp - (d * out).sum(-1, keepdim=True)) / 8
+    coarse = p * (d.abs() * out.abs()).sum(-1, keepdim=True) / 8     # times u: dout.out of the rounded out
+    fine = p * (d.abs() @ v.abs().mT) / 8                            # times 2^-16: dout.v in fp32
+
+    def heads(y):
+        return y.unflatten(1, (Hk, G)).sum(2)
+
+    return ((ds @ k, heads(ds.mT @ q), heads(p.mT @ d)),
+            (ds.abs() @ k.abs(), heads(ds.abs().mT @ q.abs()), heads(p.mT @ d.abs())),
+            (coarse @ k.abs(), heads(coarse.mT @ q.abs()), 0.0),
+            (fine @ k.abs(), heads(fine.mT @ q.abs()), 0.0))

@@ -224,3 +224,52 @@ def test_attention_lists(dl):
     assert not seen[:, :, 7].any() and seen[:, :, 6].sum() == 128
     out, lse = attend(dl, case, Q, K, V, blocks, save_lse=True)
     check_attention(out, lse, Q, K, V, seen)
+
+
+def check_gradients(got, Q, K, V, D, seen):
+    want, mass, coarse, fine = ref.gradients(Q, K, V, D, seen)
+    for y, w, a, c, f in zip(got, want, mass, coarse, fine):
+        # the result's rounding; P's or dS's as an operand, and 2^-11 from the scores; delta's and dout.v's share
+        bound = U[BF] * w.abs() + (U[BF] + 2.0 ** -11) * a + 1.1 * U[BF] * c + 2.0 ** -16 * f
+        assert ((y.double().cpu() - w).abs() <= bound).all()
+
+
+def backward(dl, case, Q, K, V, blocks, out, lse, D, **kw):
+    B, Hq, Hk, n, m, top, sink, local, causal, lengths, starts = case
+    return dl.diffuser_selected_attention_backward(Q.cuda(), K.cuda(), V.cuda(), blocks.cuda(), out, lse, D.cuda(),
+                                                   causal=causal, lengths=cuda(ints(lengths)), starts=cuda(ints(starts)), **kw)
+
+
+# more rows than an item holds, lists of all lengths, heads that share a key block's items
+LARGE = [
+    (1, 2, 1, 1500, 1500, 4, 1, 1, True, None, None),
+    (2, 2, 2, 1030, 1030, 5, 1, 2, False, [1030, 900], [0, 0]),
+    (1, 16, 2, 300, 2000, 7, 2, 1, True, None, None),
+    (1, 5, 1, 700, 700, 64, 0, 1, True, None, None),
+]
+
+
+@pytest.mark.parametrize("case", LARGE)
+def test_attention_of_many_queries(dl, case):
+    B, Hq, Hk, n, m, top, sink, local, causal, lengths, starts = case
+    Q, K, V, D, mean = inputs(case)
+    blocks = dl.diffuser_select_blocks(Q.cuda(), mean.cuda(), top, keys=m, sink_blocks=sink, local_blocks=local,
+                                       causal=causal, lengths=cuda(ints(lengths)), starts=cuda(ints(starts))).cpu()
+    assert torch.equal(blocks, ref.select(Q, mean, top, m, sink, local, causal, lengths, starts))
+    seen = ref.mask(blocks, n, m, causal, lengths, starts)
+    out, lse = attend(dl, case, Q, K, V, blocks, save_lse=True)
+    check_attention(out, lse, Q, K, V, seen)
+    assert torch.equal(attend(dl, case, Q, K, V, blocks), out)
+    got = backward(dl, case, Q, K, V, blocks, out, lse, D)
+    check_gradients(got, Q, K, V, D, seen)
+    for x, y in zip(got, backward(dl, case, Q, K, V, blocks, out, lse, D)):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_backward(dl, case):
+    B, Hq, Hk, n, m, top, sink, local, causal, lengths, starts = case
+    Q, K, V, D, mean = inputs(case)
+    blocks = ref.select(Q, mean, top, m, sink, local, causal, lengths, starts)
+    out, lse = attend(dl, case, Q, K, V, blocks, save_lse=True)
+    check_gradients(backward(dl, case, Q, K, V, blocks, out, lse, D), Q, K, V, D, ref.mask(blocks, n, m, causal, lengths, starts))
