@@ -13,12 +13,13 @@ struct BlockLists {
     uint32_t* entries;             // [units][n ranks]
     int32_t* base;                 // [units][nb + 1]: where a block's entries begin
     int32_t* item_base;            // [units][nb + 1]: where its items do
-    int2* items;                   // [units][most_items]: block, first row
+    int4* items;                   // [units][most_items]: block, first row, rows, the block's first entry
     int32_t* live;                 // [units][n]: blocks of a query that count
     int32_t* counts;               // [units][chunks][nb], while they are built
     int32_t ranks;                 // blocks of a query that count, at most: min(top, nb)
     int32_t most_items, item_rows;
     int32_t words, chunks;         // queries of a chunk / 32; chunks
+    int32_t width;                 // lanes that read a query's list
 };
 
 #ifdef __CUDACC__
@@ -27,16 +28,21 @@ struct ItemRows {
     const uint32_t* entries;       // the block's
 };
 // Item `at` of unit u; rows 0: there is none.
-__device__ __forceinline__ ItemRows item_of(const BlockLists& l, const SelectShape& s, int64_t u, int32_t at) {
-    ItemRows r{0, 0, 0, nullptr};
-    if (at >= l.item_base[u * (s.nb + 1) + s.nb]) return r;
-    const int2 item = l.items[u * l.most_items + at];
-    const int32_t* base = l.base + u * (s.nb + 1) + item.x;
-    r.block = item.x;
-    r.first = item.y;
-    r.rows = min(l.item_rows, (base[1] - base[0]) * s.G - item.y);
-    r.entries = l.entries + u * s.n * l.ranks + base[0];
-    return r;
+__device__ __forceinline__ ItemRows item_of(const BlockLists& l, const SelectShape& s, int64_t u, uint32_t at) {
+    const int4 item = l.items[u * l.most_items + at];        // (whatever it holds where there is none)
+    const bool live = (int32_t)at < l.item_base[u * (s.nb + 1) + s.nb];
+    return {item.x, item.y, live ? item.z : 0, l.entries + u * s.n * l.ranks + (live ? item.w : 0)};
+}
+// Row ((u - u0) n + i) G + h of a group of units that begins with u0 (fewer than 2^31 rows).
+struct RowOf {
+    uint32_t entry;                // (u - u0) n + i
+    int64_t place;                 // the row of [B][Hq][n]
+};
+__device__ __forceinline__ RowOf row_of(const SelectShape& s, int64_t u0, uint32_t row) {
+    const uint32_t entry = s.G == 1 ? row : row / s.G, h = row - entry * s.G;
+    const uint32_t ul = entry / (uint32_t)s.n, i = entry - ul * (uint32_t)s.n;
+    // unit u = b Hk + x: head (b Hk + x) G + h of B Hq
+    return {entry, ((u0 + ul) * s.G + h) * s.n + i};
 }
 #endif
 

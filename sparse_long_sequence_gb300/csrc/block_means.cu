@@ -14,15 +14,15 @@ constexpr unsigned kFull = 0xffffffffu;
 
 // `per` blocks of each sequence and head are looked at: all, or the `recent` form's few.
 __global__ void __launch_bounds__(kThreads)
-block_means_kernel(const __nv_bfloat16* K, int64_t units, int64_t heads, int64_t m, int64_t nb, const int32_t* lengths,
-                   int64_t recent, int64_t per, __nv_bfloat16* means) {
+block_means_kernel(const __nv_bfloat16* K, uint32_t units, uint32_t heads, int64_t m, int64_t nb, const int32_t* lengths,
+                   int64_t recent, uint32_t per, __nv_bfloat16* means) {
     const int lane = threadIdx.x & 31;
-    const int64_t at = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (at >= units * per) return;
-    const int64_t u = at / per, b = u / heads;
+    const uint32_t at = blockIdx.x * kWarps + (threadIdx.x >> 5), ul = at / per;
+    if (ul >= units) return;
+    const int64_t u = ul, b = ul / heads;
     const int64_t len = lengths ? min(max((int64_t)lengths[b], (int64_t)0), m) : m;
     const int64_t first = recent ? max(len - recent, (int64_t)0) / kBlockKeys : 0;
-    const int64_t c = first + (at - u * per), row0 = c * kBlockKeys;
+    const int64_t c = first + (at - ul * per), row0 = c * kBlockKeys;
     if (row0 >= len) return;
     const int rows = (int)min((int64_t)kBlockKeys, len - row0);
     const uint4* src = reinterpret_cast<const uint4*>(K + (u * m + row0) * kHeadDim) + lane;
@@ -66,11 +66,11 @@ int launch_block_means(const void* K, int64_t B, int64_t Hk, int64_t m, const in
     if (recent && recent < m) per = (recent + kBlockKeys - 2) / kBlockKeys + 1;
     if (per > nb) per = nb;
     const int64_t blocks = (B * Hk * per + kWarps - 1) / kWarps;
-    if (blocks > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many key blocks");
+    if (B * Hk * per > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many key blocks");
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        block_means_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(static_cast<const __nv_bfloat16*>(K), B * Hk, Hk, m, nb,
-                                                                      lengths, recent, per, static_cast<__nv_bfloat16*>(means));
+        block_means_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(static_cast<const __nv_bfloat16*>(K), (uint32_t)(B * Hk), (uint32_t)Hk, m, nb,
+                                                                      lengths, recent, (uint32_t)per, static_cast<__nv_bfloat16*>(means));
     }
     const cudaError_t err = cudaGetLastError();
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "block_means_kernel");

@@ -5,7 +5,8 @@
 //
 // A block of eight warps takes up to 16 queries of a unit (sequence and key head).  First the scores
 // on m16n8k16 products (16 blocks by 8 queries, the heads one after the other along the summed index),
-// kept in shared memory as fp32; then a warp a query: the top-th largest value by bisection on values.
+// kept in shared memory as fp32; then a warp a query: candidates by the lanes' maxima, and among them the
+// top-th largest value by bisection on values.
 // The products are exact in fp32, their sums are not: a tensor core adds 16 products and the sum so
 // far with an error of at most 17 2^-23 of the largest of them, so a score is off by at most
 //   eps = 4 G 17 2^-23 sum_f |q_f| max |mean|.
@@ -92,17 +93,122 @@ struct Best {
     }
 };
 
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, off));
+    return x;
+}
+__device__ __forceinline__ uint64_t ballot2(bool a, bool b) {
+    const unsigned lo = __ballot_sync(kFull, a), hi = __ballot_sync(kFull, b);
+    return lo | (uint64_t)hi << 32;
+}
+
+constexpr int kCandidates = 64;
+
+// The `want` (1 to 32) largest of v[0 .. nv), finite but for -infinity in places that take no part;
+// more than `want` take part.  Some x that the maxima of at least `want` lanes reach bounds the
+// want-th largest value from below, so that only the values above it, a few more than `want`, need
+// a closer look: the candidates, by rising index, two a lane (place lane and lane + 32).  Returns
+// their number, and in `taken` a bit for the place of each that is chosen; -1 where there are too many.
+template <class Exact>
+__device__ __forceinline__ int narrow(const float* v, int nv, int want, float eps, int lane, float* cand_x, int* cand_c,
+                                      int (&cand)[2], uint64_t* taken, Exact exact) {
+    float best = -INFINITY;
+#pragma unroll 4
+    for (int c = lane; c < nv; c += 32) best = fmaxf(best, v[c]);
+    const float most = warp_max(best);
+    float lo = -warp_max(best == -INFINITY ? -INFINITY : -best), hi = most;
+    if (__popc(__ballot_sync(kFull, best > -INFINITY)) < want) {
+        lo = -INFINITY;                                      // (few values: all are candidates)
+    } else {
+        for (int k = 0; k < 12; ++k) {
+            const float mid = lo + 0.5f * (hi - lo);
+            const int n = __popc(__ballot_sync(kFull, best >= mid));
+            if (n >= want) lo = mid;
+            else hi = mid;
+            if (n >= want && n <= want + 2) break;
+        }
+    }
+    const float floor = lo - eps;
+    int few = 0;
+    for (int c0 = 0; c0 < nv; c0 += 32) {
+        const float y = v[c0 + lane];
+        const bool in = y >= floor && y > -INFINITY;
+        const unsigned m = __ballot_sync(kFull, in);
+        const int place = few + __popc(m & ((1u << lane) - 1));
+        few += __popc(m);
+        if (few > kCandidates) return -1;
+        if (in) {
+            cand_x[place] = y;
+            cand_c[place] = c0 + lane;
+        }
+    }
+    __syncwarp();
+    float x[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const bool on = lane + 32 * j < few;
+        x[j] = on ? cand_x[lane + 32 * j] : -INFINITY;
+        cand[j] = on ? cand_c[lane + 32 * j] : INT32_MAX;
+    }
+    __syncwarp();                                            // (the next query's candidates go to the same places)
+    if (few == want) {
+        *taken = ballot2(x[0] > -INFINITY, x[1] > -INFINITY);
+        return few;
+    }
+    // the want-th largest: more than `want` reach lo, fewer reach hi (or hi is the largest)
+    float kth;
+    lo = -warp_max(fmaxf(x[0] > -INFINITY ? -x[0] : -INFINITY, x[1] > -INFINITY ? -x[1] : -INFINITY));
+    hi = most;
+    if (__popcll(ballot2(x[0] >= hi, x[1] >= hi)) >= want) {
+        kth = hi;
+    } else {
+        for (;;) {
+            const float mid = lo + 0.5f * (hi - lo);
+            if (!(mid > lo && mid < hi)) {
+                kth = lo;
+                break;
+            }
+            const int n = __popcll(ballot2(x[0] >= mid, x[1] >= mid));
+            if (n == want) {
+                kth = -warp_max(fmaxf(x[0] >= mid ? -x[0] : -INFINITY, x[1] >= mid ? -x[1] : -INFINITY));
+                break;
+            }
+            if (n > want) lo = mid;
+            else hi = mid;
+        }
+    }
+    const uint64_t sure = ballot2(x[0] > kth + eps, x[1] > kth + eps);
+    const uint64_t open = ballot2(x[0] >= kth - eps, x[1] >= kth - eps) & ~sure;
+    if (__popcll(sure | open) == want) {
+        *taken = sure | open;
+        return few;
+    }
+    const int rest = want - __popcll(sure);
+    Best fine;
+    for (uint64_t m = open; m; m &= m - 1) {
+        const int place = __ffsll((long long)m) - 1;
+        fine.offer(exact(__shfl_sync(kFull, place < 32 ? cand[0] : cand[1], place & 31)), place, rest, lane);
+    }
+    const int a = lane < rest ? fine.c[0] : 64;              // (rest is 32 at most: one place a lane)
+    *taken = sure | __reduce_or_sync(kFull, a < 32 ? 1u << a : 0u) |
+             (uint64_t)__reduce_or_sync(kFull, a >= 32 && a < 64 ? 1u << (a - 32) : 0u) << 32;
+    return few;
+}
+
 __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_constant__ Choice a) {
     extern __shared__ __align__(16) float scores[];          // [tile][stride]
     __shared__ int32_t limit[kMostQueries];
     __shared__ float mass[kMostQueries];                     // sum |q| over the group's heads
     __shared__ unsigned largest;                             // bits of max |mean|
+    __shared__ float cand_x[kWarps][kCandidates];
+    __shared__ int cand_c[kWarps][kCandidates];
     const SelectShape& s = a.s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int64_t tiles = (s.n + a.tile - 1) / a.tile, u = blockIdx.x / tiles, i0 = (blockIdx.x % tiles) * a.tile;
-    const int64_t b = u / s.Hk, head = u % s.Hk;
+    const uint32_t tiles = (uint32_t)(s.n + a.tile - 1) / a.tile, ul = blockIdx.x / tiles;
+    const int64_t u = ul, i0 = (int64_t)(blockIdx.x - ul * tiles) * a.tile, b = sequence_of(s, u);
     const int queries = (int)min((int64_t)a.tile, s.n - i0);
-    const __nv_bfloat16* q = a.q + ((b * s.Hq + head * s.G) * s.n + i0) * kHeadDim;    // head h: + h n 64
+    const __nv_bfloat16* q = a.q + (u * s.G * s.n + i0) * kHeadDim;                    // head h: + h n 64
     const __nv_bfloat16* means = a.means + u * s.nb * kHeadDim;
 
     if (threadIdx.x == 0) largest = 0;
@@ -119,8 +225,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
     for (int r = 0; r < queries; ++r) most = max(most, limit[r]);
     const int seen = (most + kBlockKeys - 1) / kBlockKeys;   // blocks that some query sees
 
-    float top_mean = 0.f;
-    bool odd = false;                                        // a mean that is no number
+    __nv_bfloat162 tops = __floats2bfloat162_rn(0.f, 0.f);   // max |mean|; NaN where a mean is
     for (int c0 = 16 * warp; c0 < seen; c0 += 16 * kWarps) {
         uint32_t k[2][8];
 #pragma unroll
@@ -128,11 +233,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
             const int c = c0 + 8 * o + g;
             load_row(means + (int64_t)c * kHeadDim, c < seen, t, k[o]);
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                const float x = fabsf(__uint_as_float(k[o][w] << 16)), y = fabsf(__uint_as_float(k[o][w] & 0xffff0000u));
-                top_mean = fmaxf(top_mean, fmaxf(x, y));
-                odd |= x != x || y != y;
-            }
+            for (int w = 0; w < 8; ++w) tops = __hmax2_nan(tops, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&k[o][w])));
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -153,47 +254,75 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
             }
         }
     }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) top_mean = fmaxf(top_mean, __shfl_xor_sync(kFull, top_mean, off));
-    if (__any_sync(kFull, odd)) top_mean = INFINITY;
+    const float2 two = __bfloat1622float2(tops);
+    const bool odd = two.x != two.x || two.y != two.y;
+    float top_mean = __any_sync(kFull, odd) ? INFINITY : warp_max(fmaxf(two.x, two.y));
     if (lane == 0) atomicMax(&largest, __float_as_uint(top_mean));
     __syncthreads();
     top_mean = __uint_as_float(largest);
 
     for (int r = warp; r < queries; r += kWarps) {
-        int32_t* out = a.blocks + ((u * s.n) + i0 + r) * s.top;
         const int lim = limit[r], nv = (lim + kBlockKeys - 1) / kBlockKeys;
+        int32_t* out = a.blocks + ((u * s.n) + i0 + r) * s.top;
         if (nv <= s.top) {
             for (int x = lane; x < s.top; x += 32) out[x] = x < nv ? x : -1;
             continue;
         }
         float* v = scores + r * a.stride;
         // the query's own position: its limit is one behind it, or (not causal) the length is
-        const int64_t len = key_count(s, b);
-        const int64_t p = s.causal ? lim - 1 : (s.starts ? (int64_t)s.starts[b] : len - s.n) + i0 + r;
+        const int64_t p = s.causal ? lim - 1 : (s.starts ? (int64_t)s.starts[b] : lim - s.n) + i0 + r;
         const int home = (int)(p / kBlockKeys);
+        // forced: below `sink`, and from near0 (not below sink) to near1
+        const int sink = min(a.sink, nv), near0 = max(home - a.local + 1, sink), near1 = min(home + a.local, nv);
+        const int near = max(near1 - near0, 0), forced = sink + near, want = s.top - forced;
+        for (int x = lane; x < forced; x += 32) v[x < sink ? x : near0 + x - sink] = -INFINITY;
+        for (int c = nv + lane; c < (nv + 31) / 32 * 32; c += 32) v[c] = -INFINITY;
+        __syncwarp();
+        // 2 eps, and what products of denormal size may lose
+        const float eps = 2.02f * 68.f * 1.1920929e-7f * (float)s.G * mass[r] * top_mean + 1e-35f;
+        uint64_t taken = 0;                                  // of the candidates: first those of lane 0 .. 31, then the others
+        int cand[2] = {0, 0}, few = -1;                      // a lane's candidates by rising index; their number, -1: not had
+        if (want == 0) {
+            few = 0;
+        } else if (want <= 32 && eps < 1e30f) {
+            few = narrow(v, nv, want, eps, lane, cand_x[warp], cand_c[warp], cand, &taken, [&](int c) {
+                return exact_score(reinterpret_cast<const uint32_t*>(q + r * kHeadDim), s.n * (kHeadDim / 2), s.G,
+                                   reinterpret_cast<const uint32_t*>(means + (int64_t)c * kHeadDim), lane);
+            });
+        }
+        if (few >= 0) {                                      // ranks among the chosen and the forced
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (!(taken >> (32 * j + lane) & 1)) continue;
+                const uint64_t below = taken & ((uint64_t(1) << (32 * j + lane)) - 1);
+                const int c = cand[j];
+                out[__popcll(below) + (c >= sink ? sink + min(max(c - near0, 0), near) : 0)] = c;
+            }
+            for (int x = 0; x < forced; ++x) {
+                const int c = x < sink ? x : near0 + x - sink;
+                const unsigned lo = __ballot_sync(kFull, cand[0] < c), hi = __ballot_sync(kFull, cand[1] < c);
+                if (lane == 0) out[x + __popcll(taken & (lo | (uint64_t)hi << 32))] = c;
+            }
+            continue;
+        }
+        // the long way: any number of blocks and any scores
+        for (int x = lane; x < forced; x += 32) v[x < sink ? x : near0 + x - sink] = INFINITY;
+        __syncwarp();
         float lo = INFINITY, hi = -INFINITY;
         const int padded = (nv + 127) / 128 * 128;
         for (int c = lane; c < padded; c += 32) {
-            float x = -INFINITY;
-            if (c < nv) {
-                if (c < a.sink || abs(c - home) < a.local) {
-                    x = INFINITY;
-                } else {
-                    x = fminf(fmaxf(v[c], -FLT_MAX), FLT_MAX);       // (NaN: the lowest)
-                    lo = fminf(lo, x);
-                    hi = fmaxf(hi, x);
-                }
+            float x = c < nv ? v[c] : -INFINITY;
+            if (c < nv && !((unsigned)c < (unsigned)sink || (c >= near0 && c < near1))) {
+                x = fminf(fmaxf(x, -FLT_MAX), FLT_MAX);      // (NaN: the lowest)
+                lo = fminf(lo, x);
+                hi = fmaxf(hi, x);
             }
             v[c] = x;
         }
         __syncwarp();
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) {
-            lo = fminf(lo, __shfl_xor_sync(kFull, lo, off));
-            hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, off));
-        }
-        // the top-th largest value, kth: at least top values reach lo, fewer than top pass hi
+        lo = -warp_max(-lo);
+        hi = warp_max(hi);
+        // the top-th largest value, kth: at least top values reach lo, fewer than top reach hi
         float kth;
         auto reach = [&](float x) {
             int n = 0;
@@ -217,17 +346,13 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
                     float least = INFINITY;
                     for (int c = lane; c < nv; c += 32)
                         if (v[c] >= mid) least = fminf(least, v[c]);
-#pragma unroll
-                    for (int off = 16; off >= 1; off >>= 1) least = fminf(least, __shfl_xor_sync(kFull, least, off));
-                    kth = least;
+                    kth = -warp_max(-least);
                     break;
                 }
                 if (n > s.top) lo = mid;
                 else hi = mid;
             }
         }
-        // 2 eps (and what products of denormal size may lose)
-        const float eps = 2.02f * 68.f * 1.1920929e-7f * (float)s.G * mass[r] * top_mean + 1e-35f;
         const bool far = !(eps < 1e30f) || !(fabsf(kth) < 1e30f);
         const float above = far ? INFINITY : kth + eps, below = far ? -INFINITY : kth - eps;
         int sure = 0, open = 0;
@@ -239,25 +364,25 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
         sure = __reduce_add_sync(kFull, sure);
         open = __reduce_add_sync(kFull, open);
         if (sure + open > s.top) {
-            const int want = s.top - sure;                   // 0 where the forced blocks are all
+            const int rest = s.top - sure;                   // 0 where the forced blocks are all
             Best best;
             const uint32_t* row = reinterpret_cast<const uint32_t*>(q + r * kHeadDim);
             for (int c0 = 0; c0 < nv; c0 += 32) {
                 const int c = c0 + lane;
                 const float x = c < nv ? v[c] : -INFINITY;
-                const bool near = c < nv && x != INFINITY && !(x > above) && x >= below;
-                for (unsigned m = __ballot_sync(kFull, near); want && m; m &= m - 1) {
+                const bool close = c < nv && x != INFINITY && !(x > above) && x >= below;
+                for (unsigned m = __ballot_sync(kFull, close); rest && m; m &= m - 1) {
                     const int index = c0 + __ffs(m) - 1;
                     const double score = exact_score(row, s.n * (kHeadDim / 2), s.G,
                                                      reinterpret_cast<const uint32_t*>(means + (int64_t)index * kHeadDim), lane);
-                    best.offer(score, index, want, lane);
+                    best.offer(score, index, rest, lane);
                 }
-                if (near) v[c] = -INFINITY;
+                if (close) v[c] = -INFINITY;
             }
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                if (lane + 32 * j < want) v[best.c[j]] = INFINITY;
+                if (lane + 32 * j < rest) v[best.c[j]] = INFINITY;
             __syncwarp();
         } else {
             for (int c = lane; c < nv; c += 32)

@@ -35,6 +35,8 @@ __device__ __forceinline__ int32_t row_limit(const SelectShape& s, int64_t b, in
     if (p < 0 || p >= len) return 0;
     return (int32_t)(s.causal ? p + 1 : len);
 }
+// Unit u = b Hk + h of a launch (units are fewer than 2^31).
+__device__ __forceinline__ uint32_t sequence_of(const SelectShape& s, int64_t u) { return (uint32_t)u / (uint32_t)s.Hk; }
 __device__ __forceinline__ int32_t key_count(const SelectShape& s, int64_t b) {
     return s.lengths ? min(max(s.lengths[b], 0), (int32_t)s.m) : (int32_t)s.m;
 }

@@ -51,11 +51,12 @@ __global__ void __launch_bounds__(32 * kFewWarps) selected_few_kernel(const __gr
     const SelectShape& s = a.s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int warps = blockDim.x >> 5, octets = (s.G + 7) / 8;
-    const int64_t row = blockIdx.x / octets, u = row / s.n, i = row % s.n, b = u / s.Hk;
-    const int h0 = (int)(blockIdx.x % octets) * 8, heads = min(8, s.G - h0);
-    const int64_t first = (b * s.Hq + (u % s.Hk) * s.G + h0) * s.n + i;      // row of head h: + h n
+    const uint32_t row = octets == 1 ? blockIdx.x : blockIdx.x / octets;
+    const int64_t u = s.n == 1 ? row : row / (uint32_t)s.n, i = row - u * s.n, b = sequence_of(s, u);
+    const int h0 = (int)(blockIdx.x - row * octets) * 8, heads = min(8, s.G - h0);
+    const int64_t first = (u * s.G + h0) * s.n + i;                // row of head h: + h n
     const int32_t limit = row_limit(s, b, i);
-    const int32_t* list = a.blocks + row * s.top;
+    const int32_t* list = a.blocks + (int64_t)row * s.top;
 
     uint32_t q[8];
     load_row(a.q + (first + g * s.n) * kHeadDim, g < heads, t, q);
@@ -156,11 +157,19 @@ struct Partials {
     int64_t u0;
 };
 
-__global__ void __launch_bounds__(32 * kItemWarps)
+// 32 bytes, a whole sector, in one store.
+__device__ __forceinline__ void store32(float* p, float a, float b, float c, float d, float e, float f, float g, float h) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d), "f"(e),
+                 "f"(f), "f"(g), "f"(h)
+                 : "memory");
+}
+
+__global__ void __launch_bounds__(32 * kItemWarps, 2)
 selected_items_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials out) {
     const SelectShape& s = a.s;
-    const int64_t u = out.u0 + blockIdx.x / l.most_items, b = u / s.Hk;
-    const ItemRows item = item_of(l, s, u, blockIdx.x % l.most_items);
+    const uint32_t ul = blockIdx.x / (uint32_t)l.most_items;
+    const int64_t u = out.u0 + ul, b = sequence_of(s, u);
+    const ItemRows item = item_of(l, s, u, blockIdx.x - ul * l.most_items);
     if (!item.rows) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int32_t key0 = item.block * kBlockKeys;
@@ -169,92 +178,135 @@ selected_items_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     load_keys(a.k + (u * s.m + key0) * kHeadDim, rows, lane, keys);
     load_keys(a.v + (u * s.m + key0) * kHeadDim, rows, lane, values);
     turn_values(values);
-    const __nv_bfloat16* q0 = a.q + (b * s.Hq + (u % s.Hk) * s.G) * s.n * kHeadDim;
-    const int64_t slot0 = (u - out.u0) * s.n * s.G * l.ranks;
+    const __nv_bfloat16* q0 = a.q + u * s.G * s.n * kHeadDim;
+    const int64_t slot0 = (int64_t)ul * s.n * s.G * l.ranks;
 
-    for (int r0 = 8 * warp; r0 < item.rows; r0 += 8 * kItemWarps) {
-        const bool live = r0 + g < item.rows;
-        const uint32_t r = item.first + (live ? r0 + g : 0), e = r / s.G, h = r - e * s.G;
-        const uint32_t entry = item.entries[e], i = entry >> 6;
-        uint32_t q[8];
-        load_row(q0 + ((int64_t)h * s.n + i) * kHeadDim, live, t, q);
-        const uint32_t mine = live ? (i * s.G + h) * l.ranks + (entry & 63) : ~0u;
-        const int sees = live ? row_limit(s, b, i) - key0 : 0;
-        float x[4][4];
-        score(keys, q, x);
-        int limit[2];
-        uint32_t slot[2];
+    // rows r0 + g and r0 + 8 + g of this lane: their entries two steps ahead, their queries one
+    struct Rows {
+        uint32_t entry[2], head[2];
+    };
+    auto look = [&](int r0) {
+        Rows x;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            limit[c] = __shfl_sync(kFull, sees, 8 * t + 4 * c);
-            slot[c] = __shfl_sync(kFull, mine, 8 * t + 4 * c);
+        for (int j = 0; j < 2; ++j) {
+            const int row = r0 + 8 * j + g;
+            const uint32_t r = item.first + (row < item.rows ? row : 0), e = s.G == 1 ? r : r / s.G;
+            x.head[j] = r - e * s.G;
+            x.entry[j] = item.entries[e];
         }
-        float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+        return x;
+    };
+    auto fetch = [&](const Rows& x, int r0, uint32_t (&q)[2][8]) {
 #pragma unroll
-        for (int M = 0; M < 4; ++M)
+        for (int j = 0; j < 2; ++j)
+            load_row(q0 + ((int64_t)x.head[j] * s.n + (x.entry[j] >> 6)) * kHeadDim, r0 + 8 * j + g < item.rows, t, q[j]);
+    };
+    constexpr int kStep = 16 * kItemWarps;
+    Rows now = look(16 * warp), next = look(16 * warp + kStep);
+    uint32_t q[2][8];
+    fetch(now, 16 * warp, q);
+    for (int r0 = 16 * warp; r0 < item.rows; r0 += kStep) {
+        float x[2][4][4];
+        uint32_t mine[2];
+        int sees[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[M][j] = 16 * M + 8 * (j >> 1) + g < limit[j & 1] ? x[M][j] * kScale2 : -INFINITY;
-                m[j & 1] = fmaxf(m[j & 1], x[M][j]);
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t i = now.entry[j] >> 6;
+            const bool live = r0 + 8 * j + g < item.rows;
+            mine[j] = live ? (i * s.G + now.head[j]) * l.ranks + (now.entry[j] & 63) : ~0u;
+            sees[j] = live ? row_limit(s, b, i) - key0 : 0;
+            score(keys, q[j], x[j]);
+        }
+        now = next;
+        fetch(now, r0 + kStep, q);
+        next = look(r0 + 2 * kStep);
+        const bool whole = __all_sync(kFull, min(sees[0], sees[1]) >= kBlockKeys);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (!whole) {
+                const int limit[2] = {__shfl_sync(kFull, sees[j], 8 * t), __shfl_sync(kFull, sees[j], 8 * t + 4)};
+#pragma unroll
+                for (int M = 0; M < 4; ++M)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (16 * M + 8 * (c >> 1) + g >= limit[c & 1]) x[j][M][c] = -INFINITY;
             }
+            float m[2], sum[2] = {0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            m[c] = column_max(m[c]);
-            const float base = m[c] == -INFINITY ? 0.f : m[c];
+            for (int c = 0; c < 2; ++c) {
+                m[c] = fmaxf(x[j][0][c], x[j][0][c + 2]);
 #pragma unroll
-            for (int M = 0; M < 4; ++M)
+                for (int M = 1; M < 4; ++M) m[c] = fmaxf(m[c], fmaxf(x[j][M][c], x[j][M][c + 2]));
+                m[c] = column_max(m[c]) * kScale2;
+                const float base = m[c] == -INFINITY ? 0.f : m[c];
 #pragma unroll
-                for (int j = c; j < 4; j += 2) {
-                    x[M][j] = exp2_fast(x[M][j] - base);
-                    sum[c] += x[M][j];
-                }
-            sum[c] = column_sum(sum[c]);
-        }
-        float o[4][4];
+                for (int M = 0; M < 4; ++M)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) o[j >> 2][j & 3] = 0.f;
-        weigh(values, x, o);
+                    for (int k = c; k < 4; k += 2) {
+                        x[j][M][k] = exp2_fast(fmaf(x[j][M][k], kScale2, -base));
+                        sum[c] += x[j][M][k];
+                    }
+            }
+            float o[4][4];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            if (slot[c] == ~0u) continue;
-            float4* dst = reinterpret_cast<float4*>(out.sums + (slot0 + slot[c]) * kHeadDim) + 2 * g;
-            dst[0] = make_float4(o[0][c], o[0][c + 2], o[1][c], o[1][c + 2]);
-            dst[1] = make_float4(o[2][c], o[2][c + 2], o[3][c], o[3][c + 2]);
-            if (g == 0) out.stat[slot0 + slot[c]] = make_float2(m[c], sum[c]);
+            for (int k = 0; k < 16; ++k) o[k >> 2][k & 3] = 0.f;
+            weigh(values, x[j], o);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                sum[c] = column_sum(sum[c]);
+                const uint32_t slot = __shfl_sync(kFull, mine[j], 8 * t + 4 * c);
+                if (slot == ~0u) continue;
+                store32(out.sums + (slot0 + slot) * kHeadDim + 8 * g, o[0][c], o[0][c + 2], o[1][c], o[1][c + 2], o[2][c],
+                        o[2][c + 2], o[3][c], o[3][c + 2]);
+                if (g == 0) out.stat[slot0 + slot] = make_float2(m[c], sum[c]);
+            }
         }
     }
 }
 
+constexpr int kJoined = 8;                   // partials in flight
+
 // Sixteen lanes join a row's partials.
 __global__ void __launch_bounds__(256)
 selected_join_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials in,
-                     int64_t rows) {
+                     uint32_t rows) {
     const SelectShape& s = a.s;
     const int lane = threadIdx.x & 15;
     const unsigned half = 0xffffu << (threadIdx.x & 16);
-    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);       // ((u - u0) n + i) G + h
+    const uint32_t row = blockIdx.x * 16 + (threadIdx.x >> 4);
     if (row >= rows) return;
-    const int64_t entry = row / s.G, u = in.u0 + entry / s.n, i = entry % s.n, h = row % s.G;
-    const int count = l.live[in.u0 * s.n + entry];
-    const float2* stat = in.stat + row * l.ranks;
-    float top = -INFINITY;
-    for (int x = lane; x < count; x += 16) top = fmaxf(top, stat[x].x);
-#pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(half, top, off));
-    const float base = top == -INFINITY ? 0.f : top;
-    const float4* part = reinterpret_cast<const float4*>(in.sums + row * l.ranks * kHeadDim) + lane;
+    const RowOf at = row_of(s, in.u0, row);
+    const int count = l.live[in.u0 * s.n + at.entry];
+    const float2* stat = in.stat + (int64_t)row * l.ranks;
+    const float4* part = reinterpret_cast<const float4*>(in.sums + (int64_t)row * l.ranks * kHeadDim) + lane;
+    // eight partials at a time, under a running maximum
+    float top = -INFINITY, sum = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int x = 0; x < count; ++x) {
-        const float4 p = part[x * 16];
-        const float2 st = stat[x];
-        const float w = exp2_fast(st.x - base);
-        sum += w * st.y;
-        y.x += w * p.x;
-        y.y += w * p.y;
-        y.z += w * p.z;
-        y.w += w * p.w;
+    for (int x0 = 0; x0 < count; x0 += kJoined) {
+        float4 p[kJoined];
+        float2 st[kJoined];
+#pragma unroll
+        for (int x = 0; x < kJoined; ++x) {
+            const bool on = x0 + x < count;
+            p[x] = on ? part[(x0 + x) * 16] : make_float4(0.f, 0.f, 0.f, 0.f);
+            st[x] = on ? stat[x0 + x] : make_float2(-INFINITY, 0.f);
+        }
+        float now = top;
+#pragma unroll
+        for (int x = 0; x < kJoined; ++x) now = fmaxf(now, st[x].x);
+        const float base = now == -INFINITY ? 0.f : now, shrink = exp2_fast(top - base);
+        sum *= shrink;
+        y = make_float4(y.x * shrink, y.y * shrink, y.z * shrink, y.w * shrink);
+#pragma unroll
+        for (int x = 0; x < kJoined; ++x) {
+            const float w = exp2_fast(st[x].x - base);
+            sum += w * st[x].y;
+            y.x += w * p[x].x;
+            y.y += w * p[x].y;
+            y.z += w * p[x].z;
+            y.w += w * p[x].w;
+        }
+        top = now;
     }
     const float r = top != -INFINITY ? 1.f / sum : 0.f;
     // this lane has features 2k + e of an eight, k = 0 .. 3, its neighbour two lanes on the other e
@@ -262,9 +314,8 @@ selected_join_kernel(const __grid_constant__ SelectedArgs a, const __grid_consta
     const float z[4] = {y.x * r, y.y * r, y.z * r, y.w * r};
     const float got0 = __shfl_xor_sync(half, e ? z[0] : z[2], 2), got1 = __shfl_xor_sync(half, e ? z[1] : z[3], 2);
     const uint2 w = e ? make_uint2(pack(got0, z[2]), pack(got1, z[3])) : make_uint2(pack(z[0], got0), pack(z[1], got1));
-    const int64_t at = ((u / s.Hk * s.Hq) + (u % s.Hk) * s.G + h) * s.n + i;
-    *reinterpret_cast<uint2*>(a.out + at * kHeadDim + 32 * (lane & 1) + 8 * (g >> 1) + 4 * e) = w;
-    if (a.lse && lane == 0) a.lse[at] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+    *reinterpret_cast<uint2*>(a.out + at.place * kHeadDim + 32 * (lane & 1) + 8 * (g >> 1) + 4 * e) = w;
+    if (a.lse && lane == 0) a.lse[at.place] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 struct Plan {
@@ -292,7 +343,7 @@ int launch_items(const SelectedArgs& a, char* ws, cudaStream_t stream) {
     for (int64_t u0 = 0; u0 < units; u0 += p.group) {
         const int64_t here = units - u0 < p.group ? units - u0 : p.group, rows = here * s.n * s.G;
         const Partials part{reinterpret_cast<float*>(ws + p.sums), reinterpret_cast<float2*>(ws + p.stat), u0};
-        if (here * p.lists.most_items > INT32_MAX || (rows + 15) / 16 > INT32_MAX)
+        if (here * p.lists.most_items > INT32_MAX || rows > INT32_MAX)
             return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
         {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
@@ -300,7 +351,7 @@ int launch_items(const SelectedArgs& a, char* ws, cudaStream_t stream) {
         }
         {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-            selected_join_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, stream>>>(a, p.lists, part, rows);
+            selected_join_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, stream>>>(a, p.lists, part, (uint32_t)rows);
         }
     }
     const cudaError_t err = cudaGetLastError();

@@ -51,6 +51,9 @@ __device__ __forceinline__ void ldmatrix_turned(uint32_t at, uint32_t (&r)[4]) {
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy8(uint32_t to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
 
@@ -78,20 +81,21 @@ __global__ void __launch_bounds__(256) selected_delta_kernel(const __grid_consta
     if (row < rows && lane == 0) stat[row] = make_float2(a.lse[row] * kLog2e, d);
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials out) {
     __shared__ __align__(128) char rows_smem[2][2][kTile * kRowBytes];       // [stage][queries, dout]; first the keys, values
     __shared__ __align__(128) char turn_smem[kBlockKeys * kTurnStride];      // dS [key][row]
     __shared__ float2 stat_smem[2][kTile];
     __shared__ int2 meta_smem[2][kTile];                                     // visible keys of the block, slot
     const SelectShape& s = a.s;
-    const int64_t ul = blockIdx.x / l.most_items, u = out.u0 + ul, b = u / s.Hk;
-    const ItemRows item = item_of(l, s, u, blockIdx.x % l.most_items);
+    const uint32_t ul = blockIdx.x / (uint32_t)l.most_items;
+    const int64_t u = out.u0 + ul, b = sequence_of(s, u);
+    const ItemRows item = item_of(l, s, u, blockIdx.x - ul * l.most_items);
     if (!item.rows) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int32_t key0 = item.block * kBlockKeys;
     const int keys = min(kBlockKeys, key_count(s, b) - key0);
-    const int64_t head0 = b * s.Hq + (u % s.Hk) * s.G;
+    const int64_t head0 = u * s.G;
     const uint32_t smem = ptx::smem_u32(rows_smem), turned = ptx::smem_u32(turn_smem);
 
     // the keys' and values' operands, by way of the rows' buffers
@@ -122,7 +126,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     // rows of step x: this thread's two entries, and their copies
     const int steps = (item.rows + kTile - 1) / kTile;
     auto entry_of = [&](int row, uint32_t* h) -> uint32_t {                  // of a row of the item
-        const uint32_t r = item.first + (row < item.rows ? row : 0), e = r / s.G;
+        const uint32_t r = item.first + (row < item.rows ? row : 0), e = s.G == 1 ? r : r / s.G;
         *h = r - e * s.G;
         return item.entries[e];
     };
@@ -143,7 +147,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
             copy16(to, a.q + row * kHeadDim + 8 * c, live);
             copy16(to + kTile * kRowBytes, a.dout + row * kHeadDim + 8 * c, live);
             if (c == 0) {
-                stat_smem[stage][r] = out.stat[row];
+                copy8(ptx::smem_u32(&stat_smem[stage][r]), out.stat + row);
                 meta_smem[stage][r] = live ? make_int2(row_limit(s, b, i) - key0, (i * s.G + head[j]) * l.ranks + (entry[j] & 63))
                                            : make_int2(0, -1);
             }
@@ -157,7 +161,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     float dk[8][4], dv[8][4];
 #pragma unroll
     for (int j = 0; j < 32; ++j) dk[j >> 2][j & 3] = dv[j >> 2][j & 3] = 0.f;
-    const int64_t slot0 = ul * s.n * s.G * l.ranks;
+    const int64_t slot0 = (int64_t)ul * s.n * s.G * l.ranks;
 
     for (int x = 0; x < steps; ++x) {
         copies_wait<0>();
@@ -244,7 +248,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
             }
         }
     }
-    float* dst = out.dkv + (ul * l.most_items + blockIdx.x % l.most_items) * (2 * kBlockKeys * kHeadDim) +
+    float* dst = out.dkv + (int64_t)blockIdx.x * (2 * kBlockKeys * kHeadDim) +
                  (16 * warp + g) * kHeadDim + 2 * t;
 #pragma unroll
     for (int f = 0; f < 8; ++f)
@@ -258,52 +262,46 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
 
 // dq of a row: the sum of its partials, sixteen lanes a row.
 __global__ void __launch_bounds__(256)
-selected_dq_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials in, int64_t rows) {
+selected_dq_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials in, uint32_t rows) {
     const SelectShape& s = a.s;
     const int lane = threadIdx.x & 15;
-    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);       // ((u - u0) n + i) G + h
+    const uint32_t row = blockIdx.x * 16 + (threadIdx.x >> 4);
     if (row >= rows) return;
-    const int64_t entry = row / s.G, u = in.u0 + entry / s.n, i = entry % s.n, h = row % s.G;
-    const int count = l.live[in.u0 * s.n + entry];
-    const float4* part = reinterpret_cast<const float4*>(in.dq + row * l.ranks * kHeadDim) + lane;
+    const RowOf at = row_of(s, in.u0, row);
+    const int count = l.live[in.u0 * s.n + at.entry];
+    const float4* part = reinterpret_cast<const float4*>(in.dq + (int64_t)row * l.ranks * kHeadDim) + lane;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int x = 0; x < count; ++x) {
         const float4 p = part[x * 16];
         y = make_float4(y.x + p.x, y.y + p.y, y.z + p.z, y.w + p.w);
     }
-    const int64_t at = ((u / s.Hk * s.Hq) + (u % s.Hk) * s.G + h) * s.n + i;
-    reinterpret_cast<uint2*>(a.dq + at * kHeadDim)[lane] = make_uint2(pack(y.x, y.y), pack(y.z, y.w));
+    reinterpret_cast<uint2*>(a.dq + at.place * kHeadDim)[lane] = make_uint2(pack(y.x, y.y), pack(y.z, y.w));
 }
 
-// dk and dv of a key block: the sums of its items'.
+// dk and dv of a key block: the sums of its items', by sixteen rows of keys; eight items in flight.
+constexpr int kSplit = 4;
 __global__ void __launch_bounds__(256)
 selected_dkv_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials in) {
     const SelectShape& s = a.s;
-    const int64_t ul = blockIdx.x / s.nb, u = in.u0 + ul;
-    const int c = blockIdx.x % s.nb;
+    const int split = blockIdx.x % (2 * kSplit), part = split % kSplit, which = split / kSplit;
+    const uint32_t at = blockIdx.x / (2 * kSplit), ul = at / (uint32_t)s.nb;
+    const int64_t u = in.u0 + ul;
+    const int c = at - ul * s.nb;
     const int32_t* base = l.item_base + u * (s.nb + 1) + c;
     const int from = base[0], to = base[1];
-    const int64_t key0 = (int64_t)c * kBlockKeys;
-    const int keys = (int)min((int64_t)kBlockKeys, s.m - key0);
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-        __nv_bfloat16* dst = (which ? a.dv : a.dk) + (u * s.m + key0) * kHeadDim;
-        const float4* part = reinterpret_cast<const float4*>(in.dkv) + ((ul * l.most_items + from) * 2 + which) * 1024 + threadIdx.x;
-        float4 y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int x = from; x < to; ++x, part += 2048)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 p = part[256 * j];
-                y[j] = make_float4(y[j].x + p.x, y[j].y + p.y, y[j].z + p.z, y[j].w + p.w);
-            }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if ((threadIdx.x >> 4) + 16 * j < keys)
-                reinterpret_cast<uint2*>(dst)[threadIdx.x + 256 * j] = make_uint2(pack(y[j].x, y[j].y), pack(y[j].z, y[j].w));
+    const int64_t key = (int64_t)c * kBlockKeys + 16 * part + (threadIdx.x >> 4);
+    if (key >= s.m) return;
+    const float4* src = reinterpret_cast<const float4*>(in.dkv) +
+                        (((int64_t)ul * l.most_items + from) * 2 + which) * 1024 + 256 * part + threadIdx.x;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int x = 0; x < to - from; ++x) {
+        const float4 p = src[(int64_t)x * 2048];
+        y = make_float4(y.x + p.x, y.y + p.y, y.z + p.z, y.w + p.w);
     }
+    __nv_bfloat16* dst = (which ? a.dv : a.dk) + (u * s.m + key) * kHeadDim;
+    reinterpret_cast<uint2*>(dst)[threadIdx.x & 15] = make_uint2(pack(y.x, y.y), pack(y.z, y.w));
 }
 
 struct Plan {
@@ -346,7 +344,7 @@ int launch_selected_backward(const SelectedArgs& a, char* ws, cudaStream_t strea
         const int64_t here = units - u0 < p.group ? units - u0 : p.group, rows = here * s.n * s.G;
         const Partials part{reinterpret_cast<float*>(ws + p.dq), reinterpret_cast<float*>(ws + p.dkv),
                             reinterpret_cast<const float2*>(ws + p.stat), u0};
-        if (here * p.lists.most_items > INT32_MAX || (rows + 15) / 16 > INT32_MAX || here * s.nb > INT32_MAX)
+        if (here * p.lists.most_items > INT32_MAX || rows > INT32_MAX || here * s.nb * 2 * kSplit > INT32_MAX)
             return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
         {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
@@ -354,11 +352,11 @@ int launch_selected_backward(const SelectedArgs& a, char* ws, cudaStream_t strea
         }
         {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-            selected_dq_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, stream>>>(a, p.lists, part, rows);
+            selected_dq_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, stream>>>(a, p.lists, part, (uint32_t)rows);
         }
         {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-            selected_dkv_kernel<<<(unsigned)(here * s.nb), 256, 0, stream>>>(a, p.lists, part);
+            selected_dkv_kernel<<<(unsigned)(here * s.nb * 2 * kSplit), 256, 0, stream>>>(a, p.lists, part);
         }
     }
     const cudaError_t err = cudaGetLastError();
