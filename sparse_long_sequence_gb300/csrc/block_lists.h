@@ -46,6 +46,13 @@ __device__ __forceinline__ RowOf row_of(const SelectShape& s, int64_t u0, uint32
 }
 #endif
 
+// Rows of an item: four tiles of 128, fewer where there would be no two rounds of `resident` items
+// an SM.
+inline int32_t item_rows(const SelectShape& s, int resident) {
+    const int64_t rows = s.B * s.Hq * s.n * (s.top < s.nb ? s.top : s.nb), wave = 152 * 2 * (int64_t)resident;
+    return rows >= 512 * wave ? 512 : rows >= 256 * wave ? 256 : 128;
+}
+
 // Sizes, and the addresses in `ws` (null: sizes alone); returns the bytes.
 size_t plan_block_lists(const SelectShape& s, int32_t item_rows, char* ws, BlockLists* l);
 int launch_block_lists(const SelectShape& s, const int32_t* blocks, const BlockLists& l, cudaStream_t stream);

@@ -22,6 +22,8 @@ struct ProjStatus {
     int* h = nullptr;
 };
 int projection_status(ProjStatus* out);
+// its device word, or DIFFUSER_ERR_DEVICE where a kernel has reported a failure (layer_ops_abi.cu)
+int ready_status(int** word);
 int check_workspace_bytes(size_t need, void* ws, size_t ws_bytes);
 
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel and device.

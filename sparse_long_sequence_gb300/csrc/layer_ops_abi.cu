@@ -63,16 +63,6 @@ int check_dense(int64_t T, int64_t D, int64_t F, int32_t act) {
     return DIFFUSER_OK;
 }
 
-int ready_status(int** word) {
-    ProjStatus ps;
-    const int st = projection_status(&ps);
-    if (st) return st;
-    if (*reinterpret_cast<volatile int*>(ps.h) != 0)
-        return fail(DIFFUSER_ERR_DEVICE, "a projection or dense product kernel reported a failure (see diffuser_projection_status)");
-    *word = ps.d;
-    return DIFFUSER_OK;
-}
-
 int zero(void* p, size_t bytes, cudaStream_t stream) {
     if (!p) return DIFFUSER_OK;
     const cudaError_t err = cudaMemsetAsync(p, 0, bytes, stream);
@@ -116,6 +106,17 @@ int launch_both(const DenseArgs& a, const void* W, void* dX, const void* X, void
 }
 
 }  // namespace
+
+int ready_status(int** word) {
+    ProjStatus ps;
+    const int st = projection_status(&ps);
+    if (st) return st;
+    if (*reinterpret_cast<volatile int*>(ps.h) != 0)
+        return fail(DIFFUSER_ERR_DEVICE, "a projection or dense product kernel reported a failure (see diffuser_projection_status)");
+    *word = ps.d;
+    return DIFFUSER_OK;
+}
+
 }  // namespace dfs
 
 using namespace dfs;

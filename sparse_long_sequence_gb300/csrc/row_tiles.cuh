@@ -1,0 +1,75 @@
+// Tiles of 128 gathered rows against a block of 64 keys on the tcgen05 tensor cores: what the
+// attention over chosen blocks (selected_attention.cu) and its backward (selected_backward.cu) share.
+//
+// A tile in shared memory has rows of 128 bytes (64 bf16 values) under the 128-byte swizzle, 1024-byte
+// aligned: as it lies it is a K-major operand whose rows are the product's rows (or columns) and, read
+// MN-major, one whose rows are summed over.
+#pragma once
+
+#include "block_lists.h"
+#include "dense_ptx.cuh"
+#include "selected.h"
+
+namespace dfs {
+namespace tiles {
+
+constexpr int kTileRows = 128;
+constexpr int kRowBytes = kHeadDim * 2;
+constexpr int kTileBytes = kTileRows * kRowBytes;
+constexpr int kKeyBytes = kBlockKeys * kRowBytes;
+
+// Byte of 16-byte chunk `chunk` of a row.
+__device__ __forceinline__ uint32_t place(int row, int chunk) { return row * kRowBytes + ((chunk ^ (row & 7)) << 4); }
+
+// 16 bytes into shared memory; zeros, and nothing read, where `live` is false.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live ? 16 : 0) : "memory");
+}
+// The 64 keys (or values) at `from`, rows from `rows` on as zeros, by `threads` threads.
+template <int kThreads>
+__device__ __forceinline__ void copy_keys(uint32_t to, const __nv_bfloat16* from, int rows, int tid) {
+#pragma unroll
+    for (int x = tid; x < kBlockKeys * 8; x += kThreads) {
+        const int r = x >> 3, c = x & 7;
+        copy16(to + place(r, c), from + (r < rows ? r : 0) * kHeadDim + 8 * c, r < rows);
+    }
+}
+
+// A lane's row of a tile.
+struct Row {
+    uint32_t at;                   // of [G][n]: head * n + query
+    int32_t limit;                 // keys of the block that it sees (up to 64 or more)
+    uint32_t slot;                 // (query G + head) ranks + rank; ~0: there is no such row
+};
+// Its entry, and what follows from it.
+__device__ __forceinline__ uint32_t entry_of(const ItemRows& item, int G, int row, uint32_t* head) {
+    const uint32_t r = item.first + (row < item.rows ? row : 0), e = G == 1 ? r : r / G;
+    *head = r - e * G;
+    return item.entries[e];
+}
+__device__ __forceinline__ Row row_from(const SelectShape& s, int32_t ranks, int64_t b, int32_t key0, uint32_t entry,
+                                        uint32_t head, bool live) {
+    const uint32_t i = entry >> 6;
+    return {head * (uint32_t)s.n + i, live ? row_limit(s, b, i) - key0 : 0,
+            live ? (i * s.G + head) * ranks + (entry & 63) : ~0u};
+}
+// Copies a warp's 32 rows (its lanes' own) of a tile from [G][n][64] at `from`.
+__device__ __forceinline__ void copy_rows(uint32_t tile, const __nv_bfloat16* from, const Row& mine, int quarter, int lane) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int r = 4 * j + (lane >> 3), c = lane & 7;
+        const uint32_t at = __shfl_sync(0xffffffffu, mine.at, r);
+        const bool live = __shfl_sync(0xffffffffu, mine.slot, r) != ~0u;
+        copy16(tile + place(32 * quarter + r, c), from + (int64_t)at * kHeadDim + 8 * c, live);
+    }
+}
+
+// 32 bytes, a whole sector, in one store.
+__device__ __forceinline__ void store32(float* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+}  // namespace tiles
+}  // namespace dfs

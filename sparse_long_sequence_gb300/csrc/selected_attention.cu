@@ -6,10 +6,19 @@
 // columns of the products).  Its warps take the listed blocks in turn, each with a running maximum
 // and sum in registers, and join through shared memory.  A block's keys and values go from global
 // memory into the products' registers.  Bound by the cache's bytes, or by a launch.
+//
+// Many queries: block by block.  A block of four warps takes up to 512 rows (a query of a head)
+// that list a key block (block_lists.cu), 128 at a time: the rows' queries are gathered into shared
+// memory a tile ahead, S = Q K^T and O = P V run on tcgen05 with P handed over through tensor memory,
+// and each thread has one row's scores, maximum and sum, without exchanges.  Each (row, block) leaves
+// a partial result: 64 fp32 sums, its maximum and its sum, in the workspace; a second kernel joins a
+// row's partials.  The units go in groups whose partials stay in the L2.
 #include <atomic>
 
 #include "block_lists.h"
+#include "layer_ops.h"
 #include "mma_tiles.cuh"
+#include "row_tiles.cuh"
 #include "selected.h"
 
 namespace dfs {
@@ -146,122 +155,140 @@ int launch_few(const SelectedArgs& a, cudaStream_t stream) {
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "selected_few_kernel");
 }
 
-constexpr int kItemRows = 256;
-constexpr int kItemWarps = 4;
-constexpr size_t kGroupBytes = 64 << 20;     // partials of a group of units
+constexpr int kItemThreads = 128;
+constexpr int kItemSmem = 2 * kKeyBytes + 2 * kTileBytes;    // keys, values, two tiles of queries
+constexpr uint32_t kItemColumns = 128;                       // tensor memory: S (then P) and O
+constexpr size_t kGroupBytes = 64 << 20;                     // partials of a group of units
 
 // Partials of the units u0 .. : slot x = ((u - u0) n + i) G + h) ranks + rank.
 struct Partials {
-    float* sums;                             // [slots][64], features by place_of
+    float* sums;                             // [slots][64]
     float2* stat;                            // [slots]: maximum (units of log 2), sum
     int64_t u0;
 };
 
-// 32 bytes, a whole sector, in one store.
-__device__ __forceinline__ void store32(float* p, float a, float b, float c, float d, float e, float f, float g, float h) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d), "f"(e),
-                 "f"(f), "f"(g), "f"(h)
-                 : "memory");
-}
-
-__global__ void __launch_bounds__(32 * kItemWarps, 2)
-selected_items_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials out) {
+__global__ void __launch_bounds__(kItemThreads, 4)
+selected_items_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials out,
+                      int* status) {
+    extern __shared__ __align__(1024) char smem[];
+    __shared__ uint64_t bars[2];             // S is there; O is
+    __shared__ uint32_t tmem_slot;
     const SelectShape& s = a.s;
     const uint32_t ul = blockIdx.x / (uint32_t)l.most_items;
     const int64_t u = out.u0 + ul, b = sequence_of(s, u);
     const ItemRows item = item_of(l, s, u, blockIdx.x - ul * l.most_items);
     if (!item.rows) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t key0 = item.block * kBlockKeys;
-    const int rows = min(kBlockKeys, key_count(s, b) - key0);
-    uint32_t keys[8][8], values[8][8];
-    load_keys(a.k + (u * s.m + key0) * kHeadDim, rows, lane, keys);
-    load_keys(a.v + (u * s.m + key0) * kHeadDim, rows, lane, values);
-    turn_values(values);
+    const uint32_t keys = ptx::smem_u32(smem), values = keys + kKeyBytes, queries = values + kKeyBytes;
     const __nv_bfloat16* q0 = a.q + u * s.G * s.n * kHeadDim;
+    {
+        const int rows = min(kBlockKeys, key_count(s, b) - key0);
+        copy_keys<kItemThreads>(keys, a.k + (u * s.m + key0) * kHeadDim, rows, tid);
+        copy_keys<kItemThreads>(values, a.v + (u * s.m + key0) * kHeadDim, rows, tid);
+    }
+    uint32_t head, entry = entry_of(item, s.G, tid, &head);
+    Row now, next = row_from(s, l.ranks, b, key0, entry, head, tid < item.rows);
+    copy_rows(queries, q0, next, warp, lane);
+    entry = entry_of(item, s.G, kTileRows + tid, &head);
+    if (warp == 0) ptx::tmem_alloc(&tmem_slot, kItemColumns);
+    if (tid == 0) {
+        ptx::mbar_init(&bars[0], 1);
+        ptx::mbar_init(&bars[1], 1);
+        ptx::fence_mbar_init();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = tmem_slot, mine = tmem + ((uint32_t)(32 * warp) << 16);
+    constexpr uint32_t kScores = ptx::mma_idesc_bf16(kTileRows, kBlockKeys, false, false);
+    constexpr uint32_t kSums = ptx::mma_idesc_bf16(kTileRows, kHeadDim, false, true);
     const int64_t slot0 = (int64_t)ul * s.n * s.G * l.ranks;
+    const int tiles = (item.rows + kTileRows - 1) / kTileRows;
 
-    // rows r0 + g and r0 + 8 + g of this lane: their entries two steps ahead, their queries one
-    struct Rows {
-        uint32_t entry[2], head[2];
-    };
-    auto look = [&](int r0) {
-        Rows x;
+    for (int x = 0; x < tiles; ++x) {
+        ptx::cp_async_wait_all();
+        ptx::fence_proxy_async_smem();
+        __syncthreads();                     // the tile is there, and all have read the last O
+        if (warp == 0 && ptx::elect_one()) {
+            ptx::tc_fence_after();
+            const uint64_t qd = ptx::sw128_kmajor_desc(queries + (x & 1) * kTileBytes), kd = ptx::sw128_kmajor_desc(keys);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int row = r0 + 8 * j + g;
-            const uint32_t r = item.first + (row < item.rows ? row : 0), e = s.G == 1 ? r : r / s.G;
-            x.head[j] = r - e * s.G;
-            x.entry[j] = item.entries[e];
+            for (int e = 0; e < 4; ++e) ptx::mma_bf16_ss(tmem, qd + 2 * e, kd + 2 * e, kScores, e > 0);
+            ptx::mma_commit(&bars[0]);
         }
-        return x;
-    };
-    auto fetch = [&](const Rows& x, int r0, uint32_t (&q)[2][8]) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            load_row(q0 + ((int64_t)x.head[j] * s.n + (x.entry[j] >> 6)) * kHeadDim, r0 + 8 * j + g < item.rows, t, q[j]);
-    };
-    constexpr int kStep = 16 * kItemWarps;
-    Rows now = look(16 * warp), next = look(16 * warp + kStep);
-    uint32_t q[2][8];
-    fetch(now, 16 * warp, q);
-    for (int r0 = 16 * warp; r0 < item.rows; r0 += kStep) {
-        float x[2][4][4];
-        uint32_t mine[2];
-        int sees[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t i = now.entry[j] >> 6;
-            const bool live = r0 + 8 * j + g < item.rows;
-            mine[j] = live ? (i * s.G + now.head[j]) * l.ranks + (now.entry[j] & 63) : ~0u;
-            sees[j] = live ? row_limit(s, b, i) - key0 : 0;
-            score(keys, q[j], x[j]);
-        }
+        __syncwarp();
         now = next;
-        fetch(now, r0 + kStep, q);
-        next = look(r0 + 2 * kStep);
-        const bool whole = __all_sync(kFull, min(sees[0], sees[1]) >= kBlockKeys);
+        if (x + 1 < tiles) {
+            const int row = (x + 1) * kTileRows + tid;
+            next = row_from(s, l.ranks, b, key0, entry, head, row < item.rows);
+            copy_rows(queries + (~x & 1) * kTileBytes, q0, next, warp, lane);
+            entry = entry_of(item, s.G, row + kTileRows, &head);
+        }
+        ptx::mbar_wait(&bars[0], x & 1, status);
+        __syncwarp();
+        ptx::tc_fence_after();
+        uint32_t lo[32], hi[32];
+        ptx::tmem_ld32_issue(mine, lo);
+        ptx::tmem_ld32_issue(mine + 32, hi);
+        ptx::tmem_ld_wait32(lo);
+        ptx::tmem_ld_wait32(hi);
+        float top = -INFINITY;
+        if (__all_sync(kFull, now.limit >= kBlockKeys)) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (!whole) {
-                const int limit[2] = {__shfl_sync(kFull, sees[j], 8 * t), __shfl_sync(kFull, sees[j], 8 * t + 4)};
+            for (int j = 0; j < 32; ++j) top = fmaxf(top, fmaxf(__uint_as_float(lo[j]), __uint_as_float(hi[j])));
+        } else {
 #pragma unroll
-                for (int M = 0; M < 4; ++M)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (16 * M + 8 * (c >> 1) + g >= limit[c & 1]) x[j][M][c] = -INFINITY;
+            for (int j = 0; j < 32; ++j) {
+                if (j >= now.limit) lo[j] = 0xff800000u;     // -infinity
+                if (j + 32 >= now.limit) hi[j] = 0xff800000u;
+                top = fmaxf(top, fmaxf(__uint_as_float(lo[j]), __uint_as_float(hi[j])));
             }
-            float m[2], sum[2] = {0.f, 0.f};
+        }
+        top *= kScale2;
+        const float base = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        uint32_t p[2][16];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                m[c] = fmaxf(x[j][0][c], x[j][0][c + 2]);
+        for (int j = 0; j < 16; ++j) {
+            const float w0 = exp2_fast(fmaf(__uint_as_float(lo[2 * j]), kScale2, -base));
+            const float w1 = exp2_fast(fmaf(__uint_as_float(lo[2 * j + 1]), kScale2, -base));
+            const float w2 = exp2_fast(fmaf(__uint_as_float(hi[2 * j]), kScale2, -base));
+            const float w3 = exp2_fast(fmaf(__uint_as_float(hi[2 * j + 1]), kScale2, -base));
+            sum += (w0 + w1) + (w2 + w3);
+            p[0][j] = pack(w0, w1);
+            p[1][j] = pack(w2, w3);
+        }
+        ptx::tmem_st16x2(mine, p[0], mine + 16, p[1]);
+        ptx::tc_fence_before();
+        __syncthreads();                     // P is whole
+        if (warp == 0 && ptx::elect_one()) {
+            ptx::tc_fence_after();
+            const uint64_t vd = ptx::sw128_mnmajor_desc(values, kKeyBytes);
 #pragma unroll
-                for (int M = 1; M < 4; ++M) m[c] = fmaxf(m[c], fmaxf(x[j][M][c], x[j][M][c + 2]));
-                m[c] = column_max(m[c]) * kScale2;
-                const float base = m[c] == -INFINITY ? 0.f : m[c];
+            for (int e = 0; e < 4; ++e) ptx::mma_bf16_ts(tmem + 64, tmem + 8 * e, vd + 128 * e, kSums, e > 0);
+            ptx::mma_commit(&bars[1]);
+        }
+        __syncwarp();
+        if (now.slot != ~0u) out.stat[slot0 + now.slot] = make_float2(top, sum);
+        ptx::mbar_wait(&bars[1], x & 1, status);
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_ld32_issue(mine + 64, lo);
+        ptx::tmem_ld32_issue(mine + 96, hi);
+        ptx::tmem_ld_wait32(lo);
+        ptx::tmem_ld_wait32(hi);
+        ptx::tc_fence_before();
+        if (now.slot != ~0u) {
+            float* dst = out.sums + (slot0 + now.slot) * kHeadDim;
 #pragma unroll
-                for (int M = 0; M < 4; ++M)
+            for (int j = 0; j < 4; ++j) store32(dst + 8 * j, lo + 8 * j);
 #pragma unroll
-                    for (int k = c; k < 4; k += 2) {
-                        x[j][M][k] = exp2_fast(fmaf(x[j][M][k], kScale2, -base));
-                        sum[c] += x[j][M][k];
-                    }
-            }
-            float o[4][4];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) o[k >> 2][k & 3] = 0.f;
-            weigh(values, x[j], o);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                sum[c] = column_sum(sum[c]);
-                const uint32_t slot = __shfl_sync(kFull, mine[j], 8 * t + 4 * c);
-                if (slot == ~0u) continue;
-                store32(out.sums + (slot0 + slot) * kHeadDim + 8 * g, o[0][c], o[0][c + 2], o[1][c], o[1][c + 2], o[2][c],
-                        o[2][c + 2], o[3][c], o[3][c + 2]);
-                if (g == 0) out.stat[slot0 + slot] = make_float2(m[c], sum[c]);
-            }
+            for (int j = 0; j < 4; ++j) store32(dst + 32 + 8 * j, hi + 8 * j);
         }
     }
+    __syncthreads();
+    if (warp == 0) ptx::tmem_dealloc(tmem, kItemColumns);
 }
 
 constexpr int kJoined = 8;                   // partials in flight
@@ -272,7 +299,6 @@ selected_join_kernel(const __grid_constant__ SelectedArgs a, const __grid_consta
                      uint32_t rows) {
     const SelectShape& s = a.s;
     const int lane = threadIdx.x & 15;
-    const unsigned half = 0xffffu << (threadIdx.x & 16);
     const uint32_t row = blockIdx.x * 16 + (threadIdx.x >> 4);
     if (row >= rows) return;
     const RowOf at = row_of(s, in.u0, row);
@@ -309,12 +335,7 @@ selected_join_kernel(const __grid_constant__ SelectedArgs a, const __grid_consta
         top = now;
     }
     const float r = top != -INFINITY ? 1.f / sum : 0.f;
-    // this lane has features 2k + e of an eight, k = 0 .. 3, its neighbour two lanes on the other e
-    const int g = lane >> 1, e = g & 1;
-    const float z[4] = {y.x * r, y.y * r, y.z * r, y.w * r};
-    const float got0 = __shfl_xor_sync(half, e ? z[0] : z[2], 2), got1 = __shfl_xor_sync(half, e ? z[1] : z[3], 2);
-    const uint2 w = e ? make_uint2(pack(got0, z[2]), pack(got1, z[3])) : make_uint2(pack(z[0], got0), pack(z[1], got1));
-    *reinterpret_cast<uint2*>(a.out + at.place * kHeadDim + 32 * (lane & 1) + 8 * (g >> 1) + 4 * e) = w;
+    reinterpret_cast<uint2*>(a.out + at.place * kHeadDim)[lane] = make_uint2(pack(y.x * r, y.y * r), pack(y.z * r, y.w * r));
     if (a.lse && lane == 0) a.lse[at.place] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
@@ -325,7 +346,7 @@ struct Plan {
 };
 Plan plan_items(const SelectShape& s, char* ws) {
     Plan p;
-    p.sums = plan_block_lists(s, kItemRows, ws, &p.lists);
+    p.sums = plan_block_lists(s, item_rows(s, 4), ws, &p.lists);
     const int64_t units = s.B * s.Hk, slots = s.n * s.G * p.lists.ranks;
     p.group = slots ? (int64_t)(kGroupBytes / (slots * 264)) : 1;
     p.group = p.group < 1 ? 1 : p.group > units ? units : p.group;
@@ -337,8 +358,13 @@ Plan plan_items(const SelectShape& s, char* ws) {
 int launch_items(const SelectedArgs& a, char* ws, cudaStream_t stream) {
     const SelectShape& s = a.s;
     const Plan p = plan_items(s, ws);
-    int st = launch_block_lists(s, a.blocks, p.lists, stream);
+    static std::atomic<uint64_t> ready{0};
+    int* status = nullptr;
+    int st = ready_status(&status);
     if (st) return st;
+    cudaError_t err = allow_smem(selected_items_kernel, kItemSmem, ready);
+    if (err != cudaSuccess) return cuda_fail(err, "selected_items_kernel");
+    if ((st = launch_block_lists(s, a.blocks, p.lists, stream))) return st;
     const int64_t units = s.B * s.Hk;
     for (int64_t u0 = 0; u0 < units; u0 += p.group) {
         const int64_t here = units - u0 < p.group ? units - u0 : p.group, rows = here * s.n * s.G;
@@ -347,14 +373,15 @@ int launch_items(const SelectedArgs& a, char* ws, cudaStream_t stream) {
             return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
         {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-            selected_items_kernel<<<(unsigned)(here * p.lists.most_items), 32 * kItemWarps, 0, stream>>>(a, p.lists, part);
+            selected_items_kernel<<<(unsigned)(here * p.lists.most_items), kItemThreads, kItemSmem, stream>>>(a, p.lists, part,
+                                                                                                              status);
         }
         {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
             selected_join_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, stream>>>(a, p.lists, part, (uint32_t)rows);
         }
     }
-    const cudaError_t err = cudaGetLastError();
+    err = cudaGetLastError();
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "selected_items_kernel");
 }
 
