@@ -1,7 +1,7 @@
 // For each key block the list of the queries that name it, in rising order (so that what is summed
 // over a list is summed in a fixed order), and the lists cut into items of equal work.
 //
-// Three launches.  (1) A block of threads sets, for a chunk of 64 to 256 queries, one bit a query in
+// Three launches.  (1) A block of threads sets, for a chunk of 32 to 256 queries, one bit a query in
 // a bitmap of each key block in shared memory (atomic ors, whose order does not matter) and counts
 // the bits.  (2) One block of threads a unit turns the counts into places: a running sum over the
 // chunks for each key block, then over the key blocks, and writes the items.  (3) The bitmaps again:
@@ -11,83 +11,99 @@
 
 #include "block_lists.h"
 #include "layer_ops.h"
+#include "sm100_ptx.cuh"
 
 namespace dfs {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;                    // loads of a lane in flight
 constexpr int kScanThreads = 1024;
+constexpr int kScanBlocks = 256;             // key blocks that the scan takes at a time, by four runs of chunks
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kBitmapBytes = 128 * 1024;
+constexpr int kBitmapBytes = 64 * 1024;
 
-// A warp's 32 queries, `width` lanes a query (a power of two, at least top or 32): calls
-// use(query of the 32, block, rank) for the blocks of a query that count, and all(query, their
-// number).  Entry x of a query's list counts if it is above all entries before it (which -1 is
-// not) and has visible keys.
+// A warp's 32 queries, `width` lanes a query (a power of two) and four entries of its list a lane:
+// calls use(query of the 32, block, rank) for the blocks of a query that count, and all(query, their
+// number).  An entry counts if it is above all entries before it (which -1 is not) and has visible keys.
 template <class Use, class All>
 __device__ __forceinline__ void each_live(const SelectShape& s, const int32_t* blocks, uint32_t u, int64_t i0, int width,
                                           Use use, All all) {
-    const int64_t b = u / (uint32_t)s.Hk;
-    const int lane = threadIdx.x & 31, x = lane & (width - 1), first = lane - x;
-    const unsigned mine = width == 32 ? kFull : ((1u << width) - 1) << first;
-    const int32_t* list = blocks + ((int64_t)u * s.n + i0) * s.top;
-    for (int k0 = 0; k0 < width; k0 += kAhead) {             // 32 / width queries a turn
-        int c[kAhead][2];
+    const int lane = threadIdx.x & 31, x = lane & (width - 1), per = 32 / width;
+    const uint32_t b = sequence_of(s, u);
+    const int32_t len = key_count(s, b);
+    const int64_t first = (s.starts ? (int64_t)s.starts[b] : len - s.n) + i0;
+    const int32_t* list = blocks + ((int64_t)u * s.n + i0) * s.top + 4 * x;
+    const bool whole = (s.top & 3) == 0;
+#pragma unroll 2
+    for (int k = 0; k < width; ++k) {
+        const int q = k * per + lane / width;
+        const bool on = i0 + q < s.n && 4 * x < s.top;
+        int c[4] = {-1, -1, -1, -1};
+        if (on && whole) {
+            const int4 v = *reinterpret_cast<const int4*>(list + q * s.top);
+            c[0] = v.x;
+            c[1] = v.y;
+            c[2] = v.z;
+            c[3] = v.w;
+        } else if (on) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int q = (k0 + k) * (32 / width) + first / width;
-            const bool on = k0 + k < width && i0 + q < s.n;
-            c[k][0] = on && x < s.top ? list[(int64_t)q * s.top + x] : -1;
-            c[k][1] = on && x + 32 < s.top ? list[(int64_t)q * s.top + x + 32] : -1;
+            for (int j = 0; j < 4; ++j)
+                if (4 * x + j < s.top) c[j] = list[q * s.top + j];
         }
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            if (k0 + k >= width) break;
-            const int q = (k0 + k) * (32 / width) + first / width;
-            const int32_t limit = i0 + q < s.n ? row_limit(s, b, i0 + q) : 0;
-            int before = -1, rank = 0;
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                if (part && s.top <= 32) break;
-                int high = c[k][part];                       // the largest up to this lane
-                for (int off = 1; off < width; off *= 2) {
-                    const int o = __shfl_up_sync(kFull, high, off, width);
-                    if (x >= off) high = max(high, o);
-                }
-                const int prev = __shfl_up_sync(kFull, high, 1, width);
-                const int over = max(x ? prev : -1, before);
-                const bool in = c[k][part] > over && (int64_t)c[k][part] * kBlockKeys < limit;
-                const unsigned m = __ballot_sync(kFull, in) & mine;
-                if (in) use(q, c[k][part], rank + __popc(m & ((1u << lane) - 1)));
-                rank += __popc(m);
-                before = max(before, __shfl_sync(kFull, high, width - 1, width));
+        const int64_t p = first + q;
+        const int32_t limit = p < 0 || p >= len || i0 + q >= s.n ? 0 : s.causal ? (int32_t)p + 1 : len;
+        const int32_t blocks_seen = (limit + kBlockKeys - 1) / kBlockKeys;
+        int high = max(max(c[0], c[1]), max(c[2], c[3])), before = -1;       // the largest of the lanes before
+        for (int off = 1; off < width; off *= 2) {
+            const int o = __shfl_up_sync(kFull, high, off, width);
+            if (x >= off) {
+                before = max(before, o);
+                high = max(high, o);
             }
-            if (x == 0 && i0 + q < s.n) all(q, rank);
         }
+        bool in[4];
+        int count = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            in[j] = c[j] > before && c[j] < blocks_seen;
+            before = max(before, c[j]);
+            count += in[j];
+        }
+        int rank = count;
+        for (int off = 1; off < width; off *= 2) {
+            const int o = __shfl_up_sync(kFull, rank, off, width);
+            if (x >= off) rank += o;
+        }
+        if (x == width - 1 && i0 + q < s.n) all(q, rank);
+        rank -= count;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (in[j]) use(q, c[j], rank++);
     }
 }
 
-// One bit a query in each block's words.
-__device__ __forceinline__ void set_bits(const SelectShape& s, const int32_t* blocks, const BlockLists& l, int64_t u,
+// bits[word][block]: one bit a query of the chunk.
+__device__ __forceinline__ void set_bits(const SelectShape& s, const int32_t* blocks, const BlockLists& l, uint32_t u,
                                          int64_t chunk, uint32_t* bits) {
     for (int x = threadIdx.x; x < s.nb * l.words; x += blockDim.x) bits[x] = 0;
     __syncthreads();
-    for (int w = threadIdx.x >> 5; w < l.words; w += blockDim.x >> 5)
-        each_live(s, blocks, u, (chunk * l.words + w) * 32, l.width,
-                  [&](int q, int c, int) { atomicOr(&bits[c * l.words + w], 1u << q); }, [](int, int) {});
+    const int w = threadIdx.x >> 5;          // a warp a word
+    each_live(s, blocks, u, (chunk * l.words + w) * 32, l.width,
+              [&](int q, int c, int) { atomicOr(&bits[w * s.nb + c], 1u << q); }, [](int, int) {});
     __syncthreads();
 }
 
 __global__ void __launch_bounds__(kThreads)
 count_lists_kernel(const __grid_constant__ SelectShape s, const int32_t* blocks, const __grid_constant__ BlockLists l) {
-    extern __shared__ uint32_t bits[];       // [nb][words]
-    const int64_t u = blockIdx.x / (uint32_t)l.chunks, chunk = blockIdx.x % (uint32_t)l.chunks;
+    extern __shared__ uint32_t bits[];       // [words][nb]
+    ptx::griddep_launch_dependents();
+    const uint32_t u = blockIdx.x / (uint32_t)l.chunks, chunk = blockIdx.x - u * l.chunks;
     set_bits(s, blocks, l, u, chunk, bits);
+    ptx::griddep_wait();                     // (what runs before it is none of its inputs', but has to be over for the others)
     for (int c = threadIdx.x; c < s.nb; c += blockDim.x) {
         int n = 0;
-        for (int w = 0; w < l.words; ++w) n += __popc(bits[c * l.words + w]);
-        l.counts[(u * l.chunks + chunk) * s.nb + c] = n;
+        for (int w = 0; w < l.words; ++w) n += __popc(bits[w * s.nb + c]);
+        l.counts[((int64_t)u * l.chunks + chunk) * s.nb + c] = n;
     }
 }
 
@@ -103,7 +119,7 @@ __device__ __forceinline__ int2 before_and_all(int2 x, int2* sums, int2* all) {
     if (lane == 31) sums[warp] = run;
     __syncthreads();
     int2 before = make_int2(run.x - x.x, run.y - x.y), total = make_int2(0, 0);
-    for (int w = 0; w < kScanThreads / 32; ++w) {
+    for (int w = 0; w < kScanBlocks / 32; ++w) {
         if (w == warp) before = make_int2(before.x + total.x, before.y + total.y);
         total = make_int2(total.x + sums[w].x, total.y + sums[w].y);
     }
@@ -114,38 +130,47 @@ __device__ __forceinline__ int2 before_and_all(int2 x, int2* sums, int2* all) {
 
 __global__ void __launch_bounds__(kScanThreads)
 place_lists_kernel(const __grid_constant__ SelectShape s, const __grid_constant__ BlockLists l) {
+    constexpr int kRuns = kScanThreads / kScanBlocks;
     __shared__ int2 sums[kScanThreads / 32];
+    __shared__ int32_t runs[kRuns][kScanBlocks];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const int64_t u = blockIdx.x;
     int32_t* counts = l.counts + u * l.chunks * s.nb;
     int32_t *base = l.base + u * (s.nb + 1), *item_base = l.item_base + u * (s.nb + 1);
+    const int run = threadIdx.x / kScanBlocks, per = (l.chunks + kRuns - 1) / kRuns;
+    const int k0 = min(run * per, l.chunks), k1 = min(k0 + per, l.chunks);
     int2 done = make_int2(0, 0);
-    for (int c0 = 0; c0 < s.nb; c0 += kScanThreads) {
-        const int c = c0 + threadIdx.x;
+    for (int c0 = 0; c0 < s.nb; c0 += kScanBlocks) {
+        const int c = c0 + threadIdx.x % kScanBlocks;
         int n = 0;
         if (c < s.nb) {
-            int32_t* at = counts + c;
-            int k = 0;
-            for (; k + 8 <= l.chunks; k += 8) {              // eight loads in flight
-                int32_t x[8];
+#pragma unroll 16
+            for (int k = k0; k < k1; ++k) n += counts[(int64_t)k * s.nb + c];
+        }
+        runs[run][threadIdx.x % kScanBlocks] = n;
+        __syncthreads();
+        n = 0;
+        int mine = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = at[(int64_t)(k + j) * s.nb];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    at[(int64_t)(k + j) * s.nb] = n;
-                    n += x[j];
-                }
-            }
-            for (; k < l.chunks; ++k) {
-                const int32_t x = at[(int64_t)k * s.nb];
-                at[(int64_t)k * s.nb] = n;
-                n += x;
+        for (int r = 0; r < kRuns; ++r) {
+            if (r == run) mine = n;
+            n += runs[r][threadIdx.x % kScanBlocks];
+        }
+        if (c < s.nb) {
+#pragma unroll 16
+            for (int k = k0; k < k1; ++k) {
+                const int32_t x = counts[(int64_t)k * s.nb + c];
+                counts[(int64_t)k * s.nb + c] = mine;
+                mine += x;
             }
         }
+        if (run || c >= s.nb) n = 0;         // (the first run's threads sum over the blocks)
         const int64_t rows = (int64_t)n * s.G;
         const int items = (int)((rows + l.item_rows - 1) / l.item_rows);
         int2 all;
         const int2 before = before_and_all(make_int2(n, items), sums, &all);
-        if (c < s.nb) {
+        if (run == 0 && c < s.nb) {
             base[c] = done.x + before.x;
             item_base[c] = done.y + before.y;
             int4* out = l.items + u * l.most_items + done.y + before.y;
@@ -162,26 +187,29 @@ place_lists_kernel(const __grid_constant__ SelectShape s, const __grid_constant_
 
 __global__ void __launch_bounds__(kThreads)
 fill_lists_kernel(const __grid_constant__ SelectShape s, const int32_t* blocks, const __grid_constant__ BlockLists l) {
-    extern __shared__ uint32_t bits[];       // [nb][words], then [nb]
-    const int64_t u = blockIdx.x / (uint32_t)l.chunks, chunk = blockIdx.x % (uint32_t)l.chunks;
-    set_bits(s, blocks, l, u, chunk, bits);
-    // where the chunk's queries of each block begin
+    extern __shared__ uint32_t bits[];       // [words][nb], then where each word's queries begin, [words][nb]
+    const uint32_t u = blockIdx.x / (uint32_t)l.chunks, chunk = blockIdx.x - u * l.chunks;
+    set_bits(s, blocks, l, u, chunk, bits);  // (the lists of blocks are no earlier kernel's)
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     int32_t* begin = reinterpret_cast<int32_t*>(bits + s.nb * l.words);
-    for (int c = threadIdx.x; c < s.nb; c += blockDim.x)
-        begin[c] = l.base[u * (s.nb + 1) + c] + l.counts[(u * l.chunks + chunk) * s.nb + c];
+    for (int c = threadIdx.x; c < s.nb; c += blockDim.x) {
+        int at = l.base[(int64_t)u * (s.nb + 1) + c] + l.counts[((int64_t)u * l.chunks + chunk) * s.nb + c];
+        for (int w = 0; w < l.words; ++w) {
+            begin[w * s.nb + c] = at;
+            at += __popc(bits[w * s.nb + c]);
+        }
+    }
     __syncthreads();
     uint32_t* entries = l.entries + u * s.n * l.ranks;
-    for (int w = threadIdx.x >> 5; w < l.words; w += blockDim.x >> 5) {
-        const int64_t i0 = (chunk * l.words + w) * 32;
-        each_live(s, blocks, u, i0, l.width,
-                  [&](int q, int c, int rank) {
-                      const uint32_t* b = bits + c * l.words;
-                      int at = begin[c] + __popc(b[w] & ((1u << q) - 1));
-                      for (int k = 0; k < w; ++k) at += __popc(b[k]);
-                      entries[at] = (uint32_t)(i0 + q) << 6 | rank;
-                  },
-                  [&](int q, int count) { l.live[u * s.n + i0 + q] = count; });
-    }
+    const int w = threadIdx.x >> 5;
+    const int64_t i0 = ((int64_t)chunk * l.words + w) * 32;
+    each_live(s, blocks, u, i0, l.width,
+              [&](int q, int c, int rank) {
+                  const int at = begin[w * s.nb + c] + __popc(bits[w * s.nb + c] & ((1u << q) - 1));
+                  entries[at] = (uint32_t)(i0 + q) << 6 | rank;
+              },
+              [&](int q, int count) { l.live[u * s.n + i0 + q] = count; });
 }
 
 }  // namespace
@@ -191,9 +219,9 @@ size_t plan_block_lists(const SelectShape& s, int32_t item_rows, char* ws, Block
     l->ranks = s.top < s.nb ? s.top : s.nb;
     l->item_rows = item_rows;
     l->width = 1;
-    while (l->width < s.top && l->width < 32) l->width *= 2;
+    while (4 * l->width < s.top) l->width *= 2;
     l->words = 8;
-    while (l->words > 2 && (int64_t)s.nb * l->words * 4 > kBitmapBytes) l->words /= 2;
+    while (l->words > 1 && (int64_t)s.nb * l->words * 4 > kBitmapBytes) l->words /= 2;
     l->chunks = (int32_t)((s.n + 32 * l->words - 1) / (32 * l->words));
     const int64_t named = s.n * l->ranks;    // (query, block) pairs of a unit
     l->most_items = (int32_t)((named < s.nb ? named : s.nb) + named * s.G / item_rows);
@@ -212,28 +240,32 @@ size_t plan_block_lists(const SelectShape& s, int32_t item_rows, char* ws, Block
     return at;
 }
 
-int launch_block_lists(const SelectShape& s, const int32_t* blocks, const BlockLists& l, cudaStream_t stream) {
+int launch_block_lists(const SelectShape& s, const int32_t* blocks, const BlockLists& l, bool beside, cudaStream_t stream) {
     static std::atomic<uint64_t> count_ready{0}, fill_ready{0};
     const int64_t units = s.B * s.Hk, grid = units * l.chunks;
     if (grid > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
     cudaError_t err = allow_smem(count_lists_kernel, kBitmapBytes, count_ready);
-    if (err == cudaSuccess) err = allow_smem(fill_lists_kernel, kBitmapBytes + kMaxKeys / kBlockKeys * 4, fill_ready);
+    if (err == cudaSuccess) err = allow_smem(fill_lists_kernel, 2 * kBitmapBytes, fill_ready);
     if (err != cudaSuccess) return cuda_fail(err, "the block lists");
     const size_t smem = (size_t)s.nb * l.words * 4;
     const int threads = 32 * l.words;
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        count_lists_kernel<<<(unsigned)grid, threads, smem, stream>>>(s, blocks, l);
+        if (beside) {
+            err = launch_pdl(count_lists_kernel, dim3((unsigned)grid), dim3(threads), smem, stream, s, blocks, l);
+        } else {
+            count_lists_kernel<<<(unsigned)grid, threads, smem, stream>>>(s, blocks, l);
+            err = cudaGetLastError();
+        }
     }
-    {
+    if (err == cudaSuccess) {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        place_lists_kernel<<<(unsigned)units, kScanThreads, 0, stream>>>(s, l);
+        err = launch_pdl(place_lists_kernel, dim3((unsigned)units), dim3(kScanThreads), 0, stream, s, l);
     }
-    {
+    if (err == cudaSuccess) {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        fill_lists_kernel<<<(unsigned)grid, threads, smem + (size_t)s.nb * 4, stream>>>(s, blocks, l);
+        err = launch_pdl(fill_lists_kernel, dim3((unsigned)grid), dim3(threads), 2 * smem, stream, s, blocks, l);
     }
-    err = cudaGetLastError();
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "the block lists");
 }
 

@@ -55,6 +55,8 @@ inline int32_t item_rows(const SelectShape& s, int resident) {
 
 // Sizes, and the addresses in `ws` (null: sizes alone); returns the bytes.
 size_t plan_block_lists(const SelectShape& s, int32_t item_rows, char* ws, BlockLists* l);
-int launch_block_lists(const SelectShape& s, const int32_t* blocks, const BlockLists& l, cudaStream_t stream);
+// The last kernel allows dependent launches.  `beside`: the launch before on the stream is the caller's own,
+// allows dependent launches and writes nothing that the lists are made of.
+int launch_block_lists(const SelectShape& s, const int32_t* blocks, const BlockLists& l, bool beside, cudaStream_t stream);
 
 }  // namespace dfs

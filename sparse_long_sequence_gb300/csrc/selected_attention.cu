@@ -165,6 +165,7 @@ struct Partials {
     float* sums;                             // [slots][64]
     float2* stat;                            // [slots]: maximum (units of log 2), sum
     int64_t u0;
+    bool first;                              // the group after the lists (the others: after a join)
 };
 
 __global__ void __launch_bounds__(kItemThreads, 4)
@@ -174,10 +175,16 @@ selected_items_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     __shared__ uint64_t bars[2];             // S is there; O is
     __shared__ uint32_t tmem_slot;
     const SelectShape& s = a.s;
+    // A group starts while the one before is joined (which the lists are older than), and writes no partial
+    // before that is over.
+    if (out.first) ptx::griddep_wait();
     const uint32_t ul = blockIdx.x / (uint32_t)l.most_items;
     const int64_t u = out.u0 + ul, b = sequence_of(s, u);
     const ItemRows item = item_of(l, s, u, blockIdx.x - ul * l.most_items);
-    if (!item.rows) return;
+    if (!item.rows) {
+        ptx::griddep_wait();
+        return;
+    }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t key0 = item.block * kBlockKeys;
     const uint32_t keys = ptx::smem_u32(smem), values = keys + kKeyBytes, queries = values + kKeyBytes;
@@ -270,6 +277,10 @@ selected_items_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
             ptx::mma_commit(&bars[1]);
         }
         __syncwarp();
+        if (x == 0) {
+            ptx::griddep_wait();
+            ptx::griddep_launch_dependents();
+        }
         if (now.slot != ~0u) out.stat[slot0 + now.slot] = make_float2(top, sum);
         ptx::mbar_wait(&bars[1], x & 1, status);
         __syncwarp();
@@ -299,6 +310,8 @@ selected_join_kernel(const __grid_constant__ SelectedArgs a, const __grid_consta
                      uint32_t rows) {
     const SelectShape& s = a.s;
     const int lane = threadIdx.x & 15;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
     const uint32_t row = blockIdx.x * 16 + (threadIdx.x >> 4);
     if (row >= rows) return;
     const RowOf at = row_of(s, in.u0, row);
@@ -364,24 +377,25 @@ int launch_items(const SelectedArgs& a, char* ws, cudaStream_t stream) {
     if (st) return st;
     cudaError_t err = allow_smem(selected_items_kernel, kItemSmem, ready);
     if (err != cudaSuccess) return cuda_fail(err, "selected_items_kernel");
-    if ((st = launch_block_lists(s, a.blocks, p.lists, stream))) return st;
+    if ((st = launch_block_lists(s, a.blocks, p.lists, false, stream))) return st;
     const int64_t units = s.B * s.Hk;
     for (int64_t u0 = 0; u0 < units; u0 += p.group) {
         const int64_t here = units - u0 < p.group ? units - u0 : p.group, rows = here * s.n * s.G;
-        const Partials part{reinterpret_cast<float*>(ws + p.sums), reinterpret_cast<float2*>(ws + p.stat), u0};
+        const Partials part{reinterpret_cast<float*>(ws + p.sums), reinterpret_cast<float2*>(ws + p.stat), u0, u0 == 0};
         if (here * p.lists.most_items > INT32_MAX || rows > INT32_MAX)
             return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
         {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-            selected_items_kernel<<<(unsigned)(here * p.lists.most_items), kItemThreads, kItemSmem, stream>>>(a, p.lists, part,
-                                                                                                              status);
+            err = launch_pdl(selected_items_kernel, dim3((unsigned)(here * p.lists.most_items)), dim3(kItemThreads), kItemSmem,
+                             stream, a, p.lists, part, status);
         }
-        {
+        if (err == cudaSuccess) {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-            selected_join_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, stream>>>(a, p.lists, part, (uint32_t)rows);
+            err = launch_pdl(selected_join_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, stream, a, p.lists, part,
+                             (uint32_t)rows);
         }
+        if (err != cudaSuccess) break;
     }
-    err = cudaGetLastError();
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "selected_items_kernel");
 }
 

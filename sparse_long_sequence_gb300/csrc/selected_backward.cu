@@ -9,7 +9,7 @@
 //   [dout | Q]^T [P | dS] = [dv^T, .; ., dk^T],
 // adds up dv and dk in tensor memory over all the rows (its other two quarters are not used: 64-row
 // accumulators would save half of a product that is a tenth of the time).  A (row, block) leaves 64 fp32
-// sums of dq, an item its sums of dk and dv, and two kernels join them in a fixed order.  The units go in
+// sums of dq, an item its sums of dk and dv, and a second kernel joins them in a fixed order.  The units go in
 // groups whose partials stay in the L2.
 #include <atomic>
 
@@ -38,10 +38,12 @@ struct Partials {
     float* dkv;                              // [items][dv, dk][64 features][64 keys]
     const float2* stat;                      // [B][Hq][n]: lse in units of log 2, delta
     int64_t u0;
+    bool first;                              // the group after the lists (the others: after the joining kernel)
 };
 
 // stat = (lse in units of log 2, delta): eight lanes a row.
 __global__ void __launch_bounds__(256) selected_delta_kernel(const __grid_constant__ SelectedArgs a, int64_t rows, float2* stat) {
+    ptx::griddep_launch_dependents();
     const int64_t row = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
     const int lane = threadIdx.x & 7;
     float d = 0.f;
@@ -68,10 +70,16 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     __shared__ uint64_t bars[3];             // S and dout V^T are there; dq is; dv and dk have taken the tile
     __shared__ uint32_t tmem_slot;
     const SelectShape& s = a.s;
+    // A group starts while the one before is joined (which the lists are older than), and writes no partial
+    // before that is over.
+    if (out.first) ptx::griddep_wait();
     const uint32_t ul = blockIdx.x / (uint32_t)l.most_items;
     const int64_t u = out.u0 + ul, b = sequence_of(s, u);
     const ItemRows item = item_of(l, s, u, blockIdx.x - ul * l.most_items);
-    if (!item.rows) return;
+    if (!item.rows) {
+        ptx::griddep_wait();
+        return;
+    }
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int quarter = warp & 3, half = warp >> 2;          // rows 32 quarter .. and columns 32 half .. of a tile
     const int32_t key0 = item.block * kBlockKeys;
@@ -180,6 +188,10 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
             ptx::mma_commit(&bars[2]);
         }
         __syncwarp();
+        if (x == 0) {
+            ptx::griddep_wait();
+            ptx::griddep_launch_dependents();
+        }
         ptx::mbar_wait(&bars[1], x & 1, status);
         __syncwarp();
         ptx::tc_fence_after();
@@ -207,13 +219,10 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     if (warp == 0) ptx::tmem_dealloc(tmem, kColumns);
 }
 
-// dq of a row: the sum of its partials, sixteen lanes a row.
-__global__ void __launch_bounds__(256)
-selected_dq_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials in, uint32_t rows) {
+// dq of a row: the sum of its partials, sixteen lanes a row, sixteen rows a block of threads.
+__device__ __forceinline__ void join_dq(const SelectedArgs& a, const BlockLists& l, const Partials& in, uint32_t row) {
     const SelectShape& s = a.s;
     const int lane = threadIdx.x & 15;
-    const uint32_t row = blockIdx.x * 16 + (threadIdx.x >> 4);
-    if (row >= rows) return;
     const RowOf at = row_of(s, in.u0, row);
     const int count = l.live[in.u0 * s.n + at.entry];
     const float4* part = reinterpret_cast<const float4*>(in.dq + (int64_t)row * l.ranks * kHeadDim) + lane;
@@ -228,12 +237,11 @@ selected_dq_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant
 
 // dk and dv of a key block: the sums of its items', turned, sixteen keys a block of threads.
 constexpr int kSplit = 4;
-__global__ void __launch_bounds__(256)
-selected_dkv_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials in) {
+__device__ __forceinline__ void join_dkv(const SelectedArgs& a, const BlockLists& l, const Partials& in, uint32_t share) {
     __shared__ float sums[16][kHeadDim + 1];
     const SelectShape& s = a.s;
-    const int split = blockIdx.x % (2 * kSplit), part = split % kSplit, which = split / kSplit;
-    const uint32_t at = blockIdx.x / (2 * kSplit), ul = at / (uint32_t)s.nb;
+    const int split = share % (2 * kSplit), part = split % kSplit, which = split / kSplit;
+    const uint32_t at = share / (2 * kSplit), ul = at / (uint32_t)s.nb;
     const int64_t u = in.u0 + ul;
     const int c = at - ul * s.nb, feature = threadIdx.x >> 2, four = threadIdx.x & 3;
     const int32_t* base = l.item_base + u * (s.nb + 1) + c;
@@ -256,6 +264,16 @@ selected_dkv_kernel(const __grid_constant__ SelectedArgs a, const __grid_constan
     if (key >= s.m) return;
     __nv_bfloat16* dst = (which ? a.dk : a.dv) + (u * s.m + key) * kHeadDim + f;
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack(sums[row][f], sums[row][f + 1]), pack(sums[row][f + 2], sums[row][f + 3]));
+}
+
+__global__ void __launch_bounds__(256)
+selected_join_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials in,
+                           uint32_t rows, uint32_t row_blocks) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    if (blockIdx.x >= row_blocks) return join_dkv(a, l, in, blockIdx.x - row_blocks);
+    const uint32_t row = blockIdx.x * 16 + (threadIdx.x >> 4);
+    if (row < rows) join_dq(a, l, in, row);
 }
 
 struct Plan {
@@ -292,33 +310,34 @@ int launch_selected_backward(const SelectedArgs& a, char* ws, cudaStream_t strea
     if (st) return st;
     cudaError_t err = allow_smem(selected_grads_kernel, kSmem, ready);
     if (err != cudaSuccess) return cuda_fail(err, "selected_grads_kernel");
-    if ((st = launch_block_lists(s, a.blocks, p.lists, stream))) return st;
     const int64_t units = s.B * s.Hk, all = s.B * s.Hq * s.n;
     if ((all + 31) / 32 > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
         selected_delta_kernel<<<(unsigned)((all + 31) / 32), 256, 0, stream>>>(a, all, reinterpret_cast<float2*>(ws + p.stat));
     }
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return cuda_fail(err, "selected_delta_kernel");
+    if ((st = launch_block_lists(s, a.blocks, p.lists, true, stream))) return st;
     for (int64_t u0 = 0; u0 < units; u0 += p.group) {
         const int64_t here = units - u0 < p.group ? units - u0 : p.group, rows = here * s.n * s.G;
         const Partials part{reinterpret_cast<float*>(ws + p.dq), reinterpret_cast<float*>(ws + p.dkv),
-                            reinterpret_cast<const float2*>(ws + p.stat), u0};
-        if (here * p.lists.most_items > INT32_MAX || rows > INT32_MAX || here * s.nb * 2 * kSplit > INT32_MAX)
+                            reinterpret_cast<const float2*>(ws + p.stat), u0, u0 == 0};
+        if (here * p.lists.most_items > INT32_MAX || rows + here * s.nb * 2 * kSplit > INT32_MAX)
             return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
         {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-            selected_grads_kernel<<<(unsigned)(here * p.lists.most_items), kThreads, kSmem, stream>>>(a, p.lists, part, status);
+            err = launch_pdl(selected_grads_kernel, dim3((unsigned)(here * p.lists.most_items)), dim3(kThreads), kSmem, stream,
+                             a, p.lists, part, status);
         }
-        {
+        if (err == cudaSuccess) {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-            selected_dq_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, stream>>>(a, p.lists, part, (uint32_t)rows);
+            const int64_t row_blocks = (rows + 15) / 16;
+            err = launch_pdl(selected_join_grads_kernel, dim3((unsigned)(row_blocks + here * s.nb * 2 * kSplit)), dim3(256), 0,
+                             stream, a, p.lists, part, (uint32_t)rows, (uint32_t)row_blocks);
         }
-        {
-            LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-            selected_dkv_kernel<<<(unsigned)(here * s.nb * 2 * kSplit), 256, 0, stream>>>(a, p.lists, part);
-        }
+        if (err != cudaSuccess) break;
     }
-    err = cudaGetLastError();
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "selected_grads_kernel");
 }
 
