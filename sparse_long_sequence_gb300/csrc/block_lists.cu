@@ -1,10 +1,10 @@
 // For each key block the list of the queries that name it, in rising order (so that what is summed
-// over a list is summed in a fixed order), and the lists cut into items of equal work.
+// over a list is summed in a fixed order), and where each block's tiles of rows begin.
 //
 // Three launches.  (1) A block of threads sets, for a chunk of 32 to 256 queries, one bit a query in
 // a bitmap of each key block in shared memory (atomic ors, whose order does not matter) and counts
 // the bits.  (2) One block of threads a unit turns the counts into places: a running sum over the
-// chunks for each key block, then over the key blocks, and writes the items.  (3) The bitmaps again:
+// chunks for each key block, then over the key blocks.  (3) The bitmaps again:
 // a query's place in a list is the number of bits before its own.  Bound by the latency of a few
 // dependent loads; the lists' own bytes are a few percent of what the attention moves.
 #include <atomic>
@@ -107,21 +107,29 @@ count_lists_kernel(const __grid_constant__ SelectShape s, const int32_t* blocks,
     }
 }
 
-// Sums of a block's threads before this one, and of all.
-__device__ __forceinline__ int2 before_and_all(int2 x, int2* sums, int2* all) {
+struct Three {
+    int32_t entries, tiles, filled;
+};
+__device__ __forceinline__ Three operator+(Three a, Three b) {
+    return {a.entries + b.entries, a.tiles + b.tiles, a.filled + b.filled};
+}
+
+// Sums over the first kScanBlocks threads: of those before this one, and (in *all) of all.
+__device__ __forceinline__ Three before_and_all(Three x, Three* sums, Three* all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int2 run = x;
+    Three run = x;
 #pragma unroll
     for (int off = 1; off < 32; off *= 2) {
-        const int a = __shfl_up_sync(kFull, run.x, off), b = __shfl_up_sync(kFull, run.y, off);
-        if (lane >= off) run = make_int2(run.x + a, run.y + b);
+        const Three o = {__shfl_up_sync(kFull, run.entries, off), __shfl_up_sync(kFull, run.tiles, off),
+                         __shfl_up_sync(kFull, run.filled, off)};
+        if (lane >= off) run = run + o;
     }
     if (lane == 31) sums[warp] = run;
     __syncthreads();
-    int2 before = make_int2(run.x - x.x, run.y - x.y), total = make_int2(0, 0);
+    Three before = {run.entries - x.entries, run.tiles - x.tiles, run.filled - x.filled}, total = {0, 0, 0};
     for (int w = 0; w < kScanBlocks / 32; ++w) {
-        if (w == warp) before = make_int2(before.x + total.x, before.y + total.y);
-        total = make_int2(total.x + sums[w].x, total.y + sums[w].y);
+        if (w == warp) before = before + total;
+        total = total + sums[w];
     }
     __syncthreads();
     *all = total;
@@ -131,16 +139,16 @@ __device__ __forceinline__ int2 before_and_all(int2 x, int2* sums, int2* all) {
 __global__ void __launch_bounds__(kScanThreads)
 place_lists_kernel(const __grid_constant__ SelectShape s, const __grid_constant__ BlockLists l) {
     constexpr int kRuns = kScanThreads / kScanBlocks;
-    __shared__ int2 sums[kScanThreads / 32];
+    __shared__ Three sums[kScanThreads / 32];
     __shared__ int32_t runs[kRuns][kScanBlocks];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int64_t u = blockIdx.x;
     int32_t* counts = l.counts + u * l.chunks * s.nb;
-    int32_t *base = l.base + u * (s.nb + 1), *item_base = l.item_base + u * (s.nb + 1);
+    int32_t *base = l.base + u * (s.nb + 1), *tile_base = l.tile_base + u * (s.nb + 1);
     const int run = threadIdx.x / kScanBlocks, per = (l.chunks + kRuns - 1) / kRuns;
     const int k0 = min(run * per, l.chunks), k1 = min(k0 + per, l.chunks);
-    int2 done = make_int2(0, 0);
+    Three done = {0, 0, 0};
     for (int c0 = 0; c0 < s.nb; c0 += kScanBlocks) {
         const int c = c0 + threadIdx.x % kScanBlocks;
         int n = 0;
@@ -166,22 +174,19 @@ place_lists_kernel(const __grid_constant__ SelectShape s, const __grid_constant_
             }
         }
         if (run || c >= s.nb) n = 0;         // (the first run's threads sum over the blocks)
-        const int64_t rows = (int64_t)n * s.G;
-        const int items = (int)((rows + l.item_rows - 1) / l.item_rows);
-        int2 all;
-        const int2 before = before_and_all(make_int2(n, items), sums, &all);
+        const int tiles = (int)(((int64_t)n * s.G + kTileRows - 1) / kTileRows);
+        Three all;
+        const Three before = done + before_and_all({n, tiles, n > 0}, sums, &all);
         if (run == 0 && c < s.nb) {
-            base[c] = done.x + before.x;
-            item_base[c] = done.y + before.y;
-            int4* out = l.items + u * l.most_items + done.y + before.y;
-            for (int k = 0; k < items; ++k)
-                out[k] = make_int4(c, k * l.item_rows, min(l.item_rows, (int)rows - k * l.item_rows), done.x + before.x);
+            base[c] = before.entries;
+            tile_base[c] = before.tiles;
+            l.filled[u * s.nb + c] = before.filled;
         }
-        done = make_int2(done.x + all.x, done.y + all.y);
+        done = done + all;
     }
     if (threadIdx.x == 0) {
-        base[s.nb] = done.x;
-        item_base[s.nb] = done.y;
+        base[s.nb] = done.entries;
+        tile_base[s.nb] = done.tiles;
     }
 }
 
@@ -214,17 +219,17 @@ fill_lists_kernel(const __grid_constant__ SelectShape s, const int32_t* blocks, 
 
 }  // namespace
 
-size_t plan_block_lists(const SelectShape& s, int32_t item_rows, char* ws, BlockLists* l) {
+size_t plan_block_lists(const SelectShape& s, char* ws, BlockLists* l) {
     const size_t units = (size_t)s.B * s.Hk;
     l->ranks = s.top < s.nb ? s.top : s.nb;
-    l->item_rows = item_rows;
     l->width = 1;
     while (4 * l->width < s.top) l->width *= 2;
     l->words = 8;
     while (l->words > 1 && (int64_t)s.nb * l->words * 4 > kBitmapBytes) l->words /= 2;
     l->chunks = (int32_t)((s.n + 32 * l->words - 1) / (32 * l->words));
     const int64_t named = s.n * l->ranks;    // (query, block) pairs of a unit
-    l->most_items = (int32_t)((named < s.nb ? named : s.nb) + named * s.G / item_rows);
+    l->most_filled = (int32_t)(named < s.nb ? named : s.nb);
+    l->shares = 1;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         char* p = ws ? ws + at : nullptr;
@@ -233,8 +238,8 @@ size_t plan_block_lists(const SelectShape& s, int32_t item_rows, char* ws, Block
     };
     l->entries = reinterpret_cast<uint32_t*>(take(units * named * 4));
     l->base = reinterpret_cast<int32_t*>(take(units * (s.nb + 1) * 4));
-    l->item_base = reinterpret_cast<int32_t*>(take(units * (s.nb + 1) * 4));
-    l->items = reinterpret_cast<int4*>(take(units * l->most_items * 16));
+    l->tile_base = reinterpret_cast<int32_t*>(take(units * (s.nb + 1) * 4));
+    l->filled = reinterpret_cast<int32_t*>(take(units * s.nb * 4));
     l->live = reinterpret_cast<int32_t*>(take(units * s.n * 4));
     l->counts = reinterpret_cast<int32_t*>(take(units * l->chunks * s.nb * 4));
     return at;

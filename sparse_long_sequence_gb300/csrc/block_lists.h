@@ -5,34 +5,91 @@
 
 namespace dfs {
 
+constexpr int kTileRows = 128;               // rows of a tile
+
 // In device memory, for each unit (sequence and key head).  An entry is a query i and its rank
 // among the query's blocks that count, i 64 + rank; a block's entries stand in rising order of i.
-// Entry e of a block stands for G rows, e G + h for head h of the group; an item is up to
-// `item_rows` rows of one block.
+// Entry e of a block stands for G rows, e G + h for head h of the group, and a block's rows make
+// tiles of 128, the last one shorter.  A unit's tiles, block after block, go to `shares` blocks of
+// threads in runs of equal length: share j has tiles [j N / shares, (j + 1) N / shares) of N (with
+// fewer tiles than shares there are N shares).
 struct BlockLists {
     uint32_t* entries;             // [units][n ranks]
     int32_t* base;                 // [units][nb + 1]: where a block's entries begin
-    int32_t* item_base;            // [units][nb + 1]: where its items do
-    int4* items;                   // [units][most_items]: block, first row, rows, the block's first entry
+    int32_t* tile_base;            // [units][nb + 1]: where its tiles do
+    int32_t* filled;               // [units][nb]: blocks before it that have entries
     int32_t* live;                 // [units][n]: blocks of a query that count
     int32_t* counts;               // [units][chunks][nb], while they are built
     int32_t ranks;                 // blocks of a query that count, at most: min(top, nb)
-    int32_t most_items, item_rows;
+    int32_t shares;
+    int32_t most_filled;           // blocks that have entries, at most
     int32_t words, chunks;         // queries of a chunk / 32; chunks
     int32_t width;                 // lanes that read a query's list
 };
 
-#ifdef __CUDACC__
-struct ItemRows {
-    int32_t block, first, rows;    // rows first .. first + rows - 1 of the block's
-    const uint32_t* entries;       // the block's
-};
-// Item `at` of unit u; rows 0: there is none.
-__device__ __forceinline__ ItemRows item_of(const BlockLists& l, const SelectShape& s, int64_t u, uint32_t at) {
-    const int4 item = l.items[u * l.most_items + at];        // (whatever it holds where there is none)
-    const bool live = (int32_t)at < l.item_base[u * (s.nb + 1) + s.nb];
-    return {item.x, item.y, live ? item.z : 0, l.entries + u * s.n * l.ranks + (live ? item.w : 0)};
+// Sizes, and the addresses in `ws` (null: sizes alone); returns the bytes.  `shares` is the caller's.
+size_t plan_block_lists(const SelectShape& s, char* ws, BlockLists* l);
+// Shares of a unit where `here` units have `resident` blocks of threads on each of 152 SMs: `rounds` times as
+// many as run at once, and a tile at least for each.  (One round where the units have alike lengths.)
+constexpr int kUnlikeRounds = 3;
+inline int32_t tile_shares(const SelectShape& s, const BlockLists& l, int64_t here, int resident, int rounds) {
+    const int64_t at_once = 152 * resident / here, tiles = l.most_filled + s.n * l.ranks * s.G / kTileRows;
+    const int64_t shares = (at_once < 1 ? 1 : at_once) * rounds;
+    return (int32_t)(shares < tiles ? shares : tiles < 1 ? 1 : tiles);
 }
+// The last kernel allows dependent launches.  `beside`: the launch before on the stream is the caller's own,
+// allows dependent launches and writes nothing that the lists are made of.
+int launch_block_lists(const SelectShape& s, const int32_t* blocks, const BlockLists& l, bool beside, cudaStream_t stream);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ int32_t share_begin(int32_t tiles, int32_t share, int32_t shares) {
+    return (int32_t)((uint64_t)(uint32_t)tiles * (uint32_t)share / (uint32_t)shares);
+}
+// the share that has tile t
+__device__ __forceinline__ int32_t share_of_tile(int32_t tiles, int32_t t, int32_t shares) {
+    return (int32_t)((((uint64_t)(uint32_t)t + 1) * (uint32_t)shares - 1) / (uint32_t)tiles);
+}
+
+// A walk over a unit's tiles.
+struct Walk {
+    const int32_t *base, *tile_base;         // the unit's
+    int32_t block, begin, end;               // a key block, its tiles
+    int32_t first_entry, rows;               // its entries, its rows
+
+    // to the block that has tile t (warp-wide)
+    __device__ __forceinline__ void find(const BlockLists& l, const SelectShape& s, int64_t u, int32_t t) {
+        base = l.base + u * (s.nb + 1);
+        tile_base = l.tile_base + u * (s.nb + 1);
+        const int lane = threadIdx.x & 31;
+        int lo = 0, n = s.nb;                // among blocks lo .. lo + n - 1: the last with tile_base <= t
+        while (n > 1) {
+            const int step = (n + 31) / 32, c = lo + lane * step;
+            const unsigned m = __ballot_sync(0xffffffffu, lane * step < n && tile_base[c] <= t);
+            const int k = 31 - __clz(m);     // (lane 0's always is)
+            lo += k * step;
+            n = min(step, n - k * step);
+        }
+        block = lo;
+        begin = tile_base[lo];
+        end = tile_base[lo + 1];
+        load(s);
+    }
+    // on to tile t, the next one
+    __device__ __forceinline__ void go(const SelectShape& s, int32_t t) {
+        if (t < end) return;
+        do {
+            ++block;
+            begin = end;
+            end = tile_base[block + 1];
+        } while (t >= end);
+        load(s);
+    }
+    __device__ __forceinline__ void load(const SelectShape& s) {
+        first_entry = base[block];
+        rows = (base[block + 1] - first_entry) * s.G;
+    }
+};
+
 // Row ((u - u0) n + i) G + h of a group of units that begins with u0 (fewer than 2^31 rows).
 struct RowOf {
     uint32_t entry;                // (u - u0) n + i
@@ -45,18 +102,5 @@ __device__ __forceinline__ RowOf row_of(const SelectShape& s, int64_t u0, uint32
     return {entry, ((u0 + ul) * s.G + h) * s.n + i};
 }
 #endif
-
-// Rows of an item: four tiles of 128, fewer where there would be no two rounds of `resident` items
-// an SM.
-inline int32_t item_rows(const SelectShape& s, int resident) {
-    const int64_t rows = s.B * s.Hq * s.n * (s.top < s.nb ? s.top : s.nb), wave = 152 * 2 * (int64_t)resident;
-    return rows >= 512 * wave ? 512 : rows >= 256 * wave ? 256 : 128;
-}
-
-// Sizes, and the addresses in `ws` (null: sizes alone); returns the bytes.
-size_t plan_block_lists(const SelectShape& s, int32_t item_rows, char* ws, BlockLists* l);
-// The last kernel allows dependent launches.  `beside`: the launch before on the stream is the caller's own,
-// allows dependent launches and writes nothing that the lists are made of.
-int launch_block_lists(const SelectShape& s, const int32_t* blocks, const BlockLists& l, bool beside, cudaStream_t stream);
 
 }  // namespace dfs

@@ -13,7 +13,6 @@
 namespace dfs {
 namespace tiles {
 
-constexpr int kTileRows = 128;
 constexpr int kRowBytes = kHeadDim * 2;
 constexpr int kTileBytes = kTileRows * kRowBytes;
 constexpr int kKeyBytes = kBlockKeys * kRowBytes;
@@ -41,11 +40,11 @@ struct Row {
     int32_t limit;                 // keys of the block that it sees (up to 64 or more)
     uint32_t slot;                 // (query G + head) ranks + rank; ~0: there is no such row
 };
-// Its entry, and what follows from it.
-__device__ __forceinline__ uint32_t entry_of(const ItemRows& item, int G, int row, uint32_t* head) {
-    const uint32_t r = item.first + (row < item.rows ? row : 0), e = G == 1 ? r : r / G;
+// The entry of row `row` of the walk's block (any one of it where there is no such row).
+__device__ __forceinline__ uint32_t entry_of(const Walk& w, const uint32_t* entries, int G, int row, uint32_t* head) {
+    const uint32_t r = row < w.rows ? row : 0, e = G == 1 ? r : r / G;
     *head = r - e * G;
-    return item.entries[e];
+    return entries[w.first_entry + e];
 }
 __device__ __forceinline__ Row row_from(const SelectShape& s, int32_t ranks, int64_t b, int32_t key0, uint32_t entry,
                                         uint32_t head, bool live) {

@@ -7,12 +7,12 @@
 // and sum in registers, and join through shared memory.  A block's keys and values go from global
 // memory into the products' registers.  Bound by the cache's bytes, or by a launch.
 //
-// Many queries: block by block.  A block of four warps takes up to 512 rows (a query of a head)
-// that list a key block (block_lists.cu), 128 at a time: the rows' queries are gathered into shared
-// memory a tile ahead, S = Q K^T and O = P V run on tcgen05 with P handed over through tensor memory,
-// and each thread has one row's scores, maximum and sum, without exchanges.  Each (row, block) leaves
-// a partial result: 64 fp32 sums, its maximum and its sum, in the workspace; a second kernel joins a
-// row's partials.  The units go in groups whose partials stay in the L2.
+// Many queries: block by block.  The rows (a query of a head) that list a key block (block_lists.cu) make
+// tiles of 128, and a block of four warps walks over a run of tiles: the rows' queries are gathered
+// into shared memory a tile ahead, S = Q K^T and O = P V run on tcgen05 with P handed over through tensor
+// memory, and each thread has one row's scores, maximum and sum, without exchanges.  Each (row, block)
+// leaves a partial result: 64 fp32 sums, its maximum and its sum, in the workspace; a second kernel joins
+// a row's partials.
 #include <atomic>
 
 #include "block_lists.h"
@@ -155,10 +155,11 @@ int launch_few(const SelectedArgs& a, cudaStream_t stream) {
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "selected_few_kernel");
 }
 
-constexpr int kItemThreads = 128;
-constexpr int kItemSmem = 2 * kKeyBytes + 2 * kTileBytes;    // keys, values, two tiles of queries
-constexpr uint32_t kItemColumns = 128;                       // tensor memory: S (then P) and O
-constexpr size_t kGroupBytes = 64 << 20;                     // partials of a group of units
+constexpr int kTileThreads = 128;
+constexpr int kTileSmem = 3 * kKeyBytes + kTileBytes;        // keys, two blocks' values, a tile of queries
+constexpr int kTileResident = 4;                             // blocks of threads an SM
+constexpr uint32_t kTileColumns = 128;                       // tensor memory: S (then P) and O
+constexpr size_t kGroupBytes = size_t(1280) << 20;           // partials of a group of units
 
 // Partials of the units u0 .. : slot x = ((u - u0) n + i) G + h) ranks + rank.
 struct Partials {
@@ -168,8 +169,8 @@ struct Partials {
     bool first;                              // the group after the lists (the others: after a join)
 };
 
-__global__ void __launch_bounds__(kItemThreads, 4)
-selected_items_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials out,
+__global__ void __launch_bounds__(kTileThreads, kTileResident)
+selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials out,
                       int* status) {
     extern __shared__ __align__(1024) char smem[];
     __shared__ uint64_t bars[2];             // S is there; O is
@@ -178,27 +179,44 @@ selected_items_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     // A group starts while the one before is joined (which the lists are older than), and writes no partial
     // before that is over.
     if (out.first) ptx::griddep_wait();
-    const uint32_t ul = blockIdx.x / (uint32_t)l.most_items;
+    const uint32_t ul = blockIdx.x / (uint32_t)l.shares;
+    const int32_t share = blockIdx.x - ul * l.shares;
     const int64_t u = out.u0 + ul, b = sequence_of(s, u);
-    const ItemRows item = item_of(l, s, u, blockIdx.x - ul * l.most_items);
-    if (!item.rows) {
+    const int32_t tiles = l.tile_base[u * (s.nb + 1) + s.nb];
+    const int32_t shares = min(l.shares, tiles);
+    if (share >= shares) {
         ptx::griddep_wait();
         return;
     }
+    const int32_t first = share_begin(tiles, share, shares), last = share_begin(tiles, share + 1, shares);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int32_t key0 = item.block * kBlockKeys;
-    const uint32_t keys = ptx::smem_u32(smem), values = keys + kKeyBytes, queries = values + kKeyBytes;
+    const uint32_t keys = ptx::smem_u32(smem), values = keys + kKeyBytes, queries = values + 2 * kKeyBytes;
     const __nv_bfloat16* q0 = a.q + u * s.G * s.n * kHeadDim;
-    {
-        const int rows = min(kBlockKeys, key_count(s, b) - key0);
-        copy_keys<kItemThreads>(keys, a.k + (u * s.m + key0) * kHeadDim, rows, tid);
-        copy_keys<kItemThreads>(values, a.v + (u * s.m + key0) * kHeadDim, rows, tid);
-    }
-    uint32_t head, entry = entry_of(item, s.G, tid, &head);
-    Row now, next = row_from(s, l.ranks, b, key0, entry, head, tid < item.rows);
+    const uint32_t* entries = l.entries + u * s.n * l.ranks;
+    const int32_t len = key_count(s, b);
+    auto copy_block = [&](int32_t block, uint32_t to_values) {
+        const int64_t from = (u * s.m + (int64_t)block * kBlockKeys) * kHeadDim;
+        const int rows = min(kBlockKeys, len - block * kBlockKeys);
+        copy_keys<kTileThreads>(keys, a.k + from, rows, tid);
+        copy_keys<kTileThreads>(to_values, a.v + from, rows, tid);
+    };
+    // tile x is worked on, the rows of x + 1 are known, the entries of x + 2 are being looked up
+    Walk walk;
+    walk.find(l, s, u, first);
+    uint32_t head, entry;
+    int32_t row = (first - walk.begin) * kTileRows + tid, block = walk.block, block_next;
+    entry = entry_of(walk, entries, s.G, row, &head);
+    copy_block(block, values);
+    Row now, next = row_from(s, l.ranks, b, block * kBlockKeys, entry, head, row < walk.rows);
     copy_rows(queries, q0, next, warp, lane);
-    entry = entry_of(item, s.G, kTileRows + tid, &head);
-    if (warp == 0) ptx::tmem_alloc(&tmem_slot, kItemColumns);
+    auto look = [&](int32_t x) {
+        if (x >= last) return;
+        walk.go(s, x);
+        row = (x - walk.begin) * kTileRows + tid;
+        entry = entry_of(walk, entries, s.G, row, &head);
+    };
+    look(first + 1);
+    if (warp == 0) ptx::tmem_alloc(&tmem_slot, kTileColumns);
     if (tid == 0) {
         ptx::mbar_init(&bars[0], 1);
         ptx::mbar_init(&bars[1], 1);
@@ -211,30 +229,36 @@ selected_items_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     constexpr uint32_t kScores = ptx::mma_idesc_bf16(kTileRows, kBlockKeys, false, false);
     constexpr uint32_t kSums = ptx::mma_idesc_bf16(kTileRows, kHeadDim, false, true);
     const int64_t slot0 = (int64_t)ul * s.n * s.G * l.ranks;
-    const int tiles = (item.rows + kTileRows - 1) / kTileRows;
+    uint32_t side = 0, phase = 0;            // which values; the barriers' phase
 
-    for (int x = 0; x < tiles; ++x) {
+    for (int32_t x = first; x < last; ++x, phase ^= 1) {
         ptx::cp_async_wait_all();
         ptx::fence_proxy_async_smem();
         __syncthreads();                     // the tile is there, and all have read the last O
         if (warp == 0 && ptx::elect_one()) {
             ptx::tc_fence_after();
-            const uint64_t qd = ptx::sw128_kmajor_desc(queries + (x & 1) * kTileBytes), kd = ptx::sw128_kmajor_desc(keys);
+            const uint64_t qd = ptx::sw128_kmajor_desc(queries), kd = ptx::sw128_kmajor_desc(keys);
 #pragma unroll
             for (int e = 0; e < 4; ++e) ptx::mma_bf16_ss(tmem, qd + 2 * e, kd + 2 * e, kScores, e > 0);
             ptx::mma_commit(&bars[0]);
         }
         __syncwarp();
         now = next;
-        if (x + 1 < tiles) {
-            const int row = (x + 1) * kTileRows + tid;
-            next = row_from(s, l.ranks, b, key0, entry, head, row < item.rows);
-            copy_rows(queries + (~x & 1) * kTileBytes, q0, next, warp, lane);
-            entry = entry_of(item, s.G, row + kTileRows, &head);
-        }
-        ptx::mbar_wait(&bars[0], x & 1, status);
+        block_next = walk.block;
+        next = row_from(s, l.ranks, b, block_next * kBlockKeys, entry, head, row < walk.rows);
+        look(x + 2);
+        ptx::mbar_wait(&bars[0], phase, status);
         __syncwarp();
         ptx::tc_fence_after();
+        const uint32_t values_now = values + side * kKeyBytes;
+        if (x + 1 < last) {                  // S is there: the queries' and the keys' places are free
+            if (block_next != block) {
+                side ^= 1;
+                block = block_next;
+                copy_block(block, values + side * kKeyBytes);
+            }
+            copy_rows(queries, q0, next, warp, lane);
+        }
         uint32_t lo[32], hi[32];
         ptx::tmem_ld32_issue(mine, lo);
         ptx::tmem_ld32_issue(mine + 32, hi);
@@ -271,18 +295,18 @@ selected_items_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         __syncthreads();                     // P is whole
         if (warp == 0 && ptx::elect_one()) {
             ptx::tc_fence_after();
-            const uint64_t vd = ptx::sw128_mnmajor_desc(values, kKeyBytes);
+            const uint64_t vd = ptx::sw128_mnmajor_desc(values_now, kKeyBytes);
 #pragma unroll
             for (int e = 0; e < 4; ++e) ptx::mma_bf16_ts(tmem + 64, tmem + 8 * e, vd + 128 * e, kSums, e > 0);
             ptx::mma_commit(&bars[1]);
         }
         __syncwarp();
-        if (x == 0) {
+        if (x == first) {
             ptx::griddep_wait();
             ptx::griddep_launch_dependents();
         }
         if (now.slot != ~0u) out.stat[slot0 + now.slot] = make_float2(top, sum);
-        ptx::mbar_wait(&bars[1], x & 1, status);
+        ptx::mbar_wait(&bars[1], phase, status);
         __syncwarp();
         ptx::tc_fence_after();
         ptx::tmem_ld32_issue(mine + 64, lo);
@@ -299,7 +323,7 @@ selected_items_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         }
     }
     __syncthreads();
-    if (warp == 0) ptx::tmem_dealloc(tmem, kItemColumns);
+    if (warp == 0) ptx::tmem_dealloc(tmem, kTileColumns);
 }
 
 constexpr int kJoined = 8;                   // partials in flight
@@ -357,36 +381,37 @@ struct Plan {
     int64_t group;                           // units whose partials are held at once
     size_t sums, stat, total;
 };
-Plan plan_items(const SelectShape& s, char* ws) {
+Plan plan_tiles(const SelectShape& s, char* ws) {
     Plan p;
-    p.sums = plan_block_lists(s, item_rows(s, 4), ws, &p.lists);
+    p.sums = plan_block_lists(s, ws, &p.lists);
     const int64_t units = s.B * s.Hk, slots = s.n * s.G * p.lists.ranks;
-    p.group = slots ? (int64_t)(kGroupBytes / (slots * 264)) : 1;
-    p.group = p.group < 1 ? 1 : p.group > units ? units : p.group;
+    const int64_t groups = (units * slots * 264 + (int64_t)kGroupBytes - 1) / (int64_t)kGroupBytes;
+    p.group = groups < 1 ? units : groups < units ? (units + groups - 1) / groups : 1;
     p.stat = p.sums + p.group * slots * kHeadDim * 4;
     p.total = p.stat + (p.group * slots * 8 + 255) / 256 * 256;
+    p.lists.shares = tile_shares(s, p.lists, p.group, kTileResident, s.lengths ? kUnlikeRounds : 1);
     return p;
 }
 
-int launch_items(const SelectedArgs& a, char* ws, cudaStream_t stream) {
+int launch_tiles(const SelectedArgs& a, char* ws, cudaStream_t stream) {
     const SelectShape& s = a.s;
-    const Plan p = plan_items(s, ws);
+    const Plan p = plan_tiles(s, ws);
     static std::atomic<uint64_t> ready{0};
     int* status = nullptr;
     int st = ready_status(&status);
     if (st) return st;
-    cudaError_t err = allow_smem(selected_items_kernel, kItemSmem, ready);
-    if (err != cudaSuccess) return cuda_fail(err, "selected_items_kernel");
+    cudaError_t err = allow_smem(selected_tiles_kernel, kTileSmem, ready);
+    if (err != cudaSuccess) return cuda_fail(err, "selected_tiles_kernel");
+    if (p.group * p.lists.shares > INT32_MAX || p.group * s.n * s.G > INT32_MAX)
+        return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
     if ((st = launch_block_lists(s, a.blocks, p.lists, false, stream))) return st;
     const int64_t units = s.B * s.Hk;
-    for (int64_t u0 = 0; u0 < units; u0 += p.group) {
+    for (int64_t u0 = 0; u0 < units && err == cudaSuccess; u0 += p.group) {
         const int64_t here = units - u0 < p.group ? units - u0 : p.group, rows = here * s.n * s.G;
         const Partials part{reinterpret_cast<float*>(ws + p.sums), reinterpret_cast<float2*>(ws + p.stat), u0, u0 == 0};
-        if (here * p.lists.most_items > INT32_MAX || rows > INT32_MAX)
-            return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
         {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-            err = launch_pdl(selected_items_kernel, dim3((unsigned)(here * p.lists.most_items)), dim3(kItemThreads), kItemSmem,
+            err = launch_pdl(selected_tiles_kernel, dim3((unsigned)(here * p.lists.shares)), dim3(kTileThreads), kTileSmem,
                              stream, a, p.lists, part, status);
         }
         if (err == cudaSuccess) {
@@ -394,9 +419,8 @@ int launch_items(const SelectedArgs& a, char* ws, cudaStream_t stream) {
             err = launch_pdl(selected_join_kernel, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, stream, a, p.lists, part,
                              (uint32_t)rows);
         }
-        if (err != cudaSuccess) break;
     }
-    return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "selected_items_kernel");
+    return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "selected_tiles_kernel");
 }
 
 // Few queries: what the lists, the partials and their joining would cost outweighs reading a block's
@@ -405,10 +429,10 @@ bool by_query(const SelectShape& s) { return s.m == 0 || s.B * s.Hk * s.n * s.to
 
 }  // namespace
 
-size_t selected_workspace(const SelectShape& s) { return by_query(s) || s.B * s.n == 0 ? 0 : plan_items(s, nullptr).total; }
+size_t selected_workspace(const SelectShape& s) { return by_query(s) || s.B * s.n == 0 ? 0 : plan_tiles(s, nullptr).total; }
 
 int launch_selected(const SelectedArgs& a, char* ws, cudaStream_t stream) {
-    return by_query(a.s) ? launch_few(a, stream) : launch_items(a, ws, stream);
+    return by_query(a.s) ? launch_few(a, stream) : launch_tiles(a, ws, stream);
 }
 
 }  // namespace dfs

@@ -2,15 +2,15 @@
 //   P_ij = exp(q_i.k_j / 8 - lse_i),  dS_ij = P_ij (dout_i.v_j - delta_i) / 8,  delta_i = dout_i.out_i,
 //   dv_j = sum_i P_ij dout_i,  dk_j = sum_i dS_ij q_i,  dq_i = sum_j dS_ij k_j.
 //
-// A block of eight warps takes up to 512 rows (a query of a head) that list a key block
-// (block_lists.cu), 128 at a time, their q and dout gathered into shared memory a tile ahead.  On
+// The rows (a query of a head) that list a key block (block_lists.cu) make tiles of 128, and a block of
+// eight warps walks over a run of tiles, their q and dout gathered into shared memory a tile ahead.  On
 // tcgen05: S = Q K^T and dout V^T; then P and dS, two threads a row, go to shared memory as bf16, from
 // where dS K gives the rows' dq and one product of 128 x 128,
 //   [dout | Q]^T [P | dS] = [dv^T, .; ., dk^T],
-// adds up dv and dk in tensor memory over all the rows (its other two quarters are not used: 64-row
+// adds up dv and dk in tensor memory over a block's rows (its other two quarters are not used: 64-row
 // accumulators would save half of a product that is a tenth of the time).  A (row, block) leaves 64 fp32
-// sums of dq, an item its sums of dk and dv, and a second kernel joins them in a fixed order.  The units go in
-// groups whose partials stay in the L2.
+// sums of dq, a run of one block's tiles its sums of dk and dv, and a second kernel joins them in a fixed
+// order.
 #include <atomic>
 
 #include "block_lists.h"
@@ -31,11 +31,13 @@ constexpr int kThreads = 256;
 constexpr int kStage = 2 * kTileBytes;       // a tile's dout and queries
 constexpr int kSmem = 2 * kKeyBytes + 2 * kStage + 2 * kTileBytes;       // keys, values; two stages; P and dS
 constexpr uint32_t kColumns = 256;           // tensor memory: S (then dq), dout V^T, dv^T and dk^T
-constexpr size_t kGroupBytes = 96 << 20;     // partials of a group of units
+constexpr int kResident = 2;                 // blocks of threads an SM
+constexpr size_t kGroupBytes = size_t(1536) << 20;       // partials of a group of units
 
 struct Partials {
     float* dq;                               // [slots][64], slot ((u - u0) n + i) G + h) ranks + rank
-    float* dkv;                              // [items][dv, dk][64 features][64 keys]
+    float* dkv;                              // [runs][dv, dk][64 features][64 keys], run (u - u0) runs + share + filled[block]
+    int32_t runs;                            // of a unit
     const float2* stat;                      // [B][Hq][n]: lse in units of log 2, delta
     int64_t u0;
     bool first;                              // the group after the lists (the others: after the joining kernel)
@@ -63,7 +65,7 @@ __global__ void __launch_bounds__(256) selected_delta_kernel(const __grid_consta
     if (row < rows && lane == 0) stat[row] = make_float2(a.lse[row] * kLog2e, d);
 }
 
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kResident)
 selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_constant__ BlockLists l, const Partials out,
                       int* status) {
     extern __shared__ __align__(1024) char smem[];
@@ -73,32 +75,49 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     // A group starts while the one before is joined (which the lists are older than), and writes no partial
     // before that is over.
     if (out.first) ptx::griddep_wait();
-    const uint32_t ul = blockIdx.x / (uint32_t)l.most_items;
+    const uint32_t ul = blockIdx.x / (uint32_t)l.shares;
+    const int32_t share = blockIdx.x - ul * l.shares;
     const int64_t u = out.u0 + ul, b = sequence_of(s, u);
-    const ItemRows item = item_of(l, s, u, blockIdx.x - ul * l.most_items);
-    if (!item.rows) {
+    const int32_t tiles = l.tile_base[u * (s.nb + 1) + s.nb];
+    const int32_t shares = min(l.shares, tiles);
+    if (share >= shares) {
         ptx::griddep_wait();
         return;
     }
+    const int32_t first = share_begin(tiles, share, shares), last = share_begin(tiles, share + 1, shares);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int quarter = warp & 3, half = warp >> 2;          // rows 32 quarter .. and columns 32 half .. of a tile
-    const int32_t key0 = item.block * kBlockKeys;
     const uint32_t keys = ptx::smem_u32(smem), values = keys + kKeyBytes, stages = values + kKeyBytes;
     const uint32_t weights = stages + 2 * kStage;            // P, then dS
     const int64_t head0 = u * s.G * s.n;                     // row 0 of the unit's [G][n]
     // half 0 copies dout, half 1 the queries
     const __nv_bfloat16* from = (half ? a.q : a.dout) + head0 * kHeadDim;
-    {
-        const int rows = min(kBlockKeys, key_count(s, b) - key0);
-        copy_keys<kThreads>(keys, a.k + (u * s.m + key0) * kHeadDim, rows, tid);
-        copy_keys<kThreads>(values, a.v + (u * s.m + key0) * kHeadDim, rows, tid);
-    }
+    const uint32_t* entries = l.entries + u * s.n * l.ranks;
+    const int32_t len = key_count(s, b);
+    auto copy_block = [&](int32_t block) {
+        const int64_t at = (u * s.m + (int64_t)block * kBlockKeys) * kHeadDim;
+        const int rows = min(kBlockKeys, len - block * kBlockKeys);
+        copy_keys<kThreads>(keys, a.k + at, rows, tid);
+        copy_keys<kThreads>(values, a.v + at, rows, tid);
+    };
     const int mine = 32 * quarter + lane;                    // this thread's row of a tile
-    uint32_t head, entry = entry_of(item, s.G, mine, &head);
-    Row now, next = row_from(s, l.ranks, b, key0, entry, head, mine < item.rows);
+    // tile x is worked on, the rows of x + 1 are known, the entries of x + 2 are being looked up
+    Walk walk;
+    walk.find(l, s, u, first);
+    uint32_t head, entry;
+    int32_t row = (first - walk.begin) * kTileRows + mine, block = walk.block, block_next;
+    entry = entry_of(walk, entries, s.G, row, &head);
+    copy_block(block);
+    Row now, next = row_from(s, l.ranks, b, block * kBlockKeys, entry, head, row < walk.rows);
     copy_rows(stages + half * kTileBytes, from, next, quarter, lane);
     float2 stat, stat_next = out.stat[head0 + next.at];
-    entry = entry_of(item, s.G, kTileRows + mine, &head);
+    auto look = [&](int32_t x) {
+        if (x >= last) return;
+        walk.go(s, x);
+        row = (x - walk.begin) * kTileRows + mine;
+        entry = entry_of(walk, entries, s.G, row, &head);
+    };
+    look(first + 1);
     if (warp == 0) ptx::tmem_alloc(&tmem_slot, kColumns);
     if (tid == 0) {
 #pragma unroll
@@ -113,10 +132,11 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     constexpr uint32_t kQueryGrad = ptx::mma_idesc_bf16(kTileRows, kHeadDim, false, true);
     constexpr uint32_t kKeyGrad = ptx::mma_idesc_bf16(2 * kHeadDim, 2 * kBlockKeys, true, true);
     const int64_t slot0 = (int64_t)ul * s.n * s.G * l.ranks;
-    const int tiles = (item.rows + kTileRows - 1) / kTileRows;
+    uint32_t phase = 0;                      // of the barriers, and the stage
+    bool fresh = true;                       // no tile of the block is in dv and dk yet
 
-    for (int x = 0; x < tiles; ++x) {
-        const uint32_t stage = stages + (x & 1) * kStage;
+    for (int32_t x = first; x < last; ++x, phase ^= 1) {
+        const uint32_t stage = stages + phase * kStage;
         ptx::cp_async_wait_all();
         ptx::fence_proxy_async_smem();
         __syncthreads();                     // the tile is there, and all have read the last dq
@@ -134,16 +154,16 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         __syncwarp();
         now = next;
         stat = stat_next;
-        if (x > 0) ptx::mbar_wait(&bars[2], ~x & 1, status);             // the other stage, P and dS are free
-        if (x + 1 < tiles) {
+        block_next = walk.block;
+        if (x > first) ptx::mbar_wait(&bars[2], phase ^ 1, status);      // the other stage, P and dS are free
+        if (x + 1 < last) {
             __syncwarp();
-            const int row = (x + 1) * kTileRows + mine;
-            next = row_from(s, l.ranks, b, key0, entry, head, row < item.rows);
-            copy_rows(stages + (~x & 1) * kStage + half * kTileBytes, from, next, quarter, lane);
+            next = row_from(s, l.ranks, b, block_next * kBlockKeys, entry, head, row < walk.rows);
+            copy_rows(stages + (phase ^ 1) * kStage + half * kTileBytes, from, next, quarter, lane);
             stat_next = out.stat[head0 + next.at];
-            entry = entry_of(item, s.G, row + kTileRows, &head);
+            look(x + 2);
         }
-        ptx::mbar_wait(&bars[0], x & 1, status);
+        ptx::mbar_wait(&bars[0], phase, status);
         __syncwarp();
         ptx::tc_fence_after();
         uint32_t sc[32], dp[32];
@@ -184,37 +204,41 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
             ptx::mma_commit(&bars[1]);
             const uint64_t ad = ptx::sw128_mnmajor_desc(stage, kTileBytes), bd = ptx::sw128_mnmajor_desc(weights, kTileBytes);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ptx::mma_bf16_ss(tmem + 128, ad + 128 * e, bd + 128 * e, kKeyGrad, x > 0 || e > 0);
+            for (int e = 0; e < 8; ++e) ptx::mma_bf16_ss(tmem + 128, ad + 128 * e, bd + 128 * e, kKeyGrad, !fresh || e > 0);
             ptx::mma_commit(&bars[2]);
         }
         __syncwarp();
-        if (x == 0) {
+        if (x == first) {
             ptx::griddep_wait();
             ptx::griddep_launch_dependents();
         }
-        ptx::mbar_wait(&bars[1], x & 1, status);
+        ptx::mbar_wait(&bars[1], phase, status);
         __syncwarp();
         ptx::tc_fence_after();
         ptx::tmem_ld32_issue(col, sc);
         ptx::tmem_ld_wait32(sc);
-        ptx::tc_fence_before();
         if (now.slot != ~0u) {
             float* dst = out.dq + (slot0 + now.slot) * kHeadDim + 32 * half;
 #pragma unroll
             for (int j = 0; j < 4; ++j) store32(dst + 8 * j, sc + 8 * j);
         }
-    }
-    // lanes 0 .. 63: feature of dout, dv^T in the first 64 columns; 64 .. 127: feature of q, dk^T in the others
-    ptx::mbar_wait(&bars[2], ~tiles & 1, status);
-    __syncwarp();
-    ptx::tc_fence_after();
-    uint32_t g[32];
-    ptx::tmem_ld32_issue(col + 128 + (quarter >> 1) * 64, g);
-    ptx::tmem_ld_wait32(g);
-    float* dst = out.dkv + ((int64_t)blockIdx.x * 2 * kHeadDim + mine) * kBlockKeys + 32 * half;
+        fresh = x + 1 == last || block_next != block;
+        if (fresh) {                         // the run's last tile of the block
+            if (x + 1 < last) copy_block(block_next);        // (dq is there: keys and values are done with)
+            ptx::mbar_wait(&bars[2], phase, status);
+            __syncwarp();
+            ptx::tc_fence_after();
+            // lanes 0 .. 63: feature of dout, dv^T in the first 64 columns; 64 .. 127: feature of q, dk^T in the others
+            ptx::tmem_ld32_issue(col + 128 + (quarter >> 1) * 64, sc);
+            ptx::tmem_ld_wait32(sc);
+            const int64_t run = (int64_t)ul * out.runs + share + l.filled[u * s.nb + block];
+            float* dst = out.dkv + (run * 2 * kHeadDim + mine) * kBlockKeys + 32 * half;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) store32(dst + 8 * j, g + 8 * j);
-    ptx::tc_fence_before();
+            for (int j = 0; j < 4; ++j) store32(dst + 8 * j, sc + 8 * j);
+            block = block_next;
+        }
+        ptx::tc_fence_before();
+    }
     __syncthreads();
     if (warp == 0) ptx::tmem_dealloc(tmem, kColumns);
 }
@@ -235,7 +259,7 @@ __device__ __forceinline__ void join_dq(const SelectedArgs& a, const BlockLists&
     reinterpret_cast<uint2*>(a.dq + at.place * kHeadDim)[lane] = make_uint2(pack(y.x, y.y), pack(y.z, y.w));
 }
 
-// dk and dv of a key block: the sums of its items', turned, sixteen keys a block of threads.
+// dk and dv of a key block: the sums of its runs', turned, sixteen keys a block of threads.
 constexpr int kSplit = 4;
 __device__ __forceinline__ void join_dkv(const SelectedArgs& a, const BlockLists& l, const Partials& in, uint32_t share) {
     __shared__ float sums[16][kHeadDim + 1];
@@ -244,10 +268,15 @@ __device__ __forceinline__ void join_dkv(const SelectedArgs& a, const BlockLists
     const uint32_t at = share / (2 * kSplit), ul = at / (uint32_t)s.nb;
     const int64_t u = in.u0 + ul;
     const int c = at - ul * s.nb, feature = threadIdx.x >> 2, four = threadIdx.x & 3;
-    const int32_t* base = l.item_base + u * (s.nb + 1) + c;
-    const int from = base[0], to = base[1];
-    const float* src = in.dkv + (((int64_t)ul * l.most_items + from) * 2 * kHeadDim + which * kHeadDim + feature) * kBlockKeys +
-                       16 * part + 4 * four;
+    const int32_t* tile_base = l.tile_base + u * (s.nb + 1);
+    const int32_t tiles = tile_base[s.nb], begin = tile_base[c], end = tile_base[c + 1];
+    int from = 0, to = 0;                    // the shares that have its tiles
+    if (begin < end) {
+        from = share_of_tile(tiles, begin, min(l.shares, tiles));
+        to = share_of_tile(tiles, end - 1, min(l.shares, tiles)) + 1;
+    }
+    const int64_t run = (int64_t)ul * in.runs + l.filled[u * s.nb + c] + from;
+    const float* src = in.dkv + ((run * 2 + which) * kHeadDim + feature) * kBlockKeys + 16 * part + 4 * four;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int x = 0; x < to - from; ++x) {
@@ -279,19 +308,21 @@ selected_join_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_
 struct Plan {
     BlockLists lists;
     int64_t group;                           // units whose partials are held at once
+    int32_t runs;
     size_t stat, dq, dkv, total;
 };
 Plan plan_backward(const SelectShape& s, char* ws) {
     Plan p;
-    p.stat = plan_block_lists(s, item_rows(s, 2), ws, &p.lists);
+    p.stat = plan_block_lists(s, ws, &p.lists);
     p.dq = p.stat + (s.B * s.Hq * s.n * 8 + 255) / 256 * 256;
-    const int64_t units = s.B * s.Hk;
-    const size_t dq = (size_t)s.n * s.G * p.lists.ranks * kHeadDim * 4;
-    const size_t dkv = (size_t)p.lists.most_items * 2 * kBlockKeys * kHeadDim * 4;
-    p.group = (int64_t)(kGroupBytes / (dq + dkv));
-    p.group = p.group < 1 ? 1 : p.group > units ? units : p.group;
+    const int64_t units = s.B * s.Hk, dq = s.n * s.G * p.lists.ranks * kHeadDim * 4;
+    const int64_t groups = (units * dq + (int64_t)kGroupBytes - 1) / (int64_t)kGroupBytes;
+    p.group = groups < 1 ? units : groups < units ? (units + groups - 1) / groups : 1;
+    // each run begins with a share or a block (room for any lengths, which a size query does not know)
+    p.runs = tile_shares(s, p.lists, p.group, kResident, kUnlikeRounds) + p.lists.most_filled;
+    p.lists.shares = tile_shares(s, p.lists, p.group, kResident, s.lengths ? kUnlikeRounds : 1);
     p.dkv = p.dq + p.group * dq;
-    p.total = p.dkv + p.group * dkv;
+    p.total = p.dkv + (size_t)p.group * p.runs * 2 * kBlockKeys * kHeadDim * 4;
     return p;
 }
 
@@ -311,7 +342,9 @@ int launch_selected_backward(const SelectedArgs& a, char* ws, cudaStream_t strea
     cudaError_t err = allow_smem(selected_grads_kernel, kSmem, ready);
     if (err != cudaSuccess) return cuda_fail(err, "selected_grads_kernel");
     const int64_t units = s.B * s.Hk, all = s.B * s.Hq * s.n;
-    if ((all + 31) / 32 > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
+    if ((all + 31) / 32 > INT32_MAX || p.group * p.lists.shares > INT32_MAX ||
+        p.group * (s.n * s.G + s.nb * 2 * kSplit) > INT32_MAX)
+        return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
         selected_delta_kernel<<<(unsigned)((all + 31) / 32), 256, 0, stream>>>(a, all, reinterpret_cast<float2*>(ws + p.stat));
@@ -319,16 +352,14 @@ int launch_selected_backward(const SelectedArgs& a, char* ws, cudaStream_t strea
     err = cudaGetLastError();
     if (err != cudaSuccess) return cuda_fail(err, "selected_delta_kernel");
     if ((st = launch_block_lists(s, a.blocks, p.lists, true, stream))) return st;
-    for (int64_t u0 = 0; u0 < units; u0 += p.group) {
+    for (int64_t u0 = 0; u0 < units && err == cudaSuccess; u0 += p.group) {
         const int64_t here = units - u0 < p.group ? units - u0 : p.group, rows = here * s.n * s.G;
-        const Partials part{reinterpret_cast<float*>(ws + p.dq), reinterpret_cast<float*>(ws + p.dkv),
+        const Partials part{reinterpret_cast<float*>(ws + p.dq), reinterpret_cast<float*>(ws + p.dkv), p.runs,
                             reinterpret_cast<const float2*>(ws + p.stat), u0, u0 == 0};
-        if (here * p.lists.most_items > INT32_MAX || rows + here * s.nb * 2 * kSplit > INT32_MAX)
-            return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
         {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-            err = launch_pdl(selected_grads_kernel, dim3((unsigned)(here * p.lists.most_items)), dim3(kThreads), kSmem, stream,
-                             a, p.lists, part, status);
+            err = launch_pdl(selected_grads_kernel, dim3((unsigned)(here * p.lists.shares)), dim3(kThreads), kSmem, stream, a,
+                             p.lists, part, status);
         }
         if (err == cudaSuccess) {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
@@ -336,7 +367,6 @@ int launch_selected_backward(const SelectedArgs& a, char* ws, cudaStream_t strea
             err = launch_pdl(selected_join_grads_kernel, dim3((unsigned)(row_blocks + here * s.nb * 2 * kSplit)), dim3(256), 0,
                              stream, a, p.lists, part, (uint32_t)rows, (uint32_t)row_blocks);
         }
-        if (err != cudaSuccess) break;
     }
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "selected_grads_kernel");
 }
