@@ -199,7 +199,7 @@ fill_lists_kernel(const __grid_constant__ SelectShape s, const int32_t* blocks, 
     ptx::griddep_launch_dependents();
     int32_t* begin = reinterpret_cast<int32_t*>(bits + s.nb * l.words);
     for (int c = threadIdx.x; c < s.nb; c += blockDim.x) {
-        int at = l.base[(int64_t)u * (s.nb + 1) + c] + l.counts[((int64_t)u * l.chunks + chunk) * s.nb + c];
+        int at = l.counts[((int64_t)u * l.chunks + chunk) * s.nb + c];
         for (int w = 0; w < l.words; ++w) {
             begin[w * s.nb + c] = at;
             at += __popc(bits[w * s.nb + c]);
@@ -207,12 +207,15 @@ fill_lists_kernel(const __grid_constant__ SelectShape s, const int32_t* blocks, 
     }
     __syncthreads();
     uint32_t* entries = l.entries + u * s.n * l.ranks;
+    uint32_t* positions = l.positions + u * s.n * l.ranks;
+    const int32_t *base = l.base + (int64_t)u * (s.nb + 1), *tile_base = l.tile_base + (int64_t)u * (s.nb + 1);
     const int w = threadIdx.x >> 5;
     const int64_t i0 = ((int64_t)chunk * l.words + w) * 32;
     each_live(s, blocks, u, i0, l.width,
               [&](int q, int c, int rank) {
                   const int at = begin[w * s.nb + c] + __popc(bits[w * s.nb + c] & ((1u << q) - 1));
-                  entries[at] = (uint32_t)(i0 + q) << 6 | rank;
+                  entries[base[c] + at] = (uint32_t)(i0 + q);
+                  positions[(i0 + q) * l.ranks + rank] = (uint32_t)tile_base[c] * kTileRows + (uint32_t)at * s.G;
               },
               [&](int q, int count) { l.live[u * s.n + i0 + q] = count; });
 }
@@ -229,6 +232,7 @@ size_t plan_block_lists(const SelectShape& s, char* ws, BlockLists* l) {
     l->chunks = (int32_t)((s.n + 32 * l->words - 1) / (32 * l->words));
     const int64_t named = s.n * l->ranks;    // (query, block) pairs of a unit
     l->most_filled = (int32_t)(named < s.nb ? named : s.nb);
+    l->most_tiles = l->most_filled + named * s.G / kTileRows;
     l->shares = 1;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -241,6 +245,7 @@ size_t plan_block_lists(const SelectShape& s, char* ws, BlockLists* l) {
     l->tile_base = reinterpret_cast<int32_t*>(take(units * (s.nb + 1) * 4));
     l->filled = reinterpret_cast<int32_t*>(take(units * s.nb * 4));
     l->live = reinterpret_cast<int32_t*>(take(units * s.n * 4));
+    l->positions = reinterpret_cast<uint32_t*>(take(units * named * 4));
     l->counts = reinterpret_cast<int32_t*>(take(units * l->chunks * s.nb * 4));
     return at;
 }

@@ -7,9 +7,8 @@ namespace dfs {
 
 constexpr int kTileRows = 128;               // rows of a tile
 
-// In device memory, for each unit (sequence and key head).  An entry is a query i and its rank
-// among the query's blocks that count, i 64 + rank; a block's entries stand in rising order of i.
-// Entry e of a block stands for G rows, e G + h for head h of the group, and a block's rows make
+// In device memory, for each unit (sequence and key head).  An entry is a query; a block's entries
+// stand in rising order.  Entry e of a block stands for G rows, e G + h for head h of the group, and a block's rows make
 // tiles of 128, the last one shorter.  A unit's tiles, block after block, go to `shares` blocks of
 // threads in runs of equal length: share j has tiles [j N / shares, (j + 1) N / shares) of N (with
 // fewer tiles than shares there are N shares).
@@ -19,10 +18,12 @@ struct BlockLists {
     int32_t* tile_base;            // [units][nb + 1]: where its tiles do
     int32_t* filled;               // [units][nb]: blocks before it that have entries
     int32_t* live;                 // [units][n]: blocks of a query that count
+    uint32_t* positions;           // [units][n][ranks]: for each of them, where head 0's row is: tile 128 + row of it
     int32_t* counts;               // [units][chunks][nb], while they are built
     int32_t ranks;                 // blocks of a query that count, at most: min(top, nb)
     int32_t shares;
     int32_t most_filled;           // blocks that have entries, at most
+    int64_t most_tiles;            // tiles of a unit, at most
     int32_t words, chunks;         // queries of a chunk / 32; chunks
     int32_t width;                 // lanes that read a query's list
 };
@@ -33,7 +34,7 @@ size_t plan_block_lists(const SelectShape& s, char* ws, BlockLists* l);
 // many as run at once, and a tile at least for each.  (One round where the units have alike lengths.)
 constexpr int kUnlikeRounds = 3;
 inline int32_t tile_shares(const SelectShape& s, const BlockLists& l, int64_t here, int resident, int rounds) {
-    const int64_t at_once = 152 * resident / here, tiles = l.most_filled + s.n * l.ranks * s.G / kTileRows;
+    const int64_t at_once = 152 * resident / here, tiles = l.most_tiles;
     const int64_t shares = (at_once < 1 ? 1 : at_once) * rounds;
     return (int32_t)(shares < tiles ? shares : tiles < 1 ? 1 : tiles);
 }
@@ -93,13 +94,14 @@ struct Walk {
 // Row ((u - u0) n + i) G + h of a group of units that begins with u0 (fewer than 2^31 rows).
 struct RowOf {
     uint32_t entry;                // (u - u0) n + i
+    uint32_t unit, head;           // u - u0, h
     int64_t place;                 // the row of [B][Hq][n]
 };
 __device__ __forceinline__ RowOf row_of(const SelectShape& s, int64_t u0, uint32_t row) {
     const uint32_t entry = s.G == 1 ? row : row / s.G, h = row - entry * s.G;
     const uint32_t ul = entry / (uint32_t)s.n, i = entry - ul * (uint32_t)s.n;
     // unit u = b Hk + x: head (b Hk + x) G + h of B Hq
-    return {entry, ((u0 + ul) * s.G + h) * s.n + i};
+    return {entry, ul, h, ((u0 + ul) * s.G + h) * s.n + i};
 }
 #endif
 

@@ -24,6 +24,7 @@ __device__ __forceinline__ uint32_t place(int row, int chunk) { return row * kRo
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live ? 16 : 0) : "memory");
 }
+template <int kLeft> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
 // The 64 keys (or values) at `from`, rows from `rows` on as zeros, by `threads` threads.
 template <int kThreads>
 __device__ __forceinline__ void copy_keys(uint32_t to, const __nv_bfloat16* from, int rows, int tid) {
@@ -37,8 +38,7 @@ __device__ __forceinline__ void copy_keys(uint32_t to, const __nv_bfloat16* from
 // A lane's row of a tile.
 struct Row {
     uint32_t at;                   // of [G][n]: head * n + query
-    int32_t limit;                 // keys of the block that it sees (up to 64 or more)
-    uint32_t slot;                 // (query G + head) ranks + rank; ~0: there is no such row
+    int32_t limit;                 // keys of the block that it sees (up to 64 or more); 0: there is no such row
 };
 // The entry of row `row` of the walk's block (any one of it where there is no such row).
 __device__ __forceinline__ uint32_t entry_of(const Walk& w, const uint32_t* entries, int G, int row, uint32_t* head) {
@@ -46,20 +46,17 @@ __device__ __forceinline__ uint32_t entry_of(const Walk& w, const uint32_t* entr
     *head = r - e * G;
     return entries[w.first_entry + e];
 }
-__device__ __forceinline__ Row row_from(const SelectShape& s, int32_t ranks, int64_t b, int32_t key0, uint32_t entry,
-                                        uint32_t head, bool live) {
-    const uint32_t i = entry >> 6;
-    return {head * (uint32_t)s.n + i, live ? row_limit(s, b, i) - key0 : 0,
-            live ? (i * s.G + head) * ranks + (entry & 63) : ~0u};
+__device__ __forceinline__ Row row_from(const SelectShape& s, int64_t b, int32_t key0, uint32_t entry, uint32_t head, bool live) {
+    return {head * (uint32_t)s.n + entry, live ? row_limit(s, b, entry) - key0 : 0};
 }
 // Copies a warp's 32 rows (its lanes' own) of a tile from [G][n][64] at `from`.
 __device__ __forceinline__ void copy_rows(uint32_t tile, const __nv_bfloat16* from, const Row& mine, int quarter, int lane) {
+    const unsigned live = __ballot_sync(0xffffffffu, mine.limit > 0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int r = 4 * j + (lane >> 3), c = lane & 7;
         const uint32_t at = __shfl_sync(0xffffffffu, mine.at, r);
-        const bool live = __shfl_sync(0xffffffffu, mine.slot, r) != ~0u;
-        copy16(tile + place(32 * quarter + r, c), from + (int64_t)at * kHeadDim + 8 * c, live);
+        copy16(tile + place(32 * quarter + r, c), from + (int64_t)at * kHeadDim + 8 * c, live >> r & 1);
     }
 }
 
@@ -68,6 +65,26 @@ __device__ __forceinline__ void store32(float* p, const uint32_t* v) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
                  "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
+}
+
+// Partial sums of a tile, fp32 [2 halves of 32 features][128 rows][32], in the workspace as in shared memory: rows
+// of 128 bytes, their 16-byte chunks under the swizzle of `place`.  A warp's 32 rows of a half are one bulk copy:
+// the copy engine takes them out while the warp goes on.  (Stores from registers fill the SM's queue to the
+// memory, and everything behind them waits: 365 us where the whole kernel takes 123 without them.)
+constexpr int kSumsBytes = 2 * kTileBytes;
+__device__ __forceinline__ void stage_sums(char* rows, float* to, const uint32_t (&v)[32], int count, int lane) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4*>(rows + place(lane, c)) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && count > 0) ptx::bulk_store(to, rows, min(count, 32) * kRowBytes);
+}
+// Four features of row `position` (tile 128 + row) of the partial sums: lane 0 .. 15's.
+__device__ __forceinline__ float4 sums_at(const float* sums, uint32_t position, int lane) {
+    const uint32_t row = position & (kTileRows - 1);
+    const char* tile = reinterpret_cast<const char*>(sums) + (int64_t)(position / kTileRows) * kSumsBytes;
+    return *reinterpret_cast<const float4*>(tile + (lane >> 3) * kTileBytes + place(row, lane & 7));
 }
 
 }  // namespace tiles

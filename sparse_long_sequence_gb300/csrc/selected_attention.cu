@@ -11,8 +11,8 @@
 // tiles of 128, and a block of four warps walks over a run of tiles: the rows' queries are gathered
 // into shared memory a tile ahead, S = Q K^T and O = P V run on tcgen05 with P handed over through tensor
 // memory, and each thread has one row's scores, maximum and sum, without exchanges.  Each (row, block)
-// leaves a partial result: 64 fp32 sums, its maximum and its sum, in the workspace; a second kernel joins
-// a row's partials.
+// leaves a partial result in the order of the tiles: 64 fp32 sums, its maximum and its sum; a second kernel
+// joins a row's partials.
 #include <atomic>
 
 #include "block_lists.h"
@@ -156,15 +156,15 @@ int launch_few(const SelectedArgs& a, cudaStream_t stream) {
 }
 
 constexpr int kTileThreads = 128;
-constexpr int kTileSmem = 3 * kKeyBytes + kTileBytes;        // keys, two blocks' values, a tile of queries
-constexpr int kTileResident = 4;                             // blocks of threads an SM
+constexpr int kTileSmem = 3 * kKeyBytes + kTileBytes + kSumsBytes;       // keys, two blocks' values, queries, sums
+constexpr int kTileResident = 3;                             // blocks of threads an SM
 constexpr uint32_t kTileColumns = 128;                       // tensor memory: S (then P) and O
 constexpr size_t kGroupBytes = size_t(1280) << 20;           // partials of a group of units
 
-// Partials of the units u0 .. : slot x = ((u - u0) n + i) G + h) ranks + rank.
+// Partials of the units u0 .., [units][tiles].
 struct Partials {
-    float* sums;                             // [slots][64]
-    float2* stat;                            // [slots]: maximum (units of log 2), sum
+    float* sums;                             // [128][64] of a tile (row_tiles.cuh)
+    float2* stat;                            // [128] of a tile: maximum (units of log 2), sum
     int64_t u0;
     bool first;                              // the group after the lists (the others: after a join)
 };
@@ -191,6 +191,7 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     const int32_t first = share_begin(tiles, share, shares), last = share_begin(tiles, share + 1, shares);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t keys = ptx::smem_u32(smem), values = keys + kKeyBytes, queries = values + 2 * kKeyBytes;
+    char* sums = smem + 3 * kKeyBytes + kTileBytes + 32 * warp * kRowBytes;  // this warp's rows on their way out
     const __nv_bfloat16* q0 = a.q + u * s.G * s.n * kHeadDim;
     const uint32_t* entries = l.entries + u * s.n * l.ranks;
     const int32_t len = key_count(s, b);
@@ -205,10 +206,12 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     walk.find(l, s, u, first);
     uint32_t head, entry;
     int32_t row = (first - walk.begin) * kTileRows + tid, block = walk.block, block_next;
+    int32_t count = walk.rows - (row - lane), count_next;    // rows from this warp's first on
     entry = entry_of(walk, entries, s.G, row, &head);
     copy_block(block, values);
-    Row now, next = row_from(s, l.ranks, b, block * kBlockKeys, entry, head, row < walk.rows);
+    Row now, next = row_from(s, b, block * kBlockKeys, entry, head, row < walk.rows);
     copy_rows(queries, q0, next, warp, lane);
+    count_next = count;
     auto look = [&](int32_t x) {
         if (x >= last) return;
         walk.go(s, x);
@@ -228,7 +231,7 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     const uint32_t tmem = tmem_slot, mine = tmem + ((uint32_t)(32 * warp) << 16);
     constexpr uint32_t kScores = ptx::mma_idesc_bf16(kTileRows, kBlockKeys, false, false);
     constexpr uint32_t kSums = ptx::mma_idesc_bf16(kTileRows, kHeadDim, false, true);
-    const int64_t slot0 = (int64_t)ul * s.n * s.G * l.ranks;
+    const int64_t tile0 = (int64_t)ul * l.most_tiles;
     uint32_t side = 0, phase = 0;            // which values; the barriers' phase
 
     for (int32_t x = first; x < last; ++x, phase ^= 1) {
@@ -244,8 +247,10 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         }
         __syncwarp();
         now = next;
+        count = count_next;
         block_next = walk.block;
-        next = row_from(s, l.ranks, b, block_next * kBlockKeys, entry, head, row < walk.rows);
+        next = row_from(s, b, block_next * kBlockKeys, entry, head, row < walk.rows);
+        count_next = walk.rows - (row - lane);
         look(x + 2);
         ptx::mbar_wait(&bars[0], phase, status);
         __syncwarp();
@@ -305,7 +310,7 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
             ptx::griddep_wait();
             ptx::griddep_launch_dependents();
         }
-        if (now.slot != ~0u) out.stat[slot0 + now.slot] = make_float2(top, sum);
+        out.stat[(tile0 + x) * kTileRows + tid] = make_float2(top, sum);
         ptx::mbar_wait(&bars[1], phase, status);
         __syncwarp();
         ptx::tc_fence_after();
@@ -314,14 +319,14 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::tmem_ld_wait32(lo);
         ptx::tmem_ld_wait32(hi);
         ptx::tc_fence_before();
-        if (now.slot != ~0u) {
-            float* dst = out.sums + (slot0 + now.slot) * kHeadDim;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) store32(dst + 8 * j, lo + 8 * j);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) store32(dst + 32 + 8 * j, hi + 8 * j);
-        }
+        if (lane == 0) ptx::bulk_wait_read<0>();             // the last rows have left
+        __syncwarp();
+        float* dst = out.sums + (tile0 + x) * (kSumsBytes / 4) + 32 * warp * (kRowBytes / 4);
+        stage_sums(sums, dst, lo, count, lane);
+        stage_sums(sums + kTileBytes, dst + kTileBytes / 4, hi, count, lane);
+        if (lane == 0) ptx::bulk_commit();
     }
+    if (lane == 0) ptx::bulk_wait<0>();
     __syncthreads();
     if (warp == 0) ptx::tmem_dealloc(tmem, kTileColumns);
 }
@@ -340,19 +345,23 @@ selected_join_kernel(const __grid_constant__ SelectedArgs a, const __grid_consta
     if (row >= rows) return;
     const RowOf at = row_of(s, in.u0, row);
     const int count = l.live[in.u0 * s.n + at.entry];
-    const float2* stat = in.stat + (int64_t)row * l.ranks;
-    const float4* part = reinterpret_cast<const float4*>(in.sums + (int64_t)row * l.ranks * kHeadDim) + lane;
+    const uint32_t* position = l.positions + (in.u0 * s.n + at.entry) * l.ranks;
+    const float* sums = in.sums + at.unit * l.most_tiles * (kSumsBytes / 4);
+    const float2* stat = in.stat + at.unit * l.most_tiles * kTileRows;
     // eight partials at a time, under a running maximum
     float top = -INFINITY, sum = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int x0 = 0; x0 < count; x0 += kJoined) {
-        float4 p[kJoined];
+        uint32_t p[kJoined];
+        float4 v[kJoined];
         float2 st[kJoined];
+#pragma unroll
+        for (int x = 0; x < kJoined; ++x) p[x] = x0 + x < count ? position[x0 + x] + at.head : ~0u;
 #pragma unroll
         for (int x = 0; x < kJoined; ++x) {
             const bool on = x0 + x < count;
-            p[x] = on ? part[(x0 + x) * 16] : make_float4(0.f, 0.f, 0.f, 0.f);
-            st[x] = on ? stat[x0 + x] : make_float2(-INFINITY, 0.f);
+            v[x] = on ? sums_at(sums, p[x], lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+            st[x] = on ? stat[p[x]] : make_float2(-INFINITY, 0.f);
         }
         float now = top;
 #pragma unroll
@@ -364,10 +373,10 @@ selected_join_kernel(const __grid_constant__ SelectedArgs a, const __grid_consta
         for (int x = 0; x < kJoined; ++x) {
             const float w = exp2_fast(st[x].x - base);
             sum += w * st[x].y;
-            y.x += w * p[x].x;
-            y.y += w * p[x].y;
-            y.z += w * p[x].z;
-            y.w += w * p[x].w;
+            y.x += w * v[x].x;
+            y.y += w * v[x].y;
+            y.z += w * v[x].z;
+            y.w += w * v[x].w;
         }
         top = now;
     }
@@ -384,11 +393,11 @@ struct Plan {
 Plan plan_tiles(const SelectShape& s, char* ws) {
     Plan p;
     p.sums = plan_block_lists(s, ws, &p.lists);
-    const int64_t units = s.B * s.Hk, slots = s.n * s.G * p.lists.ranks;
-    const int64_t groups = (units * slots * 264 + (int64_t)kGroupBytes - 1) / (int64_t)kGroupBytes;
+    const int64_t units = s.B * s.Hk;
+    const int64_t groups = (units * p.lists.most_tiles * kSumsBytes + (int64_t)kGroupBytes - 1) / (int64_t)kGroupBytes;
     p.group = groups < 1 ? units : groups < units ? (units + groups - 1) / groups : 1;
-    p.stat = p.sums + p.group * slots * kHeadDim * 4;
-    p.total = p.stat + (p.group * slots * 8 + 255) / 256 * 256;
+    p.stat = p.sums + p.group * p.lists.most_tiles * kSumsBytes;
+    p.total = p.stat + p.group * p.lists.most_tiles * kTileRows * 8;
     p.lists.shares = tile_shares(s, p.lists, p.group, kTileResident, s.lengths ? kUnlikeRounds : 1);
     return p;
 }

@@ -9,7 +9,7 @@
 //   [dout | Q]^T [P | dS] = [dv^T, .; ., dk^T],
 // adds up dv and dk in tensor memory over a block's rows (its other two quarters are not used: 64-row
 // accumulators would save half of a product that is a tenth of the time).  A (row, block) leaves 64 fp32
-// sums of dq, a run of one block's tiles its sums of dk and dv, and a second kernel joins them in a fixed
+// sums of dq in the order of the tiles, a run of one block's tiles its sums of dk and dv, and a second kernel joins them in a fixed
 // order.
 #include <atomic>
 
@@ -35,7 +35,7 @@ constexpr int kResident = 2;                 // blocks of threads an SM
 constexpr size_t kGroupBytes = size_t(1536) << 20;       // partials of a group of units
 
 struct Partials {
-    float* dq;                               // [slots][64], slot ((u - u0) n + i) G + h) ranks + rank
+    float* dq;                               // [units][tiles] of [128][64] (row_tiles.cuh)
     float* dkv;                              // [runs][dv, dk][64 features][64 keys], run (u - u0) runs + share + filled[block]
     int32_t runs;                            // of a unit
     const float2* stat;                      // [B][Hq][n]: lse in units of log 2, delta
@@ -108,7 +108,8 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     int32_t row = (first - walk.begin) * kTileRows + mine, block = walk.block, block_next;
     entry = entry_of(walk, entries, s.G, row, &head);
     copy_block(block);
-    Row now, next = row_from(s, l.ranks, b, block * kBlockKeys, entry, head, row < walk.rows);
+    int32_t count, count_next = walk.rows - (row - lane);    // rows from this warp's first on
+    Row next = row_from(s, b, block * kBlockKeys, entry, head, row < walk.rows);
     copy_rows(stages + half * kTileBytes, from, next, quarter, lane);
     float2 stat, stat_next = out.stat[head0 + next.at];
     auto look = [&](int32_t x) {
@@ -131,15 +132,17 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     constexpr uint32_t kScores = ptx::mma_idesc_bf16(kTileRows, kBlockKeys, false, false);
     constexpr uint32_t kQueryGrad = ptx::mma_idesc_bf16(kTileRows, kHeadDim, false, true);
     constexpr uint32_t kKeyGrad = ptx::mma_idesc_bf16(2 * kHeadDim, 2 * kBlockKeys, true, true);
-    const int64_t slot0 = (int64_t)ul * s.n * s.G * l.ranks;
+    const int64_t tile0 = (int64_t)ul * l.most_tiles;
+    char* sums = smem + (weights - keys) + half * kTileBytes + 32 * quarter * kRowBytes;   // this warp's part of dq on its way out
     uint32_t phase = 0;                      // of the barriers, and the stage
     bool fresh = true;                       // no tile of the block is in dv and dk yet
 
     for (int32_t x = first; x < last; ++x, phase ^= 1) {
         const uint32_t stage = stages + phase * kStage;
         ptx::cp_async_wait_all();
+        if (lane == 0) ptx::bulk_wait_read<0>();
         ptx::fence_proxy_async_smem();
-        __syncthreads();                     // the tile is there, and all have read the last dq
+        __syncthreads();                     // the tile is there, and the last dq has left
         if (warp == 0 && ptx::elect_one()) {
             ptx::tc_fence_after();
             const uint64_t dd = ptx::sw128_kmajor_desc(stage), qd = ptx::sw128_kmajor_desc(stage + kTileBytes);
@@ -152,13 +155,13 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
             ptx::mma_commit(&bars[0]);
         }
         __syncwarp();
-        now = next;
+        const int limit = next.limit - 32 * half;
+        count = count_next;
         stat = stat_next;
         block_next = walk.block;
-        if (x > first) ptx::mbar_wait(&bars[2], phase ^ 1, status);      // the other stage, P and dS are free
-        if (x + 1 < last) {
-            __syncwarp();
-            next = row_from(s, l.ranks, b, block_next * kBlockKeys, entry, head, row < walk.rows);
+        if (x + 1 < last) {                  // (the other stage is free: dv and dk have taken it)
+            next = row_from(s, b, block_next * kBlockKeys, entry, head, row < walk.rows);
+            count_next = walk.rows - (row - lane);
             copy_rows(stages + (phase ^ 1) * kStage + half * kTileBytes, from, next, quarter, lane);
             stat_next = out.stat[head0 + next.at];
             look(x + 2);
@@ -171,7 +174,6 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::tmem_ld32_issue(col + 64, dp);
         ptx::tmem_ld_wait32(sc);
         ptx::tmem_ld_wait32(dp);
-        const int limit = now.limit - 32 * half;
         char* to = smem + (weights - keys);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -217,16 +219,13 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::tc_fence_after();
         ptx::tmem_ld32_issue(col, sc);
         ptx::tmem_ld_wait32(sc);
-        if (now.slot != ~0u) {
-            float* dst = out.dq + (slot0 + now.slot) * kHeadDim + 32 * half;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) store32(dst + 8 * j, sc + 8 * j);
-        }
+        ptx::mbar_wait(&bars[2], phase, status);             // P and dS are free: dq leaves by their place
+        __syncwarp();
+        stage_sums(sums, out.dq + (tile0 + x) * (kSumsBytes / 4) + (half * kTileBytes + 32 * quarter * kRowBytes) / 4, sc, count, lane);
+        if (lane == 0) ptx::bulk_commit();
         fresh = x + 1 == last || block_next != block;
         if (fresh) {                         // the run's last tile of the block
             if (x + 1 < last) copy_block(block_next);        // (dq is there: keys and values are done with)
-            ptx::mbar_wait(&bars[2], phase, status);
-            __syncwarp();
             ptx::tc_fence_after();
             // lanes 0 .. 63: feature of dout, dv^T in the first 64 columns; 64 .. 127: feature of q, dk^T in the others
             ptx::tmem_ld32_issue(col + 128 + (quarter >> 1) * 64, sc);
@@ -239,9 +238,12 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         }
         ptx::tc_fence_before();
     }
+    if (lane == 0) ptx::bulk_wait<0>();
     __syncthreads();
     if (warp == 0) ptx::tmem_dealloc(tmem, kColumns);
 }
+
+constexpr int kJoined = 8;                   // partials in flight
 
 // dq of a row: the sum of its partials, sixteen lanes a row, sixteen rows a block of threads.
 __device__ __forceinline__ void join_dq(const SelectedArgs& a, const BlockLists& l, const Partials& in, uint32_t row) {
@@ -249,12 +251,18 @@ __device__ __forceinline__ void join_dq(const SelectedArgs& a, const BlockLists&
     const int lane = threadIdx.x & 15;
     const RowOf at = row_of(s, in.u0, row);
     const int count = l.live[in.u0 * s.n + at.entry];
-    const float4* part = reinterpret_cast<const float4*>(in.dq + (int64_t)row * l.ranks * kHeadDim) + lane;
+    const uint32_t* position = l.positions + (in.u0 * s.n + at.entry) * l.ranks;
+    const float* sums = in.dq + at.unit * l.most_tiles * (kSumsBytes / 4);
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int x = 0; x < count; ++x) {
-        const float4 p = part[x * 16];
-        y = make_float4(y.x + p.x, y.y + p.y, y.z + p.z, y.w + p.w);
+    for (int x0 = 0; x0 < count; x0 += kJoined) {            // eight partials at a time
+        uint32_t p[kJoined];
+        float4 v[kJoined];
+#pragma unroll
+        for (int x = 0; x < kJoined; ++x) p[x] = x0 + x < count ? position[x0 + x] + at.head : ~0u;
+#pragma unroll
+        for (int x = 0; x < kJoined; ++x) v[x] = x0 + x < count ? sums_at(sums, p[x], lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < kJoined; ++x) y = make_float4(y.x + v[x].x, y.y + v[x].y, y.z + v[x].z, y.w + v[x].w);
     }
     reinterpret_cast<uint2*>(a.dq + at.place * kHeadDim)[lane] = make_uint2(pack(y.x, y.y), pack(y.z, y.w));
 }
@@ -315,7 +323,7 @@ Plan plan_backward(const SelectShape& s, char* ws) {
     Plan p;
     p.stat = plan_block_lists(s, ws, &p.lists);
     p.dq = p.stat + (s.B * s.Hq * s.n * 8 + 255) / 256 * 256;
-    const int64_t units = s.B * s.Hk, dq = s.n * s.G * p.lists.ranks * kHeadDim * 4;
+    const int64_t units = s.B * s.Hk, dq = p.lists.most_tiles * kSumsBytes;
     const int64_t groups = (units * dq + (int64_t)kGroupBytes - 1) / (int64_t)kGroupBytes;
     p.group = groups < 1 ? units : groups < units ? (units + groups - 1) / groups : 1;
     // each run begins with a share or a block (room for any lengths, which a size query does not know)
