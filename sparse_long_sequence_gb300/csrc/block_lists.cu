@@ -192,14 +192,17 @@ place_lists_kernel(const __grid_constant__ SelectShape s, const __grid_constant_
 
 __global__ void __launch_bounds__(kThreads)
 fill_lists_kernel(const __grid_constant__ SelectShape s, const int32_t* blocks, const __grid_constant__ BlockLists l) {
-    extern __shared__ uint32_t bits[];       // [words][nb], then where each word's queries begin, [words][nb]
+    extern __shared__ uint32_t bits[];       // [words][nb]; where each word's queries begin, [words][nb]; [nb]
     const uint32_t u = blockIdx.x / (uint32_t)l.chunks, chunk = blockIdx.x - u * l.chunks;
     set_bits(s, blocks, l, u, chunk, bits);  // (the lists of blocks are no earlier kernel's)
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     int32_t* begin = reinterpret_cast<int32_t*>(bits + s.nb * l.words);
+    uint32_t* shift = bits + 2 * s.nb * l.words;             // from G times an entry's place to its rows' position
+    const int32_t *base = l.base + (int64_t)u * (s.nb + 1), *tile_base = l.tile_base + (int64_t)u * (s.nb + 1);
     for (int c = threadIdx.x; c < s.nb; c += blockDim.x) {
-        int at = l.counts[((int64_t)u * l.chunks + chunk) * s.nb + c];
+        int at = base[c] + l.counts[((int64_t)u * l.chunks + chunk) * s.nb + c];
+        shift[c] = (uint32_t)tile_base[c] * kTileRows - (uint32_t)base[c] * s.G;
         for (int w = 0; w < l.words; ++w) {
             begin[w * s.nb + c] = at;
             at += __popc(bits[w * s.nb + c]);
@@ -208,14 +211,13 @@ fill_lists_kernel(const __grid_constant__ SelectShape s, const int32_t* blocks, 
     __syncthreads();
     uint32_t* entries = l.entries + u * s.n * l.ranks;
     uint32_t* positions = l.positions + u * s.n * l.ranks;
-    const int32_t *base = l.base + (int64_t)u * (s.nb + 1), *tile_base = l.tile_base + (int64_t)u * (s.nb + 1);
     const int w = threadIdx.x >> 5;
     const int64_t i0 = ((int64_t)chunk * l.words + w) * 32;
     each_live(s, blocks, u, i0, l.width,
               [&](int q, int c, int rank) {
                   const int at = begin[w * s.nb + c] + __popc(bits[w * s.nb + c] & ((1u << q) - 1));
-                  entries[base[c] + at] = (uint32_t)(i0 + q);
-                  positions[(i0 + q) * l.ranks + rank] = (uint32_t)tile_base[c] * kTileRows + (uint32_t)at * s.G;
+                  entries[at] = (uint32_t)(i0 + q);
+                  positions[(i0 + q) * l.ranks + rank] = (uint32_t)at * s.G + shift[c];
               },
               [&](int q, int count) { l.live[u * s.n + i0 + q] = count; });
 }
@@ -255,7 +257,7 @@ int launch_block_lists(const SelectShape& s, const int32_t* blocks, const BlockL
     const int64_t units = s.B * s.Hk, grid = units * l.chunks;
     if (grid > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
     cudaError_t err = allow_smem(count_lists_kernel, kBitmapBytes, count_ready);
-    if (err == cudaSuccess) err = allow_smem(fill_lists_kernel, 2 * kBitmapBytes, fill_ready);
+    if (err == cudaSuccess) err = allow_smem(fill_lists_kernel, 3 * kBitmapBytes, fill_ready);
     if (err != cudaSuccess) return cuda_fail(err, "the block lists");
     const size_t smem = (size_t)s.nb * l.words * 4;
     const int threads = 32 * l.words;
@@ -274,7 +276,7 @@ int launch_block_lists(const SelectShape& s, const int32_t* blocks, const BlockL
     }
     if (err == cudaSuccess) {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        err = launch_pdl(fill_lists_kernel, dim3((unsigned)grid), dim3(threads), 2 * smem, stream, s, blocks, l);
+        err = launch_pdl(fill_lists_kernel, dim3((unsigned)grid), dim3(threads), 2 * smem + (size_t)s.nb * 4, stream, s, blocks, l);
     }
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "the block lists");
 }

@@ -67,24 +67,22 @@ __device__ __forceinline__ void store32(float* p, const uint32_t* v) {
                  : "memory");
 }
 
-// Partial sums of a tile, fp32 [2 halves of 32 features][128 rows][32], in the workspace as in shared memory: rows
-// of 128 bytes, their 16-byte chunks under the swizzle of `place`.  A warp's 32 rows of a half are one bulk copy:
-// the copy engine takes them out while the warp goes on.  (Stores from registers fill the SM's queue to the
-// memory, and everything behind them waits: 365 us where the whole kernel takes 123 without them.)
-constexpr int kSumsBytes = 2 * kTileBytes;
-__device__ __forceinline__ void stage_sums(char* rows, float* to, const uint32_t (&v)[32], int count, int lane) {
+// Partial sums of a tile, fp32 [128 rows][64], in the workspace as in shared memory: rows of 256 bytes, chunk c of
+// 16 bytes in place c ^ (row & 7), so that the lanes of a warp, each with a row, fall in different banks.  A
+// warp's 32 rows are one bulk copy: the copy engine takes them out while the warp goes on.  (Stores from registers
+// fill the SM's queue to the memory, and everything behind them waits: 365 us where the whole kernel takes 123
+// without them.)
+constexpr int kSumsPitch = kHeadDim * 4;
+constexpr int kSumsBytes = kTileRows * kSumsPitch;
+// 32 of a row's 64 sums, to chunks 8 half ..
+__device__ __forceinline__ void stage_sums(char* row, const uint32_t (&v)[32], int half, int lane) {
 #pragma unroll
     for (int c = 0; c < 8; ++c)
-        *reinterpret_cast<uint4*>(rows + place(lane, c)) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-    ptx::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0 && count > 0) ptx::bulk_store(to, rows, min(count, 32) * kRowBytes);
+        *reinterpret_cast<uint4*>(row + ((8 * half + c) ^ (lane & 7)) * 16) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
 }
 // Four features of row `position` (tile 128 + row) of the partial sums: lane 0 .. 15's.
 __device__ __forceinline__ float4 sums_at(const float* sums, uint32_t position, int lane) {
-    const uint32_t row = position & (kTileRows - 1);
-    const char* tile = reinterpret_cast<const char*>(sums) + (int64_t)(position / kTileRows) * kSumsBytes;
-    return *reinterpret_cast<const float4*>(tile + (lane >> 3) * kTileBytes + place(row, lane & 7));
+    return reinterpret_cast<const float4*>(sums)[(int64_t)position * 16 + (lane ^ (position & 7))];
 }
 
 }  // namespace tiles

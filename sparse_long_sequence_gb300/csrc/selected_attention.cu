@@ -191,7 +191,7 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     const int32_t first = share_begin(tiles, share, shares), last = share_begin(tiles, share + 1, shares);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t keys = ptx::smem_u32(smem), values = keys + kKeyBytes, queries = values + 2 * kKeyBytes;
-    char* sums = smem + 3 * kKeyBytes + kTileBytes + 32 * warp * kRowBytes;  // this warp's rows on their way out
+    char* sums = smem + 3 * kKeyBytes + kTileBytes + 32 * warp * kSumsPitch; // this warp's rows on their way out
     const __nv_bfloat16* q0 = a.q + u * s.G * s.n * kHeadDim;
     const uint32_t* entries = l.entries + u * s.n * l.ranks;
     const int32_t len = key_count(s, b);
@@ -321,10 +321,14 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::tc_fence_before();
         if (lane == 0) ptx::bulk_wait_read<0>();             // the last rows have left
         __syncwarp();
-        float* dst = out.sums + (tile0 + x) * (kSumsBytes / 4) + 32 * warp * (kRowBytes / 4);
-        stage_sums(sums, dst, lo, count, lane);
-        stage_sums(sums + kTileBytes, dst + kTileBytes / 4, hi, count, lane);
-        if (lane == 0) ptx::bulk_commit();
+        stage_sums(sums + lane * kSumsPitch, lo, 0, lane);
+        stage_sums(sums + lane * kSumsPitch, hi, 1, lane);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && count > 0) {
+            ptx::bulk_store(out.sums + ((tile0 + x) * kTileRows + 32 * warp) * kHeadDim, sums, min(count, 32) * kSumsPitch);
+            ptx::bulk_commit();
+        }
     }
     if (lane == 0) ptx::bulk_wait<0>();
     __syncthreads();

@@ -133,7 +133,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     constexpr uint32_t kQueryGrad = ptx::mma_idesc_bf16(kTileRows, kHeadDim, false, true);
     constexpr uint32_t kKeyGrad = ptx::mma_idesc_bf16(2 * kHeadDim, 2 * kBlockKeys, true, true);
     const int64_t tile0 = (int64_t)ul * l.most_tiles;
-    char* sums = smem + (weights - keys) + half * kTileBytes + 32 * quarter * kRowBytes;   // this warp's part of dq on its way out
+    char* sums = smem + (weights - keys) + 32 * quarter * kSumsPitch;    // its rows' dq on their way out, two warps'
     uint32_t phase = 0;                      // of the barriers, and the stage
     bool fresh = true;                       // no tile of the block is in dv and dk yet
 
@@ -221,8 +221,14 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::tmem_ld_wait32(sc);
         ptx::mbar_wait(&bars[2], phase, status);             // P and dS are free: dq leaves by their place
         __syncwarp();
-        stage_sums(sums, out.dq + (tile0 + x) * (kSumsBytes / 4) + (half * kTileBytes + 32 * quarter * kRowBytes) / 4, sc, count, lane);
-        if (lane == 0) ptx::bulk_commit();
+        stage_sums(sums + lane * kSumsPitch, sc, half, lane);
+        ptx::fence_proxy_async_smem();
+        ptx::named_barrier_sync(1 + quarter, 64);            // the rows' two warps
+        if (half == 0 && lane == 0 && count > 0) {
+            ptx::bulk_store(out.dq + ((tile0 + x) * kTileRows + 32 * quarter) * kHeadDim, sums, min(count, 32) * kSumsPitch);
+            ptx::bulk_commit();
+        }
+        __syncwarp();
         fresh = x + 1 == last || block_next != block;
         if (fresh) {                         // the run's last tile of the block
             if (x + 1 < last) copy_block(block_next);        // (dq is there: keys and values are done with)
