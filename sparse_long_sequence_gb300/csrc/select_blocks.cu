@@ -3,7 +3,7 @@
 // ties to the lowest index, the forced blocks (the first `sink`, and those less than `local` from the
 // query's own) before all others, written in ascending order with -1 behind them.
 //
-// A block of eight warps takes up to 16 queries of a unit (sequence and key head).  First the scores
+// A block of eight warps takes up to 32 queries of a unit (sequence and key head).  First the scores
 // on m16n8k16 products (16 blocks by 8 queries, the heads one after the other along the summed index),
 // kept in shared memory as fp32; then a warp a query: candidates by the lanes' maxima, and among them the
 // top-th largest value by bisection on values.
@@ -27,14 +27,14 @@ using namespace tiles;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMostQueries = 16;
+constexpr int kMostQueries = 32;
 
 struct Choice {
     SelectShape s;
     const __nv_bfloat16 *q, *means;
     int32_t sink, local;
     int32_t* blocks;
-    int32_t tile;                  // queries of a block of threads: 16, or fewer for many key blocks
+    int32_t tile;                  // queries of a block of threads: 32, or fewer for many key blocks
     int32_t stride;                // floats of a query's scores
 };
 
@@ -93,10 +93,16 @@ struct Best {
     }
 };
 
+// Over a warp, of numbers.
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, off));
-    return x;
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float warp_min(float x) {
+    float y;
+    asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ uint64_t ballot2(bool a, bool b) {
     const unsigned lo = __ballot_sync(kFull, a), hi = __ballot_sync(kFull, b);
@@ -105,23 +111,41 @@ __device__ __forceinline__ uint64_t ballot2(bool a, bool b) {
 
 constexpr int kCandidates = 64;
 
-// The `want` (1 to 32) largest of v[0 .. nv), finite but for -infinity in places that take no part;
-// more than `want` take part.  Some x that the maxima of at least `want` lanes reach bounds the
-// want-th largest value from below, so that only the values above it, a few more than `want`, need
-// a closer look: the candidates, by rising index, two a lane (place lane and lane + 32).  Returns
-// their number, and in `taken` a bit for the place of each that is chosen; -1 where there are too many.
+// The want-th largest of a warp's values, two a lane (-infinity: none), more than `want` of them: by
+// bisection on values.
+__device__ __forceinline__ float nth_largest(const float (&x)[2], int want) {
+    float lo = fminf(x[0] > -INFINITY ? x[0] : INFINITY, x[1] > -INFINITY ? x[1] : INFINITY);
+    float hi = fmaxf(x[0] < INFINITY ? x[0] : -INFINITY, x[1] < INFINITY ? x[1] : -INFINITY);
+    lo = warp_min(lo);
+    hi = warp_max(hi);
+    if (__popcll(ballot2(x[0] >= hi, x[1] >= hi)) >= want) return hi;
+    for (;;) {                               // more than `want` reach lo, fewer reach hi
+        const float mid = lo + 0.5f * (hi - lo);
+        if (!(mid > lo && mid < hi)) return lo;
+        const int n = __popcll(ballot2(x[0] >= mid, x[1] >= mid));
+        if (n == want) return warp_min(fminf(x[0] >= mid ? x[0] : INFINITY, x[1] >= mid ? x[1] : INFINITY));
+        if (n > want) lo = mid;
+        else hi = mid;
+    }
+}
+
+// The `want` (1 to 32) largest of v[0 .. nv), of which more than `want` are above -infinity and at most `want`
+// infinite (those are in), the others finite; v goes on as -infinity to a multiple of 32.  Some x that the
+// maxima of at least `want` lanes reach bounds the want-th largest value from below, so that only the values
+// above it, a few more than `want`, need a closer look: the candidates, by rising index, two a lane (place
+// lane and lane + 32).  Returns false where there are too many of them; else in `taken` a bit for the place of
+// each that is chosen.
 template <class Exact>
-__device__ __forceinline__ int narrow(const float* v, int nv, int want, float eps, int lane, float* cand_x, int* cand_c,
-                                      int (&cand)[2], uint64_t* taken, Exact exact) {
+__device__ __forceinline__ bool narrow(const float* v, int nv, int want, float eps, int lane, float* cand_x, int* cand_c,
+                                       int (&cand)[2], uint64_t* taken, Exact exact) {
     float best = -INFINITY;
 #pragma unroll 4
     for (int c = lane; c < nv; c += 32) best = fmaxf(best, v[c]);
-    const float most = warp_max(best);
-    float lo = -warp_max(best == -INFINITY ? -INFINITY : -best), hi = most;
-    if (__popc(__ballot_sync(kFull, best > -INFINITY)) < want) {
-        lo = -INFINITY;                                      // (few values: all are candidates)
-    } else {
-        for (int k = 0; k < 12; ++k) {
+    float lo = -INFINITY;                    // (fewer lanes than `want` have any: all values are candidates)
+    if (__popc(__ballot_sync(kFull, best > -INFINITY)) >= want) {
+        lo = warp_min(best > -INFINITY ? best : INFINITY);
+        float hi = warp_max(best < INFINITY ? best : -INFINITY);
+        for (int k = 0; k < 12 && lo < hi; ++k) {
             const float mid = lo + 0.5f * (hi - lo);
             const int n = __popc(__ballot_sync(kFull, best >= mid));
             if (n >= want) lo = mid;
@@ -129,60 +153,49 @@ __device__ __forceinline__ int narrow(const float* v, int nv, int want, float ep
             if (n >= want && n <= want + 2) break;
         }
     }
-    const float floor = lo - eps;
+    const float floor = fmaxf(lo - eps, -FLT_MAX);
     int few = 0;
-    for (int c0 = 0; c0 < nv; c0 += 32) {
-        const float y = v[c0 + lane];
-        const bool in = y >= floor && y > -INFINITY;
+    for (int c = lane; c - lane < nv; c += 32) {
+        const float y = v[c];
+        const bool in = y >= floor;
         const unsigned m = __ballot_sync(kFull, in);
         const int place = few + __popc(m & ((1u << lane) - 1));
         few += __popc(m);
-        if (few > kCandidates) return -1;
+        if (few > kCandidates) return false;
         if (in) {
             cand_x[place] = y;
-            cand_c[place] = c0 + lane;
+            cand_c[place] = c;
         }
     }
     __syncwarp();
-    float x[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const bool on = lane + 32 * j < few;
-        x[j] = on ? cand_x[lane + 32 * j] : -INFINITY;
-        cand[j] = on ? cand_c[lane + 32 * j] : INT32_MAX;
-    }
-    __syncwarp();                                            // (the next query's candidates go to the same places)
-    if (few == want) {
-        *taken = ballot2(x[0] > -INFINITY, x[1] > -INFINITY);
-        return few;
-    }
-    // the want-th largest: more than `want` reach lo, fewer reach hi (or hi is the largest)
-    float kth;
-    lo = -warp_max(fmaxf(x[0] > -INFINITY ? -x[0] : -INFINITY, x[1] > -INFINITY ? -x[1] : -INFINITY));
-    hi = most;
-    if (__popcll(ballot2(x[0] >= hi, x[1] >= hi)) >= want) {
-        kth = hi;
-    } else {
-        for (;;) {
-            const float mid = lo + 0.5f * (hi - lo);
-            if (!(mid > lo && mid < hi)) {
-                kth = lo;
-                break;
-            }
-            const int n = __popcll(ballot2(x[0] >= mid, x[1] >= mid));
-            if (n == want) {
-                kth = -warp_max(fmaxf(x[0] >= mid ? -x[0] : -INFINITY, x[1] >= mid ? -x[1] : -INFINITY));
-                break;
-            }
-            if (n > want) lo = mid;
-            else hi = mid;
+    const float x0 = lane < few ? cand_x[lane] : -INFINITY;
+    cand[0] = lane < few ? cand_c[lane] : 0;
+    float kth, next = -INFINITY;             // the want-th largest and the largest below it
+    if (few <= 32) {                         // the least go one by one
+        float x = lane < few ? x0 : INFINITY;
+        int left = few;
+        while (left > want) {
+            next = warp_min(x);
+            const bool out = x == next;
+            left -= __popc(__ballot_sync(kFull, out));
+            if (out) x = INFINITY;
         }
+        kth = left == want ? warp_min(x) : next;             // (left < want: equals on the border)
+        if (left == want && kth - next > eps) {
+            *taken = __ballot_sync(kFull, lane < few && x0 >= kth);
+            return true;
+        }
+    } else {
+        cand[1] = lane + 32 < few ? cand_c[lane + 32] : 0;
+        const float x[2] = {x0, lane + 32 < few ? cand_x[lane + 32] : -INFINITY};
+        kth = nth_largest(x, want);
     }
-    const uint64_t sure = ballot2(x[0] > kth + eps, x[1] > kth + eps);
-    const uint64_t open = ballot2(x[0] >= kth - eps, x[1] >= kth - eps) & ~sure;
+    const float x1 = lane + 32 < few ? cand_x[lane + 32] : -INFINITY;
+    const uint64_t sure = ballot2(x0 > kth + eps, x1 > kth + eps);
+    const uint64_t open = ballot2(x0 >= kth - eps, x1 >= kth - eps) & ~sure;
     if (__popcll(sure | open) == want) {
         *taken = sure | open;
-        return few;
+        return true;
     }
     const int rest = want - __popcll(sure);
     Best fine;
@@ -193,12 +206,12 @@ __device__ __forceinline__ int narrow(const float* v, int nv, int want, float ep
     const int a = lane < rest ? fine.c[0] : 64;              // (rest is 32 at most: one place a lane)
     *taken = sure | __reduce_or_sync(kFull, a < 32 ? 1u << a : 0u) |
              (uint64_t)__reduce_or_sync(kFull, a >= 32 && a < 64 ? 1u << (a - 32) : 0u) << 32;
-    return few;
+    return true;
 }
 
 __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_constant__ Choice a) {
     extern __shared__ __align__(16) float scores[];          // [tile][stride]
-    __shared__ int32_t limit[kMostQueries];
+    __shared__ int32_t limit[kMostQueries], home[kMostQueries];
     __shared__ float mass[kMostQueries];                     // sum |q| over the group's heads
     __shared__ unsigned largest;                             // bits of max |mean|
     __shared__ float cand_x[kWarps][kCandidates];
@@ -212,7 +225,13 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
     const __nv_bfloat16* means = a.means + u * s.nb * kHeadDim;
 
     if (threadIdx.x == 0) largest = 0;
-    if (threadIdx.x < kMostQueries) limit[threadIdx.x] = threadIdx.x < queries ? row_limit(s, b, i0 + threadIdx.x) : 0;
+    if (threadIdx.x < kMostQueries) {
+        const int lim = threadIdx.x < queries ? row_limit(s, b, i0 + threadIdx.x) : 0;
+        // the query's own position: its limit is one behind it, or (not causal) the length is
+        const int64_t p = s.causal ? lim - 1 : (s.starts ? (int64_t)s.starts[b] : lim - s.n) + i0 + threadIdx.x;
+        limit[threadIdx.x] = lim;
+        home[threadIdx.x] = (int)(p / kBlockKeys);
+    }
     for (int r = warp; r < queries; r += kWarps) {
         float x = 0.f;
         for (int h = 0; h < s.G; ++h) x += abs_sum(reinterpret_cast<const uint32_t*>(q + (h * s.n + r) * kHeadDim)[lane]);
@@ -221,8 +240,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
         if (lane == 0) mass[r] = x;
     }
     __syncthreads();
-    int most = 0;
-    for (int r = 0; r < queries; ++r) most = max(most, limit[r]);
+    const int most = __reduce_max_sync(kFull, limit[lane]);
     const int seen = (most + kBlockKeys - 1) / kBlockKeys;   // blocks that some query sees
 
     __nv_bfloat162 tops = __floats2bfloat162_rn(0.f, 0.f);   // max |mean|; NaN where a mean is
@@ -236,7 +254,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
             for (int w = 0; w < 8; ++w) tops = __hmax2_nan(tops, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&k[o][w])));
         }
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < kMostQueries / 8; ++half) {
             if (8 * half >= queries) break;
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
             for (int h = 0; h < s.G; ++h) {
@@ -269,45 +287,28 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
             continue;
         }
         float* v = scores + r * a.stride;
-        // the query's own position: its limit is one behind it, or (not causal) the length is
-        const int64_t p = s.causal ? lim - 1 : (s.starts ? (int64_t)s.starts[b] : lim - s.n) + i0 + r;
-        const int home = (int)(p / kBlockKeys);
         // forced: below `sink`, and from near0 (not below sink) to near1
-        const int sink = min(a.sink, nv), near0 = max(home - a.local + 1, sink), near1 = min(home + a.local, nv);
-        const int near = max(near1 - near0, 0), forced = sink + near, want = s.top - forced;
-        for (int x = lane; x < forced; x += 32) v[x < sink ? x : near0 + x - sink] = -INFINITY;
-        for (int c = nv + lane; c < (nv + 31) / 32 * 32; c += 32) v[c] = -INFINITY;
+        const int sink = min(a.sink, nv), near0 = max(home[r] - a.local + 1, sink), near1 = min(home[r] + a.local, nv);
+        const int forced = sink + max(near1 - near0, 0);
+        for (int x = lane; x < forced; x += 32) v[x < sink ? x : near0 + x - sink] = INFINITY;
+        if (nv + lane < (nv + 31) / 32 * 32) v[nv + lane] = -INFINITY;
         __syncwarp();
         // 2 eps, and what products of denormal size may lose
         const float eps = 2.02f * 68.f * 1.1920929e-7f * (float)s.G * mass[r] * top_mean + 1e-35f;
-        uint64_t taken = 0;                                  // of the candidates: first those of lane 0 .. 31, then the others
-        int cand[2] = {0, 0}, few = -1;                      // a lane's candidates by rising index; their number, -1: not had
-        if (want == 0) {
-            few = 0;
-        } else if (want <= 32 && eps < 1e30f) {
-            few = narrow(v, nv, want, eps, lane, cand_x[warp], cand_c[warp], cand, &taken, [&](int c) {
+        uint64_t taken = 0;
+        int cand[2];
+        if (s.top <= 32 && eps < 1e30f &&
+            narrow(v, nv, s.top, eps, lane, cand_x[warp], cand_c[warp], cand, &taken, [&](int c) {
                 return exact_score(reinterpret_cast<const uint32_t*>(q + r * kHeadDim), s.n * (kHeadDim / 2), s.G,
                                    reinterpret_cast<const uint32_t*>(means + (int64_t)c * kHeadDim), lane);
-            });
-        }
-        if (few >= 0) {                                      // ranks among the chosen and the forced
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (!(taken >> (32 * j + lane) & 1)) continue;
-                const uint64_t below = taken & ((uint64_t(1) << (32 * j + lane)) - 1);
-                const int c = cand[j];
-                out[__popcll(below) + (c >= sink ? sink + min(max(c - near0, 0), near) : 0)] = c;
-            }
-            for (int x = 0; x < forced; ++x) {
-                const int c = x < sink ? x : near0 + x - sink;
-                const unsigned lo = __ballot_sync(kFull, cand[0] < c), hi = __ballot_sync(kFull, cand[1] < c);
-                if (lane == 0) out[x + __popcll(taken & (lo | (uint64_t)hi << 32))] = c;
-            }
+            })) {
+            const unsigned lo = (unsigned)taken, hi = (unsigned)(taken >> 32), below = (1u << lane) - 1;
+            if (lo >> lane & 1) out[__popc(lo & below)] = cand[0];
+            if (hi >> lane & 1) out[__popc(lo) + __popc(hi & below)] = cand[1];
+            __syncwarp();                                    // (the next query's candidates go to the same places)
             continue;
         }
         // the long way: any number of blocks and any scores
-        for (int x = lane; x < forced; x += 32) v[x < sink ? x : near0 + x - sink] = INFINITY;
-        __syncwarp();
         float lo = INFINITY, hi = -INFINITY;
         const int padded = (nv + 127) / 128 * 128;
         for (int c = lane; c < padded; c += 32) {
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
             v[c] = x;
         }
         __syncwarp();
-        lo = -warp_max(-lo);
+        lo = warp_min(lo);
         hi = warp_max(hi);
         // the top-th largest value, kth: at least top values reach lo, fewer than top reach hi
         float kth;
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
                     float least = INFINITY;
                     for (int c = lane; c < nv; c += 32)
                         if (v[c] >= mid) least = fminf(least, v[c]);
-                    kth = -warp_max(-least);
+                    kth = warp_min(least);
                     break;
                 }
                 if (n > s.top) lo = mid;
