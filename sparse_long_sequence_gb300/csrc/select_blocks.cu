@@ -18,116 +18,19 @@
 
 #include "layer_ops.h"
 #include "mma_tiles.cuh"
-#include "selected.h"
+#include "select_common.cuh"
 
 namespace dfs {
 namespace {
 
 using namespace tiles;
+using namespace select;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostQueries = 32;
 
-struct Choice {
-    SelectShape s;
-    const __nv_bfloat16 *q, *means;
-    int32_t sink, local;
-    int32_t* blocks;
-    int32_t tile;                  // queries of a block of threads: 32, or fewer for many key blocks
-    int32_t stride;                // floats of a query's scores
-};
-
-__device__ __forceinline__ float abs_sum(uint32_t w) {
-    return fabsf(__uint_as_float(w << 16)) + fabsf(__uint_as_float(w & 0xffff0000u));
-}
-
-// The score in fp64, in every lane; NaN counts as -infinity.
-__device__ __forceinline__ double exact_score(const uint32_t* q, int64_t head_words, int G, const uint32_t* mean, int lane) {
-    const uint32_t w = mean[lane];
-    const double m0 = __uint_as_float(w << 16), m1 = __uint_as_float(w & 0xffff0000u);
-    double t = 0.0;
-    for (int h = 0; h < G; ++h) {
-        const uint32_t x = q[h * head_words + lane];
-        t += (double)__uint_as_float(x << 16) * m0 + (double)__uint_as_float(x & 0xffff0000u) * m1;
-    }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) t += __shfl_xor_sync(kFull, t, off);
-    return t == t ? t : -INFINITY;
-}
-
-// The best `want` (up to 64) of the scores handed in by rising index, two places a lane.
-struct Best {
-    double t[2];
-    int c[2];
-    int have = 0;
-
-    __device__ __forceinline__ void put(int place, double x, int index, int lane) {
-        if (lane != (place & 31)) return;
-        t[place >> 5] = x;
-        c[place >> 5] = index;
-    }
-    __device__ void offer(double x, int index, int want, int lane) {
-        if (have < want) return put(have++, x, index, lane);
-        // the worst: the least score, among equals the highest index
-        double wt = INFINITY;
-        int wc = -1, wp = 0;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (lane + 32 * j < want && (wc < 0 || t[j] < wt || (t[j] == wt && c[j] > wc))) {
-                wt = t[j];
-                wc = c[j];
-                wp = lane + 32 * j;
-            }
-#pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) {
-            const double ot = __shfl_xor_sync(kFull, wt, off);
-            const int oc = __shfl_xor_sync(kFull, wc, off), op = __shfl_xor_sync(kFull, wp, off);
-            if (oc >= 0 && (wc < 0 || ot < wt || (ot == wt && oc > wc))) {
-                wt = ot;
-                wc = oc;
-                wp = op;
-            }
-        }
-        if (x > wt) put(wp, x, index, lane);
-    }
-};
-
-// Over a warp, of numbers.
-__device__ __forceinline__ float warp_max(float x) {
-    float y;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float warp_min(float x) {
-    float y;
-    asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint64_t ballot2(bool a, bool b) {
-    const unsigned lo = __ballot_sync(kFull, a), hi = __ballot_sync(kFull, b);
-    return lo | (uint64_t)hi << 32;
-}
-
 constexpr int kCandidates = 64;
-
-// The want-th largest of a warp's values, two a lane (-infinity: none), more than `want` of them: by
-// bisection on values.
-__device__ __forceinline__ float nth_largest(const float (&x)[2], int want) {
-    float lo = fminf(x[0] > -INFINITY ? x[0] : INFINITY, x[1] > -INFINITY ? x[1] : INFINITY);
-    float hi = fmaxf(x[0] < INFINITY ? x[0] : -INFINITY, x[1] < INFINITY ? x[1] : -INFINITY);
-    lo = warp_min(lo);
-    hi = warp_max(hi);
-    if (__popcll(ballot2(x[0] >= hi, x[1] >= hi)) >= want) return hi;
-    for (;;) {                               // more than `want` reach lo, fewer reach hi
-        const float mid = lo + 0.5f * (hi - lo);
-        if (!(mid > lo && mid < hi)) return lo;
-        const int n = __popcll(ballot2(x[0] >= mid, x[1] >= mid));
-        if (n == want) return warp_min(fminf(x[0] >= mid ? x[0] : INFINITY, x[1] >= mid ? x[1] : INFINITY));
-        if (n > want) lo = mid;
-        else hi = mid;
-    }
-}
 
 // The `want` (1 to 32) largest of v[0 .. nv), of which more than `want` are above -infinity and at most `want`
 // infinite (those are in), the others finite; v goes on as -infinity to a multiple of 32.  Some x that the
@@ -287,14 +190,11 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
             continue;
         }
         float* v = scores + r * a.stride;
-        // forced: below `sink`, and from near0 (not below sink) to near1
-        const int sink = min(a.sink, nv), near0 = max(home[r] - a.local + 1, sink), near1 = min(home[r] + a.local, nv);
-        const int forced = sink + max(near1 - near0, 0);
-        for (int x = lane; x < forced; x += 32) v[x < sink ? x : near0 + x - sink] = INFINITY;
+        const Forced forced(a.sink, a.local, home[r], nv);
+        for (int x = lane; x < forced.count(); x += 32) v[forced.at(x)] = INFINITY;
         if (nv + lane < (nv + 31) / 32 * 32) v[nv + lane] = -INFINITY;
         __syncwarp();
-        // 2 eps, and what products of denormal size may lose
-        const float eps = 2.02f * 68.f * 1.1920929e-7f * (float)s.G * mass[r] * top_mean + 1e-35f;
+        const float eps = twice_eps(s.G, mass[r], top_mean);
         uint64_t taken = 0;
         int cand[2];
         if (s.top <= 32 && eps < 1e30f &&
@@ -313,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
         const int padded = (nv + 127) / 128 * 128;
         for (int c = lane; c < padded; c += 32) {
             float x = c < nv ? v[c] : -INFINITY;
-            if (c < nv && !((unsigned)c < (unsigned)sink || (c >= near0 && c < near1))) {
+            if (c < nv && !forced.has(c)) {
                 x = fminf(fmaxf(x, -FLT_MAX), FLT_MAX);      // (NaN: the lowest)
                 lo = fminf(lo, x);
                 hi = fmaxf(hi, x);
@@ -410,6 +310,8 @@ int launch_select_blocks(const SelectShape& s, const void* Q, const void* means,
     Choice a{s, static_cast<const __nv_bfloat16*>(Q), static_cast<const __nv_bfloat16*>(means), sink, local, blocks, kMostQueries, 0};
     // whole loads of a warp, and 4 more floats: the lanes of a product's column fall in other banks
     a.stride = (s.nb + 127) / 128 * 128 + 4;
+    // Tiles of 128 queries, a thread each: 16 x 16384 queries of 256 blocks take 194 us here.
+    if (s.top <= kTilesTop && s.n >= 64 && s.B * s.Hk * s.n >= 8192) return launch_select_tiles(a, stream);
     while ((int64_t)a.tile * a.stride * 4 > kMostSmem) a.tile /= 2;
     const int64_t grid = s.B * s.Hk * ((s.n + a.tile - 1) / a.tile);
     if (grid > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");

@@ -1,0 +1,140 @@
+// What the two kernels of the choice of blocks share (select_blocks.cu, select_tiles.cu): a query's exact
+// scores, the best of them, and reductions over a warp.
+#pragma once
+
+#include "mma_tiles.cuh"
+#include "selected.h"
+
+namespace dfs {
+
+struct Choice {
+    SelectShape s;
+    const __nv_bfloat16 *q, *means;
+    int32_t sink, local;
+    int32_t* blocks;
+    int32_t tile;                  // queries of a block of threads: 32, or fewer for many key blocks
+    int32_t stride;                // floats of a query's scores
+};
+// many queries, top up to kTilesTop (select_tiles.cu)
+constexpr int kTilesTop = 20;
+int launch_select_tiles(const Choice& a, cudaStream_t stream);
+
+#ifdef __CUDACC__
+namespace select {
+
+using tiles::kFull;
+
+// Twice what a score in fp32 is off by at most, for `mass` = sum |q| over G heads (select_blocks.cu), and what
+// products of denormal size may lose.
+__device__ __forceinline__ float twice_eps(int G, float mass, float top_mean) {
+    return 2.02f * 68.f * 1.1920929e-7f * (float)G * mass * top_mean + 1e-35f;
+}
+
+__device__ __forceinline__ float abs_sum(uint32_t w) {
+    return fabsf(__uint_as_float(w << 16)) + fabsf(__uint_as_float(w & 0xffff0000u));
+}
+
+// The score in fp64, in every lane; NaN counts as -infinity.
+__device__ __forceinline__ double exact_score(const uint32_t* q, int64_t head_words, int G, const uint32_t* mean, int lane) {
+    const uint32_t w = mean[lane];
+    const double m0 = __uint_as_float(w << 16), m1 = __uint_as_float(w & 0xffff0000u);
+    double t = 0.0;
+    for (int h = 0; h < G; ++h) {
+        const uint32_t x = q[h * head_words + lane];
+        t += (double)__uint_as_float(x << 16) * m0 + (double)__uint_as_float(x & 0xffff0000u) * m1;
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) t += __shfl_xor_sync(kFull, t, off);
+    return t == t ? t : -INFINITY;
+}
+
+// The best `want` (up to 64) of the scores handed in by rising index, two places a lane.
+struct Best {
+    double t[2];
+    int c[2];
+    int have = 0;
+
+    __device__ __forceinline__ void put(int place, double x, int index, int lane) {
+        if (lane != (place & 31)) return;
+        t[place >> 5] = x;
+        c[place >> 5] = index;
+    }
+    __device__ void offer(double x, int index, int want, int lane) {
+        if (have < want) return put(have++, x, index, lane);
+        // the worst: the least score, among equals the highest index
+        double wt = INFINITY;
+        int wc = -1, wp = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (lane + 32 * j < want && (wc < 0 || t[j] < wt || (t[j] == wt && c[j] > wc))) {
+                wt = t[j];
+                wc = c[j];
+                wp = lane + 32 * j;
+            }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) {
+            const double ot = __shfl_xor_sync(kFull, wt, off);
+            const int oc = __shfl_xor_sync(kFull, wc, off), op = __shfl_xor_sync(kFull, wp, off);
+            if (oc >= 0 && (wc < 0 || ot < wt || (ot == wt && oc > wc))) {
+                wt = ot;
+                wc = oc;
+                wp = op;
+            }
+        }
+        if (x > wt) put(wp, x, index, lane);
+    }
+};
+
+// Over a warp, of numbers.
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float warp_min(float x) {
+    float y;
+    asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t ballot2(bool a, bool b) {
+    const unsigned lo = __ballot_sync(kFull, a), hi = __ballot_sync(kFull, b);
+    return lo | (uint64_t)hi << 32;
+}
+
+// The want-th largest of a warp's values, two a lane (-infinity: none), more than `want` of them: by
+// bisection on values.
+__device__ __forceinline__ float nth_largest(const float (&x)[2], int want) {
+    float lo = fminf(x[0] > -INFINITY ? x[0] : INFINITY, x[1] > -INFINITY ? x[1] : INFINITY);
+    float hi = fmaxf(x[0] < INFINITY ? x[0] : -INFINITY, x[1] < INFINITY ? x[1] : -INFINITY);
+    lo = warp_min(lo);
+    hi = warp_max(hi);
+    if (__popcll(ballot2(x[0] >= hi, x[1] >= hi)) >= want) return hi;
+    for (;;) {                               // more than `want` reach lo, fewer reach hi
+        const float mid = lo + 0.5f * (hi - lo);
+        if (!(mid > lo && mid < hi)) return lo;
+        const int n = __popcll(ballot2(x[0] >= mid, x[1] >= mid));
+        if (n == want) return warp_min(fminf(x[0] >= mid ? x[0] : INFINITY, x[1] >= mid ? x[1] : INFINITY));
+        if (n > want) lo = mid;
+        else hi = mid;
+    }
+}
+
+// A query's forced blocks among its first nv: those below `sink`, and near0 .. near1 - 1 (none below sink).
+struct Forced {
+    int sink, near0, near;         // near = near1 - near0
+    __device__ __forceinline__ Forced(int sinks, int local, int home, int nv) {
+        sink = min(sinks, nv);
+        near0 = max(home - local + 1, sink);
+        near = max(min(home + local, nv) - near0, 0);
+    }
+    __device__ __forceinline__ int count() const { return sink + near; }
+    __device__ __forceinline__ int at(int x) const { return x < sink ? x : near0 + x - sink; }
+    __device__ __forceinline__ bool has(int c) const { return c < sink || (unsigned)(c - near0) < (unsigned)near; }
+    // of them below c
+    __device__ __forceinline__ int below(int c) const { return c < sink ? c : sink + min(max(c - near0, 0), near); }
+};
+
+}  // namespace select
+#endif
+
+}  // namespace dfs

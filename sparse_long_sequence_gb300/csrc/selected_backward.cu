@@ -38,12 +38,12 @@ struct Partials {
     float* dq;                               // [units][tiles] of [128][64] (row_tiles.cuh)
     float* dkv;                              // [runs][dv, dk][64 features][64 keys], run (u - u0) runs + share + filled[block]
     int32_t runs;                            // of a unit
-    const float2* stat;                      // [B][Hq][n]: lse in units of log 2, delta
+    const float2* stat;                      // [B][Hq][n]: lse in units of log 2, delta / 8
     int64_t u0;
     bool first;                              // the group after the lists (the others: after the joining kernel)
 };
 
-// stat = (lse in units of log 2, delta): eight lanes a row.
+// stat = (lse in units of log 2, delta / 8): eight lanes a row.
 __global__ void __launch_bounds__(256) selected_delta_kernel(const __grid_constant__ SelectedArgs a, int64_t rows, float2* stat) {
     ptx::griddep_launch_dependents();
     const int64_t row = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(256) selected_delta_kernel(const __grid_consta
     d += __shfl_xor_sync(kFull, d, 1);
     d += __shfl_xor_sync(kFull, d, 2);
     d += __shfl_xor_sync(kFull, d, 4);
-    if (row < rows && lane == 0) stat[row] = make_float2(a.lse[row] * kLog2e, d);
+    if (row < rows && lane == 0) stat[row] = make_float2(a.lse[row] * kLog2e, d * kScale);
 }
 
 __global__ void __launch_bounds__(kThreads, kResident)
@@ -140,9 +140,8 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     for (int32_t x = first; x < last; ++x, phase ^= 1) {
         const uint32_t stage = stages + phase * kStage;
         ptx::cp_async_wait_all();
-        if (lane == 0) ptx::bulk_wait_read<0>();
         ptx::fence_proxy_async_smem();
-        __syncthreads();                     // the tile is there, and the last dq has left
+        __syncthreads();                     // the tile is there, and all have read the last dq
         if (warp == 0 && ptx::elect_one()) {
             ptx::tc_fence_after();
             const uint64_t dd = ptx::sw128_kmajor_desc(stage), qd = ptx::sw128_kmajor_desc(stage + kTileBytes);
@@ -174,26 +173,28 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::tmem_ld32_issue(col + 64, dp);
         ptx::tmem_ld_wait32(sc);
         ptx::tmem_ld_wait32(dp);
+        // sc and dp become P and dS, two bf16 a register, in their first halves
+        const bool whole = __all_sync(kFull, limit >= 32);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+            float w[2], g[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                w[e] = exp2_fast(fmaf(__uint_as_float(sc[k + e]), kScale * kLog2e, -stat.x));
+                g[e] = w[e] * (__uint_as_float(dp[k + e]) * kScale - stat.y);
+                if (!whole && k + e >= limit) w[e] = g[e] = 0.f;
+            }
+            sc[k / 2] = pack(w[0], w[1]);
+            dp[k / 2] = pack(g[0], g[1]);
+        }
+        if (lane == 0) ptx::bulk_wait_read<0>();             // the last dq has left by the place of P and dS
+        __syncthreads();
         char* to = smem + (weights - keys);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            uint32_t p[4], d[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float w[2], g[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int k = 8 * c + 2 * j + e;
-                    const bool on = k < limit;
-                    w[e] = on ? exp2_fast(fmaf(__uint_as_float(sc[k]), kScale * kLog2e, -stat.x)) : 0.f;
-                    g[e] = on ? w[e] * (__uint_as_float(dp[k]) - stat.y) * kScale : 0.f;
-                }
-                p[j] = pack(w[0], w[1]);
-                d[j] = pack(g[0], g[1]);
-            }
             const uint32_t at = place(mine, 4 * half + c);
-            *reinterpret_cast<uint4*>(to + at) = make_uint4(p[0], p[1], p[2], p[3]);
-            *reinterpret_cast<uint4*>(to + kTileBytes + at) = make_uint4(d[0], d[1], d[2], d[3]);
+            *reinterpret_cast<uint4*>(to + at) = make_uint4(sc[4 * c], sc[4 * c + 1], sc[4 * c + 2], sc[4 * c + 3]);
+            *reinterpret_cast<uint4*>(to + kTileBytes + at) = make_uint4(dp[4 * c], dp[4 * c + 1], dp[4 * c + 2], dp[4 * c + 3]);
         }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();

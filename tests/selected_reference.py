@@ -49,22 +49,26 @@ def means(K, lengths, old, recent=0):
 
 def select(Q, mean, top, m, sink, local, causal, lengths, starts):
     B, Hq, n, _ = Q.shape
-    Hk = mean.shape[1]
-    G = Hq // Hk
+    Hk, nb = mean.shape[1:3]
     out = torch.full((B, Hk, n, top), -1, dtype=torch.int32)
+    c = torch.arange(nb)
     for b, length, start in _sequences(B, n, m, lengths, starts):
         first = length - n if start is None else start
-        lim = limits(n, m, causal, length, start)
+        count = -(-torch.tensor(limits(n, m, causal, length, start)) // BLOCK)     # blocks that each query sees
+        home = torch.div(first + torch.arange(n), BLOCK, rounding_mode="floor")[:, None]
+        forced = (c < sink) | ((c - home).abs() < local)
+        most = max(1, int(count.max())) if n else 1
         for h in range(Hk):
-            q = Q[b, h * G:(h + 1) * G].double()
-            for i in range(n):
-                nv = -(-lim[i] // BLOCK)
-                score = (q[:, i] @ mean[b, h, :nv].double().T).sum(0).tolist()
-                score = [-math.inf if x != x else x for x in score]
-                home = (first + i) // BLOCK
-                rank = sorted(range(nv), key=lambda c: (not (c < sink or abs(c - home) < local), -score[c], c))
-                picked = sorted(rank[:top])
-                out[b, h, i, :len(picked)] = torch.tensor(picked, dtype=torch.int32)
+            score = torch.zeros((n, nb), dtype=torch.float64)
+            used = mean[b, h, :most].double().repeat(1, Hq // Hk)      # (others are not read)
+            score[:, :most] = Q[b, h * (Hq // Hk):(h + 1) * (Hq // Hk)].double().transpose(0, 1).flatten(1) @ used.T
+            score = torch.where(score != score, -math.inf, score)
+            rank = torch.sort(score, dim=1, descending=True, stable=True).indices      # equals by rising index
+            group = torch.where(c[None] >= count[:, None], 2, torch.where(forced, 0, 1))
+            rank = rank.gather(1, torch.sort(group.gather(1, rank), dim=1, stable=True).indices)[:, :top]
+            taken = torch.where(torch.arange(rank.shape[1])[None] < count[:, None], rank, nb)
+            taken = torch.sort(taken, dim=1).values
+            out[b, h, :, :taken.shape[1]] = torch.where(taken < nb, taken, -1).to(torch.int32)
     return out
 
 
