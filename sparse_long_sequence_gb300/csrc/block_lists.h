@@ -31,7 +31,9 @@ struct BlockLists {
 // Sizes, and the addresses in `ws` (null: sizes alone); returns the bytes.  `shares` is the caller's.
 size_t plan_block_lists(const SelectShape& s, char* ws, BlockLists* l);
 // Shares of a unit where `here` units have `resident` blocks of threads on each of 152 SMs: `rounds` times as
-// many as run at once, and a tile at least for each.  (One round where the units have alike lengths.)
+// many as run at once, and a tile at least for each.  One round where the units have alike lengths; three
+// where they do not, and where a block of threads has 64 tiles or more, of which some take longer (16 x 16384
+// queries: 513 us for 535, the backward 819 for 835; 24 x 4096 queries, 15 tiles each: 134 for 128).
 constexpr int kUnlikeRounds = 3;
 inline int32_t tile_shares(const SelectShape& s, const BlockLists& l, int64_t here, int resident, int rounds) {
     const int64_t at_once = 152 * resident / here, tiles = l.most_tiles;

@@ -1,8 +1,8 @@
 // The choice of key blocks (select_blocks.cu says what is chosen and why the result is that of exact scores)
 // for many queries: a thread a query.
 //
-// A block of four warps takes 128 queries of a unit.  Their scores against 256 block means at a time are one
-// tcgen05 product (128 x 256, the group's heads one after the other along the summed index), and a query's scores
+// A block of four warps takes 128 queries of a unit.  Their scores against 128 block means at a time are one
+// tcgen05 product (128 x 128, the group's heads one after the other along the summed index), and a query's scores
 // lie in its thread's lane of tensor memory.  The thread reads them twice: first for the maxima of 32 groups of
 // columns, whose want-th largest bounds the want-th largest score from below; then for the scores above that
 // bound, a few more than `want`, which it lists in shared memory.  Among those it finds the want-th largest.  Both
@@ -27,7 +27,7 @@ using namespace tiles;
 using namespace select;
 
 constexpr int kThreads = kTileRows;
-constexpr int kRound = 256;                  // block means of a product
+constexpr int kRound = 128;                  // block means of a product
 constexpr int kMaxima = 32;
 constexpr int kList = 32;                    // a query's candidates
 static_assert(kList > kTilesTop + 1, "a full list holds more than are wanted");
@@ -71,7 +71,7 @@ __device__ __forceinline__ float pick(const float (&x)[32], int i) {
     return y;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) select_tiles_kernel(const __grid_constant__ Choice a, int* status) {
+__global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_constant__ Choice a, int* status) {
     extern __shared__ __align__(1024) char smem[];
     __shared__ uint64_t bar;
     __shared__ uint32_t tmem_slot;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_tiles_kernel(const __grid_
             }
             if (first && h == 0) {
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < kRound / 16; ++c) {
                     const uint4 w = *reinterpret_cast<const uint4*>(smem + kTileBytes + place(tid + (c >> 3) * kThreads, c & 7));
                     const uint32_t y[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll

@@ -335,7 +335,7 @@ Plan plan_backward(const SelectShape& s, char* ws) {
     p.group = groups < 1 ? units : groups < units ? (units + groups - 1) / groups : 1;
     // each run begins with a share or a block (room for any lengths, which a size query does not know)
     p.runs = tile_shares(s, p.lists, p.group, kResident, kUnlikeRounds) + p.lists.most_filled;
-    p.lists.shares = tile_shares(s, p.lists, p.group, kResident, s.lengths ? kUnlikeRounds : 1);
+    p.lists.shares = tile_shares(s, p.lists, p.group, kResident, s.lengths || p.lists.most_tiles * p.group >= 64 * 152 * kResident ? kUnlikeRounds : 1);
     p.dkv = p.dq + p.group * dq;
     p.total = p.dkv + (size_t)p.group * p.runs * 2 * kBlockKeys * kHeadDim * 4;
     return p;
