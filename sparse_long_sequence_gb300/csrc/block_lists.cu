@@ -1,7 +1,7 @@
 // For each key block the list of the queries that name it, in rising order (so that what is summed
 // over a list is summed in a fixed order), and where each block's tiles of rows begin.
 //
-// Three launches.  (1) A block of threads sets, for a chunk of 32 to 256 queries, one bit a query in
+// Sums launches.  (1) A block of threads sets, for a chunk of 32 to 256 queries, one bit a query in
 // a bitmap of each key block in shared memory (atomic ors, whose order does not matter) and counts
 // the bits.  (2) One block of threads a unit turns the counts into places: a running sum over the
 // chunks for each key block, then over the key blocks.  (3) The bitmaps again:
@@ -107,26 +107,23 @@ count_lists_kernel(const __grid_constant__ SelectShape s, const int32_t* blocks,
     }
 }
 
-struct Three {
-    int32_t entries, tiles, filled;
+struct Sums {
+    int32_t entries, tiles;
 };
-__device__ __forceinline__ Three operator+(Three a, Three b) {
-    return {a.entries + b.entries, a.tiles + b.tiles, a.filled + b.filled};
-}
+__device__ __forceinline__ Sums operator+(Sums a, Sums b) { return {a.entries + b.entries, a.tiles + b.tiles}; }
 
 // Sums over the first kScanBlocks threads: of those before this one, and (in *all) of all.
-__device__ __forceinline__ Three before_and_all(Three x, Three* sums, Three* all) {
+__device__ __forceinline__ Sums before_and_all(Sums x, Sums* sums, Sums* all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Three run = x;
+    Sums run = x;
 #pragma unroll
     for (int off = 1; off < 32; off *= 2) {
-        const Three o = {__shfl_up_sync(kFull, run.entries, off), __shfl_up_sync(kFull, run.tiles, off),
-                         __shfl_up_sync(kFull, run.filled, off)};
+        const Sums o = {__shfl_up_sync(kFull, run.entries, off), __shfl_up_sync(kFull, run.tiles, off)};
         if (lane >= off) run = run + o;
     }
     if (lane == 31) sums[warp] = run;
     __syncthreads();
-    Three before = {run.entries - x.entries, run.tiles - x.tiles, run.filled - x.filled}, total = {0, 0, 0};
+    Sums before = {run.entries - x.entries, run.tiles - x.tiles}, total = {0, 0};
     for (int w = 0; w < kScanBlocks / 32; ++w) {
         if (w == warp) before = before + total;
         total = total + sums[w];
@@ -139,7 +136,7 @@ __device__ __forceinline__ Three before_and_all(Three x, Three* sums, Three* all
 __global__ void __launch_bounds__(kScanThreads)
 place_lists_kernel(const __grid_constant__ SelectShape s, const __grid_constant__ BlockLists l) {
     constexpr int kRuns = kScanThreads / kScanBlocks;
-    __shared__ Three sums[kScanThreads / 32];
+    __shared__ Sums sums[kScanThreads / 32];
     __shared__ int32_t runs[kRuns][kScanBlocks];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -148,7 +145,7 @@ place_lists_kernel(const __grid_constant__ SelectShape s, const __grid_constant_
     int32_t *base = l.base + u * (s.nb + 1), *tile_base = l.tile_base + u * (s.nb + 1);
     const int run = threadIdx.x / kScanBlocks, per = (l.chunks + kRuns - 1) / kRuns;
     const int k0 = min(run * per, l.chunks), k1 = min(k0 + per, l.chunks);
-    Three done = {0, 0, 0};
+    Sums done = {0, 0};
     for (int c0 = 0; c0 < s.nb; c0 += kScanBlocks) {
         const int c = c0 + threadIdx.x % kScanBlocks;
         int n = 0;
@@ -175,12 +172,11 @@ place_lists_kernel(const __grid_constant__ SelectShape s, const __grid_constant_
         }
         if (run || c >= s.nb) n = 0;         // (the first run's threads sum over the blocks)
         const int tiles = (int)(((int64_t)n * s.G + kTileRows - 1) / kTileRows);
-        Three all;
-        const Three before = done + before_and_all({n, tiles, n > 0}, sums, &all);
+        Sums all;
+        const Sums before = done + before_and_all({n, tiles}, sums, &all);
         if (run == 0 && c < s.nb) {
             base[c] = before.entries;
             tile_base[c] = before.tiles;
-            l.filled[u * s.nb + c] = before.filled;
         }
         done = done + all;
     }
@@ -245,7 +241,6 @@ size_t plan_block_lists(const SelectShape& s, char* ws, BlockLists* l) {
     l->entries = reinterpret_cast<uint32_t*>(take(units * named * 4));
     l->base = reinterpret_cast<int32_t*>(take(units * (s.nb + 1) * 4));
     l->tile_base = reinterpret_cast<int32_t*>(take(units * (s.nb + 1) * 4));
-    l->filled = reinterpret_cast<int32_t*>(take(units * s.nb * 4));
     l->live = reinterpret_cast<int32_t*>(take(units * s.n * 4));
     l->positions = reinterpret_cast<uint32_t*>(take(units * named * 4));
     l->counts = reinterpret_cast<int32_t*>(take(units * l->chunks * s.nb * 4));

@@ -16,7 +16,6 @@ struct BlockLists {
     uint32_t* entries;             // [units][n ranks]
     int32_t* base;                 // [units][nb + 1]: where a block's entries begin
     int32_t* tile_base;            // [units][nb + 1]: where its tiles do
-    int32_t* filled;               // [units][nb]: blocks before it that have entries
     int32_t* live;                 // [units][n]: blocks of a query that count
     uint32_t* positions;           // [units][n][ranks]: for each of them, where head 0's row is: tile 128 + row of it
     int32_t* counts;               // [units][chunks][nb], while they are built

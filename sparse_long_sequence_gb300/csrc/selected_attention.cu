@@ -189,7 +189,7 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         return;
     }
     const int32_t first = share_begin(tiles, share, shares), last = share_begin(tiles, share + 1, shares);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);      // (one value a warp)
     const uint32_t keys = ptx::smem_u32(smem), values = keys + kKeyBytes, queries = values + 2 * kKeyBytes;
     char* sums = smem + 3 * kKeyBytes + kTileBytes + 32 * warp * kSumsPitch; // this warp's rows on their way out
     const __nv_bfloat16* q0 = a.q + u * s.G * s.n * kHeadDim;
@@ -238,12 +238,12 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::cp_async_wait_all();
         ptx::fence_proxy_async_smem();
         __syncthreads();                     // the tile is there, and all have read the last O
-        if (warp == 0 && ptx::elect_one()) {
+        if (warp == 0) {
             ptx::tc_fence_after();
             const uint64_t qd = ptx::sw128_kmajor_desc(queries), kd = ptx::sw128_kmajor_desc(keys);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ptx::mma_bf16_ss(tmem, qd + 2 * e, kd + 2 * e, kScores, e > 0);
-            ptx::mma_commit(&bars[0]);
+            for (int e = 0; e < 4; ++e) if (ptx::elect_one()) ptx::mma_bf16_ss(tmem, qd + 2 * e, kd + 2 * e, kScores, e > 0);
+            if (ptx::elect_one()) ptx::mma_commit(&bars[0]);
         }
         __syncwarp();
         now = next;
@@ -298,12 +298,12 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::tmem_st16x2(mine, p[0], mine + 16, p[1]);
         ptx::tc_fence_before();
         __syncthreads();                     // P is whole
-        if (warp == 0 && ptx::elect_one()) {
+        if (warp == 0) {
             ptx::tc_fence_after();
             const uint64_t vd = ptx::sw128_mnmajor_desc(values_now, kKeyBytes);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ptx::mma_bf16_ts(tmem + 64, tmem + 8 * e, vd + 128 * e, kSums, e > 0);
-            ptx::mma_commit(&bars[1]);
+            for (int e = 0; e < 4; ++e) if (ptx::elect_one()) ptx::mma_bf16_ts(tmem + 64, tmem + 8 * e, vd + 128 * e, kSums, e > 0);
+            if (ptx::elect_one()) ptx::mma_commit(&bars[1]);
         }
         __syncwarp();
         if (x == first) {

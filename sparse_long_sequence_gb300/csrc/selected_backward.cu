@@ -9,8 +9,9 @@
 //   [dout | Q]^T [P | dS] = [dv^T, .; ., dk^T],
 // adds up dv and dk in tensor memory over a block's rows (its other two quarters are not used: 64-row
 // accumulators would save half of a product that is a tenth of the time).  A (row, block) leaves 64 fp32
-// sums of dq in the order of the tiles, a run of one block's tiles its sums of dk and dv, and a second kernel joins them in a fixed
-// order.
+// sums of dq in the order of the tiles, which a second kernel joins in a fixed order.  dk and dv of a block
+// whose tiles one block of threads has are written at once; a run of tiles that holds a part of a block leaves
+// its sums to the second kernel.
 #include <atomic>
 
 #include "block_lists.h"
@@ -36,8 +37,8 @@ constexpr size_t kGroupBytes = size_t(1536) << 20;       // partials of a group 
 
 struct Partials {
     float* dq;                               // [units][tiles] of [128][64] (row_tiles.cuh)
-    float* dkv;                              // [runs][dv, dk][64 features][64 keys], run (u - u0) runs + share + filled[block]
-    int32_t runs;                            // of a unit
+    float* dkv;                              // [units][shares][2][dv, dk][64 features][64 keys]: the share's part of a
+                                             // block that begins before it, and of one that goes on after it
     const float2* stat;                      // [B][Hq][n]: lse in units of log 2, delta / 8
     int64_t u0;
     bool first;                              // the group after the lists (the others: after the joining kernel)
@@ -85,7 +86,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         return;
     }
     const int32_t first = share_begin(tiles, share, shares), last = share_begin(tiles, share + 1, shares);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);      // (one value a warp)
     const int quarter = warp & 3, half = warp >> 2;          // rows 32 quarter .. and columns 32 half .. of a tile
     const uint32_t keys = ptx::smem_u32(smem), values = keys + kKeyBytes, stages = values + kKeyBytes;
     const uint32_t weights = stages + 2 * kStage;            // P, then dS
@@ -106,6 +107,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     walk.find(l, s, u, first);
     uint32_t head, entry;
     int32_t row = (first - walk.begin) * kTileRows + mine, block = walk.block, block_next;
+    int32_t begin = walk.begin, end = walk.end, begin_next, end_next;        // their tiles
     entry = entry_of(walk, entries, s.G, row, &head);
     copy_block(block);
     int32_t count, count_next = walk.rows - (row - lane);    // rows from this warp's first on
@@ -142,22 +144,24 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::cp_async_wait_all();
         ptx::fence_proxy_async_smem();
         __syncthreads();                     // the tile is there, and all have read the last dq
-        if (warp == 0 && ptx::elect_one()) {
+        if (warp == 0) {
             ptx::tc_fence_after();
             const uint64_t dd = ptx::sw128_kmajor_desc(stage), qd = ptx::sw128_kmajor_desc(stage + kTileBytes);
             const uint64_t kd = ptx::sw128_kmajor_desc(keys), vd = ptx::sw128_kmajor_desc(values);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                ptx::mma_bf16_ss(tmem, qd + 2 * e, kd + 2 * e, kScores, e > 0);
-                ptx::mma_bf16_ss(tmem + 64, dd + 2 * e, vd + 2 * e, kScores, e > 0);
+                if (ptx::elect_one()) ptx::mma_bf16_ss(tmem, qd + 2 * e, kd + 2 * e, kScores, e > 0);
+                if (ptx::elect_one()) ptx::mma_bf16_ss(tmem + 64, dd + 2 * e, vd + 2 * e, kScores, e > 0);
             }
-            ptx::mma_commit(&bars[0]);
+            if (ptx::elect_one()) ptx::mma_commit(&bars[0]);
         }
         __syncwarp();
         const int limit = next.limit - 32 * half;
         count = count_next;
         stat = stat_next;
         block_next = walk.block;
+        begin_next = walk.begin;
+        end_next = walk.end;
         if (x + 1 < last) {                  // (the other stage is free: dv and dk have taken it)
             next = row_from(s, b, block_next * kBlockKeys, entry, head, row < walk.rows);
             count_next = walk.rows - (row - lane);
@@ -199,16 +203,16 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncthreads();                     // P and dS are whole
-        if (warp == 0 && ptx::elect_one()) {
+        if (warp == 0) {
             ptx::tc_fence_after();
             const uint64_t sd = ptx::sw128_kmajor_desc(weights + kTileBytes), kd = ptx::sw128_mnmajor_desc(keys, kKeyBytes);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ptx::mma_bf16_ss(tmem, sd + 2 * e, kd + 128 * e, kQueryGrad, e > 0);
-            ptx::mma_commit(&bars[1]);
+            for (int e = 0; e < 4; ++e) if (ptx::elect_one()) ptx::mma_bf16_ss(tmem, sd + 2 * e, kd + 128 * e, kQueryGrad, e > 0);
+            if (ptx::elect_one()) ptx::mma_commit(&bars[1]);
             const uint64_t ad = ptx::sw128_mnmajor_desc(stage, kTileBytes), bd = ptx::sw128_mnmajor_desc(weights, kTileBytes);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ptx::mma_bf16_ss(tmem + 128, ad + 128 * e, bd + 128 * e, kKeyGrad, !fresh || e > 0);
-            ptx::mma_commit(&bars[2]);
+            for (int e = 0; e < 8; ++e) if (ptx::elect_one()) ptx::mma_bf16_ss(tmem + 128, ad + 128 * e, bd + 128 * e, kKeyGrad, !fresh || e > 0);
+            if (ptx::elect_one()) ptx::mma_commit(&bars[2]);
         }
         __syncwarp();
         if (x == first) {
@@ -237,11 +241,27 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
             // lanes 0 .. 63: feature of dout, dv^T in the first 64 columns; 64 .. 127: feature of q, dk^T in the others
             ptx::tmem_ld32_issue(col + 128 + (quarter >> 1) * 64, sc);
             ptx::tmem_ld_wait32(sc);
-            const int64_t run = (int64_t)ul * out.runs + share + l.filled[u * s.nb + block];
-            float* dst = out.dkv + (run * 2 * kHeadDim + mine) * kBlockKeys + 32 * half;
+            const int which = quarter >> 1, feature = mine & 63;
+            if (begin >= first && end <= last) {             // all of the block: turned by the place of its last tile
+                __nv_bfloat16* turned = reinterpret_cast<__nv_bfloat16*>(smem + (stage - keys) + which * kKeyBytes);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) store32(dst + 8 * j, sc + 8 * j);
+                for (int k = 0; k < 32; ++k) turned[(32 * half + k) * kHeadDim + feature] = __float2bfloat16_rn(__uint_as_float(sc[k]));
+                ptx::named_barrier_sync(5 + which, 128);
+                const int rows = (int)min((int64_t)kBlockKeys, s.m - (int64_t)block * kBlockKeys);
+                uint4* dst = reinterpret_cast<uint4*>((which ? a.dk : a.dv) + (u * s.m + (int64_t)block * kBlockKeys) * kHeadDim);
+                const int x0 = 64 * (quarter & 1) + 32 * half + lane;        // of the four warps' threads
+#pragma unroll
+                for (int x = x0; x < kBlockKeys * 8; x += 128)
+                    if (x < rows * 8) dst[x] = reinterpret_cast<const uint4*>(turned)[x];
+            } else {
+                const int64_t run = ((int64_t)blockIdx.x * 2 + (begin < first ? 0 : 1)) * 2 * kHeadDim;
+                float* dst = out.dkv + (run + mine) * kBlockKeys + 32 * half;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) store32(dst + 8 * j, sc + 8 * j);
+            }
             block = block_next;
+            begin = begin_next;
+            end = end_next;
         }
         ptx::tc_fence_before();
     }
@@ -289,13 +309,16 @@ __device__ __forceinline__ void join_dkv(const SelectedArgs& a, const BlockLists
     if (begin < end) {
         from = share_of_tile(tiles, begin, min(l.shares, tiles));
         to = share_of_tile(tiles, end - 1, min(l.shares, tiles)) + 1;
+        if (to == from + 1) return;          // (written already)
     }
-    const int64_t run = (int64_t)ul * in.runs + l.filled[u * s.nb + c] + from;
-    const float* src = in.dkv + ((run * 2 + which) * kHeadDim + feature) * kBlockKeys + 16 * part + 4 * four;
+    // the first share's part goes on after it, the others' begin before them
+    const int64_t unit = (int64_t)ul * l.shares * 2;
+    const float* src = in.dkv + ((unit * 2 + which) * kHeadDim + feature) * kBlockKeys + 16 * part + 4 * four;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int x = 0; x < to - from; ++x) {
-        const float4 p = *reinterpret_cast<const float4*>(src + (int64_t)x * 2 * kHeadDim * kBlockKeys);
+        const int64_t run = 2 * (from + x) + (x == 0);
+        const float4 p = *reinterpret_cast<const float4*>(src + run * 2 * kHeadDim * kBlockKeys);
         y = make_float4(y.x + p.x, y.y + p.y, y.z + p.z, y.w + p.w);
     }
     sums[4 * four][feature] = y.x;
@@ -323,7 +346,6 @@ selected_join_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_
 struct Plan {
     BlockLists lists;
     int64_t group;                           // units whose partials are held at once
-    int32_t runs;
     size_t stat, dq, dkv, total;
 };
 Plan plan_backward(const SelectShape& s, char* ws) {
@@ -333,11 +355,11 @@ Plan plan_backward(const SelectShape& s, char* ws) {
     const int64_t units = s.B * s.Hk, dq = p.lists.most_tiles * kSumsBytes;
     const int64_t groups = (units * dq + (int64_t)kGroupBytes - 1) / (int64_t)kGroupBytes;
     p.group = groups < 1 ? units : groups < units ? (units + groups - 1) / groups : 1;
-    // each run begins with a share or a block (room for any lengths, which a size query does not know)
-    p.runs = tile_shares(s, p.lists, p.group, kResident, kUnlikeRounds) + p.lists.most_filled;
+    // (room for any lengths, which a size query does not know)
+    const int64_t most = tile_shares(s, p.lists, p.group, kResident, kUnlikeRounds);
     p.lists.shares = tile_shares(s, p.lists, p.group, kResident, s.lengths || p.lists.most_tiles * p.group >= 64 * 152 * kResident ? kUnlikeRounds : 1);
     p.dkv = p.dq + p.group * dq;
-    p.total = p.dkv + (size_t)p.group * p.runs * 2 * kBlockKeys * kHeadDim * 4;
+    p.total = p.dkv + p.group * most * 2 * 2 * kBlockKeys * kHeadDim * 4;
     return p;
 }
 
@@ -369,7 +391,7 @@ int launch_selected_backward(const SelectedArgs& a, char* ws, cudaStream_t strea
     if ((st = launch_block_lists(s, a.blocks, p.lists, true, stream))) return st;
     for (int64_t u0 = 0; u0 < units && err == cudaSuccess; u0 += p.group) {
         const int64_t here = units - u0 < p.group ? units - u0 : p.group, rows = here * s.n * s.G;
-        const Partials part{reinterpret_cast<float*>(ws + p.dq), reinterpret_cast<float*>(ws + p.dkv), p.runs,
+        const Partials part{reinterpret_cast<float*>(ws + p.dq), reinterpret_cast<float*>(ws + p.dkv),
                             reinterpret_cast<const float2*>(ws + p.stat), u0, u0 == 0};
         {
             LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
