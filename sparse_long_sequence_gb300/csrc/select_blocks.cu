@@ -9,9 +9,10 @@
 // top-th largest value by bisection on values.
 // The products are exact in fp32, their sums are not: a tensor core adds 16 products and the sum so
 // far with an error of at most 17 2^-23 of the largest of them, so a score is off by at most
-//   eps = 4 G 17 2^-23 sum_f |q_f| max |mean|.
+//   eps = 4 G 17 2^-23 |Q| |K|,
+// |Q| the norm of the group's queries, |K| the largest of the means' (taken once for each head).
 // Blocks more than 2 eps above the top-th value are in, those more than 2 eps below are out, and what
-// lies between is summed again in fp64, where 64 G products of bf16 values lose nothing that matters.
+// lies between is summed again as fp64 would, where 64 G products of bf16 values lose nothing that matters.
 // So the choice is that of exact scores, whatever order they are added in.
 #include <atomic>
 #include <cfloat>
@@ -115,8 +116,8 @@ __device__ __forceinline__ bool narrow(const float* v, int nv, int want, float e
 __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_constant__ Choice a) {
     extern __shared__ __align__(16) float scores[];          // [tile][stride]
     __shared__ int32_t limit[kMostQueries], home[kMostQueries];
-    __shared__ float mass[kMostQueries];                     // sum |q| over the group's heads
-    __shared__ unsigned largest;                             // bits of max |mean|
+    __shared__ float mass[kMostQueries];                     // sum of q^2 over the group's heads
+    __shared__ unsigned largest;                             // bits of the largest sum of a mean's squares
     __shared__ float cand_x[kWarps][kCandidates];
     __shared__ int cand_c[kWarps][kCandidates];
     const SelectShape& s = a.s;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
     }
     for (int r = warp; r < queries; r += kWarps) {
         float x = 0.f;
-        for (int h = 0; h < s.G; ++h) x += abs_sum(reinterpret_cast<const uint32_t*>(q + (h * s.n + r) * kHeadDim)[lane]);
+        for (int h = 0; h < s.G; ++h) x = squares(reinterpret_cast<const uint32_t*>(q + (h * s.n + r) * kHeadDim)[lane], x);
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) x += __shfl_xor_sync(kFull, x, off);
         if (lane == 0) mass[r] = x;
@@ -146,15 +147,19 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
     const int most = __reduce_max_sync(kFull, limit[lane]);
     const int seen = (most + kBlockKeys - 1) / kBlockKeys;   // blocks that some query sees
 
-    __nv_bfloat162 tops = __floats2bfloat162_rn(0.f, 0.f);   // max |mean|; NaN where a mean is
+    unsigned top_squares = 0;
     for (int c0 = 16 * warp; c0 < seen; c0 += 16 * kWarps) {
         uint32_t k[2][8];
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
             const int c = c0 + 8 * o + g;
             load_row(means + (int64_t)c * kHeadDim, c < seen, t, k[o]);
+            float x = 0.f;                   // four lanes a row
 #pragma unroll
-            for (int w = 0; w < 8; ++w) tops = __hmax2_nan(tops, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&k[o][w])));
+            for (int w = 0; w < 8; ++w) x = squares(k[o][w], x);
+            x += __shfl_xor_sync(kFull, x, 1);
+            x += __shfl_xor_sync(kFull, x, 2);
+            top_squares = max(top_squares, __float_as_uint(fabsf(x)));
         }
 #pragma unroll
         for (int half = 0; half < kMostQueries / 8; ++half) {
@@ -175,12 +180,10 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
             }
         }
     }
-    const float2 two = __bfloat1622float2(tops);
-    const bool odd = two.x != two.x || two.y != two.y;
-    float top_mean = __any_sync(kFull, odd) ? INFINITY : warp_max(fmaxf(two.x, two.y));
-    if (lane == 0) atomicMax(&largest, __float_as_uint(top_mean));
+    top_squares = __reduce_max_sync(kFull, top_squares);
+    if (lane == 0) atomicMax(&largest, top_squares);
     __syncthreads();
-    top_mean = __uint_as_float(largest);
+    const float mean_squares = __uint_as_float(largest);
 
     for (int r = warp; r < queries; r += kWarps) {
         const int lim = limit[r], nv = (lim + kBlockKeys - 1) / kBlockKeys;
@@ -194,13 +197,13 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
         for (int x = lane; x < forced.count(); x += 32) v[forced.at(x)] = INFINITY;
         if (nv + lane < (nv + 31) / 32 * 32) v[nv + lane] = -INFINITY;
         __syncwarp();
-        const float eps = twice_eps(s.G, mass[r], top_mean);
+        const float reach = reach_of(s.G, mass[r], mean_squares), eps = twice_eps(s.G, reach);
         uint64_t taken = 0;
         int cand[2];
         if (s.top <= 32 && eps < 1e30f &&
             narrow(v, nv, s.top, eps, lane, cand_x[warp], cand_c[warp], cand, &taken, [&](int c) {
                 return exact_score(reinterpret_cast<const uint32_t*>(q + r * kHeadDim), s.n * (kHeadDim / 2), s.G,
-                                   reinterpret_cast<const uint32_t*>(means + (int64_t)c * kHeadDim), lane);
+                                   reinterpret_cast<const uint32_t*>(means + (int64_t)c * kHeadDim), reach, lane);
             })) {
             const unsigned lo = (unsigned)taken, hi = (unsigned)(taken >> 32), below = (1u << lane) - 1;
             if (lo >> lane & 1) out[__popc(lo & below)] = cand[0];
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
         hi = warp_max(hi);
         // the top-th largest value, kth: at least top values reach lo, fewer than top reach hi
         float kth;
-        auto reach = [&](float x) {
+        auto reaching = [&](float x) {
             int n = 0;
             for (int c = 4 * lane; c < padded; c += 128) {
                 const float4 y = *reinterpret_cast<const float4*>(v + c);
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
             }
             return __reduce_add_sync(kFull, n);
         };
-        if (reach(hi) >= s.top) {
+        if (reaching(hi) >= s.top) {
             kth = hi;                                        // (the forced and hi's equals are enough)
         } else {
             for (;;) {
@@ -242,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
                     kth = lo;
                     break;
                 }
-                const int n = reach(mid);
+                const int n = reaching(mid);
                 if (n == s.top) {
                     float least = INFINITY;
                     for (int c = lane; c < nv; c += 32)
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
                 for (unsigned m = __ballot_sync(kFull, close); rest && m; m &= m - 1) {
                     const int index = c0 + __ffs(m) - 1;
                     const double score = exact_score(row, s.n * (kHeadDim / 2), s.G,
-                                                     reinterpret_cast<const uint32_t*>(means + (int64_t)index * kHeadDim), lane);
+                                                     reinterpret_cast<const uint32_t*>(means + (int64_t)index * kHeadDim), reach, lane);
                     best.offer(score, index, rest, lane);
                 }
                 if (close) v[c] = -INFINITY;
@@ -310,9 +313,12 @@ int launch_select_blocks(const SelectShape& s, const void* Q, const void* means,
     Choice a{s, static_cast<const __nv_bfloat16*>(Q), static_cast<const __nv_bfloat16*>(means), sink, local, blocks, kMostQueries, 0};
     // whole loads of a warp, and 4 more floats: the lanes of a product's column fall in other banks
     a.stride = (s.nb + 127) / 128 * 128 + 4;
-    // Tiles of 128 queries, a thread each: 16 x 16384 queries of 256 blocks take 194 us here.
-    if (s.top <= kTilesTop && s.n >= 64 && s.B * s.Hk * s.n >= 8192) return launch_select_tiles(a, stream);
-    while ((int64_t)a.tile * a.stride * 4 > kMostSmem) a.tile /= 2;
+    // Many queries have a thread each: 16 x 16384 queries of 256 blocks take 101 us there and 194 here, 32 x 4096 of
+    // 64 blocks 30 and 77; but 4 x 4096 of 128 blocks, 4 heads a group, take 36 there and 23 here.
+    if (s.top <= kTilesTop && s.n >= 64 && s.B * s.Hk * s.n >= 24576) return launch_select_tiles(a, stream);
+    // fewer queries a block of threads where they are many key blocks', or where there are few of them for the SMs
+    while (a.tile > 1 && ((int64_t)a.tile * a.stride * 4 > kMostSmem || a.tile / 2 >= s.n)) a.tile /= 2;
+    while (a.tile > kWarps && s.B * s.Hk * ((s.n + a.tile - 1) / a.tile) < 2 * 152) a.tile /= 2;
     const int64_t grid = s.B * s.Hk * ((s.n + a.tile - 1) / a.tile);
     if (grid > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
     cudaError_t err = allow_smem(select_blocks_kernel, kMostSmem, ready);

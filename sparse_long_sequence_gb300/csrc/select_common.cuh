@@ -24,24 +24,59 @@ namespace select {
 
 using tiles::kFull;
 
-// Twice what a score in fp32 is off by at most, for `mass` = sum |q| over G heads (select_blocks.cu), and what
-// products of denormal size may lose.
-__device__ __forceinline__ float twice_eps(int G, float mass, float top_mean) {
-    return 2.02f * 68.f * 1.1920929e-7f * (float)G * mass * top_mean + 1e-35f;
+// Norms are kept away from 0, where squares of denormal size are lost.
+constexpr float kLeastNorm = 1e-16f;
+
+// The bits of a sum of squares, which order as it does (infinities and NaN above all).
+__device__ __forceinline__ float squares(uint32_t w, float sum) {
+    const float x = __uint_as_float(w << 16), y = __uint_as_float(w & 0xffff0000u);
+    return fmaf(y, y, fmaf(x, x, sum));
 }
 
-__device__ __forceinline__ float abs_sum(uint32_t w) {
-    return fabsf(__uint_as_float(w << 16)) + fabsf(__uint_as_float(w & 0xffff0000u));
+// |Q| |K| of a query whose group's heads have squares adding up to `query`, against means with up to `mean`; K is the mean
+// once for each head.  No sum of products of theirs is larger.
+__device__ __forceinline__ float reach_of(int G, float query, float mean) {
+    return sqrtf((float)G) * (sqrtf(query) + kLeastNorm) * (sqrtf(mean) + kLeastNorm);
+}
+// Twice what a score in fp32 is off by at most (select_blocks.cu), and what products of denormal size may lose.
+__device__ __forceinline__ float twice_eps(int G, float reach) { return 2.02f * 68.f * 1.1920929e-7f * (float)G * reach + 1e-35f; }
+
+// x + y = sum + error, without rounding (Knuth's two-sum)
+__device__ __forceinline__ float two_sum(float x, float y, float* error) {
+    const float s = __fadd_rn(x, y), z = __fsub_rn(s, x);
+    *error = __fadd_rn(__fsub_rn(x, __fsub_rn(s, z)), __fsub_rn(y, z));
+    return s;
 }
 
-// The score in fp64, in every lane; NaN counts as -infinity.
-__device__ __forceinline__ double exact_score(const uint32_t* q, int64_t head_words, int G, const uint32_t* mean, int lane) {
+// The score as fp64 would have it or better, in every lane; NaN counts as -infinity.  Products of two bf16 values
+// are exact in fp32, and their sum is held in three fp32 parts (the machine's fp64 rate is a sixtieth of its fp32's:
+// with 16 heads a group most of the choice's time went there); in fp64 where `reach` is so large or small that
+// fp32 products may not be exact.
+__device__ __forceinline__ double exact_score(const uint32_t* q, int64_t head_words, int G, const uint32_t* mean, float reach,
+                                              int lane) {
     const uint32_t w = mean[lane];
-    const double m0 = __uint_as_float(w << 16), m1 = __uint_as_float(w & 0xffff0000u);
+    const float m0 = __uint_as_float(w << 16), m1 = __uint_as_float(w & 0xffff0000u);
     double t = 0.0;
-    for (int h = 0; h < G; ++h) {
-        const uint32_t x = q[h * head_words + lane];
-        t += (double)__uint_as_float(x << 16) * m0 + (double)__uint_as_float(x & 0xffff0000u) * m1;
+    if (reach > 1e-20f && reach < 1e30f) {
+        float a = 0.f, b = 0.f, c = 0.f;
+        auto add = [&](float product) {
+            float e, f;
+            a = two_sum(a, product, &e);
+            b = two_sum(b, e, &f);
+            c = __fadd_rn(c, f);
+        };
+#pragma unroll 4
+        for (int h = 0; h < G; ++h) {
+            const uint32_t x = q[h * head_words + lane];
+            add(__fmul_rn(__uint_as_float(x << 16), m0));
+            add(__fmul_rn(__uint_as_float(x & 0xffff0000u), m1));
+        }
+        t = (double)a + ((double)b + (double)c);
+    } else {
+        for (int h = 0; h < G; ++h) {
+            const uint32_t x = q[h * head_words + lane];
+            t += (double)__uint_as_float(x << 16) * (double)m0 + (double)__uint_as_float(x & 0xffff0000u) * (double)m1;
+        }
     }
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) t += __shfl_xor_sync(kFull, t, off);

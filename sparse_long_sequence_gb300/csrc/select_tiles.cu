@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
     __shared__ uint64_t bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int seen_smem;
-    __shared__ unsigned largest;             // bits of max |mean|
+    __shared__ unsigned largest;             // bits of the largest sum of a mean's squares
     const SelectShape& s = a.s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t parts = (uint32_t)(s.n + kTileRows - 1) / kTileRows, ul = blockIdx.x / parts;
@@ -113,9 +113,9 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
     const uint32_t tmem = tmem_slot, mine = tmem + ((uint32_t)(32 * warp) << 16);
 
     uint32_t phase = 0;
-    float mass = 0.f;                        // sum |q| over the group's heads
-    __nv_bfloat162 tops = __floats2bfloat162_rn(0.f, 0.f);   // max |mean| of this thread's rows; NaN where one is
-    // The scores of round `round` into tensor memory; the first time through also mass and tops.
+    float mass = 0.f;                        // sum of q^2 over the group's heads
+    unsigned top_squares = 0;                // of this thread's means
+    // The scores of round `round` into tensor memory; the first time through also mass and top_squares.
     auto score_round = [&](int round, bool first) {
         const int c0 = round * kRound, rows = min(kRound, seen - c0);
 #pragma unroll
@@ -148,17 +148,18 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const uint4 w = *reinterpret_cast<const uint4*>(smem + place(tid, c));
-                    mass += (abs_sum(w.x) + abs_sum(w.y)) + (abs_sum(w.z) + abs_sum(w.w));
+                    mass = squares(w.w, squares(w.z, squares(w.y, squares(w.x, mass))));
                 }
             }
             if (first && h == 0) {
+                static_assert(kRound == kThreads, "a mean a thread");
+                float x = 0.f;
 #pragma unroll
-                for (int c = 0; c < kRound / 16; ++c) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(smem + kTileBytes + place(tid + (c >> 3) * kThreads, c & 7));
-                    const uint32_t y[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) tops = __hmax2_nan(tops, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&y[j])));
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(smem + kTileBytes + place(tid, c));
+                    x = squares(w.w, squares(w.z, squares(w.y, squares(w.x, x))));
                 }
+                top_squares = max(top_squares, __float_as_uint(fabsf(x)));
             }
             ptx::mbar_wait(&bar, phase, status);
             phase ^= 1;
@@ -203,12 +204,11 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
         sort32(top);
         bound = pick(top, want - 1);         // (-infinity where fewer groups have any: all blocks are candidates)
     }
-    const float2 two = __bfloat1622float2(tops);
-    float top_mean = __any_sync(kFull, two.x != two.x || two.y != two.y) ? INFINITY : warp_max(fmaxf(two.x, two.y));
-    if (lane == 0) atomicMax(&largest, __float_as_uint(top_mean));
+    top_squares = __reduce_max_sync(kFull, top_squares);
+    if (lane == 0) atomicMax(&largest, top_squares);
     ptx::tc_fence_before();
     __syncthreads();
-    const float eps = twice_eps(s.G, mass, __uint_as_float(largest));
+    const float reach = reach_of(s.G, mass, __uint_as_float(largest)), eps = twice_eps(s.G, reach);
     const bool far = !(eps < 1e30f);
     float floor = choose && want && !far ? fmaxf(bound - eps, -FLT_MAX) : INFINITY;
     if (rounds > 1) score_round(0, false);   // (all have read the last scores)
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
     for (unsigned todo = __ballot_sync(kFull, close); todo; todo &= todo - 1) {
         const int l = __ffs(todo) - 1, row = 32 * warp + l;  // the query's lane and row
         const int n = __shfl_sync(kFull, few, l), rest = __shfl_sync(kFull, want, l), blocks = __shfl_sync(kFull, nv, l);
-        const float e = __shfl_sync(kFull, eps, l);
+        const float e = __shfl_sync(kFull, eps, l), far_reach = __shfl_sync(kFull, reach, l);
         const bool all = __shfl_sync(kFull, (int)hard, l);
         Forced f = forced;
         f.sink = __shfl_sync(kFull, forced.sink, l);
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
         f.near = __shfl_sync(kFull, forced.near, l);
         auto exact = [&](int c) {
             return exact_score(reinterpret_cast<const uint32_t*>(q0 + row * kHeadDim), s.n * (kHeadDim / 2), s.G,
-                               reinterpret_cast<const uint32_t*>(means + (int64_t)c * kHeadDim), lane);
+                               reinterpret_cast<const uint32_t*>(means + (int64_t)c * kHeadDim), far_reach, lane);
         };
         int32_t* out = result + (l - lane) * pitch;
         Best best;

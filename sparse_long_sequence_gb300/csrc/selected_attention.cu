@@ -437,8 +437,9 @@ int launch_tiles(const SelectedArgs& a, char* ws, cudaStream_t stream) {
 }
 
 // Few queries: what the lists, the partials and their joining would cost outweighs reading a block's
-// keys once for each query that lists it.
-bool by_query(const SelectShape& s) { return s.m == 0 || s.B * s.Hk * s.n * s.top <= 8192; }
+// keys once for each query that lists it.  (4 heads, 16 blocks a query: 19.5 us by query and 25.6 by block for 128
+// queries, 37 and 27 for 256; 32 heads of 8 key heads, 4 blocks: 18.6 and 24.9 for 64, 34 and 28 for 128.)
+bool by_query(const SelectShape& s) { return s.m == 0 || s.B * s.Hk * s.n * s.top <= 10240; }
 
 }  // namespace
 

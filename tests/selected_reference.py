@@ -60,8 +60,11 @@ def select(Q, mean, top, m, sink, local, causal, lengths, starts):
         most = max(1, int(count.max())) if n else 1
         for h in range(Hk):
             score = torch.zeros((n, nb), dtype=torch.float64)
-            used = mean[b, h, :most].double().repeat(1, Hq // Hk)      # (others are not read)
-            score[:, :most] = Q[b, h * (Hq // Hk):(h + 1) * (Hq // Hk)].double().transpose(0, 1).flatten(1) @ used.T
+            q, used = Q[b, h * (Hq // Hk):(h + 1) * (Hq // Hk)].double().transpose(0, 1), mean[b, h, :most].double()
+            # (others are not read.)  The first two features by themselves: where they are large and cancel, a sum
+            # that went on from them would lose 2^-33 of the others, and equal one score in 1e5 with another
+            for part in (slice(0, 2), slice(2, 64)):
+                score[:, :most] += q[..., part].flatten(1) @ used[:, part].repeat(1, Hq // Hk).T
             score = torch.where(score != score, -math.inf, score)
             rank = torch.sort(score, dim=1, descending=True, stable=True).indices      # equals by rising index
             group = torch.where(c[None] >= count[:, None], 2, torch.where(forced, 0, 1))

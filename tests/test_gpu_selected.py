@@ -180,13 +180,13 @@ def test_select_hard_scores(dl, kind, top, n=20, nb=150):
     assert int((got != ref.select(Q, mean, top, nb * 64 - 3, 1, 0, False, None, None)).sum()) == 0
 
 
-MANY = [   # enough queries for a thread each; the last tile short, more than a product's 256 blocks, many heads a group
-    (1, 1, 1, 8200, 8200, 16, 1, 2, True, None, None),
-    (2, 4, 2, 2100, 2100, 7, 0, 1, False, [2100, 1200], [0, 0]),
-    (1, 12, 4, 2050, 20000, 20, 2, 1, True, None, None),
-    (3, 30, 3, 1000, 1300, 4, 1, 1, True, [1300, 900, 0], None),
-    (64, 2, 2, 70, 300, 3, 0, 0, False, None, None),
-    (1, 1, 1, 9000, 40000, 1, 0, 0, False, None, None),
+MANY = [   # enough queries for a thread each; the last tile short, more than a product's 128 blocks, many heads a group
+    (1, 1, 1, 24650, 24650, 16, 1, 2, True, None, None),
+    (2, 4, 2, 6200, 6200, 7, 0, 1, False, [6200, 1200], [0, 0]),
+    (1, 12, 4, 6200, 20000, 20, 2, 1, True, None, None),
+    (3, 30, 3, 2750, 3000, 4, 1, 1, True, [3000, 900, 0], None),
+    (180, 2, 2, 70, 300, 3, 0, 0, False, None, None),
+    (1, 1, 1, 24600, 40000, 1, 0, 0, False, None, None),
 ]
 
 
@@ -199,7 +199,7 @@ def test_select_many(dl, case):
 @pytest.mark.parametrize("top", [1, 7, 20, 32])
 @pytest.mark.parametrize("nb", [150, 300])
 def test_select_many_hard_scores(dl, kind, top, nb):
-    test_select_hard_scores(dl, kind, top, n=4100, nb=nb)
+    test_select_hard_scores(dl, kind, top, n=12300, nb=nb)
 
 
 # ---------------------------------------------------------------- attention
