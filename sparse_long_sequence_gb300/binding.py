@@ -774,18 +774,24 @@ def diffuser_rope_backward(dQo, dKo, frequencies, magnitude: float = 1.0, interl
 
 
 # ---------------------------------------------------------------- attention over chosen blocks
+@functools.lru_cache(maxsize=1)
+def _dtypes():
+    """bfloat16, int32 (an import statement a check would cost more than the check)."""
+    import torch
+    return torch.bfloat16, torch.int32
+
+
 def _per_sequence(t, name, B, dev):
-    import torch
-    return None if t is None else _need(t, name, (B,), dev, torch.int32)
+    return None if t is None else _need(t, name, (B,), dev, _dtypes()[1])
 
 
-def _bf16_4d(t, name, shape="[B][H][n][64]"):
-    import torch
-    if t.dtype != torch.bfloat16:
+def _bf16_4d(t, name):
+    if t.dtype != _dtypes()[0]:
         raise TypeError(f"{name} must be torch.bfloat16, not {t.dtype}")
-    if t.dim() != 4:
-        raise ValueError(f"expected {name} {shape}, got {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 4:
+        raise ValueError(f"expected {name} [B][H][n][64], got {tuple(shape)}")
+    return shape
 
 
 @_on_stream
@@ -826,6 +832,7 @@ def diffuser_select_blocks(Q, means, top_k: int, keys: int, sink_blocks: int = 0
     return blocks
 
 
+@functools.lru_cache(maxsize=256)
 def diffuser_selected_attention_workspace_size(B: int, Hq: int, Hk: int, n: int, m: int, top_k: int, d: int = 64) -> int:
     b = ctypes.c_size_t()
     _check(_lib.diffuser_selected_attention_workspace_size(B, Hq, Hk, n, m, d, top_k, ctypes.byref(b)),
@@ -835,7 +842,6 @@ def diffuser_selected_attention_workspace_size(B: int, Hq: int, Hk: int, n: int,
 
 def _selected_shapes(Q, K, V, blocks):
     """Sizes of a call and the addresses of its first four tensors, after their checks."""
-    import torch
     B, Hq, n, d = _bf16_4d(Q, "Q")
     Hk, m = _bf16_4d(K, "K")[1:3]
     dev, bf, keys = Q.get_device(), Q.dtype, (B, Hk, m, d)
@@ -843,7 +849,7 @@ def _selected_shapes(Q, K, V, blocks):
         raise ValueError(f"expected blocks [B][Hk][n][top_k], got {tuple(blocks.shape)}")
     top = blocks.shape[3]
     return (dev, B, Hq, Hk, n, m, d, top, _flat(Q, "Q", dev, bf), _need(K, "K", keys, dev, bf),
-            _need(V, "V", keys, dev, bf), _need(blocks, "blocks", (B, Hk, n, top), dev, torch.int32))
+            _need(V, "V", keys, dev, bf), _need(blocks, "blocks", (B, Hk, n, top), dev, _dtypes()[1]))
 
 
 @_on_stream
@@ -865,6 +871,7 @@ def diffuser_selected_attention(Q, K, V, blocks, causal: bool = True, lengths=No
     return out if lse is None else (out, lse)
 
 
+@functools.lru_cache(maxsize=256)
 def diffuser_selected_attention_backward_workspace_size(B: int, Hq: int, Hk: int, n: int, m: int, top_k: int,
                                                         d: int = 64) -> int:
     b = ctypes.c_size_t()

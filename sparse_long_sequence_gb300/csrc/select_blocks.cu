@@ -27,8 +27,8 @@ namespace {
 using namespace tiles;
 using namespace select;
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kWarps = 8;                    // of a block of threads; kMostWarps where few queries have many blocks
+constexpr int kMostWarps = 32;
 constexpr int kMostQueries = 32;
 
 constexpr int kCandidates = 64;
@@ -113,15 +113,15 @@ __device__ __forceinline__ bool narrow(const float* v, int nv, int want, float e
     return true;
 }
 
-__global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_constant__ Choice a) {
+__global__ void __launch_bounds__(32 * kMostWarps) select_blocks_kernel(const __grid_constant__ Choice a) {
     extern __shared__ __align__(16) float scores[];          // [tile][stride]
     __shared__ int32_t limit[kMostQueries], home[kMostQueries];
     __shared__ float mass[kMostQueries];                     // sum of q^2 over the group's heads
     __shared__ unsigned largest;                             // bits of the largest sum of a mean's squares
-    __shared__ float cand_x[kWarps][kCandidates];
-    __shared__ int cand_c[kWarps][kCandidates];
+    __shared__ float cand_x[kMostWarps][kCandidates];
+    __shared__ int cand_c[kMostWarps][kCandidates];
     const SelectShape& s = a.s;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t tiles = (uint32_t)(s.n + a.tile - 1) / a.tile, ul = blockIdx.x / tiles;
     const int64_t u = ul, i0 = (int64_t)(blockIdx.x - ul * tiles) * a.tile, b = sequence_of(s, u);
     const int queries = (int)min((int64_t)a.tile, s.n - i0);
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
         limit[threadIdx.x] = lim;
         home[threadIdx.x] = (int)(p / kBlockKeys);
     }
-    for (int r = warp; r < queries; r += kWarps) {
+    for (int r = warp; r < queries; r += warps) {
         float x = 0.f;
         for (int h = 0; h < s.G; ++h) x = squares(reinterpret_cast<const uint32_t*>(q + (h * s.n + r) * kHeadDim)[lane], x);
 #pragma unroll
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
     const int seen = (most + kBlockKeys - 1) / kBlockKeys;   // blocks that some query sees
 
     unsigned top_squares = 0;
-    for (int c0 = 16 * warp; c0 < seen; c0 += 16 * kWarps) {
+    for (int c0 = 16 * warp; c0 < seen; c0 += 16 * warps) {
         uint32_t k[2][8];
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) select_blocks_kernel(const __grid_co
     __syncthreads();
     const float mean_squares = __uint_as_float(largest);
 
-    for (int r = warp; r < queries; r += kWarps) {
+    for (int r = warp; r < queries; r += warps) {
         const int lim = limit[r], nv = (lim + kBlockKeys - 1) / kBlockKeys;
         int32_t* out = a.blocks + ((u * s.n) + i0 + r) * s.top;
         if (nv <= s.top) {
@@ -319,13 +319,15 @@ int launch_select_blocks(const SelectShape& s, const void* Q, const void* means,
     // fewer queries a block of threads where they are many key blocks', or where there are few of them for the SMs
     while (a.tile > 1 && ((int64_t)a.tile * a.stride * 4 > kMostSmem || a.tile / 2 >= s.n)) a.tile /= 2;
     while (a.tile > kWarps && s.B * s.Hk * ((s.n + a.tile - 1) / a.tile) < 2 * 152) a.tile /= 2;
+    // (16 queries of 1024 blocks, 4 heads a group: 15.9 us with 8 warps)
+    const int per_warp = (s.nb + 31) / 32, warps = a.tile > 2 || per_warp <= kWarps ? kWarps : per_warp < kMostWarps ? per_warp : kMostWarps;
     const int64_t grid = s.B * s.Hk * ((s.n + a.tile - 1) / a.tile);
     if (grid > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
     cudaError_t err = allow_smem(select_blocks_kernel, kMostSmem, ready);
     if (err != cudaSuccess) return cuda_fail(err, "select_blocks_kernel");
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        select_blocks_kernel<<<(unsigned)grid, kThreads, (size_t)a.tile * a.stride * 4, stream>>>(a);
+        select_blocks_kernel<<<(unsigned)grid, 32 * warps, (size_t)a.tile * a.stride * 4, stream>>>(a);
     }
     err = cudaGetLastError();
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "select_blocks_kernel");

@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
     const Forced forced(a.sink, a.local, (int)(p / kBlockKeys), nv);
     const int want = s.top - forced.count();                 // besides the forced
     const bool choose = nv > s.top;
+    __syncwarp();
     if (warp == 0) ptx::tmem_alloc(&tmem_slot, kRound);
     if (tid == 0) {
         ptx::mbar_init(&bar, 1);
@@ -135,6 +136,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
             ptx::cp_async_wait_all();
             ptx::fence_proxy_async_smem();
             __syncthreads();
+            __syncwarp();
             if (warp == 0 && ptx::elect_one()) {
                 ptx::tc_fence_after();
                 constexpr uint32_t kDesc = ptx::mma_idesc_bf16(kTileRows, kRound, false, false);
@@ -169,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
     };
     // columns c .. c + 31 of the round that begins with block c0; -infinity where the query sees no block, or it is forced
     auto scores = [&](int c0, int c, uint32_t (&v)[32]) {
+        __syncwarp();
         ptx::tmem_ld32_issue(mine + c, v);
         ptx::tmem_ld_wait32(v);
         if (!__all_sync(kFull, c0 + c + 32 <= nv)) {
@@ -264,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
         if (rounds > 1) score_round(0, false);
     }
     // (all have read the scores; the means' place is free for the results)
+    __syncwarp();
     if (warp == 0) ptx::tmem_dealloc(tmem, kRound);
 
     if (tid < queries && !choose) {

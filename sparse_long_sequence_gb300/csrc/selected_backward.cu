@@ -121,6 +121,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         entry = entry_of(walk, entries, s.G, row, &head);
     };
     look(first + 1);
+    __syncwarp();
     if (warp == 0) ptx::tmem_alloc(&tmem_slot, kColumns);
     if (tid == 0) {
 #pragma unroll
@@ -145,6 +146,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::fence_proxy_async_smem();
         __syncthreads();                     // the tile is there, and all have read the last dq
         if (warp == 0) {
+            __syncwarp();
             ptx::tc_fence_after();
             const uint64_t dd = ptx::sw128_kmajor_desc(stage), qd = ptx::sw128_kmajor_desc(stage + kTileBytes);
             const uint64_t kd = ptx::sw128_kmajor_desc(keys), vd = ptx::sw128_kmajor_desc(values);
@@ -204,6 +206,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::tc_fence_before();
         __syncthreads();                     // P and dS are whole
         if (warp == 0) {
+            __syncwarp();
             ptx::tc_fence_after();
             const uint64_t sd = ptx::sw128_kmajor_desc(weights + kTileBytes), kd = ptx::sw128_mnmajor_desc(keys, kKeyBytes);
 #pragma unroll
@@ -228,6 +231,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         __syncwarp();
         stage_sums(sums + lane * kSumsPitch, sc, half, lane);
         ptx::fence_proxy_async_smem();
+        __syncwarp();
         ptx::named_barrier_sync(1 + quarter, 64);            // the rows' two warps
         if (half == 0 && lane == 0 && count > 0) {
             ptx::bulk_store(out.dq + ((tile0 + x) * kTileRows + 32 * quarter) * kHeadDim, sums, min(count, 32) * kSumsPitch);
@@ -246,6 +250,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
                 __nv_bfloat16* turned = reinterpret_cast<__nv_bfloat16*>(smem + (stage - keys) + which * kKeyBytes);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) turned[(32 * half + k) * kHeadDim + feature] = __float2bfloat16_rn(__uint_as_float(sc[k]));
+                __syncwarp();
                 ptx::named_barrier_sync(5 + which, 128);
                 const int rows = (int)min((int64_t)kBlockKeys, s.m - (int64_t)block * kBlockKeys);
                 uint4* dst = reinterpret_cast<uint4*>((which ? a.dk : a.dv) + (u * s.m + (int64_t)block * kBlockKeys) * kHeadDim);
@@ -267,6 +272,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     }
     if (lane == 0) ptx::bulk_wait<0>();
     __syncthreads();
+    __syncwarp();
     if (warp == 0) ptx::tmem_dealloc(tmem, kColumns);
 }
 
