@@ -580,8 +580,11 @@ DIFFUSER_API int diffuser_rope_backward(const void* dQo, const void* dKo, int32_
  * (causal != 0) or all below the length; otherwise none: its list is empty, its result 0.
  * B >= 0, n and m 0..2^20, Hq 1..4096, top_k 1..64, d 64.  Tensors are contiguous and 16-byte aligned
  * (lengths, starts: 4), on the current device; outputs overlap nothing else.  Calls are asynchronous on
- * `stream`, may be captured, use no atomics on results (repeated calls give identical bits).
- * Errors: INVALID_ARG, UNSUPPORTED, OVERFLOW, CUDA, and WORKSPACE where there is one.
+ * `stream`, may be captured (the first call on a device too), and add nothing up by atomics (repeated
+ * calls give identical bits).  The choice for many queries, their attention and its backward pass run on
+ * the tcgen05 tensor cores; a kernel whose bounded wait gives up reports through
+ * diffuser_projection_status, as the projections do.
+ * Errors: INVALID_ARG, UNSUPPORTED, OVERFLOW, ALLOC, CUDA, DEVICE, and WORKSPACE where there is one.
  */
 
 /*
@@ -618,7 +621,8 @@ DIFFUSER_API int diffuser_select_blocks(const void* Q, const void* means, int64_
  *            of the tensor cores; their sum is taken before that)
  *   lse      fp32 [B][Hq][n] or NULL: log of the sum of exp(q_i.k_j / sqrt(d)), for the backward
  *   workspace   diffuser_selected_attention_workspace_size bytes, 256-byte aligned (0: NULL will do)
- * Infinities and NaN among the keys that a query sees reach its result.
+ * Keys and values behind a length, and those of blocks that no query lists, are not read.  An infinity or
+ * a NaN in another one may reach every query that lists its block, those before it too.
  */
 DIFFUSER_API int diffuser_selected_attention_workspace_size(int64_t B, int64_t Hq, int64_t Hk, int64_t n,
                                                             int64_t m, int32_t d, int32_t top_k, size_t* bytes);

@@ -256,9 +256,12 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         next = row_from(s, b, block_next * kBlockKeys, entry, head, row < walk.rows);
         count_next = walk.rows - (row - lane);
         look(x + 2);
+        uint32_t lo[32], hi[32];
         ptx::mbar_wait(&bars[0], phase, status);
         __syncwarp();
         ptx::tc_fence_after();
+        ptx::tmem_ld32_issue(mine, lo);
+        ptx::tmem_ld32_issue(mine + 32, hi);
         const uint32_t values_now = values + side * kKeyBytes;
         if (x + 1 < last) {                  // S is there: the queries' and the keys' places are free
             if (block_next != block) {
@@ -268,9 +271,6 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
             }
             copy_rows(queries, q0, next, warp, lane);
         }
-        uint32_t lo[32], hi[32];
-        ptx::tmem_ld32_issue(mine, lo);
-        ptx::tmem_ld32_issue(mine + 32, hi);
         ptx::tmem_ld_wait32(lo);
         ptx::tmem_ld_wait32(hi);
         float top = -INFINITY;

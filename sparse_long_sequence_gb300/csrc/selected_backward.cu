@@ -171,10 +171,10 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
             stat_next = out.stat[head0 + next.at];
             look(x + 2);
         }
+        uint32_t sc[32], dp[32];
         ptx::mbar_wait(&bars[0], phase, status);
         __syncwarp();
         ptx::tc_fence_after();
-        uint32_t sc[32], dp[32];
         ptx::tmem_ld32_issue(col, sc);
         ptx::tmem_ld32_issue(col + 64, dp);
         ptx::tmem_ld_wait32(sc);
@@ -241,6 +241,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         fresh = x + 1 == last || block_next != block;
         if (fresh) {                         // the run's last tile of the block
             if (x + 1 < last) copy_block(block_next);        // (dq is there: keys and values are done with)
+            __syncwarp();
             ptx::tc_fence_after();
             // lanes 0 .. 63: feature of dout, dv^T in the first 64 columns; 64 .. 127: feature of q, dk^T in the others
             ptx::tmem_ld32_issue(col + 128 + (quarter >> 1) * 64, sc);
