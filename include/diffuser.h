@@ -640,6 +640,8 @@ DIFFUSER_API int diffuser_selected_attention(const void* Q, const void* K, const
  * the sums for a key over the queries of all heads of its group.  A and dS are recomputed, and
  * rounded to bf16 as operands of the tensor cores; sums in fp32 in a fixed order, one rounding.
  *   dQ [B][Hq][n][64], dK, dV [B][Hk][m][64]: bf16, written whole (0 where no query sees a key)
+ * Infinities and NaN of a key may reach the queries that list its block, and those of a query or its dOut
+ * the keys of its blocks, seen or not.
  *   workspace   diffuser_selected_attention_backward_workspace_size bytes, 256-byte aligned
  */
 DIFFUSER_API int diffuser_selected_attention_backward_workspace_size(int64_t B, int64_t Hq, int64_t Hk, int64_t n,

@@ -277,7 +277,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     if (warp == 0) ptx::tmem_dealloc(tmem, kColumns);
 }
 
-constexpr int kJoined = 8;                   // partials in flight
+constexpr int kJoined = 4;                   // partials in flight
 
 // dq of a row: the sum of its partials, sixteen lanes a row, sixteen rows a block of threads.
 __device__ __forceinline__ void join_dq(const SelectedArgs& a, const BlockLists& l, const Partials& in, uint32_t row) {
@@ -288,7 +288,7 @@ __device__ __forceinline__ void join_dq(const SelectedArgs& a, const BlockLists&
     const uint32_t* position = l.positions + (in.u0 * s.n + at.entry) * l.ranks;
     const float* sums = in.dq + at.unit * l.most_tiles * (kSumsBytes / 4);
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x0 = 0; x0 < count; x0 += kJoined) {            // eight partials at a time
+    for (int x0 = 0; x0 < count; x0 += kJoined) {            // a few partials at a time
         uint32_t p[kJoined];
         float4 v[kJoined];
 #pragma unroll
