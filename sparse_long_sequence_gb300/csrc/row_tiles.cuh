@@ -80,9 +80,16 @@ __device__ __forceinline__ void stage_sums(char* row, const uint32_t (&v)[32], i
     for (int c = 0; c < 8; ++c)
         *reinterpret_cast<uint4*>(row + ((8 * half + c) ^ (lane & 7)) * 16) = make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
 }
+// A warp's rows out, first to leave the L2 again: they are read once, after all of them are written, and the
+// queries, keys and values are gathered many times meanwhile.
+__device__ __forceinline__ void bulk_store_once(float* to, const char* from, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;" ::"l"(to),
+                 "r"(ptx::smem_u32(from)), "r"(bytes), "l"(ptx::l2_evict_first())
+                 : "memory");
+}
 // Four features of row `position` (tile 128 + row) of the partial sums: lane 0 .. 15's.
 __device__ __forceinline__ float4 sums_at(const float* sums, uint32_t position, int lane) {
-    return reinterpret_cast<const float4*>(sums)[(int64_t)position * 16 + (lane ^ (position & 7))];
+    return __ldcs(reinterpret_cast<const float4*>(sums) + (int64_t)position * 16 + (lane ^ (position & 7)));
 }
 
 }  // namespace tiles

@@ -332,7 +332,7 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && count > 0) {
-            ptx::bulk_store(out.sums + ((tile0 + x) * kTileRows + 32 * warp) * kHeadDim, sums, min(count, 32) * kSumsPitch);
+            bulk_store_once(out.sums + ((tile0 + x) * kTileRows + 32 * warp) * kHeadDim, sums, min(count, 32) * kSumsPitch);
             ptx::bulk_commit();
         }
     }

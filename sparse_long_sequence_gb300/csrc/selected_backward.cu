@@ -234,7 +234,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         __syncwarp();
         ptx::named_barrier_sync(1 + quarter, 64);            // the rows' two warps
         if (half == 0 && lane == 0 && count > 0) {
-            ptx::bulk_store(out.dq + ((tile0 + x) * kTileRows + 32 * quarter) * kHeadDim, sums, min(count, 32) * kSumsPitch);
+            bulk_store_once(out.dq + ((tile0 + x) * kTileRows + 32 * quarter) * kHeadDim, sums, min(count, 32) * kSumsPitch);
             ptx::bulk_commit();
         }
         __syncwarp();
