@@ -135,10 +135,10 @@ __global__ void __launch_bounds__(32 * kFewWarps) selected_few_kernel(const __gr
             y0 += e * part[w][h][place_of(f)];
             y1 += e * part[w][h][place_of(f + 1)];
         }
-        const float r = limit && top != -INFINITY ? 1.f / sum : 0.f;
+        const float r = sum == 0.f ? 0.f : 1.f / sum;
         const int64_t at = first + h * s.n;
         *reinterpret_cast<uint32_t*>(a.out + at * kHeadDim + f) = pack(y0 * r, y1 * r);
-        if (a.lse && f == 0) a.lse[at] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+        if (a.lse && f == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
 }
 
@@ -391,9 +391,9 @@ selected_join_kernel(const __grid_constant__ SelectedArgs a, const __grid_consta
         }
         top = now;
     }
-    const float r = top != -INFINITY ? 1.f / sum : 0.f;
+    const float r = sum == 0.f ? 0.f : 1.f / sum;            // (a NaN among the scores is one in the sum)
     reinterpret_cast<uint2*>(a.out + at.place * kHeadDim)[lane] = make_uint2(pack(y.x * r, y.y * r), pack(y.z * r, y.w * r));
-    if (a.lse && lane == 0) a.lse[at.place] = top == -INFINITY ? -INFINITY : (top + log2f(sum)) * kLn2;
+    if (a.lse && lane == 0) a.lse[at.place] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 struct Plan {

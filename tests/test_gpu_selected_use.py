@@ -362,3 +362,30 @@ def test_nothing_to_do(dl):
 def test_status_is_clear(dl):
     torch.cuda.synchronize()
     assert dl.diffuser_projection_status() == 0
+
+
+@pytest.mark.parametrize("n", [5, 400])
+def test_scores_that_are_not_numbers(dl, n):
+    """NaN in a query's row, or in a key that a row sees, is NaN in that row's result and log-sum, whether
+    queries are few or many; rows that list no such block are what they were."""
+    Hq, Hk, top = 8, 4, 8
+    q, k, v = rand(1, 2, Hq, n, 64), rand(2, 2, Hk, 640, 64), rand(3, 2, Hk, 640, 64)
+    blocks = torch.arange(top, dtype=torch.int32, device="cuda").expand(2, Hk, n, top).contiguous()
+    blocks[:, :, 1] += 1                                     # row 1 lists all but block 0
+    how = dict(causal=False, save_lse=True)
+    out, lse = dl.diffuser_selected_attention(q, k, v, blocks, **how)
+    bad = q.clone()
+    bad[0, 3, 2, 5] = math.nan
+    got, sums = dl.diffuser_selected_attention(bad, k, v, blocks, **how)
+    hit = torch.zeros(2, Hq, n, dtype=torch.bool, device="cuda")
+    hit[0, 3, 2] = True
+    assert got[hit].isnan().all() and sums[hit].isnan().all()
+    assert torch.equal(got[~hit], out[~hit]) and torch.equal(sums[~hit], lse[~hit])
+    bad = k.clone()
+    bad[1, 1, :64] = math.nan                                # all keys of a block of heads 2 and 3
+    got, sums = dl.diffuser_selected_attention(q, bad, v, blocks, **how)
+    hit = torch.zeros_like(hit)
+    hit[1, 2:4] = True
+    hit[:, :, 1] = False
+    assert got[hit].isnan().all() and sums[hit].isnan().all()
+    assert torch.equal(got[~hit], out[~hit]) and torch.equal(sums[~hit], lse[~hit])
