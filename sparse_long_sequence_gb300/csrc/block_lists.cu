@@ -23,8 +23,8 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBitmapBytes = 64 * 1024;
 
 // A warp's 32 queries, `width` lanes a query (a power of two) and four entries of its list a lane:
-// calls use(query of the 32, block, rank) for the blocks of a query that count, and all(query, their
-// number).  An entry counts if it is above all entries before it (which -1 is not) and has visible keys.
+// calls use(query of the 32, four entries, which of them count, the rank of the first that does, their
+// number) a lane, and all(query, the number of all).  An entry counts if it is above all entries before it (which -1 is not) and has visible keys.
 template <class Use, class All>
 __device__ __forceinline__ void each_live(const SelectShape& s, const int32_t* blocks, uint32_t u, int64_t i0, int width,
                                           Use use, All all) {
@@ -76,9 +76,7 @@ __device__ __forceinline__ void each_live(const SelectShape& s, const int32_t* b
         }
         if (x == width - 1 && i0 + q < s.n) all(q, rank);
         rank -= count;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (in[j]) use(q, c[j], rank++);
+        use(q, c, in, rank, count);
     }
 }
 
@@ -89,7 +87,12 @@ __device__ __forceinline__ void set_bits(const SelectShape& s, const int32_t* bl
     __syncthreads();
     const int w = threadIdx.x >> 5;          // a warp a word
     each_live(s, blocks, u, (chunk * l.words + w) * 32, l.width,
-              [&](int q, int c, int) { atomicOr(&bits[w * s.nb + c], 1u << q); }, [](int, int) {});
+              [&](int q, const int (&c)[4], const bool (&in)[4], int, int) {
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                      if (in[j]) atomicOr(&bits[w * s.nb + c[j]], 1u << q);
+              },
+              [](int, int) {});
     __syncthreads();
 }
 
@@ -210,10 +213,23 @@ fill_lists_kernel(const __grid_constant__ SelectShape s, const int32_t* blocks, 
     const int w = threadIdx.x >> 5;
     const int64_t i0 = ((int64_t)chunk * l.words + w) * 32;
     each_live(s, blocks, u, i0, l.width,
-              [&](int q, int c, int rank) {
-                  const int at = begin[w * s.nb + c] + __popc(bits[w * s.nb + c] & ((1u << q) - 1));
-                  entries[at] = (uint32_t)(i0 + q);
-                  positions[(i0 + q) * l.ranks + rank] = (uint32_t)at * s.G + shift[c];
+              [&](int q, const int (&c)[4], const bool (&in)[4], int rank, int count) {
+                  uint32_t p[4];
+                  uint32_t* to = positions + (i0 + q) * l.ranks + rank;
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                      if (!in[j]) continue;
+                      const int at = begin[w * s.nb + c[j]] + __popc(bits[w * s.nb + c[j]] & ((1u << q) - 1));
+                      entries[at] = (uint32_t)(i0 + q);
+                      p[j] = (uint32_t)at * s.G + shift[c[j]];
+                  }
+                  if (count == 4 && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
+                      *reinterpret_cast<uint4*>(to) = make_uint4(p[0], p[1], p[2], p[3]);
+                  } else {
+#pragma unroll
+                      for (int j = 0; j < 4; ++j)
+                          if (in[j]) *to++ = p[j];
+                  }
               },
               [&](int q, int count) { l.live[u * s.n + i0 + q] = count; });
 }
