@@ -352,7 +352,7 @@ selected_join_kernel(const __grid_constant__ SelectedArgs a, const __grid_consta
     const int lane = threadIdx.x & 15;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    const uint32_t row = blockIdx.x * 16 + (threadIdx.x >> 4);
+    const uint32_t row = (gridDim.x - 1 - blockIdx.x) * 16 + (threadIdx.x >> 4);       // (the last tiles' partials are in the L2)
     if (row >= rows) return;
     const RowOf at = row_of(s, in.u0, row);
     const int count = l.live[in.u0 * s.n + at.entry];

@@ -346,7 +346,7 @@ selected_join_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     if (blockIdx.x >= row_blocks) return join_dkv(a, l, in, blockIdx.x - row_blocks);
-    const uint32_t row = blockIdx.x * 16 + (threadIdx.x >> 4);
+    const uint32_t row = (row_blocks - 1 - blockIdx.x) * 16 + (threadIdx.x >> 4);      // (the last tiles' partials are in the L2)
     if (row < rows) join_dq(a, l, in, row);
 }
 
