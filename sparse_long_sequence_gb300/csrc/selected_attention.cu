@@ -312,10 +312,8 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
             if (ptx::elect_one()) ptx::mma_commit(&bars[1]);
         }
         __syncwarp();
-        if (x == first) {
-            ptx::griddep_wait();
-            ptx::griddep_launch_dependents();
-        }
+        if (x == first) ptx::griddep_wait();              // (the joining kernel is let in by the end alone: its blocks, waiting
+                                                             // beside the last tiles, cost 60 us of 472 for 16 x 16384 queries)
         out.stat[(tile0 + x) * kTileRows + tid] = make_float2(top, sum);
         ptx::mbar_wait(&bars[1], phase, status);
         __syncwarp();

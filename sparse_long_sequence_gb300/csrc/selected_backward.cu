@@ -218,10 +218,7 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
             if (ptx::elect_one()) ptx::mma_commit(&bars[2]);
         }
         __syncwarp();
-        if (x == first) {
-            ptx::griddep_wait();
-            ptx::griddep_launch_dependents();
-        }
+        if (x == first) ptx::griddep_wait();              // (the joining kernel is let in by the end alone)
         ptx::mbar_wait(&bars[1], phase, status);
         __syncwarp();
         ptx::tc_fence_after();
