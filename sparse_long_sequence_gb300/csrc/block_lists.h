@@ -30,14 +30,23 @@ struct BlockLists {
 // Sizes, and the addresses in `ws` (null: sizes alone); returns the bytes.  `shares` is the caller's.
 size_t plan_block_lists(const SelectShape& s, char* ws, BlockLists* l);
 // Shares of a unit where `here` units have `resident` blocks of threads on each of 152 SMs: `rounds` times as
-// many as run at once, and a tile at least for each.  One round where the units have alike lengths; three
-// where they do not, and where a block of threads has 64 tiles or more, of which some take longer (16 x 16384
-// queries: 513 us for 535, the backward 819 for 835; 24 x 4096 queries, 15 tiles each: 134 for 128).
-constexpr int kUnlikeRounds = 3;
+// many as run at once, and a tile at least for each.
+constexpr int kMostRounds = 3;
 inline int32_t tile_shares(const SelectShape& s, const BlockLists& l, int64_t here, int resident, int rounds) {
     const int64_t at_once = 152 * resident / here, tiles = l.most_tiles;
     const int64_t shares = (at_once < 1 ? 1 : at_once) * rounds;
     return (int32_t)(shares < tiles ? shares : tiles < 1 ? 1 : tiles);
+}
+// Where the units have alike lengths one round is enough unless there are 64 tiles or more to a block of threads, of
+// which some take longer (16 x 16384 queries: 422 us with one round, 410 with three; 24 x 4096, 15 tiles each: 128 and
+// 134).  Units of unlike lengths have shares of unlike lengths, which more of them even out, and each has its
+// start (lengths from a quarter to all, 8 blocks a query: 2 x 12 units of 1024 queries, 4 tiles a block of threads,
+// 26 us with one round and 29 with two; of 4096, 17 tiles, 75 and 70, with three 74; 8 x 12 of 2048, 34 tiles, 144, 131
+// and 125; the backward of 4 x 12 of 4096, 50 tiles, 255, 228 and 228).
+inline int tile_rounds(const SelectShape& s, const BlockLists& l, int64_t here, int resident) {
+    const int64_t tiles = l.most_tiles * here / (152 * resident);
+    if (!s.lengths) return tiles < 64 ? 1 : kMostRounds;
+    return tiles < 8 ? 1 : tiles < 48 ? 2 : kMostRounds;
 }
 // The last kernel allows dependent launches.  `beside`: the launch before on the stream is the caller's own,
 // allows dependent launches and writes nothing that the lists are made of.

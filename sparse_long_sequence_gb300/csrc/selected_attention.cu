@@ -407,7 +407,7 @@ Plan plan_tiles(const SelectShape& s, char* ws) {
     p.group = groups < 1 ? units : groups < units ? (units + groups - 1) / groups : 1;
     p.stat = p.sums + p.group * p.lists.most_tiles * kSumsBytes;
     p.total = p.stat + p.group * p.lists.most_tiles * kTileRows * 8;
-    p.lists.shares = tile_shares(s, p.lists, p.group, kTileResident, s.lengths || p.lists.most_tiles * p.group >= 64 * 152 * kTileResident ? kUnlikeRounds : 1);
+    p.lists.shares = tile_shares(s, p.lists, p.group, kTileResident, tile_rounds(s, p.lists, p.group, kTileResident));
     return p;
 }
 

@@ -360,8 +360,8 @@ Plan plan_backward(const SelectShape& s, char* ws) {
     const int64_t groups = (units * dq + (int64_t)kGroupBytes - 1) / (int64_t)kGroupBytes;
     p.group = groups < 1 ? units : groups < units ? (units + groups - 1) / groups : 1;
     // (room for any lengths, which a size query does not know)
-    const int64_t most = tile_shares(s, p.lists, p.group, kResident, kUnlikeRounds);
-    p.lists.shares = tile_shares(s, p.lists, p.group, kResident, s.lengths || p.lists.most_tiles * p.group >= 64 * 152 * kResident ? kUnlikeRounds : 1);
+    const int64_t most = tile_shares(s, p.lists, p.group, kResident, kMostRounds);
+    p.lists.shares = tile_shares(s, p.lists, p.group, kResident, tile_rounds(s, p.lists, p.group, kResident));
     p.dkv = p.dq + p.group * dq;
     p.total = p.dkv + p.group * most * 2 * 2 * kBlockKeys * kHeadDim * 4;
     return p;
