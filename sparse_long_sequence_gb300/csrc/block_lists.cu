@@ -5,8 +5,10 @@
 // a bitmap of each key block in shared memory (atomic ors, whose order does not matter) and counts
 // the bits.  (2) One block of threads a unit turns the counts into places: a running sum over the
 // chunks for each key block, then over the key blocks.  (3) The bitmaps again:
-// a query's place in a list is the number of bits before its own.  Bound by the latency of a few
-// dependent loads; the lists' own bytes are a few percent of what the attention moves.
+// a query's place in a list is the number of bits before its own.  (1) and (2) are bound by the latency of a
+// few dependent loads, (3) by the scattered stores of the entries, 4 bytes each: 16 x 16384 queries of 16 blocks
+// take 10, 7 and 27 us.  (A thread that writes a block's entries in order, four a store, halves the
+// sectors and takes 64: the first blocks', which every query lists, are one thread's work.)
 #include <atomic>
 
 #include "block_lists.h"

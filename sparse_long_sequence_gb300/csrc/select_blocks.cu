@@ -14,6 +14,9 @@
 // Blocks more than 2 eps above the top-th value are in, those more than 2 eps below are out, and what
 // lies between is summed again as fp64 would, where 64 G products of bf16 values lose nothing that matters.
 // So the choice is that of exact scores, whatever order they are added in.
+//
+// For few queries bound by latency: 16 queries of up to 1024 blocks, 4 key heads with 4 heads each, take 12.4 us;
+// the search is a chain of reductions over one warp.
 #include <atomic>
 #include <cfloat>
 
@@ -313,7 +316,7 @@ int launch_select_blocks(const SelectShape& s, const void* Q, const void* means,
     Choice a{s, static_cast<const __nv_bfloat16*>(Q), static_cast<const __nv_bfloat16*>(means), sink, local, blocks, kMostQueries, 0};
     // whole loads of a warp, and 4 more floats: the lanes of a product's column fall in other banks
     a.stride = (s.nb + 127) / 128 * 128 + 4;
-    // Many queries have a thread each: 16 x 16384 queries of 256 blocks take 101 us there and 194 here, 32 x 4096 of
+    // Many queries have a thread each: 16 x 16384 queries of 256 blocks take 102 us there and 194 here, 32 x 4096 of
     // 64 blocks 30 and 77; but 4 x 4096 of 128 blocks, 4 heads a group, take 36 there and 23 here.
     if (s.top <= kTilesTop && s.n >= 64 && s.B * s.Hk * s.n >= 24576) return launch_select_tiles(a, stream);
     // fewer queries a block of threads where they are many key blocks', or where there are few of them for the SMs

@@ -1,7 +1,9 @@
 // Internal declarations of the attention over chosen key blocks: the means of key blocks
-// (block_means.cu), the choice of blocks (select_blocks.cu), the attention (selected_attention.cu)
-// and its backward pass (selected_backward.cu), the lists of queries that name a block
-// (block_lists.cu), and their entry points (selected_abi.cu).
+// (block_means.cu), the choice of blocks for few queries (select_blocks.cu) and for many
+// (select_tiles.cu; select_common.cuh has what both use), the attention (selected_attention.cu) and its
+// backward pass (selected_backward.cu) on warp tiles (mma_tiles.cuh) and on tiles of gathered rows
+// (row_tiles.cuh), the lists of queries that name a block (block_lists.cu), and their entry points
+// (selected_abi.cu).
 #pragma once
 
 #include <cuda_bf16.h>

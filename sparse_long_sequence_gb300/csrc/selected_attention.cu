@@ -5,14 +5,18 @@
 // Few queries: one block of threads for a query and up to eight heads of its group (the eight
 // columns of the products).  Its warps take the listed blocks in turn, each with a running maximum
 // and sum in registers, and join through shared memory.  A block's keys and values go from global
-// memory into the products' registers.  Bound by the cache's bytes, or by a launch.
+// memory into the products' registers.  Bound by the cache's bytes, or by a launch and the latency of two
+// dependent loads (16 tokens, 16 heads of 4 key heads, 16 blocks of a cache of up to 65536 keys: 7.4 us; the bytes 2.5).
 //
 // Many queries: block by block.  The rows (a query of a head) that list a key block (block_lists.cu) make
 // tiles of 128, and a block of four warps walks over a run of tiles: the rows' queries are gathered
 // into shared memory a tile ahead, S = Q K^T and O = P V run on tcgen05 with P handed over through tensor
 // memory, and each thread has one row's scores, maximum and sum, without exchanges.  Each (row, block)
 // leaves a partial result in the order of the tiles: 64 fp32 sums, its maximum and its sum; a second kernel
-// joins a row's partials.
+// joins a row's partials.  Bound by the partials' way to HBM and back: 256 bytes for 8192 multiplications and
+// additions of a row's scores and as many of its values.  16 x 16384 causal queries of 16 blocks: 410 us, of
+// which the lists take 43, the tiles 205 (1.07 GB out at 5.2 TB/s; without the partials 123) and the join 165
+// (6.5 TB/s).
 #include <atomic>
 
 #include "block_lists.h"
@@ -340,7 +344,7 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     if (warp == 0) ptx::tmem_dealloc(tmem, kTileColumns);
 }
 
-constexpr int kJoined = 4;                   // partials in flight (with 8 fewer warps fit an SM: 16 x 16384 queries 510 us, 492 with 4)
+constexpr int kJoined = 4;                   // partials in flight (16 x 16384 queries: 410 us, with 2 or 8 435 and 441)
 
 // Sixteen lanes join a row's partials.
 __global__ void __launch_bounds__(256)
@@ -442,8 +446,8 @@ int launch_tiles(const SelectedArgs& a, char* ws, cudaStream_t stream) {
 }
 
 // Few queries: what the lists, the partials and their joining would cost outweighs reading a block's
-// keys once for each query that lists it.  (4 heads, 16 blocks a query: 19.5 us by query and 25.6 by block for 128
-// queries, 37 and 27 for 256; 32 heads of 8 key heads, 4 blocks: 18.6 and 24.9 for 64, 34 and 28 for 128.)
+// keys once for each query that lists it.  (4 heads, 16 blocks a query: 20 us by query and 28 by block for 128
+// queries, 28.5 and 29 for 192, 37 and 29.5 for 256; 32 heads of 8 key heads, 4 blocks: 17 and 27 for 192.)
 bool by_query(const SelectShape& s) { return s.m == 0 || s.B * s.Hk * s.n * s.top <= 10240; }
 
 }  // namespace
