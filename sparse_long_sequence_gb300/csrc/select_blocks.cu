@@ -316,8 +316,8 @@ int launch_select_blocks(const SelectShape& s, const void* Q, const void* means,
     Choice a{s, static_cast<const __nv_bfloat16*>(Q), static_cast<const __nv_bfloat16*>(means), sink, local, blocks, kMostQueries, 0};
     // whole loads of a warp, and 4 more floats: the lanes of a product's column fall in other banks
     a.stride = (s.nb + 127) / 128 * 128 + 4;
-    // Many queries have a thread each: 16 x 16384 queries of 256 blocks take 102 us there and 194 here, 32 x 4096 of
-    // 64 blocks 30 and 77; but 4 x 4096 of 128 blocks, 4 heads a group, take 36 there and 23 here.
+    // Many queries have a thread each: 16 x 16384 queries of 256 blocks take 90 us there and 194 here, 32 x 4096 of
+    // 64 blocks 32 and 74, 24 x 1024 of 16 blocks 14 and 17; but 4 x 4096 of 64 blocks, 4 heads a group, 28 there and 18 here.
     if (s.top <= kTilesTop && s.n >= 64 && s.B * s.Hk * s.n >= 24576) return launch_select_tiles(a, stream);
     // fewer queries a block of threads where they are many key blocks', or where there are few of them for the SMs
     while (a.tile > 1 && ((int64_t)a.tile * a.stride * 4 > kMostSmem || a.tile / 2 >= s.n)) a.tile /= 2;

@@ -1,9 +1,9 @@
 // The choice of key blocks (select_blocks.cu says what is chosen and why the result is that of exact scores)
 // for many queries: a thread a query.
 //
-// A block of four warps takes 128 queries of a unit.  Their scores against 128 block means at a time are one
-// tcgen05 product (128 x 128, the group's heads one after the other along the summed index), and a query's scores
-// lie in its thread's lane of tensor memory.  The thread reads them twice: first for the maxima of 32 groups of
+// A block of four warps takes 128 queries of a unit.  Their scores against 128 block means at a time (the next
+// ones are on their way meanwhile) are one tcgen05 product (128 x 128, the group's heads one after the other along
+// the summed index), and a query's scores lie in its thread's lane of tensor memory.  The thread reads them twice: first for the maxima of 32 groups of
 // columns, whose want-th largest bounds the want-th largest score from below; then for the scores above that
 // bound, a few more than `want`, which it lists in shared memory.  Among those it finds the want-th largest.  Both
 // times 32 values are sorted in registers by a network (Batcher's odd-even merges: 191 comparisons, the same for
@@ -13,9 +13,9 @@
 // ones again as fp64 would; so it does, for all of a query's blocks, where a list stays full or a score is no
 // number.
 //
-// Bound by the issue of instructions and their latencies at 12 warps an SM (registers: 165 a thread): two passes
+// Bound by the issue of instructions and their latencies at 12 warps an SM (shared memory: 66 KB for four): two passes
 // over the scores and two sorts a query; the products alone would take a twentieth of the time.  16 x 16384 queries
-// of 256 blocks take 102 us, where a warp a query took 194: every step of its searches served one query.
+// of 256 blocks take 90 us, where a warp a query took 194: every step of its searches served one query.
 #include <atomic>
 #include <cfloat>
 
@@ -83,8 +83,9 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
     __shared__ unsigned largest;             // bits of the largest sum of a mean's squares
     const SelectShape& s = a.s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t parts = (uint32_t)(s.n + kTileRows - 1) / kTileRows, ul = blockIdx.x / parts;
-    const int64_t u = ul, i0 = (int64_t)(blockIdx.x - ul * parts) * kTileRows, b = sequence_of(s, u);
+    // every unit's last queries first, which see the most blocks where it is causal (90 us for 96 unit by unit)
+    const uint32_t parts = (uint32_t)(s.n + kTileRows - 1) / kTileRows, units = gridDim.x / parts, part = blockIdx.x / units;
+    const int64_t u = blockIdx.x - part * units, i0 = (int64_t)(parts - 1 - part) * kTileRows, b = sequence_of(s, u);
     const int queries = (int)min((int64_t)kTileRows, s.n - i0);
     const __nv_bfloat16* q0 = a.q + (u * s.G * s.n + i0) * kHeadDim;                   // head h: + h n 64
     const __nv_bfloat16* means = a.means + u * s.nb * kHeadDim;
@@ -120,17 +121,24 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
     uint32_t phase = 0;
     float mass = 0.f;                        // sum of q^2 over the group's heads
     unsigned top_squares = 0;                // of this thread's means
-    // The scores of round `round` into tensor memory; the first time through also mass and top_squares.
-    auto score_round = [&](int round, bool first) {
+    int held = -1;                           // the round whose means are there, or on their way
+    auto fetch = [&](int round) {
         const int c0 = round * kRound, rows = min(kRound, seen - c0);
+        held = round;
 #pragma unroll
         for (int x = tid; x < kRound * 8; x += kThreads) {
             const int r = x >> 3, c = x & 7;
             copy16(mean_tile + place(r, c), means + (int64_t)(c0 + (r < rows ? r : 0)) * kHeadDim + 8 * c, r < rows);
         }
+    };
+    // The scores of round `round` into tensor memory, then the means of round `next` (-1: none) on their way; the
+    // first time through also mass and top_squares.
+    auto score_round = [&](int round, int next, bool first) {
+        const bool begin = held < 0;
+        if (held != round) fetch(round);
         for (int h = 0; h < s.G; ++h) {
             if (h > 0) __syncthreads();      // all have read the last head's queries
-            if (s.G > 1 || (first && round == 0)) {
+            if (s.G > 1 || begin) {
 #pragma unroll
                 for (int x = tid; x < kTileRows * 8; x += kThreads) {
                     const int r = x >> 3, c = x & 7;
@@ -150,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
                 ptx::mma_commit(&bar);
             }
             __syncwarp();
-            if (first && round == 0) {
+            if (begin) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const uint4 w = *reinterpret_cast<const uint4*>(smem + place(tid, c));
@@ -172,6 +180,10 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
             __syncwarp();
         }
         ptx::tc_fence_after();
+        if (next >= 0 && next != round) {
+            __syncthreads();                 // all have read these means
+            fetch(next);
+        }
     };
     // columns c .. c + 31 of the round that begins with block c0; -infinity where the query sees no block, or it is forced
     auto scores = [&](int c0, int c, uint32_t (&v)[32]) {
@@ -195,12 +207,12 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
         float top[kMaxima];
 #pragma unroll
         for (int j = 0; j < kMaxima; ++j) top[j] = -INFINITY;
-        for (int round = 0; round < rounds; ++round) {
-            if (round) {
+        for (int round = rounds - 1; round >= 0; --round) {      // (the first one's scores stay)
+            if (round < rounds - 1) {
                 ptx::tc_fence_before();
                 __syncthreads();             // all have read the last scores
             }
-            score_round(round, true);
+            score_round(round, round ? round - 1 : min(1, rounds - 1), true);
             for (int c = 0; c < kRound && round * kRound + c < seen; c += 32) {
                 uint32_t v[32];
                 scores(round * kRound, c, v);
@@ -218,7 +230,6 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
     const float reach = reach_of(s.G, mass, __uint_as_float(largest)), eps = twice_eps(s.G, reach);
     const bool far = !(eps < 1e30f);
     float floor = choose && want && !far ? fmaxf(bound - eps, -FLT_MAX) : INFINITY;
-    if (rounds > 1) score_round(0, false);   // (all have read the last scores)
     const uint32_t list = mean_tile + kMeanBytes + 4 * tid, full = list + kList * kEntry;
     uint32_t end = list;
     int few;                                 // entries of the list
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
         if (++round < rounds) {
             ptx::tc_fence_before();
             __syncthreads();                 // all have read these scores
-            score_round(round, false);
+            score_round(round, round + 1 < rounds ? round + 1 : -1, false);
             continue;
         }
         few = (int)(end - list) / kEntry;
@@ -268,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
         if (!__syncthreads_or(again)) break;
         ++tries;
         round = 0;
-        if (rounds > 1) score_round(0, false);
+        if (rounds > 1) score_round(0, 1, false);
     }
     // (all have read the scores; the means' place is free for the results)
     __syncwarp();
