@@ -15,7 +15,7 @@
 // lies between is summed again as fp64 would, where 64 G products of bf16 values lose nothing that matters.
 // So the choice is that of exact scores, whatever order they are added in.
 //
-// For few queries bound by latency: 16 queries of up to 1024 blocks, 4 key heads with 4 heads each, take 12.4 us;
+// For few queries bound by latency: 16 queries of up to 1024 blocks, 4 key heads with 4 heads each, take 11.0 us;
 // the search is a chain of reductions over one warp.
 #include <atomic>
 #include <cfloat>
@@ -62,16 +62,26 @@ __device__ __forceinline__ bool narrow(const float* v, int nv, int want, float e
     }
     const float floor = fmaxf(lo - eps, -FLT_MAX);
     int few = 0;
-    for (int c = lane; c - lane < nv; c += 32) {
-        const float y = v[c];
-        const bool in = y >= floor;
-        const unsigned m = __ballot_sync(kFull, in);
-        const int place = few + __popc(m & ((1u << lane) - 1));
-        few += __popc(m);
-        if (few > kCandidates) return false;
-        if (in) {
-            cand_x[place] = y;
-            cand_c[place] = c;
+    for (int c0 = 0; c0 < nv; c0 += 128) {   // (a vote at a time took 1.4 us more of 12.4 for 1024 blocks)
+        float y[4];
+        unsigned m[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = c0 + 32 * j < nv ? v[c0 + 32 * j + lane] : -INFINITY;
+        int more = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            m[j] = __ballot_sync(kFull, y[j] >= floor);
+            more += __popc(m[j]);
+        }
+        if (few + more > kCandidates) return false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (y[j] >= floor) {
+                const int place = few + __popc(m[j] & ((1u << lane) - 1));
+                cand_x[place] = y[j];
+                cand_c[place] = c0 + 32 * j + lane;
+            }
+            few += __popc(m[j]);
         }
     }
     __syncwarp();
@@ -322,7 +332,7 @@ int launch_select_blocks(const SelectShape& s, const void* Q, const void* means,
     // fewer queries a block of threads where they are many key blocks', or where there are few of them for the SMs
     while (a.tile > 1 && ((int64_t)a.tile * a.stride * 4 > kMostSmem || a.tile / 2 >= s.n)) a.tile /= 2;
     while (a.tile > kWarps && s.B * s.Hk * ((s.n + a.tile - 1) / a.tile) < 2 * 152) a.tile /= 2;
-    // (16 queries of 1024 blocks, 4 heads a group: 15.9 us with 8 warps)
+    // (16 queries of 1024 blocks, 4 heads a group: 15.9 us with 8 warps, 11.0 with 32)
     const int per_warp = (s.nb + 31) / 32, warps = a.tile > 2 || per_warp <= kWarps ? kWarps : per_warp < kMostWarps ? per_warp : kMostWarps;
     const int64_t grid = s.B * s.Hk * ((s.n + a.tile - 1) / a.tile);
     if (grid > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
