@@ -202,6 +202,21 @@ def test_select_many_hard_scores(dl, kind, top, nb):
     test_select_hard_scores(dl, kind, top, n=12300, nb=nb)
 
 
+@pytest.mark.parametrize("order", ["crowded", "rising", "falling"])
+@pytest.mark.parametrize("top", [3, 12, 20])
+@pytest.mark.parametrize("n,nb,G", [(9, 150, 2), (9, 900, 1), (25000, 300, 2), (25000, 600, 1)])
+def test_select_uneven_scores(dl, order, top, n, nb, G):
+    """The best blocks in four of 32 places, so that their maxima bound the choice badly, or in rising or falling order, so
+    that the first to be looked at are the worst or the best of all."""
+    gen = torch.Generator().manual_seed(7)
+    Q, mean = normal(gen, 1, G, n, 64), normal(gen, 1, 1, nb, 64)
+    Q[..., 0] = 4.0
+    c = torch.arange(nb)
+    mean[..., 0] = {"crowded": (c % 32 < 4) * 16.0, "rising": c * 1.0, "falling": (nb - c) * 1.0}[order]
+    got = dl.diffuser_select_blocks(Q.cuda(), mean.cuda(), top, keys=nb * 64, sink_blocks=2, local_blocks=0, causal=False).cpu()
+    assert torch.equal(got, ref.select(Q, mean, top, nb * 64, 2, 0, False, None, None))
+
+
 # ---------------------------------------------------------------- attention
 def attend(dl, case, Q, K, V, blocks, **kw):
     B, Hq, Hk, n, m, top, sink, local, causal, lengths, starts = case
