@@ -3,7 +3,7 @@
 //
 // Sums launches.  (1) A block of threads sets, for a chunk of 32 to 256 queries, one bit a query in
 // a bitmap of each key block in shared memory (atomic ors, whose order does not matter) and counts
-// the bits.  (2) One block of threads a unit turns the counts into places: a running sum over the
+// the bits.  (2) One block of threads a unit (or several, and one after them) turns the counts into places: a running sum over the
 // chunks for each key block, then over the key blocks.  (3) The bitmaps again:
 // a query's place in a list is the number of bits before its own.  (1) and (2) are bound by the latency of a
 // few dependent loads, (3) by the scattered stores of the entries, 4 bytes each: 16 x 16384 queries of 16 blocks
@@ -21,6 +21,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kScanThreads = 1024;
 constexpr int kScanBlocks = 256;             // key blocks that the scan takes at a time, by four runs of chunks
+constexpr int kPartBlocks = 64;              // a block of threads', where there are more of both
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBitmapBytes = 64 * 1024;
 
@@ -117,7 +118,8 @@ struct Sums {
 };
 __device__ __forceinline__ Sums operator+(Sums a, Sums b) { return {a.entries + b.entries, a.tiles + b.tiles}; }
 
-// Sums over the first kScanBlocks threads: of those before this one, and (in *all) of all.
+// Sums over the first kWarps warps: of the threads before this one, and (in *all) of all.
+template <int kWarps>
 __device__ __forceinline__ Sums before_and_all(Sums x, Sums* sums, Sums* all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Sums run = x;
@@ -129,7 +131,7 @@ __device__ __forceinline__ Sums before_and_all(Sums x, Sums* sums, Sums* all) {
     if (lane == 31) sums[warp] = run;
     __syncthreads();
     Sums before = {run.entries - x.entries, run.tiles - x.tiles}, total = {0, 0};
-    for (int w = 0; w < kScanBlocks / 32; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         if (w == warp) before = before + total;
         total = total + sums[w];
     }
@@ -138,48 +140,64 @@ __device__ __forceinline__ Sums before_and_all(Sums x, Sums* sums, Sums* all) {
     return before;
 }
 
+// Counts of a unit's blocks c0 .. c0 + kBlocks - 1 into running sums over the chunks; returns the sum over all (to each
+// run's thread of a block).
+template <int kBlocks>
+__device__ __forceinline__ int sum_chunks(const SelectShape& s, const BlockLists& l, int32_t* counts, int c0,
+                                          int32_t (*runs)[kBlocks]) {
+    constexpr int kRuns = kScanThreads / kBlocks;
+    const int run = threadIdx.x / kBlocks, x = threadIdx.x % kBlocks, c = c0 + x, per = (l.chunks + kRuns - 1) / kRuns;
+    const int k0 = min(run * per, l.chunks), k1 = min(k0 + per, l.chunks);
+    int n = 0;
+    if (c < s.nb) {
+#pragma unroll 16
+        for (int k = k0; k < k1; ++k) n += counts[(int64_t)k * s.nb + c];
+    }
+    runs[run][x] = n;
+    __syncthreads();
+    n = 0;
+    int mine = 0;
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) {
+        if (r == run) mine = n;
+        n += runs[r][x];
+    }
+    if (c < s.nb) {
+#pragma unroll 16
+        for (int k = k0; k < k1; ++k) {
+            const int32_t y = counts[(int64_t)k * s.nb + c];
+            counts[(int64_t)k * s.nb + c] = mine;
+            mine += y;
+        }
+    }
+    return n;
+}
+
+// Where the blocks' entries and tiles begin.  kWhole: a block of threads has all of a unit, and sums its chunks too;
+// else base[c] has the number of block c's entries.
+template <bool kWhole>
 __global__ void __launch_bounds__(kScanThreads)
 place_lists_kernel(const __grid_constant__ SelectShape s, const __grid_constant__ BlockLists l) {
-    constexpr int kRuns = kScanThreads / kScanBlocks;
     __shared__ Sums sums[kScanThreads / 32];
-    __shared__ int32_t runs[kRuns][kScanBlocks];
+    __shared__ int32_t runs[kScanThreads / kScanBlocks][kScanBlocks];
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const int64_t u = blockIdx.x;
     int32_t* counts = l.counts + u * l.chunks * s.nb;
     int32_t *base = l.base + u * (s.nb + 1), *tile_base = l.tile_base + u * (s.nb + 1);
-    const int run = threadIdx.x / kScanBlocks, per = (l.chunks + kRuns - 1) / kRuns;
-    const int k0 = min(run * per, l.chunks), k1 = min(k0 + per, l.chunks);
+    constexpr int kStep = kWhole ? kScanBlocks : kScanThreads;
     Sums done = {0, 0};
-    for (int c0 = 0; c0 < s.nb; c0 += kScanBlocks) {
-        const int c = c0 + threadIdx.x % kScanBlocks;
-        int n = 0;
-        if (c < s.nb) {
-#pragma unroll 16
-            for (int k = k0; k < k1; ++k) n += counts[(int64_t)k * s.nb + c];
-        }
-        runs[run][threadIdx.x % kScanBlocks] = n;
-        __syncthreads();
-        n = 0;
-        int mine = 0;
-#pragma unroll
-        for (int r = 0; r < kRuns; ++r) {
-            if (r == run) mine = n;
-            n += runs[r][threadIdx.x % kScanBlocks];
-        }
-        if (c < s.nb) {
-#pragma unroll 16
-            for (int k = k0; k < k1; ++k) {
-                const int32_t x = counts[(int64_t)k * s.nb + c];
-                counts[(int64_t)k * s.nb + c] = mine;
-                mine += x;
-            }
-        }
-        if (run || c >= s.nb) n = 0;         // (the first run's threads sum over the blocks)
+    for (int c0 = 0; c0 < s.nb; c0 += kStep) {
+        const int c = c0 + threadIdx.x;
+        int n;
+        if (kWhole) n = sum_chunks<kScanBlocks>(s, l, counts, c0, runs);
+        else n = c < s.nb ? base[c] : 0;
+        const bool on = threadIdx.x < kStep && c < s.nb;     // (the first run's threads sum over the blocks)
+        if (!on) n = 0;
         const int tiles = (int)(((int64_t)n * s.G + kTileRows - 1) / kTileRows);
         Sums all;
-        const Sums before = done + before_and_all({n, tiles}, sums, &all);
-        if (run == 0 && c < s.nb) {
+        const Sums before = done + before_and_all<kStep / 32>({n, tiles}, sums, &all);
+        if (on) {
             base[c] = before.entries;
             tile_base[c] = before.tiles;
         }
@@ -189,6 +207,18 @@ place_lists_kernel(const __grid_constant__ SelectShape s, const __grid_constant_
         base[s.nb] = done.entries;
         tile_base[s.nb] = done.tiles;
     }
+}
+
+// The chunks' sums of kPartBlocks blocks a block of threads.
+__global__ void __launch_bounds__(kScanThreads)
+sum_lists_kernel(const __grid_constant__ SelectShape s, const __grid_constant__ BlockLists l, int parts) {
+    __shared__ int32_t runs[kScanThreads / kPartBlocks][kPartBlocks];
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    const int64_t u = blockIdx.x / (uint32_t)parts;
+    const int c0 = (blockIdx.x - (uint32_t)u * parts) * kPartBlocks, c = c0 + threadIdx.x;
+    const int n = sum_chunks<kPartBlocks>(s, l, l.counts + u * l.chunks * s.nb, c0, runs);
+    if (threadIdx.x < kPartBlocks && c < s.nb) l.base[u * (s.nb + 1) + c] = n;
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -285,7 +315,19 @@ int launch_block_lists(const SelectShape& s, const int32_t* blocks, const BlockL
     }
     if (err == cudaSuccess) {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        err = launch_pdl(place_lists_kernel, dim3((unsigned)units), dim3(kScanThreads), 0, stream, s, l);
+        // A unit of more blocks than that is shared out, where its chunks are many too (1 x 2^20 queries: 156 ms
+        // for the attention with one block of threads a unit).
+        if (s.nb <= kScanBlocks || l.chunks < 16) {
+            err = launch_pdl(place_lists_kernel<true>, dim3((unsigned)units), dim3(kScanThreads), 0, stream, s, l);
+        } else {
+            const int parts = (s.nb + kPartBlocks - 1) / kPartBlocks;
+            if (units * parts > INT32_MAX) return fail(DIFFUSER_ERR_OVERFLOW, "too many queries");
+            err = launch_pdl(sum_lists_kernel, dim3((unsigned)(units * parts)), dim3(kScanThreads), 0, stream, s, l, parts);
+            if (err == cudaSuccess) {
+                LaunchScope second(DIFFUSER_KERNEL_AUX, stream);
+                err = launch_pdl(place_lists_kernel<false>, dim3((unsigned)units), dim3(kScanThreads), 0, stream, s, l);
+            }
+        }
     }
     if (err == cudaSuccess) {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);

@@ -303,6 +303,12 @@ def test_attention_of_many_queries(dl, case):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("case", [(1, 1, 1, 3900, 17000, 6, 1, 1, True, [16900], None), (1, 1, 1, 4100, 16450, 3, 0, 1, False, None, None)])
+def test_attention_of_many_queries_and_blocks(dl, case):
+    """More key blocks than one block of threads sums up at a time, and as many chunks of queries."""
+    test_attention_of_many_queries(dl, case)
+
+
 @pytest.mark.parametrize("case", CASES)
 def test_backward(dl, case):
     B, Hq, Hk, n, m, top, sink, local, causal, lengths, starts = case
