@@ -88,8 +88,8 @@ __device__ __forceinline__ void set_bits(const SelectShape& s, const int32_t* bl
                                          int64_t chunk, uint32_t* bits) {
     for (int x = threadIdx.x; x < s.nb * l.words; x += blockDim.x) bits[x] = 0;
     __syncthreads();
-    const int w = threadIdx.x >> 5;          // a warp a word
-    each_live(s, blocks, u, (chunk * l.words + w) * 32, l.width,
+    const int w = threadIdx.x >> 5;          // a warp a word (the others have no queries)
+    each_live(s, blocks, u, w < l.words ? (chunk * l.words + w) * 32 : s.n, l.width,
               [&](int q, const int (&c)[4], const bool (&in)[4], int, int) {
 #pragma unroll
                   for (int j = 0; j < 4; ++j)
@@ -243,7 +243,7 @@ fill_lists_kernel(const __grid_constant__ SelectShape s, const int32_t* blocks, 
     uint32_t* entries = l.entries + u * s.n * l.ranks;
     uint32_t* positions = l.positions + u * s.n * l.ranks;
     const int w = threadIdx.x >> 5;
-    const int64_t i0 = ((int64_t)chunk * l.words + w) * 32;
+    const int64_t i0 = w < l.words ? ((int64_t)chunk * l.words + w) * 32 : s.n;
     each_live(s, blocks, u, i0, l.width,
               [&](int q, const int (&c)[4], const bool (&in)[4], int rank, int count) {
                   uint32_t p[4];
@@ -303,20 +303,19 @@ int launch_block_lists(const SelectShape& s, const int32_t* blocks, const BlockL
     if (err == cudaSuccess) err = allow_smem(fill_lists_kernel, 3 * kBitmapBytes, fill_ready);
     if (err != cudaSuccess) return cuda_fail(err, "the block lists");
     const size_t smem = (size_t)s.nb * l.words * 4;
-    const int threads = 32 * l.words;
     {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
         if (beside) {
-            err = launch_pdl(count_lists_kernel, dim3((unsigned)grid), dim3(threads), smem, stream, s, blocks, l);
+            err = launch_pdl(count_lists_kernel, dim3((unsigned)grid), dim3(kThreads), smem, stream, s, blocks, l);
         } else {
-            count_lists_kernel<<<(unsigned)grid, threads, smem, stream>>>(s, blocks, l);
+            count_lists_kernel<<<(unsigned)grid, kThreads, smem, stream>>>(s, blocks, l);
             err = cudaGetLastError();
         }
     }
     if (err == cudaSuccess) {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        // A unit of more blocks than that is shared out, where its chunks are many too (1 x 2^20 queries: 156 ms
-        // for the attention with one block of threads a unit).
+        // A unit of more blocks than that is shared out, where its chunks are many too (2 x 262144 queries: 2.95 ms
+        // for the attention with one block of threads a unit, 1.65 so).
         if (s.nb <= kScanBlocks || l.chunks < 16) {
             err = launch_pdl(place_lists_kernel<true>, dim3((unsigned)units), dim3(kScanThreads), 0, stream, s, l);
         } else {
@@ -331,7 +330,7 @@ int launch_block_lists(const SelectShape& s, const int32_t* blocks, const BlockL
     }
     if (err == cudaSuccess) {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        err = launch_pdl(fill_lists_kernel, dim3((unsigned)grid), dim3(threads), 2 * smem + (size_t)s.nb * 4, stream, s, blocks, l);
+        err = launch_pdl(fill_lists_kernel, dim3((unsigned)grid), dim3(kThreads), 2 * smem + (size_t)s.nb * 4, stream, s, blocks, l);
     }
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "the block lists");
 }
