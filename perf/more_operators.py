@@ -348,7 +348,7 @@ def _by_unit(c, x):
 
 
 def _by_head(c, x):
-    return x.view(c["B"], c["Hk"], c["n"], c["Hq"] // c["Hk"], -1).transpose(2, 3).reshape(c["B"], c["Hq"], c["n"], -1).contiguous()
+    return x.view(c["B"], c["Hk"], c["n"], c["Hq"] // c["Hk"], -1).transpose(2, 3).reshape(c["B"], c["Hq"], c["n"], -1)
 
 
 def _attend_plain(s):
