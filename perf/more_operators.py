@@ -401,9 +401,9 @@ def _run_own(s):
                                           local_blocks=c["local"], causal=c["causal"], lengths=s["len"],
                                           starts=s["start"])]
     how = dict(causal=c["causal"], lengths=s["len"], starts=s["start"])
-    if c["backward"]:
-        return list(dl.diffuser_selected_attention_backward(s["q"], s["k"], s["v"], s["blocks"], s["out"], s["lse"],
-                                                            s["dout"], **how))
+    if c["backward"]:                              # (the call takes contiguous tensors; the plain forward may keep a view)
+        return list(dl.diffuser_selected_attention_backward(s["q"], s["k"], s["v"], s["blocks"], s["out"].contiguous(),
+                                                            s["lse"], s["dout"], **how))
     out = dl.diffuser_selected_attention(s["q"], s["k"], s["v"], s["blocks"], save_lse=c["save"], **how)
     return list(out) if c["save"] else [out]
 
