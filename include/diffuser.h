@@ -617,8 +617,8 @@ DIFFUSER_API int diffuser_select_blocks(const void* Q, const void* means, int64_
  * blocks that query i lists; a query without such keys: out 0, lse -infinity.
  *   blocks   int32 [B][Hk][n][top_k], any values: an entry counts if it is above every entry before
  *            it, is not negative and has visible keys; others are skipped
- *   out      bf16 [B][Hq][n][64], rounded once from fp32 (the weights are rounded to bf16 as operands
- *            of the tensor cores; their sum is taken before that)
+ *   out      bf16 [B][Hq][n][64], rounded once from fp32 (the weights, operands of the tensor cores, are
+ *            pairs of bf16 values there, within 2^-15 of themselves; their sum is taken before that)
  *   lse      fp32 [B][Hq][n] or NULL: log of the sum of exp(q_i.k_j / sqrt(d)), for the backward
  *   workspace   diffuser_selected_attention_workspace_size bytes, 256-byte aligned (0: NULL will do)
  * Keys and values behind a length, and those of blocks that no query lists, are not read.  An infinity or

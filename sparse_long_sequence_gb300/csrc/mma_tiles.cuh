@@ -39,6 +39,16 @@ __device__ __forceinline__ uint32_t pack(float x, float y) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Two weights as pairs of bf16 values, high + low, so that the products lose 2^-16 of a weight and not 2^-8.  The high
+// ones are cut, not rounded, and 2^-22 of the weight goes on top: the low ones are above 0 wherever the weight is, and
+// an infinite value times both stays infinite.
+__device__ __forceinline__ void split_weights(float x, float y, uint32_t* high, uint32_t* low) {
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    constexpr float kUp = 1.f + 2.384185791015625e-7f;
+    *high = __byte_perm(a, b, 0x7632);
+    *low = pack(fmaf(x, kUp, -__uint_as_float(a & 0xffff0000u)), fmaf(y, kUp, -__uint_as_float(b & 0xffff0000u)));
+}
+
 // This lane's words of a row; zeros where the row is not to be read.
 __device__ __forceinline__ void load_row(const __nv_bfloat16* row, bool live, int t, uint32_t (&w)[8]) {
     uint4 a = make_uint4(0, 0, 0, 0), b = a;
@@ -81,10 +91,16 @@ __device__ __forceinline__ void score(const uint32_t (&k)[8][8], const uint32_t 
 __device__ __forceinline__ void weigh(const uint32_t (&v)[8][8], const float (&p)[4][4], float (&o)[4][4]) {
 #pragma unroll
     for (int M = 0; M < 4; ++M) {
-        const uint32_t b0 = transposed(pack(p[M][0], p[M][1])), b1 = transposed(pack(p[M][2], p[M][3]));
+        uint32_t w[2][2];                    // high and low, of keys 16 M + g and 16 M + 8 + g
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            mma(o[j], v[2 * M][2 * j], v[2 * M][2 * j + 1], v[2 * M + 1][2 * j], v[2 * M + 1][2 * j + 1], b0, b1);
+        for (int e = 0; e < 2; ++e) split_weights(p[M][2 * e], p[M][2 * e + 1], &w[0][e], &w[1][e]);
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+            const uint32_t b0 = transposed(w[part][0]), b1 = transposed(w[part][1]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                mma(o[j], v[2 * M][2 * j], v[2 * M][2 * j + 1], v[2 * M + 1][2 * j], v[2 * M + 1][2 * j + 1], b0, b1);
+        }
     }
 }
 __host__ __device__ __forceinline__ constexpr int feature_of(int c, int g) {

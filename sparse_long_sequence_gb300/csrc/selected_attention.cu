@@ -6,17 +6,18 @@
 // columns of the products).  Its warps take the listed blocks in turn, each with a running maximum
 // and sum in registers, and join through shared memory.  A block's keys and values go from global
 // memory into the products' registers.  Bound by the cache's bytes, or by a launch and the latency of two
-// dependent loads (16 tokens, 16 heads of 4 key heads, 16 blocks of a cache of up to 65536 keys: 7.4 us; the bytes 2.5).
+// dependent loads (16 tokens, 16 heads of 4 key heads, 16 blocks of a cache of up to 65536 keys: 7.3 us; the bytes 2.5).
 //
 // Many queries: block by block.  The rows (a query of a head) that list a key block (block_lists.cu) make
 // tiles of 128, and a block of four warps walks over a run of tiles: the rows' queries are gathered
 // into shared memory a tile ahead, S = Q K^T and O = P V run on tcgen05 with P handed over through tensor
-// memory, and each thread has one row's scores, maximum and sum, without exchanges.  Each (row, block)
+// memory in S's place (as two bf16 parts, mma_tiles.cuh: rounded to one it costs 2.2e-3 of the result in the 2-norm for
+// the 1.7e-3 of its own rounding, and saves 11 us of 421), and each thread has one row's scores, maximum and sum,
+// without exchanges.  Each (row, block)
 // leaves a partial result in the order of the tiles: 64 fp32 sums, its maximum and its sum; a second kernel
 // joins a row's partials.  Bound by the partials' way to HBM and back: 256 bytes for 8192 multiplications and
-// additions of a row's scores and as many of its values.  16 x 16384 causal queries of 16 blocks: 410 us, of
-// which the lists take 43, the tiles 205 (1.07 GB out at 5.2 TB/s; without the partials 123) and the join 165
-// (6.5 TB/s).
+// additions of a row's scores and as many of its values.  16 x 16384 causal queries of 16 blocks: 421 us, of
+// which the lists take 43, the tiles 216 (1.07 GB out at 5.0 TB/s) and the join 165 (6.5 TB/s).
 #include <atomic>
 
 #include "block_lists.h"
@@ -292,19 +293,20 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         top *= kScale2;
         const float base = top == -INFINITY ? 0.f : top;
         float sum = 0.f;
-        uint32_t p[2][16];
+        auto weights = [&](const uint32_t (&x)[32], uint32_t to) {   // to columns `to` .., and what their rounding leaves to 32 on
+            uint32_t high[16], low[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float w0 = exp2_fast(fmaf(__uint_as_float(lo[2 * j]), kScale2, -base));
-            const float w1 = exp2_fast(fmaf(__uint_as_float(lo[2 * j + 1]), kScale2, -base));
-            const float w2 = exp2_fast(fmaf(__uint_as_float(hi[2 * j]), kScale2, -base));
-            const float w3 = exp2_fast(fmaf(__uint_as_float(hi[2 * j + 1]), kScale2, -base));
-            sum += (w0 + w1) + (w2 + w3);
-            p[0][j] = pack(w0, w1);
-            p[1][j] = pack(w2, w3);
-        }
-        __syncwarp();
-        ptx::tmem_st16x2(mine, p[0], mine + 16, p[1]);
+            for (int j = 0; j < 16; ++j) {
+                const float w0 = exp2_fast(fmaf(__uint_as_float(x[2 * j]), kScale2, -base));
+                const float w1 = exp2_fast(fmaf(__uint_as_float(x[2 * j + 1]), kScale2, -base));
+                sum += w0 + w1;
+                split_weights(w0, w1, &high[j], &low[j]);
+            }
+            __syncwarp();
+            ptx::tmem_st16x2(to, high, to + 32, low);
+        };
+        weights(lo, mine);
+        weights(hi, mine + 16);
         ptx::tc_fence_before();
         __syncthreads();                     // P is whole
         if (warp == 0) {
@@ -312,7 +314,8 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
             ptx::tc_fence_after();
             const uint64_t vd = ptx::sw128_mnmajor_desc(values_now, kKeyBytes);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) if (ptx::elect_one()) ptx::mma_bf16_ts(tmem + 64, tmem + 8 * e, vd + 128 * e, kSums, e > 0);
+            for (int e = 0; e < 8; ++e)      // (the weights' high parts, then their low ones)
+                if (ptx::elect_one()) ptx::mma_bf16_ts(tmem + 64, tmem + 8 * e, vd + 128 * (e & 3), kSums, e > 0);
             if (ptx::elect_one()) ptx::mma_commit(&bars[1]);
         }
         __syncwarp();

@@ -1,0 +1,56 @@
+"""The rotation alone and the attention over chosen key blocks at the limits of what they promise,
+against their definitions in 64 bits."""
+import math
+
+import pytest
+import torch
+
+from tests import selected_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+U = 2.0 ** -8                                                # half a bf16 step
+
+
+@pytest.fixture(scope="module")
+def dl():
+    from sparse_long_sequence_gb300 import binding
+    return binding
+
+
+# ---------------------------------------------------------------- the weights of the attention
+@pytest.mark.parametrize("B,Hq,Hk,n,m,top,causal,few", [
+    (2, 8, 2, 3, 600, 5, True, True), (1, 16, 1, 1, 900, 9, False, True), (3, 2, 2, 40, 40, 3, True, True),
+    (1, 4, 2, 1500, 1500, 6, True, False), (2, 3, 1, 1100, 1200, 7, False, False)])
+def test_weights_keep_more_than_an_operands_bits(dl, B, Hq, Hk, n, m, top, causal, few):
+    """Scores that fp32 sums hold exactly, so that the weights' own error shows."""
+    gen = torch.Generator().manual_seed(1)
+    Q = torch.randint(-2, 3, (B, Hq, n, 64), generator=gen).to(BF)
+    K = (torch.randint(-2, 3, (B, Hk, m, 64), generator=gen) * 0.25).to(BF)
+    V = torch.randn((B, Hk, m, 64), generator=gen).to(BF)
+    mean = ref.means(K, None, torch.zeros((B, Hk, -(-m // 64), 64)), 0).to(BF)
+    blocks = ref.select(Q, mean, top, m, 0, 1, causal, None, None)
+    assert (dl.diffuser_selected_attention_workspace_size(B, Hq, Hk, n, m, top) == 0) == few
+    out = dl.diffuser_selected_attention(Q.cuda(), K.cuda(), V.cuda(), blocks.cuda(), causal=causal)
+    want, _, mass = ref.attend(Q, K, V, ref.mask(blocks, n, m, causal, None, None))
+    # of a weight: its low part, below 2^-7 of it, is rounded by 2^-8 of itself, 2^-15; 2^-22 on top of it; the
+    # exponential and its argument below 2^-18.  Of the sums: eight products of 16 terms with 17 2^-23 each, and the
+    # joining below 2^-20.  Together 5.2e-5, below 2^-14; and the result's rounding
+    assert ((out.double().cpu() - want).abs() <= U * want.abs() + 2.0 ** -14 * mass).all()
+
+
+def test_an_infinite_value_stays_one(dl):
+    """Rows that see one infinite value have it in their results, with its sign."""
+    gen = torch.Generator().manual_seed(2)
+    for n in (4, 800):
+        Q, K, V = (torch.randn((1, 2, x, 64), generator=gen).to(BF) for x in (n, 640, 640))
+        blocks = torch.arange(10, dtype=torch.int32).expand(1, 2, n, 10).contiguous()
+        V[0, 0, 5, 7], V[0, 1, 600, 63] = math.inf, -math.inf
+        few = dl.diffuser_selected_attention_workspace_size(1, 2, 2, n, 640, 10) == 0
+        assert few == (n == 4)
+        out = dl.diffuser_selected_attention(Q.cuda(), K.cuda(), V.cuda(), blocks.cuda(), causal=False).cpu()
+        want = torch.zeros_like(out)
+        some = slice(max(0, n - 640), n)                     # (more queries than keys: the first ones see none)
+        want[0, 0, some, 7], want[0, 1, some, 63] = math.inf, -math.inf
+        assert torch.equal(torch.where(out.isinf(), out, 0.0), want) and not out.isnan().any()
