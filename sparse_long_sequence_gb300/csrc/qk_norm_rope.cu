@@ -51,10 +51,20 @@ template <> struct Io<float> {
         v[0] = f2(r.a.x, r.a.y); v[1] = f2(r.a.z, r.a.w);
         v[2] = f2(r.b.x, r.b.y); v[3] = f2(r.b.z, r.b.w);
     }
-    static __device__ __forceinline__ void store(float* row, int oa, int ob, const F2 (&v)[4]) {
+    static __device__ __forceinline__ Raw narrow(const F2 (&v)[4]) {
         const float2 p = un(v[0]), q = un(v[1]), s = un(v[2]), t = un(v[3]);
-        *reinterpret_cast<float4*>(row + oa) = make_float4(p.x, p.y, q.x, q.y);
-        *reinterpret_cast<float4*>(row + ob) = make_float4(s.x, s.y, t.x, t.y);
+        return {make_float4(p.x, p.y, q.x, q.y), make_float4(s.x, s.y, t.x, t.y)};
+    }
+    // the values of v, or those of `kept`
+    static __device__ __forceinline__ Raw either(bool first, const F2 (&v)[4], const F2 (&kept)[4]) {
+        F2 w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = first ? v[j] : kept[j];
+        return narrow(w);
+    }
+    static __device__ __forceinline__ void store(float* row, int oa, int ob, const Raw& r) {
+        *reinterpret_cast<float4*>(row + oa) = r.a;
+        *reinterpret_cast<float4*>(row + ob) = r.b;
     }
     static __device__ __forceinline__ float round(float x) { return x; }
 };
@@ -72,9 +82,23 @@ template <> struct Io<__nv_bfloat16> {
         const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16* row, int oa, int ob, const F2 (&v)[4]) {
-        *reinterpret_cast<uint2*>(row + oa) = make_uint2(pack(v[0]), pack(v[1]));
-        *reinterpret_cast<uint2*>(row + ob) = make_uint2(pack(v[2]), pack(v[3]));
+    static __device__ __forceinline__ Raw narrow(const F2 (&v)[4]) {
+        return {make_uint2(pack(v[0]), pack(v[1])), make_uint2(pack(v[2]), pack(v[3]))};
+    }
+    // the values of v rounded, or those of `kept`, which are as they were loaded (the loaded words themselves, kept
+    // beside the next ones: 25 us for 20 on the long case)
+    static __device__ __forceinline__ Raw either(bool first, const F2 (&v)[4], const F2 (&kept)[4]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = un(kept[j]);
+            w[j] = first ? pack(v[j]) : __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+        }
+        return {make_uint2(w[0], w[1]), make_uint2(w[2], w[3])};
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* row, int oa, int ob, const Raw& r) {
+        *reinterpret_cast<uint2*>(row + oa) = r.a;
+        *reinterpret_cast<uint2*>(row + ob) = r.b;
     }
     static __device__ __forceinline__ __nv_bfloat16 round(float x) { return __float2bfloat16_rn(x); }
 };
@@ -259,7 +283,7 @@ __global__ void __launch_bounds__(kThreads) qk_forward_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = mul(mul(v[j], r), wt[j]);
             turn.apply(v);
-            if (s.live) Io<T>::store(dst + u * step, oa, ob, v);
+            if (s.live) Io<T>::store(dst + u * step, oa, ob, Io<T>::narrow(v));
         }
     }
 }
@@ -319,7 +343,7 @@ __global__ void __launch_bounds__(kThreads) qk_backward_kernel(const __grid_cons
                     dn[j] = mul(fma(x[j], m, dn[j]), r2);
                     if (s.live) acc[j] = fma(g[j], mul(x[j], r2), acc[j]);
                 }
-                if (s.live) Io<T>::store(d_row, oa, ob, dn);
+                if (s.live) Io<T>::store(d_row, oa, ob, Io<T>::narrow(dn));
                 x_row += step;
                 g_row += step;
                 d_row += step;
@@ -375,9 +399,10 @@ qk_weight_kernel(const float* partial, int q_blocks, int k_blocks, T* dwq, T* dw
 
 // The rotation alone: y = magnitude R(p) x on the turned features, the others as they are; kSign -1
 // turns back (the gradient).  The same rows, lanes and runs as above without the norm's sum: HBM alone
-// bounds it (16 + 16 heads x 16384 tokens in bf16: 20.6 us, 6.5 TB/s).
+// bounds it (16 + 16 heads x 16384 tokens in bf16: 20.8 us, 6.5 TB/s; neighbouring pairs 21.0, and 22.9 where two
+// registers too many leave three blocks an SM; fp32 needs none held to it: 42 us so, 53 with four blocks).
 template <class T, bool kInterleaved, int kSign>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ QkArgs a, const Work w) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 1) rope_kernel(const __grid_constant__ QkArgs a, const Work w) {
     const int lane = threadIdx.x & 31;
     int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (unit >= w.q_units + w.k_units) return;
@@ -395,16 +420,20 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         if (s.h0 + u < s.h1) raw[u] = Io<T>::load(src + u * step, oa, ob);
     Turn<kInterleaved> turn;
     turn.template set<kSign>(a, s.pos, lane);
-    turn.scale((lane & (kRowLanes - 1)) < a.rot / 8 ? a.magnitude : 1.f);
+    turn.scale(a.magnitude);
+    // the other lanes' features are copied as bits: 0 times an infinity would be NaN
+    const bool turned = (lane & (kRowLanes - 1)) < a.rot / 8;
     for (int h = s.h0; h < s.h1; h += kAhead, src += kAhead * step, dst += kAhead * step) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (h + u >= s.h1) break;
-            F2 v[4];
+            F2 v[4], kept[4];
             Io<T>::widen(raw[u], v);
             if (h + u + kAhead < s.h1) raw[u] = Io<T>::load(src + (u + kAhead) * step, oa, ob);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) kept[j] = v[j];
             turn.apply(v);
-            if (s.live) Io<T>::store(dst + u * step, oa, ob, v);
+            if (s.live) Io<T>::store(dst + u * step, oa, ob, Io<T>::either(turned, v, kept));
         }
     }
 }

@@ -54,3 +54,33 @@ def test_an_infinite_value_stays_one(dl):
         some = slice(max(0, n - 640), n)                     # (more queries than keys: the first ones see none)
         want[0, 0, some, 7], want[0, 1, some, 63] = math.inf, -math.inf
         assert torch.equal(torch.where(out.isinf(), out, 0.0), want) and not out.isnan().any()
+
+
+# ---------------------------------------------------------------- the rotation
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rot", [16, 32, 48])
+@pytest.mark.parametrize("inter", [False, True])
+def test_features_that_are_not_turned_are_copied(dl, dtype, rot, inter):
+    """Bit by bit, whatever they are, and nothing of them reaches the others."""
+    gen = torch.Generator().manual_seed(3)
+    word = torch.int16 if dtype == BF else torch.int32
+    q, k = (torch.randn((2, h, 37, 64), generator=gen).to(dtype) for h in (3, 1))
+    freq, mag = dl.diffuser_rope_frequencies(rot, 10000.0, dl.DIFFUSER_ROPE_YARN, 4.0, 4096)
+    top = 0x7f80 << (0 if dtype == BF else 16)               # infinity's bits; above them NaN
+    sign = -(1 << (15 if dtype == BF else 31))
+    odd = torch.tensor([top, top + sign, top + 1, top + 3, 1, sign, -1])     # infinities, NaN, the least value, -0, NaN
+    for call, names in ((dl.diffuser_rope, ("Qo", "Ko")), (dl.diffuser_rope_backward, ("dQ", "dK"))):
+        plain = call(q.cuda(), k.cuda(), freq, magnitude=mag, interleaved=inter)
+        marked = []
+        for x in (q, k):
+            y = x.clone()
+            bits = odd[torch.randint(0, 7, y[..., rot:].shape, generator=gen)].to(word)
+            y[..., rot:] = torch.where(torch.rand(bits.shape, generator=gen) < 0.5, bits.view(dtype), y[..., rot:])
+            marked.append(y.cuda())
+        got = call(*marked, freq, magnitude=mag, interleaved=inter)
+        for x, y, z in zip(marked, got, plain):
+            assert torch.equal(x[..., rot:].contiguous().view(word), y[..., rot:].contiguous().view(word))
+            assert torch.equal(y[..., :rot].contiguous().view(word), z[..., :rot].contiguous().view(word))
+        same = call(*marked, freq, magnitude=mag, interleaved=inter, **dict(zip(names, marked)))
+        for x, y in zip(same, got):
+            assert torch.equal(x.view(word), y.view(word))
