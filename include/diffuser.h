@@ -600,7 +600,9 @@ DIFFUSER_API int diffuser_block_means(const void* K, int64_t B, int64_t Hk, int6
 /*
  * For each query and key head, the blocks with visible keys that score highest,
  *   score(i, c) = sum over the group's heads of q_i . means_c
- * as if computed without rounding (ties: the lowest index; NaN counts as -infinity):
+ * from exact products, summed to 64 bits (ties: the lowest index; NaN counts as -infinity).  Where a score's products
+ * other than 0 are within a factor of 2^31 / G of each other their sum is exact too; else scores closer than
+ * (G + 8) 2^-53 sum |q| |mean| may change places.
  *   blocks   int32 [B][Hk][n][top_k], ascending, -1 behind the last
  * The first sink_blocks blocks, and those less than local_blocks from the query's own (1: its own
  * alone; causal: none after it), come before all others where they are visible; they count towards

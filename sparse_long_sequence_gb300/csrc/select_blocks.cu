@@ -12,8 +12,8 @@
 //   eps = 4 G 17 2^-23 |Q| |K|,
 // |Q| the norm of the group's queries, |K| the largest of the means' (taken once for each head).
 // Blocks more than 2 eps above the top-th value are in, those more than 2 eps below are out, and what
-// lies between is summed again as fp64 would, where 64 G products of bf16 values lose nothing that matters.
-// So the choice is that of exact scores, whatever order they are added in.
+// lies between is summed again as fp64 would, where products of bf16 values are exact, and so are their sums while
+// the products lie within 2^31 / G of each other.  So the choice is that of exact scores, whatever order they are added in.
 //
 // For few queries bound by latency: 16 queries of up to 1024 blocks, 4 key heads with 4 heads each, take 11.0 us;
 // the search is a chain of reductions over one warp.
@@ -210,13 +210,13 @@ __global__ void __launch_bounds__(32 * kMostWarps) select_blocks_kernel(const __
         for (int x = lane; x < forced.count(); x += 32) v[forced.at(x)] = INFINITY;
         if (nv + lane < (nv + 31) / 32 * 32) v[nv + lane] = -INFINITY;
         __syncwarp();
-        const float reach = reach_of(s.G, mass[r], mean_squares), eps = twice_eps(s.G, reach);
+        const float eps = twice_eps(s.G, reach_of(s.G, mass[r], mean_squares));
         uint64_t taken = 0;
         int cand[2];
         if (s.top <= 32 && eps < 1e30f &&
             narrow(v, nv, s.top, eps, lane, cand_x[warp], cand_c[warp], cand, &taken, [&](int c) {
                 return exact_score(reinterpret_cast<const uint32_t*>(q + r * kHeadDim), s.n * (kHeadDim / 2), s.G,
-                                   reinterpret_cast<const uint32_t*>(means + (int64_t)c * kHeadDim), reach, lane);
+                                   reinterpret_cast<const uint32_t*>(means + (int64_t)c * kHeadDim), lane);
             })) {
             const unsigned lo = (unsigned)taken, hi = (unsigned)(taken >> 32), below = (1u << lane) - 1;
             if (lo >> lane & 1) out[__popc(lo & below)] = cand[0];
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(32 * kMostWarps) select_blocks_kernel(const __
                 for (unsigned m = __ballot_sync(kFull, close); rest && m; m &= m - 1) {
                     const int index = c0 + __ffs(m) - 1;
                     const double score = exact_score(row, s.n * (kHeadDim / 2), s.G,
-                                                     reinterpret_cast<const uint32_t*>(means + (int64_t)index * kHeadDim), reach, lane);
+                                                     reinterpret_cast<const uint32_t*>(means + (int64_t)index * kHeadDim), lane);
                     best.offer(score, index, rest, lane);
                 }
                 if (close) v[c] = -INFINITY;

@@ -2,6 +2,8 @@
 // scores, the best of them, and reductions over a warp.
 #pragma once
 
+#include <cfloat>
+
 #include "mma_tiles.cuh"
 #include "selected.h"
 
@@ -38,8 +40,8 @@ __device__ __forceinline__ float squares(uint32_t w, float sum) {
 __device__ __forceinline__ float reach_of(int G, float query, float mean) {
     return sqrtf((float)G) * (sqrtf(query) + kLeastNorm) * (sqrtf(mean) + kLeastNorm);
 }
-// Twice what a score in fp32 is off by at most (select_blocks.cu), and what products of denormal size may lose.
-__device__ __forceinline__ float twice_eps(int G, float reach) { return 2.02f * 68.f * 1.1920929e-7f * (float)G * reach + 1e-35f; }
+// Twice what a score in fp32 is off by at most (select_blocks.cu), and what its 64 G products may lose below 2^-126.
+__device__ __forceinline__ float twice_eps(int G, float reach) { return (float)G * (2.02f * 68.f * 1.1920929e-7f * reach + 1e-35f); }
 
 // x + y = sum + error, without rounding (Knuth's two-sum)
 __device__ __forceinline__ float two_sum(float x, float y, float* error) {
@@ -49,30 +51,32 @@ __device__ __forceinline__ float two_sum(float x, float y, float* error) {
 }
 
 // The score as fp64 would have it or better, in every lane; NaN counts as -infinity.  Products of two bf16 values
-// are exact in fp32, and their sum is held in three fp32 parts (the machine's fp64 rate is a sixtieth of its fp32's:
-// with 16 heads a group most of the choice's time went there); in fp64 where `reach` is so large or small that
-// fp32 products may not be exact.
-__device__ __forceinline__ double exact_score(const uint32_t* q, int64_t head_words, int G, const uint32_t* mean, float reach,
-                                              int lane) {
+// are exact in fp32 from 2^-126 on, and their sum is held in three fp32 parts (the machine's fp64 rate is a sixtieth of
+// its fp32's: with 16 heads a group most of the choice's time went there); in fp64 where a product is smaller, and not
+// 0 by one of its factors, or so large that a sum may not be finite.
+__device__ __forceinline__ double exact_score(const uint32_t* q, int64_t head_words, int G, const uint32_t* mean, int lane) {
     const uint32_t w = mean[lane];
     const float m0 = __uint_as_float(w << 16), m1 = __uint_as_float(w & 0xffff0000u);
-    double t = 0.0;
-    if (reach > 1e-20f && reach < 1e30f) {
-        float a = 0.f, b = 0.f, c = 0.f;
-        auto add = [&](float product) {
-            float e, f;
-            a = two_sum(a, product, &e);
-            b = two_sum(b, e, &f);
-            c = __fadd_rn(c, f);
-        };
+    float a = 0.f, b = 0.f, c = 0.f;
+    bool exact = true;
+    auto add = [&](float x, float m) {
+        const float product = __fmul_rn(x, m);
+        exact &= (fabsf(product) >= FLT_MIN && fabsf(product) < 1e30f) || x == 0.f || m == 0.f;
+        float e, f;
+        a = two_sum(a, product, &e);
+        b = two_sum(b, e, &f);
+        c = __fadd_rn(c, f);
+    };
 #pragma unroll 4
-        for (int h = 0; h < G; ++h) {
-            const uint32_t x = q[h * head_words + lane];
-            add(__fmul_rn(__uint_as_float(x << 16), m0));
-            add(__fmul_rn(__uint_as_float(x & 0xffff0000u), m1));
-        }
-        t = (double)a + ((double)b + (double)c);
-    } else {
+    for (int h = 0; h < G; ++h) {
+        const uint32_t x = q[h * head_words + lane];
+        add(__uint_as_float(x << 16), m0);
+        add(__uint_as_float(x & 0xffff0000u), m1);
+    }
+    double t = (double)a + ((double)b + (double)c);
+    if (!__all_sync(kFull, exact)) {
+        t = 0.0;
+#pragma unroll 1
         for (int h = 0; h < G; ++h) {
             const uint32_t x = q[h * head_words + lane];
             t += (double)__uint_as_float(x << 16) * (double)m0 + (double)__uint_as_float(x & 0xffff0000u) * (double)m1;

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
     if (lane == 0) atomicMax(&largest, top_squares);
     ptx::tc_fence_before();
     __syncthreads();
-    const float reach = reach_of(s.G, mass, __uint_as_float(largest)), eps = twice_eps(s.G, reach);
+    const float eps = twice_eps(s.G, reach_of(s.G, mass, __uint_as_float(largest)));
     const bool far = !(eps < 1e30f);
     float floor = choose && want && !far ? fmaxf(bound - eps, -FLT_MAX) : INFINITY;
     const uint32_t list = mean_tile + kMeanBytes + 4 * tid, full = list + kList * kEntry;
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
     for (unsigned todo = __ballot_sync(kFull, close); todo; todo &= todo - 1) {
         const int l = __ffs(todo) - 1, row = 32 * warp + l;  // the query's lane and row
         const int n = __shfl_sync(kFull, few, l), rest = __shfl_sync(kFull, want, l), blocks = __shfl_sync(kFull, nv, l);
-        const float e = __shfl_sync(kFull, eps, l), far_reach = __shfl_sync(kFull, reach, l);
+        const float e = __shfl_sync(kFull, eps, l);
         const bool all = __shfl_sync(kFull, (int)hard, l);
         Forced f = forced;
         f.sink = __shfl_sync(kFull, forced.sink, l);
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 3) select_tiles_kernel(const __grid_
         f.near = __shfl_sync(kFull, forced.near, l);
         auto exact = [&](int c) {
             return exact_score(reinterpret_cast<const uint32_t*>(q0 + row * kHeadDim), s.n * (kHeadDim / 2), s.G,
-                               reinterpret_cast<const uint32_t*>(means + (int64_t)c * kHeadDim), far_reach, lane);
+                               reinterpret_cast<const uint32_t*>(means + (int64_t)c * kHeadDim), lane);
         };
         int32_t* out = result + (l - lane) * pitch;
         Best best;

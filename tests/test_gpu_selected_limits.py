@@ -84,3 +84,26 @@ def test_features_that_are_not_turned_are_copied(dl, dtype, rot, inter):
         same = call(*marked, freq, magnitude=mag, interleaved=inter, **dict(zip(names, marked)))
         for x, y in zip(same, got):
             assert torch.equal(x.view(word), y.view(word))
+
+
+# ---------------------------------------------------------------- the choice of blocks
+LEAST = 2.0 ** -133                                          # bf16's least value
+
+
+@pytest.mark.parametrize("kind", ["least queries", "least means beside a large one", "both"])
+@pytest.mark.parametrize("top", [1, 7, 20, 40])
+@pytest.mark.parametrize("n,nb", [(300, 150), (12300, 150), (12300, 300)])
+def test_choice_by_products_below_fp32s_range(dl, kind, top, n, nb):
+    """Products of 2^-143 and less, which fp32 has to round; in 64 bits scores are exact."""
+    gen = torch.Generator().manual_seed(4)
+    Hq, Hk = 4, 2
+    whole = lambda *s: torch.randint(-7, 8, s, generator=gen, dtype=torch.float64) * LEAST
+    Q, mean = torch.randn((1, Hq, n, 64), generator=gen) * 1e-3, torch.randn((1, Hk, nb, 64), generator=gen) * 1e-3
+    if kind != "least means beside a large one":
+        Q = whole(1, Hq, n, 64)
+    if kind != "least queries":
+        mean = whole(1, Hk, nb, 64)
+        mean[:, :, 0] = 1.0
+    Q, mean = Q.to(BF), mean.to(BF)
+    got = dl.diffuser_select_blocks(Q.cuda(), mean.cuda(), top, keys=nb * 64, sink_blocks=1, local_blocks=0, causal=False).cpu()
+    assert torch.equal(got, ref.select(Q, mean, top, nb * 64, 1, 0, False, None, None))
