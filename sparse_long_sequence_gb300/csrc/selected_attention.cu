@@ -448,10 +448,20 @@ int launch_tiles(const SelectedArgs& a, char* ws, cudaStream_t stream) {
     return err == cudaSuccess ? DIFFUSER_OK : cuda_fail(err, "selected_tiles_kernel");
 }
 
-// Few queries: what the lists, the partials and their joining would cost outweighs reading a block's
-// keys once for each query that lists it.  (4 heads, 16 blocks a query: 20 us by query and 28 by block for 128
-// queries, 28.5 and 29 for 192, 37 and 29.5 for 256; 32 heads of 8 key heads, 4 blocks: 17 and 27 for 192.)
-bool by_query(const SelectShape& s) { return s.m == 0 || s.B * s.Hk * s.n * s.top <= 10240; }
+// By query, a warp reads 16 KB of a block's keys and values for a query and up to eight heads, 3 us a thousand.  By block,
+// a tile takes as long whether it has a row or 128, 9 us a thousand; its rows' partials 1 us for 25000, and the lists
+// and the launches 12 more than a launch.  So what decides is how many queries a listed block has, which is at most
+// the queries of one sequence and key head: many sequences' single tokens never share one, however many they are.
+// (By query and by block, 16 blocks a query, 4 heads, us: 512 and 2048 single tokens of caches of 16384 keys 32 and 132,
+// 111 and 371; 512 with 8 tokens each 197 and 421, with 32 of 4096 keys 619 and 308.  One sequence's 256 queries of
+// 4096 keys 12 and 22; 640, 8 heads, 28 and 29; 4 heads of 256 queries, one a group, 39 and 23.)
+bool by_query(const SelectShape& s) {
+    if (s.m == 0) return true;
+    BlockLists l;
+    plan_block_lists(s, nullptr, &l);
+    const int64_t listed = s.B * s.Hk * s.n * l.ranks;       // (query, block) pairs
+    return listed * ((s.G + 7) / 8) <= 4000 + 3 * s.B * s.Hk * l.most_tiles + listed * s.G / 75;
+}
 
 }  // namespace
 

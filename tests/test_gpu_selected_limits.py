@@ -107,3 +107,44 @@ def test_choice_by_products_below_fp32s_range(dl, kind, top, n, nb):
     Q, mean = Q.to(BF), mean.to(BF)
     got = dl.diffuser_select_blocks(Q.cuda(), mean.cuda(), top, keys=nb * 64, sink_blocks=1, local_blocks=0, causal=False).cpu()
     assert torch.equal(got, ref.select(Q, mean, top, nb * 64, 1, 0, False, None, None))
+
+
+# ---------------------------------------------------------------- the attention of many sequences' tokens
+@pytest.mark.parametrize("n", [1, 3])
+def test_tokens_of_a_large_batch(dl, n):
+    """160 sequences of 8 key heads: no workspace, and each as it is by itself."""
+    B, Hq, Hk, m, top = 160, 32, 8, 700, 9
+    rand = lambda seed, *s: torch.randn(s, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda").to(BF)
+    q, k, v = rand(1, B, Hq, n, 64), rand(2, B, Hk, m, 64), rand(3, B, Hk, m, 64)
+    lengths = (torch.arange(B, device="cuda") * 37 % (m + 1)).to(torch.int32)
+    blocks = dl.diffuser_select_blocks(q, dl.diffuser_block_means(k, lengths=lengths), top, keys=m, lengths=lengths)
+    assert dl.diffuser_selected_attention_workspace_size(B, Hq, Hk, n, m, top) == 0
+    out, lse = dl.diffuser_selected_attention(q, k, v, blocks, lengths=lengths, save_lse=True)
+    for b in (0, 1, 77, 159):
+        one = [x[b:b + 1].contiguous() for x in (q, k, v, blocks)]
+        o, l = dl.diffuser_selected_attention(*one, lengths=lengths[b:b + 1].clone(), save_lse=True)
+        assert torch.equal(o[0], out[b]) and torch.equal(l[0], lse[b])
+        seen = ref.mask(one[3].cpu(), n, m, True, [int(lengths[b])], None)
+        want, sums, mass = ref.attend(*(x.cpu() for x in one[:3]), seen)
+        # 2^-11 of a weight from its score's fp32 sum, 2^-14 from its parts and the sums (above)
+        assert ((o.double().cpu() - want).abs() <= U * want.abs() + 2.0 ** -10 * mass).all()
+
+
+def test_many_queries_that_list_nothing(dl):
+    """By block: no tiles at all, or none but one head's."""
+    n, top = 800, 12
+    rand = lambda seed, *s: torch.randn(s, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda").to(BF)
+    q, k, v, d = rand(1, 1, 4, n, 64), rand(2, 1, 2, n, 64), rand(3, 1, 2, n, 64), rand(4, 1, 4, n, 64)
+    assert dl.diffuser_selected_attention_workspace_size(1, 4, 2, n, n, top) > 0
+    none = torch.full((1, 2, n, top), -1, dtype=torch.int32, device="cuda")
+    some = none.clone()
+    some[0, 1, :, 0] = 0
+    for blocks in (none, some):
+        out, lse = dl.diffuser_selected_attention(q, k, v, blocks, causal=False, save_lse=True)
+        dq, dk, dv = dl.diffuser_selected_attention_backward(q, k, v, blocks, out, lse, d, causal=False)
+        seen = ref.mask(blocks.cpu(), n, n, False, None, None)
+        want, sums, mass = ref.attend(q.cpu(), k.cpu(), v.cpu(), seen)
+        assert ((out.double().cpu() - want).abs() <= U * want.abs() + 2.0 ** -10 * mass).all()
+        assert torch.equal(lse.cpu() == -math.inf, sums == -math.inf)
+        assert not dq[0, :2].any() and not dk[0, 0].any() and not dv[0, 0].any() and not dk[0, 1, 64:].any()
+        assert bool(dv[0, 1, :64].any()) == (blocks is some)
