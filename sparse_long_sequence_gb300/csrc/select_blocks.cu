@@ -326,9 +326,14 @@ int launch_select_blocks(const SelectShape& s, const void* Q, const void* means,
     Choice a{s, static_cast<const __nv_bfloat16*>(Q), static_cast<const __nv_bfloat16*>(means), sink, local, blocks, kMostQueries, 0};
     // whole loads of a warp, and 4 more floats: the lanes of a product's column fall in other banks
     a.stride = (s.nb + 127) / 128 * 128 + 4;
-    // Many queries have a thread each: 16 x 16384 queries of 256 blocks take 90 us there and 194 here, 32 x 4096 of
-    // 64 blocks 32 and 74, 24 x 1024 of 16 blocks 14 and 17; but 4 x 4096 of 64 blocks, 4 heads a group, 28 there and 18 here.
-    if (s.top <= kTilesTop && s.n >= 64 && s.B * s.Hk * s.n >= 24576) return launch_select_tiles(a, stream);
+    // Many queries have a thread each: 16 x 16384 queries of 256 blocks take 90 us there and 205 here, 16 x 4096 of
+    // 64 blocks 22 and 43, 24 x 1024 of 16 blocks 14 and 18.  There a block of threads goes over the heads of a group one
+    // by one, which costs most where few blocks of threads run at once, and here it goes over the key blocks: 8 x 4096 of 64
+    // blocks take 31 and 32 us with 4 heads a group, 47 and 46 with 8, 102 and 77 with 16; 32 x 4096 186 and 262 with 16,
+    // 556 and 541 with 32; 2 x 32768 of 512 blocks 761 and 1006 with 32; 32768 of them 2371 and 1477 with 64.
+    const int64_t queries = s.B * s.Hk * s.n, many = int64_t(24576) / 8 * (s.G > 8 ? s.G : 8);
+    if (s.top <= kTilesTop && s.n >= 64 && queries >= 24576 && (s.nb >= 512 ? 4 * queries >= many : s.G <= 24 && queries >= many))
+        return launch_select_tiles(a, stream);
     // fewer queries a block of threads where they are many key blocks', or where there are few of them for the SMs
     while (a.tile > 1 && ((int64_t)a.tile * a.stride * 4 > kMostSmem || a.tile / 2 >= s.n)) a.tile /= 2;
     while (a.tile > kWarps && s.B * s.Hk * ((s.n + a.tile - 1) / a.tile) < 2 * 152) a.tile /= 2;

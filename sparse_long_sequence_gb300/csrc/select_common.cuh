@@ -17,7 +17,8 @@ struct Choice {
     int32_t tile;                  // queries of a block of threads: 32, or fewer for many key blocks
     int32_t stride;                // floats of a query's scores
 };
-// many queries, top up to kTilesTop (select_tiles.cu)
+// many queries, top up to kTilesTop (select_tiles.cu), which a list of 32 candidates in shared memory serves; for more a
+// warp a query (16 x 16384 queries of 256 blocks: 111 us with top 20, 215 with 21, 426 with 32, 368 with 33, 355 with 64)
 constexpr int kTilesTop = 20;
 int launch_select_tiles(const Choice& a, cudaStream_t stream);
 

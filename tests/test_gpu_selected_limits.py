@@ -148,3 +148,19 @@ def test_many_queries_that_list_nothing(dl):
         assert torch.equal(lse.cpu() == -math.inf, sums == -math.inf)
         assert not dq[0, :2].any() and not dk[0, 0].any() and not dv[0, 0].any() and not dk[0, 1, 64:].any()
         assert bool(dv[0, 1, :64].any()) == (blocks is some)
+
+
+@pytest.mark.parametrize("B,Hq,Hk,n,m,top,sink,local,causal,lengths,starts", [
+    (1, 40, 1, 24700, 6400, 9, 1, 1, False, None, None),     # many heads a group, few and many key blocks
+    (2, 32, 1, 12500, 33000, 5, 0, 1, True, [33000, 20000], None),
+    (1, 24, 1, 74000, 1500, 3, 0, 1, True, None, None),
+    (1, 8, 2, 12400, 9600, 21, 1, 2, True, None, None),      # more blocks than a thread's list serves
+    (3, 12, 3, 2800, 4000, 32, 2, 1, True, [4000, 900, 3333], None),
+    (1, 4, 1, 24700, 9600, 33, 0, 1, False, [9555], None)])
+def test_choice_for_many_queries_of_grouped_heads(dl, B, Hq, Hk, n, m, top, sink, local, causal, lengths, starts):
+    gen = torch.Generator().manual_seed(5)
+    Q, mean = torch.randn((B, Hq, n, 64), generator=gen).to(BF), torch.randn((B, Hk, -(-m // 64), 64), generator=gen).to(BF)
+    given = [None if x is None else torch.tensor(x, dtype=torch.int32, device="cuda") for x in (lengths, starts)]
+    got = dl.diffuser_select_blocks(Q.cuda(), mean.cuda(), top, keys=m, sink_blocks=sink, local_blocks=local, causal=causal,
+                                    lengths=given[0], starts=given[1]).cpu()
+    assert torch.equal(got, ref.select(Q, mean, top, m, sink, local, causal, lengths, starts))
