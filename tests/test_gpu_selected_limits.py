@@ -6,6 +6,8 @@ import pytest
 import torch
 
 from tests import selected_reference as ref
+from tests.test_gpu_selected import attend, backward, check_attention, check_gradients, inputs
+from tests import test_gpu_selected as plain
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +166,74 @@ def test_choice_for_many_queries_of_grouped_heads(dl, B, Hq, Hk, n, m, top, sink
     got = dl.diffuser_select_blocks(Q.cuda(), mean.cuda(), top, keys=m, sink_blocks=sink, local_blocks=local, causal=causal,
                                     lengths=given[0], starts=given[1]).cpu()
     assert torch.equal(got, ref.select(Q, mean, top, m, sink, local, causal, lengths, starts))
+
+
+# ---------------------------------------------------------------- lists of any values
+def any_lists(gen, B, Hk, n, top, nb):
+    """Falling, repeated, negative, too large, empty; and some as a choice would give them."""
+    blocks = torch.randint(-3, nb + 3, (B, Hk, n, top), generator=gen, dtype=torch.int32)
+    kind = torch.randint(0, 8, (B, Hk, n, 1), generator=gen)
+    blocks = torch.where(kind < 3, blocks.sort(-1).values, blocks)
+    blocks = torch.where(kind == 3, blocks.sort(-1, descending=True).values, blocks)
+    blocks = torch.where(kind == 4, blocks[..., :1], blocks)
+    blocks[:, :, 3::50] = -1
+    blocks[:, :, 4::50] = 2 ** 31 - 1
+    blocks[:, :, 5::50] = -2 ** 31
+    blocks[:, :, 6::50, 1:] = torch.arange(top - 1, dtype=torch.int32)
+    blocks[:, :, 6::50, 0] = 2 ** 31 - 1                     # nothing is above the first entry
+    blocks[:, :, 7::50] = torch.arange(top, dtype=torch.int32)
+    blocks[:, :, 7::50, top // 2] = -2 ** 31                 # one that does not count between those that do
+    return blocks
+
+
+@pytest.mark.parametrize("B,Hq,Hk,n,m,top,causal,lengths,starts", [
+    (2, 2, 2, 1200, 1100, 3, True, [1100, 700], [-20, 0]), (1, 4, 4, 1200, 1100, 4, False, None, None),
+    (2, 6, 2, 1200, 1100, 7, True, [1099, 1], [0, 0]), (1, 3, 1, 1200, 1100, 16, True, None, [0]),
+    (1, 16, 2, 1200, 1100, 12, True, [1000], [0]), (1, 4, 2, 1200, 1100, 33, False, [1090], [0]),
+    (1, 2, 2, 1200, 1100, 64, True, None, [0]), (1, 4, 2, 70, 330, 6, True, [329], None), (2, 9, 1, 5, 1000, 61, False, None, None)])
+def test_any_lists(dl, B, Hq, Hk, n, m, top, causal, lengths, starts):
+    case = (B, Hq, Hk, n, m, top, 0, 0, causal, lengths, starts)
+    Q, K, V, D, _ = inputs(case)
+    blocks = any_lists(torch.Generator().manual_seed(6), B, Hk, n, top, -(-m // 64))
+    assert (dl.diffuser_selected_attention_workspace_size(B, Hq, Hk, n, m, top) > 0) == (n == 1200)
+    seen = ref.mask(blocks, n, m, causal, lengths, starts)
+    out, lse = attend(dl, case, Q, K, V, blocks, save_lse=True)
+    check_attention(out, lse, Q, K, V, seen)
+    grads = backward(dl, case, Q, K, V, blocks, out, lse, D)
+    check_gradients(grads, Q, K, V, D, seen)
+    assert torch.equal(attend(dl, case, Q, K, V, blocks), out)
+    assert all(torch.equal(x, y) for x, y in zip(grads, backward(dl, case, Q, K, V, blocks, out, lse, D)))
+
+
+@pytest.mark.parametrize("B,Hq,Hk,n,m,top,sink,local,causal,lengths,starts", [
+    (1, 16, 2, 900, 2000, 7, 2, 1, True, None, None), (1, 2, 1, 3000, 3000, 5, 1, 1, True, None, None)])
+def test_tiles_of_grouped_heads(dl, B, Hq, Hk, n, m, top, sink, local, causal, lengths, starts):
+    assert dl.diffuser_selected_attention_workspace_size(B, Hq, Hk, n, m, top) > 0
+    plain.test_attention_of_many_queries(dl, (B, Hq, Hk, n, m, top, sink, local, causal, lengths, starts))
+
+
+# ---------------------------------------------------------------- positions of the rotation
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("offset", [0, 1, 777, -5, 3 * 2 ** 20, 2 ** 45 + 12345, -2 ** 33])
+def test_offsets_and_positions_add_up(dl, offset, inter):
+    """An offset alone, and one with positions, against the definition at their sums."""
+    gen = torch.Generator().manual_seed(7)
+    B, n = 2, 21
+    q, k = torch.randn((B, 3, n, 64), generator=gen), torch.randn((B, 2, n, 64), generator=gen)
+    freq, mag = dl.diffuser_rope_frequencies(48, 10000.0, dl.DIFFUSER_ROPE_YARN, 4.0, 4096)
+    own = torch.arange(n).expand(B, n)
+    given = torch.randint(-1000, 1 << 20, (B, n), generator=gen)
+    for call, sign in ((dl.diffuser_rope, 1), (dl.diffuser_rope_backward, -1)):
+        for pos, at in ((None, own), (given, given)):
+            how = dict(magnitude=mag, interleaved=inter)
+            got = call(q.cuda(), k.cuda(), freq, positions=None if pos is None else pos.cuda(), position_offset=offset, **how)
+            same = call(q.cuda(), k.cuda(), freq, positions=(at + offset).cuda(), **how)
+            assert all(torch.equal(x, y) for x, y in zip(got, same))
+            if abs(offset) > 1 << 32:
+                continue                                     # (the reference's angles lose their fractions there)
+            for x, y in zip((q, k), got):
+                want = ref.rope(x, freq, mag, inter, sign * (at + offset))
+                # a cosine's argument is off by 2^-31 turns and its value by 2^-23, the reference's by 2^-53 of 2^22 radians;
+                # three fp32 operations
+                pair = 2.0 ** -20 * mag * x.double().abs().amax(-1, keepdim=True)
+                assert ((y.double().cpu() - want).abs() <= 2.0 ** -24 * want.abs() + pair).all()
