@@ -314,8 +314,8 @@ int launch_block_lists(const SelectShape& s, const int32_t* blocks, const BlockL
     }
     if (err == cudaSuccess) {
         LaunchScope scope(DIFFUSER_KERNEL_AUX, stream);
-        // A unit of more blocks than that is shared out, where its chunks are many too (2 x 262144 queries: 2.95 ms
-        // for the attention with one block of threads a unit, 1.65 so).
+        // A unit of more blocks than that is shared out, where its chunks are many too (2 x 262144 queries: 2.85 ms
+        // for the attention with one block of threads a unit, 1.39 so; one head's 2^20: 108 and 24).
         if (s.nb <= kScanBlocks || l.chunks < 16) {
             err = launch_pdl(place_lists_kernel<true>, dim3((unsigned)units), dim3(kScanThreads), 0, stream, s, l);
         } else {

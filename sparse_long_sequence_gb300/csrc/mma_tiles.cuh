@@ -86,8 +86,8 @@ __device__ __forceinline__ void score(const uint32_t (&k)[8][8], const uint32_t 
             mma(s[M], k[2 * M][2 * e], k[2 * M + 1][2 * e], k[2 * M][2 * e + 1], k[2 * M + 1][2 * e + 1], q[2 * e], q[2 * e + 1]);
     }
 }
-// o[j] += the weights p (laid out as score's result) times the turned values: features
-// feature_of(2j, g) (0, 1) and feature_of(2j + 1, g) (2, 3) of queries 2t (0, 2) and 2t + 1 (1, 3).
+// o[j] += the weights p (laid out as score's result) times the turned values: features F(2j, g) (0, 1)
+// and F(2j + 1, g) (2, 3) of queries 2t (0, 2) and 2t + 1 (1, 3), F(c, g) = 32 (c / 4) + 8 (g / 2) + 2 (c % 4) + g % 2.
 __device__ __forceinline__ void weigh(const uint32_t (&v)[8][8], const float (&p)[4][4], float (&o)[4][4]) {
 #pragma unroll
     for (int M = 0; M < 4; ++M) {
@@ -103,10 +103,7 @@ __device__ __forceinline__ void weigh(const uint32_t (&v)[8][8], const float (&p
         }
     }
 }
-__host__ __device__ __forceinline__ constexpr int feature_of(int c, int g) {
-    return (c >> 2) * 32 + 8 * (g >> 1) + 2 * (c & 3) + (g & 1);
-}
-// Where that feature stands in a row that the lanes write as 8 g + c.
+// Where feature f stands in a row that the lanes write as 8 g + c.
 __host__ __device__ __forceinline__ constexpr int place_of(int f) {
     return 8 * (2 * ((f & 31) >> 3) + (f & 1)) + (f >> 5) * 4 + ((f & 7) >> 1);
 }

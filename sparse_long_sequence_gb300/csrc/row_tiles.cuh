@@ -24,7 +24,6 @@ __device__ __forceinline__ uint32_t place(int row, int chunk) { return row * kRo
 __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(live ? 16 : 0) : "memory");
 }
-template <int kLeft> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory"); }
 // The 64 keys (or values) at `from`, rows from `rows` on as zeros, by `threads` threads.
 template <int kThreads>
 __device__ __forceinline__ void copy_keys(uint32_t to, const __nv_bfloat16* from, int rows, int tid) {
