@@ -7,7 +7,7 @@
 // chunks for each key block, then over the key blocks.  (3) The bitmaps again:
 // a query's place in a list is the number of bits before its own.  (1) and (2) are bound by the latency of a
 // few dependent loads, (3) by the scattered stores of the entries, 4 bytes each: 16 x 16384 queries of 16 blocks
-// take 10, 7 and 27 us.  (A thread that writes a block's entries in order, four a store, halves the
+// take 10, 6 and 25 us.  (A thread that writes a block's entries in order, four a store, halves the
 // sectors and takes 64: the first blocks', which every query lists, are one thread's work.)
 #include <atomic>
 

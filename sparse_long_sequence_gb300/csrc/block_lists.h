@@ -38,11 +38,11 @@ inline int32_t tile_shares(const SelectShape& s, const BlockLists& l, int64_t he
     return (int32_t)(shares < tiles ? shares : tiles < 1 ? 1 : tiles);
 }
 // Where the units have alike lengths one round is enough unless there are 64 tiles or more to a block of threads, of
-// which some take longer (16 x 16384 queries: 422 us with one round, 410 with three; 24 x 4096, 15 tiles each: 128 and
-// 134).  Units of unlike lengths have shares of unlike lengths, which more of them even out, and each has its
+// which some take longer (16 x 16384 queries: 429 us with one round, 422 with three; 24 x 4096, 17 tiles each: 95 and
+// 100).  Units of unlike lengths have shares of unlike lengths, which more of them even out, and each has its
 // start (lengths from a quarter to all, 8 blocks a query: 2 x 12 units of 1024 queries, 4 tiles a block of threads,
-// 26 us with one round and 29 with two; of 4096, 17 tiles, 75 and 70, with three 74; 8 x 12 of 2048, 34 tiles, 144, 131
-// and 125; the backward of 4 x 12 of 4096, 50 tiles, 255, 228 and 228).
+// 28 us with one round and 32 with two; of 4096, 17 tiles, 53 and 53, with three 58; 8 x 12 of 2048, 34 tiles, 145, 135
+// and 130; the backward of 4 x 12 of 4096, 50 tiles, 255, 228 and 228).
 inline int tile_rounds(const SelectShape& s, const BlockLists& l, int64_t here, int resident) {
     const int64_t tiles = l.most_tiles * here / (152 * resident);
     if (!s.lengths) return tiles < 64 ? 1 : kMostRounds;

@@ -6,18 +6,18 @@
 // columns of the products).  Its warps take the listed blocks in turn, each with a running maximum
 // and sum in registers, and join through shared memory.  A block's keys and values go from global
 // memory into the products' registers.  Bound by the cache's bytes, or by a launch and the latency of two
-// dependent loads (16 tokens, 16 heads of 4 key heads, 16 blocks of a cache of up to 65536 keys: 7.3 us; the bytes 2.5).
+// dependent loads (16 tokens, 16 heads of 4 key heads, 16 blocks of a cache of up to 65536 keys: 7.5 us; the bytes 2.5).
 //
 // Many queries: block by block.  The rows (a query of a head) that list a key block (block_lists.cu) make
 // tiles of 128, and a block of four warps walks over a run of tiles: the rows' queries are gathered
 // into shared memory a tile ahead, S = Q K^T and O = P V run on tcgen05 with P handed over through tensor
 // memory in S's place (as two bf16 parts, mma_tiles.cuh: rounded to one it costs 2.2e-3 of the result in the 2-norm for
-// the 1.7e-3 of its own rounding, and saves 11 us of 421), and each thread has one row's scores, maximum and sum,
+// the 1.7e-3 of its own rounding, and saves 11 us of 422), and each thread has one row's scores, maximum and sum,
 // without exchanges.  Each (row, block)
 // leaves a partial result in the order of the tiles: 64 fp32 sums, its maximum and its sum; a second kernel
 // joins a row's partials.  Bound by the partials' way to HBM and back: 256 bytes for 8192 multiplications and
-// additions of a row's scores and as many of its values.  16 x 16384 causal queries of 16 blocks: 421 us, of
-// which the lists take 43, the tiles 216 (1.07 GB out at 5.0 TB/s) and the join 165 (6.5 TB/s).
+// additions of a row's scores and as many of its values.  16 x 16384 causal queries of 16 blocks: 422 us, of
+// which the lists take 41, the tiles 216 (1.07 GB out at 5.0 TB/s) and the join 165 (6.5 TB/s).
 #include <atomic>
 
 #include "block_lists.h"
@@ -347,7 +347,7 @@ selected_tiles_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
     if (warp == 0) ptx::tmem_dealloc(tmem, kTileColumns);
 }
 
-constexpr int kJoined = 4;                   // partials in flight (16 x 16384 queries: 410 us, with 2 or 8 435 and 441)
+constexpr int kJoined = 4;                   // partials in flight (16 x 16384 queries: 422 us, with 2 or 8 446 and 452)
 
 // Sixteen lanes join a row's partials.
 __global__ void __launch_bounds__(256)

@@ -15,7 +15,7 @@
 //
 // Bound by the latency of a tile's steps (copies, products, P and dS, products, dq out: about 6700 cycles with
 // two blocks of threads an SM, which 115 KB of shared memory each allow), then by dq's partials.  16 x 16384 causal queries
-// of 16 blocks: 652 us, of which delta takes 15, the lists 43, the tiles 410 and the join 190 (1.07 GB at 5.7 TB/s).
+// of 16 blocks: 652 us, of which delta takes 15, the lists 41, the tiles 410 and the join 190 (1.07 GB at 5.7 TB/s).
 #include <atomic>
 
 #include "block_lists.h"
@@ -183,7 +183,9 @@ selected_grads_kernel(const __grid_constant__ SelectedArgs a, const __grid_const
         ptx::tmem_ld32_issue(col + 64, dp);
         ptx::tmem_ld_wait32(sc);
         ptx::tmem_ld_wait32(dp);
-        // sc and dp become P and dS, two bf16 a register, in their first halves
+        // sc and dp become P and dS, two bf16 a register, in their first halves.  (Rounded so, half a step of each term of
+        // their sums, they put the gradients 2.8e-3 off in the 2-norm where the results' own rounding leaves 2.0e-3.  Low
+        // parts beside them, as the forward has, would take 32 KB more: one block of threads an SM.)
         const bool whole = __all_sync(kFull, limit >= 32);
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
